@@ -7,7 +7,8 @@ this module raises on import, telling how to build it.
 
 Low-level functions carry the C names (``b2b_plan_create``, ``b2b_run``,
 ...); :class:`Plan`, :class:`ChainPlan` and :class:`GemmPlan` wrap them for
-torch tensors.
+torch tensors, and :class:`PromptAttentionPlan` and
+:class:`SharedPrefixAttentionPlan` (``attention.py``) the attention operators.
 """
 from __future__ import annotations
 
@@ -22,6 +23,10 @@ __all__ = [
     "b2b_plan_device_status", "b2b_plan_set_wait_budget", "b2b_plan_set_debug", "b2b_plan_info",
     "b2b_status_string", "b2b_coordination_matrix", "b2b_probe_operand_image",
     "b2b_probe_operand_layout", "b2b_schedule_table", "b2b_probe_f64_rearrange", "b2b_run_tf32_noalloc", "coordination_matrix",
+    "PromptAttentionPlan", "SharedPrefixAttentionPlan", "b2b_attn_plan_create", "b2b_attn_plan_destroy",
+    "b2b_attn_plan_device_status", "b2b_attn_plan_set_wait_budget", "b2b_attn_plan_set_debug",
+    "b2b_prompt_attention_workspace", "b2b_prompt_attention_run", "b2b_shared_attention_workspace",
+    "b2b_shared_attention_run",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -72,6 +77,15 @@ def _load() -> ctypes.CDLL:
         "b2b_schedule_table": [i32, ctypes.POINTER(i64), i32, ctypes.POINTER(i64), i32],
         "b2b_probe_f64_rearrange": [i32, P, P, P],
         "b2b_run_tf32_noalloc": [i64, i64, i64, i64, i64, P, P, P, P, P],
+        "b2b_attn_plan_create": [ctypes.POINTER(P), i32, i64, i64, i64, ctypes.c_float],
+        "b2b_attn_plan_destroy": [P],
+        "b2b_attn_plan_device_status": [P, P],
+        "b2b_attn_plan_set_wait_budget": [P, u64],
+        "b2b_attn_plan_set_debug": [P, ctypes.c_uint32],
+        "b2b_prompt_attention_workspace": [P, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "b2b_prompt_attention_run": [P, P, P],
+        "b2b_shared_attention_workspace": [P, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "b2b_shared_attention_run": [P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -102,6 +116,15 @@ b2b_probe_operand_layout = _lib.b2b_probe_operand_layout
 b2b_schedule_table = _lib.b2b_schedule_table
 b2b_probe_f64_rearrange = _lib.b2b_probe_f64_rearrange
 b2b_run_tf32_noalloc = _lib.b2b_run_tf32_noalloc
+b2b_attn_plan_create = _lib.b2b_attn_plan_create
+b2b_attn_plan_destroy = _lib.b2b_attn_plan_destroy
+b2b_attn_plan_device_status = _lib.b2b_attn_plan_device_status
+b2b_attn_plan_set_wait_budget = _lib.b2b_attn_plan_set_wait_budget
+b2b_attn_plan_set_debug = _lib.b2b_attn_plan_set_debug
+b2b_prompt_attention_workspace = _lib.b2b_prompt_attention_workspace
+b2b_prompt_attention_run = _lib.b2b_prompt_attention_run
+b2b_shared_attention_workspace = _lib.b2b_shared_attention_workspace
+b2b_shared_attention_run = _lib.b2b_shared_attention_run
 
 
 def _check(code: int, where: str) -> None:
@@ -497,3 +520,6 @@ def probe_f64_rearrange(cfrag):
     _check(_lib.b2b_probe_f64_rearrange(tiles, _ptr(cfrag.contiguous()), _ptr(out), _stream_handle(None)),
            "b2b_probe_f64_rearrange")
     return out
+
+
+from .attention import PromptAttentionPlan, SharedPrefixAttentionPlan  # noqa: E402  (uses the names above)

@@ -1,0 +1,910 @@
+// Attention on the 5th-generation tensor cores (tcgen05), sm_103a:
+//
+//   S = Q.K^T  ->  P = 2^(c S - c m), l = sum P, rounded  ->  O = P.V / l
+//
+// the cascade (A.B).C of this library with a softmax as the step between the
+// two GEMMs.  Scores and probabilities never leave the SM: S is a tcgen05
+// accumulator in tensor memory (row = lane, key = column, fp32), each softmax
+// thread reads its row, and the 16-bit P goes back into the same columns as
+// the A operand of the second GEMM.
+//
+// Online softmax (c = scale * log2 e): a row keeps a reference m and
+// l = sum_j 2^(c s_j - c m); O accumulates sum_j 2^(c s_j - c m) v_j in
+// tensor memory.  m is the first tile's maximum and is moved only when a
+// later maximum exceeds it by more than 8 in the exponent (kRescale), so P
+// stays below 2^8 (exact powers apart, the relative rounding of P and the
+// fp32 sums do not depend on m) and O is rarely rescaled.  A masked score
+// counts as -inf whatever it holds; a row that has seen no key keeps
+// m = -inf, l = 0 and gives zeros.
+//
+// Work items.  An item is one key/value head, one block of query tokens and a
+// range of 128-key tiles.  The rows of a 128-row tile are (token, head of the
+// group), token-major, so that the heads that share a key/value head share
+// its loads and a single token still fills several rows.  Two streams
+// (softmax warpgroup, MMA-issuing thread, S and O accumulators each) run per
+// CTA, so that one stream's softmax overlaps the other's MMAs:
+//   pair items: stream t has rows of its own (tile t of the block), both
+//               read every key tile;
+//   solo items (rows for one tile only): both streams hold the same rows and
+//               take the key tiles alternately; their results are joined at
+//               the end.
+// Long key ranges with few rows are split over items; such an item writes its
+// unnormalised O with (c m, l) as one part, and attn_combine_kernel joins the
+// parts in a fixed order.
+//
+// CTA roles (384 threads, one CTA per SM; items handed out by cluster launch
+// control, so a CTA that finishes early takes the next unstarted item):
+//   warps 0-3, 4-7  softmax and epilogue of stream 0 and 1 (a row per thread)
+//   warps 8, 9      MMA issue of stream 0 and 1 (one thread each)
+//   warp 10         item decoding and TMA loads
+//   warp 11         zeroes the rows of the last value tile past its last key
+//                   (what lies there may be another sequence's, or NaN, and
+//                   0 x NaN is not 0)
+// Every wait is bounded (ptx::BoundedWait) as in the chain kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cstdint>
+
+#include "chain_tc.cuh"
+#include "ptx.cuh"
+
+namespace b2b {
+
+constexpr int kAttnThreads = 384;
+constexpr int kAttnTile = 128;        // query rows and keys of a tile
+constexpr int kAttnItems = 3;         // item descriptors in flight
+constexpr float kAttnRescale = 8.0f;  // exponent (base 2) by which a maximum may exceed its reference
+
+// Ring of key and value tiles, and the shared-memory layout, by padded head size.
+template <int DP>
+struct AttnShape {
+  static constexpr int kPanels = DP / 64;                    // 128-byte column panels of a tile
+  static constexpr int kTileBytes = kPanels * kPanelBytes;   // one Q, K or V tile
+  static constexpr int kRing = DP == 128 ? 5 : 8;
+  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
+  static constexpr int kOffItems = kOffBar + 512;
+  static constexpr int kOffExchange = kOffItems + kAttnItems * 64;
+  static constexpr int kBytes = kOffExchange + kAttnTile * 8;
+};
+
+enum : int {  // barrier slots (8 bytes each)
+  kABFull = 0,        // [8] ring tile landed
+  kABEmpty = 8,       // [8] ring tile read by both streams
+  kABQFull = 16,      // [2] stream's query tile landed
+  kABQEmpty = 18,     // [2] stream's query tile read
+  kABSFull = 20,      // [2] stream's scores computed
+  kABPFull = 22,      // [2] stream's probabilities written (and O rescaled)
+  kABOFull = 24,      // [2] stream's O complete
+  kABJoin = 26,       // [2] solo items: stream 1's (m, l) written; both O read
+  kABItemFull = 28,   // [3] descriptor written
+  kABItemEmpty = 31,  // [3] descriptor no longer read
+  kABFixed = 34,      // [3] last value tile's tail zeroed (one arrival per item)
+  kABNext = 37,       // next item handed out
+  kABDrain = 38,      // [2]
+  kABTail = 40,       // an item's last value tile landed, its tail to be zeroed
+  kASlotNext = 42,    // 16 bytes: cluster launch control's answer
+  kASlotTmem = 44,    // uint32 tensor-memory base, then the int abort flag
+};
+
+enum : int { kAttnPrompt = 0, kAttnShared = 1 };
+
+struct AttnParams {
+  int op;
+  int group, kv_heads, dim;
+  int tile_tokens;     // query tokens of a 128-row tile: 128 / group
+  int tokens;          // query rows of the packed query tensor
+  int batch;           // sequences or requests
+  int causal;          // prompt: causal; (own keys of shared items always are)
+  // prompt
+  const int* cu_q;
+  const int* cu_k;
+  int key_rows;
+  int splits;          // parts per key range (prompt, or the prefix)
+  // shared prefix
+  int fresh;           // new tokens per request
+  int prefix;          // keys of the prefix
+  int prefix_items, row_blocks, block_tokens;
+  int own_splits, own_blocks;
+  const int* lengths;
+  const int* table;    // pages of the requests' own keys, or null (dense)
+  int table_width, page_shift, room;
+  // TMA boxes: key rows of one box in the prompt/prefix and own tensors, bytes of a query box
+  int box_rows, own_box_rows;
+  uint32_t q_bytes, own_q_bytes;
+  // outputs: final (parts == 1) or parts
+  float scale_log2, scale;
+  void* out;
+  long long out_row, out_head;  // element strides
+  float* lse;
+  long long lse_row, lse_head;
+  int wide_stores;     // rows of `out` on 32-byte boundaries: 32-byte stores
+  int parts;
+  float* part_o;       // [parts][tokens * heads][dim]
+  float2* part_ml;     // [parts][tokens * heads]: (c m, l)
+  uint32_t debug;      // bit 0: arm the first ring tile but never fill it
+  int* status;
+  unsigned long long budget_ns;
+};
+
+struct AttnItem {
+  int kind;       // 0 prompt, 1 prefix, 2 own keys, -1 no more items
+  int solo;
+  int head;       // key/value head
+  int tok0, ntok; // first query token, valid tokens of the block
+  int vis0, klen; // keys the first token sees (may be negative), all keys
+  int causal;     // token i sees clamp(vis0 + i, 0, klen) keys, else klen
+  int krow;       // first row of the sequence's keys, or the request
+  int j0, n, n0;  // first key tile, tiles of stream 1 (solo: of both), tiles of stream 0
+  int last;       // keys from the item's first tile on that any row sees
+  int fix;        // rows of the last tile that hold keys (0: all of them)
+  int part;
+  int pad;
+};
+static_assert(sizeof(AttnItem) == 64, "descriptor slot");
+
+namespace attn {
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+template <int R>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
+// Keys that token i of the item's block sees.
+__device__ __forceinline__ int visible(const AttnItem& a, int i) {
+  return a.causal ? clampi(a.vis0 + i, 0, a.klen) : a.klen;
+}
+// Position in the ring of key and value tile j of an item with n tiles: the
+// two streams' first key tiles, then value and key tiles in turn.
+__device__ __forceinline__ uint32_t key_pos(int j) { return static_cast<uint32_t>(j < 2 ? j : 2 * j - 1); }
+__device__ __forceinline__ uint32_t value_pos(int j, int n) { return static_cast<uint32_t>(j + min(n, j + 2)); }
+
+// Key and value tiles of an item in ring order.
+struct RingWalk {
+  int n, keys = 0, values = 0, j = 0;
+  __device__ __forceinline__ explicit RingWalk(int tiles) : n(tiles) {}
+  // Moves to the next position: true for key tile j, false for value tile j.
+  __device__ __forceinline__ bool next() {
+    const bool is_key = keys < n && (keys < 2 || keys <= values + 1);
+    j = is_key ? keys++ : values++;
+    return is_key;
+  }
+};
+
+// Sequence b's first packed row and row count, inside the tensor whatever the table says.
+__device__ __forceinline__ void packed_range(const int* cu, int b, int rows, int& first, int& len) {
+  first = clampi(__ldg(cu + b), 0, rows);
+  len = clampi(__ldg(cu + b + 1), first, rows) - first;
+}
+
+// Fill `a` for item number x (whole warp; every lane gets the same).  False: no such item.
+__device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane, AttnItem& a) {
+  const int block = 2 * p.tile_tokens;
+  int split, splits;
+  if (p.op == kAttnPrompt) {
+    split = x % p.splits;
+    splits = p.splits;
+    x /= p.splits;
+    a.head = x % p.kv_heads;
+    int u = x / p.kv_heads;
+    // Blocks are numbered sequence after sequence, and taken from the end:
+    // under a causal mask a sequence's last blocks see the most keys, and
+    // the longest items are best begun first.
+    int total = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      int first = 0, len = 0;
+      if (b0 + lane < p.batch) packed_range(p.cu_q, b0 + lane, p.tokens, first, len);
+      total += __reduce_add_sync(0xffffffffu, (len + block - 1) / block);
+    }
+    if (u >= total) return false;
+    u = total - 1 - u;
+    int seq = 0, q0 = 0, qlen = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      int first = 0, len = 0;
+      if (b0 + lane < p.batch) packed_range(p.cu_q, b0 + lane, p.tokens, first, len);
+      int sum = (len + block - 1) / block;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const uint32_t here = __ballot_sync(0xffffffffu, sum > u);
+      if (here) {
+        const int l = __ffs(here) - 1;
+        seq = b0 + l;
+        q0 = __shfl_sync(0xffffffffu, first, l);
+        qlen = __shfl_sync(0xffffffffu, len, l);
+        const int before = __shfl_sync(0xffffffffu, sum, l) - (qlen + block - 1) / block;
+        u -= before;
+        break;
+      }
+      u -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    int k0, klen;
+    packed_range(p.cu_k, seq, p.key_rows, k0, klen);
+    a.kind = 0;
+    a.tok0 = q0 + u * block;
+    a.ntok = min(block, qlen - u * block);
+    a.causal = p.causal;
+    a.vis0 = klen - qlen + u * block + 1;
+    a.klen = klen;
+    a.krow = k0;
+    a.part = split;
+  } else if (x < p.prefix_items) {
+    // row blocks of the same keys next to each other: they share them in L2
+    const int rb = x % p.row_blocks;
+    x /= p.row_blocks;
+    split = x % p.splits;
+    splits = p.splits;
+    a.kind = 1;
+    a.head = x / p.splits;
+    a.tok0 = rb * p.block_tokens;
+    a.ntok = min(p.block_tokens, p.tokens - a.tok0);
+    a.causal = 0;
+    a.vis0 = 0;
+    a.klen = p.prefix;
+    a.krow = 0;
+    a.part = split;
+  } else {
+    x -= p.prefix_items;
+    split = x % p.own_splits;
+    splits = p.own_splits;
+    x /= p.own_splits;
+    a.head = x % p.kv_heads;
+    x /= p.kv_heads;
+    const int tb = x % p.own_blocks;
+    const int b = x / p.own_blocks;
+    if (b >= p.batch) return false;
+    const int len = clampi(__ldg(p.lengths + b), 0, p.room);
+    a.kind = 2;
+    a.tok0 = b * p.fresh + tb * block;
+    a.ntok = min(block, p.fresh - tb * block);
+    a.causal = 1;
+    a.vis0 = len - p.fresh + tb * block + 1;
+    a.klen = len;
+    a.krow = b;
+    a.part = (p.prefix_items ? p.splits : 0) + split;
+  }
+  a.solo = a.ntok <= p.tile_tokens;
+  const int seen = visible(a, a.ntok - 1);
+  const int all = (seen + kAttnTile - 1) / kAttnTile;
+  const int chunk = (all + splits - 1) / splits;
+  a.j0 = split * chunk;
+  a.n = clampi(all - a.j0, 0, chunk);
+  const int all0 = (visible(a, min(a.ntok, p.tile_tokens) - 1) + kAttnTile - 1) / kAttnTile;
+  a.n0 = a.solo ? (a.n + 1) / 2 : clampi(all0 - a.j0, 0, a.n);
+  a.last = min(seen - a.j0 * kAttnTile, a.n * kAttnTile);
+  a.fix = a.n > 0 ? a.last % kAttnTile : 0;
+  a.pad = 0;
+  return true;
+}
+
+// Key tiles of stream t.
+__device__ __forceinline__ int stream_tiles(const AttnItem& a, int t) {
+  return t == 0 ? a.n0 : (a.solo ? a.n / 2 : a.n);
+}
+
+}  // namespace attn
+
+// BF16: bf16 operands, else fp16.  DP: padded head size, 64 or 128 (TMA fills
+// the columns past the head size with zeros).
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q_own,
+                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ CUtensorMap tm_k_own, const __grid_constant__ CUtensorMap tm_v_own,
+                const __grid_constant__ AttnParams p) {
+  using namespace ptx;
+  using namespace attn;
+  using L = AttnShape<DP>;
+  constexpr uint32_t kRing = L::kRing;
+  constexpr uint32_t kFmt = BF16 ? 1u : 0u;
+  constexpr uint32_t kColO = 256;  // tensor memory: S0/P0 at 0, S1/P1 at 128, then O0, O1
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bar0 = base + L::kOffBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * kASlotTmem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  AttnItem* items = reinterpret_cast<AttnItem*>(gbase + L::kOffItems);
+  float2* exchange = reinterpret_cast<float2*>(gbase + L::kOffExchange);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (warp == 0) {
+    if (lane < 8) {
+      mbar_init(bar(kABFull + lane), 1);
+      mbar_init(bar(kABEmpty + lane), 2);
+    } else if (lane < 10) {
+      const int t = lane - 8;
+      mbar_init(bar(kABQFull + t), 1);
+      mbar_init(bar(kABQEmpty + t), 1);
+      mbar_init(bar(kABSFull + t), 1);
+      mbar_init(bar(kABPFull + t), 4);
+      mbar_init(bar(kABOFull + t), 1);
+      mbar_init(bar(kABJoin + t), 4);
+      mbar_init(bar(kABDrain + t), 1);
+    } else if (lane < 10 + kAttnItems) {
+      const int s = lane - 10;
+      mbar_init(bar(kABItemFull + s), 1);
+      mbar_init(bar(kABItemEmpty + s), 11);  // 8 softmax warps, 2 MMA threads, warp 11
+      mbar_init(bar(kABFixed + s), 1);
+    } else if (lane == 13) {
+      mbar_init(bar(kABNext), 1);
+      mbar_init(bar(kABTail), 1);
+      *abort_flag = 0;
+    }
+    if (lane < 14) fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  BoundedWait bw{abort_flag, p.status, p.budget_ns, kTimeoutCode};
+  grid_launch_dependents();
+
+  if (warp < 8) {
+    // ------------------------------------------------- softmax and epilogue
+    set_max_regs_up<216>();
+    const int t = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int row_tok = row / p.group;
+    const int row_head = row - row_tok * p.group;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_off + 128u * static_cast<uint32_t>(t);
+    const uint32_t to = tmem + lane_off + kColO + static_cast<uint32_t>(DP * t);
+    const float sl2 = p.scale_log2;
+    const uint64_t sl2x2 = pack2(sl2, sl2);
+    uint32_t nscore = 0, nout = 0, njoin = 0;
+    grid_dependency_wait();  // (the outputs may still be read by the kernel before)
+    for (uint32_t it = 0;; ++it) {
+      const uint32_t islot = it % kAttnItems;
+      if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
+      const AttnItem a = items[islot];
+      if (a.kind < 0) break;
+      const int cnt = stream_tiles(a, t);
+      const int tile0 = a.solo ? 0 : t * p.tile_tokens;  // first token of this stream's tile
+      const int vis = visible(a, tile0 + row_tok);
+      const int vis_min = visible(a, tile0);
+      float m = -INFINITY;
+      uint64_t l2 = 0;
+      bool ok = true;
+      for (int i = 0; i < cnt; ++i) {
+        const int j = a.j0 + (a.solo ? 2 * i + t : i);
+        if (!bw.wait(bar(kABSFull + t), nscore & 1u)) {
+          ok = false;
+          break;
+        }
+        ++nscore;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32u * c, s[c]);
+        tmem_wait_ld();
+        if ((j + 1) * kAttnTile > vis_min) {
+          const int lim = vis - j * kAttnTile;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c * 32 + k >= lim) s[c][k] = 0xff800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int k = 1; k < 31; k += 2)
+            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][k])), __uint_as_float(s[c][k + 1]));
+          mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
+        }
+        const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (i == 0) {
+          m = tile_max;
+        } else if (__any_sync(0xffffffffu, (tile_max - m) * sl2 > kAttnRescale)) {
+          // S complete implies the MMAs before it: O holds every earlier tile
+          // and nothing writes it until this tile's P is handed over.
+          const float m_new = fmaxf(m, tile_max);
+          const float f = m_new == m ? 1.0f : exp2_approx((m - m_new) * sl2);
+          m = m_new;
+          float la, lb;
+          unpack2(l2, la, lb);
+          l2 = pack2(la * f, lb * f);
+#pragma unroll 1
+          for (int c = 0; c < DP / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to + 16u * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st16(to + 16u * c, o);
+          }
+        }
+        const float mc = m == -INFINITY ? 0.0f : m * sl2;
+        const uint64_t mcx2 = pack2(-mc, -mc);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int e = 2 * k;
+            float x0, x1;
+            unpack2(fma2(pack2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), sl2x2, mcx2), x0, x1);
+            x0 = exp2_approx(x0);
+            x1 = exp2_approx(x1);
+            l2 = add2(l2, pack2(x0, x1));
+            w[k] = BF16 ? pack_bf16x2(__float_as_uint(x0), __float_as_uint(x1))
+                        : pack_f16x2(__float_as_uint(x0), __float_as_uint(x1));
+          }
+          tmem_st16(ts + 16u * c, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kABPFull + t));
+      }
+      if (!ok) break;
+      float l;
+      {
+        float la, lb;
+        unpack2(l2, la, lb);
+        l = la + lb;
+      }
+      if (cnt > 0) {
+        if (!bw.wait(bar(kABOFull + t), nout & 1u)) break;
+        ++nout;
+        tc_fence_after();
+      }
+      // Solo items with work in both streams: stream 0 joins the two O.
+      const bool join = a.solo && a.n > 1;
+      float f0 = 1.0f, f1 = 0.0f;
+      if (join) {
+        if (t == 1) {
+          exchange[row] = make_float2(m, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kABJoin));
+        }
+        if (!bw.wait(bar(kABJoin + t), njoin & 1u)) break;
+        ++njoin;
+        if (t == 0) {
+          tc_fence_after();
+          const float2 other = exchange[row];
+          const float m_new = fmaxf(m, other.x);
+          f0 = m == m_new ? 1.0f : exp2_approx((m - m_new) * sl2);
+          f1 = other.x == m_new ? 1.0f : exp2_approx((other.x - m_new) * sl2);
+          m = m_new;
+          l = l * f0 + other.y * f1;
+        }
+      }
+      if (!(a.solo && t == 1)) {
+        const bool valid = row_tok < p.tile_tokens && tile0 + row_tok < a.ntok;
+        const int token = a.tok0 + tile0 + row_tok;
+        const int head = a.head * p.group + row_head;
+        // 16 columns of the row's O, joined
+        auto fetch = [&](int col, float (&x)[16]) {
+          uint32_t o[16];
+          tmem_ld16(to + static_cast<uint32_t>(col), o);
+          if (join) {
+            uint32_t o1[16];
+            tmem_ld16(to + static_cast<uint32_t>(DP + col), o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1;
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]);
+          }
+        };
+        if (p.parts > 1) {
+          const long long heads = p.group * p.kv_heads;
+          const long long at = (static_cast<long long>(a.part) * p.tokens + token) * heads + head;
+          if (valid) p.part_ml[at] = make_float2(m * sl2, l);
+          float* dst = p.part_o + at * p.dim;
+          if (cnt > 0) {  // (a part with l = 0 is not read)
+#pragma unroll 1
+            for (int col = 0; col < DP; col += 16) {
+              float x[16];
+              fetch(col, x);
+#pragma unroll
+              for (int k = 0; k < 16; k += 8) {
+                uint32_t v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(x[k + e]);
+                if (valid && col + k < p.dim) st_global_v8(dst + col + k, v);
+              }
+            }
+          }
+        } else {
+          const float inv = 1.0f / l;
+          if (valid && p.lse)
+            p.lse[token * p.lse_row + head * p.lse_head] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + token * p.out_row + head * p.out_head;
+#pragma unroll 1
+          for (int col = 0; col < DP; col += 16) {
+            float x[16];
+            fetch(col, x);
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float u = l == 0.0f ? 0.0f : x[2 * k] * inv, w = l == 0.0f ? 0.0f : x[2 * k + 1] * inv;
+              v[k] = BF16 ? pack_bf16x2(__float_as_uint(u), __float_as_uint(w))
+                          : pack_f16x2(__float_as_uint(u), __float_as_uint(w));
+            }
+            if (valid) {
+              if (p.wide_stores) {
+                if (col < p.dim) st_global_v8(dst + col, v);
+              } else {
+                if (col < p.dim) *reinterpret_cast<uint4*>(dst + col) = make_uint4(v[0], v[1], v[2], v[3]);
+                if (col + 8 < p.dim) *reinterpret_cast<uint4*>(dst + col + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (join && t == 0 && lane == 0) mbar_arrive(bar(kABJoin + 1));
+      if (lane == 0) mbar_arrive(bar(kABItemEmpty + islot));
+    }
+  } else {
+    set_max_regs_down<72>();
+    if (warp < 10) {
+      // ------------------------------------------------------------ MMA issue
+      const int t = warp - 8;
+      if (lane == 0) {
+        const uint32_t d_s = tmem + 128u * static_cast<uint32_t>(t);
+        const uint32_t d_o = tmem + kColO + static_cast<uint32_t>(DP * t);
+        constexpr uint32_t idesc_qk = make_idesc(kFmt, kAttnTile, 128, false);
+        constexpr uint32_t idesc_pv = make_idesc(kFmt, DP, 128, true);
+        const uint64_t q_desc = desc_sw128(base + static_cast<uint32_t>(t) * L::kTileBytes, 16u, 1024u);
+        const uint64_t k_desc0 = desc_sw128(base + L::kOffRing, 16u, 1024u);
+        const uint64_t v_desc0 = desc_sw128(base + L::kOffRing, kPanelBytes, 1024u);
+        uint32_t ring = 0, nq = 0, np = 0;
+        bool ok = true;
+        for (uint32_t it = 0; ok; ++it) {
+          const uint32_t islot = it % kAttnItems;
+          if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
+          const int kind = items[islot].kind;
+          if (kind < 0) break;
+          const AttnItem& a = items[islot];
+          const int n = a.n, fix = a.fix;
+          const bool solo = a.solo != 0;
+          const int cnt = stream_tiles(a, t);
+          // Every ring tile is waited for and released by both streams, in
+          // order, whether they use it or not: a stream that skipped uses of
+          // a slot could not tell their completions from its own by parity.
+          auto landed = [&](uint32_t pos, uint32_t& slot) -> bool {
+            const uint32_t g = ring + pos;
+            slot = g % kRing;
+            return bw.wait(bar(kABFull + static_cast<int>(slot)), (g / kRing) & 1u);
+          };
+          auto skip = [&](uint32_t pos) -> bool {
+            uint32_t slot;
+            if (!landed(pos, slot)) return false;
+            mbar_arrive(bar(kABEmpty + static_cast<int>(slot)));
+            return true;
+          };
+          int left = cnt;  // score tiles still to issue
+          auto scores = [&](int j) -> bool {
+            uint32_t slot;
+            if (!landed(key_pos(j), slot)) return false;
+            tc_fence_after();
+            const uint64_t kd = k_desc0 + slot * (L::kTileBytes >> 4);
+#pragma unroll
+            for (uint32_t kk = 0; kk < DP / 16; ++kk) {
+              const uint32_t off = (kk / 4) * (kPanelBytes >> 4) + (kk % 4) * 2;
+              mma_ss<false>(d_s, q_desc + off, kd + off, idesc_qk, kk ? 1u : 0u);
+            }
+            tc_commit(bar(kABSFull + t));
+            tc_commit(bar(kABEmpty + static_cast<int>(slot)));
+            if (--left == 0) tc_commit(bar(kABQEmpty + t));
+            return true;
+          };
+          auto outputs = [&](int j, bool first) -> bool {
+            uint32_t slot;
+            if (!landed(value_pos(j, n), slot)) return false;
+            if (fix && j == n - 1) {
+              // (stream 1 has the last tile of every pair item)
+              if (solo || t == 1) mbar_arrive(bar(kABTail));
+              if (!bw.wait(bar(kABFixed + islot), (it / kAttnItems) & 1u)) return false;
+            }
+            if (!bw.wait(bar(kABPFull + t), np & 1u)) return false;
+            ++np;
+            tc_fence_after();
+            const uint64_t vd = v_desc0 + slot * (L::kTileBytes >> 4);
+#pragma unroll
+            for (uint32_t kk = 0; kk < kAttnTile / 16; ++kk)
+              mma_ts<false>(d_o, d_s + kk * 8u, vd + kk * (16u * 128u >> 4), idesc_pv, (kk || !first) ? 1u : 0u);
+            tc_commit(bar(kABEmpty + static_cast<int>(slot)));
+            return true;
+          };
+          if (cnt > 0) {
+            if (!bw.wait(bar(kABQFull + t), nq & 1u)) break;
+            ++nq;
+          }
+          if (solo) {
+            RingWalk w(n);
+            for (int pos = 0; pos < 2 * n && ok; ++pos) {
+              const bool is_key = w.next();
+              if ((w.j & 1) != t)
+                ok = skip(static_cast<uint32_t>(pos));
+              else
+                ok = is_key ? scores(w.j) : outputs(w.j, w.j < 2);
+            }
+          } else {
+            if (cnt > 0) ok = scores(0);
+            for (int j = 0; j < cnt && ok; ++j) ok = outputs(j, j == 0) && (j + 1 == cnt || scores(j + 1));
+            for (int j = cnt; j < n && ok; ++j) ok = skip(key_pos(j)) && skip(value_pos(j, n));
+          }
+          if (ok && cnt > 0) tc_commit(bar(kABOFull + t));
+          if (!ok) break;
+          ring += 2u * static_cast<uint32_t>(n);
+          mbar_arrive(bar(kABItemEmpty + islot));
+        }
+        // every MMA issued must be complete before tensor memory is freed
+        tc_commit(bar(kABDrain + t));
+        drain_wait(bar(kABDrain + t), 0, p.budget_ns);
+      }
+    } else if (warp == 10) {
+      // ------------------------------------------------- items and TMA loads
+      if (lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        if (p.op == kAttnShared) {
+          prefetch_tmap(&tm_q_own);
+          prefetch_tmap(&tm_k_own);
+          prefetch_tmap(&tm_v_own);
+        }
+      }
+      grid_dependency_wait();
+      const uint32_t next_slot = bar0 + 8u * kASlotNext;
+      uint32_t it = 0, ring = 0, issued = 0, nq[2] = {0, 0}, nnext = 0;
+      int x = static_cast<int>(blockIdx.x);
+      bool ok = true;
+      // all lanes: wait on lane 0's behalf
+      auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        bool r = true;
+        if (lane == 0) r = bw.wait(b, parity);
+        return __shfl_sync(0xffffffffu, r, 0);
+      };
+      while (ok) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kABNext), 16);
+          asm volatile(
+              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                  next_slot),
+              "r"(bar(kABNext))
+              : "memory");
+        }
+        AttnItem a;
+        if (decode_item(p, x, lane, a)) {
+          const uint32_t islot = it % kAttnItems;
+          ok = wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u);
+          if (ok && lane == 0) {
+            items[islot] = a;
+            mbar_arrive(bar(kABItemFull + islot));
+          }
+          ++it;
+          const bool own = a.kind == 2;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (stream_tiles(a, t) == 0) continue;
+            ok = wait(bar(kABQEmpty + t), (nq[t] & 1u) ^ 1u);
+            if (!ok) break;
+            if (lane == 0) {
+              const uint32_t fb = bar(kABQFull + t);
+              mbar_arrive_expect_tx(fb, own ? p.own_q_bytes : p.q_bytes);
+              const int tok = a.tok0 + (a.solo ? 0 : t * p.tile_tokens);
+#pragma unroll
+              for (int c = 0; c < L::kPanels; ++c)
+                tma_load_4d(base + static_cast<uint32_t>(t) * L::kTileBytes + c * kPanelBytes, own ? &tm_q_own : &tm_q,
+                            fb, c * 64, 0, a.head, tok);
+            }
+            ++nq[t];
+          }
+          const int box = own ? p.own_box_rows : p.box_rows;
+          const CUtensorMap* km = own ? &tm_k_own : &tm_k;
+          const CUtensorMap* vm = own ? &tm_v_own : &tm_v;
+          const bool paged = own && p.table != nullptr;
+          RingWalk w(a.n);
+          for (int pos = 0; pos < 2 * a.n && ok; ++pos) {
+            const bool is_k = w.next();
+            const int j = w.j;
+            const uint32_t g = ring + static_cast<uint32_t>(pos), slot = g % kRing;
+            ok = wait(bar(kABEmpty + static_cast<int>(slot)), ((g / kRing) & 1u) ^ 1u);
+            if (!ok) break;
+            const int rows = min(kAttnTile, a.last - j * kAttnTile);  // keys of this tile that are seen
+            const int boxes = (rows + box - 1) / box;
+            const int key0 = (a.j0 + j) * kAttnTile;
+            const uint32_t fb = bar(kABFull + static_cast<int>(slot));
+            const uint32_t dst = base + L::kOffRing + slot * L::kTileBytes;
+            if (lane == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(boxes * box) * 128u * L::kPanels);
+            issued = g + 1;
+            __syncwarp();
+            // test support: the very first ring tile is armed but never filled
+            if (!((p.debug & 1u) && g == 0) && lane < boxes) {
+              const int key = key0 + lane * box;
+              int r = key, b = a.krow;
+              if (!own) {
+                r = a.krow + key;
+                b = 0;
+              } else if (paged) {
+                b = __ldg(p.table + static_cast<long long>(a.krow) * p.table_width + (key >> p.page_shift));
+                r = key & ((1 << p.page_shift) - 1);
+              }
+#pragma unroll
+              for (int c = 0; c < L::kPanels; ++c)
+                tma_load_4d(dst + c * kPanelBytes + static_cast<uint32_t>(lane * box) * 128u, is_k ? km : vm, fb, c * 64,
+                            a.head, r, b);
+            }
+            __syncwarp();
+          }
+          ring += 2u * static_cast<uint32_t>(a.n);
+        }
+        // (waited for even on an abort: the answer is written to shared memory)
+        if (lane == 0) drain_wait(bar(kABNext), nnext & 1u, p.budget_ns);
+        __syncwarp();
+        ++nnext;
+        uint32_t got, nx;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+            "ld.shared.b128 h, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t"
+            "mov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+            : "=r"(got), "=r"(nx)
+            : "r"(next_slot)
+            : "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (!got) break;
+        x = static_cast<int>(nx);
+      }
+      if (ok) {
+        const uint32_t islot = it % kAttnItems;
+        if (wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u) && lane == 0) {
+          items[islot].kind = -1;
+          mbar_arrive(bar(kABItemFull + islot));
+        }
+      }
+      // copies still in flight must land before the CTA exits
+      if (lane == 0) {
+        for (int t = 0; t < 2; ++t)
+          if (nq[t] > 0) drain_wait(bar(kABQFull + t), (nq[t] - 1) & 1u, p.budget_ns);
+        for (uint32_t k = 1; k <= kRing && k <= issued; ++k)
+          drain_wait(bar(kABFull + static_cast<int>((issued - k) % kRing)), ((issued - k) / kRing) & 1u, p.budget_ns);
+      }
+    } else {
+      // --------------------------------------- tail of the last value tile
+      uint32_t ring = 0, ntail = 0;
+      for (uint32_t it = 0;; ++it) {
+        const uint32_t islot = it % kAttnItems;
+        if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
+        const int kind = items[islot].kind, n = items[islot].n, fix = items[islot].fix;
+        if (kind < 0) break;
+        if (fix) {
+          // (told by the MMA thread that waits for the tile: this warp does not
+          // follow the slot's other uses)
+          if (!bw.wait(bar(kABTail), ntail & 1u)) break;
+          ++ntail;
+          const uint32_t slot = (ring + value_pos(n - 1, n)) % kRing;
+          const uint32_t dst = base + L::kOffRing + slot * L::kTileBytes;
+          for (int e = fix * 8 + lane; e < kAttnTile * 8; e += 32)
+#pragma unroll
+            for (int c = 0; c < L::kPanels; ++c)
+              st_shared_v4(dst + c * kPanelBytes + static_cast<uint32_t>(e) * 16u, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kABFixed + islot));
+          mbar_arrive(bar(kABItemEmpty + islot));
+        }
+        ring += 2u * static_cast<uint32_t>(n);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of every row: with M = max over parts of c m_p,
+// o = sum_p 2^(c m_p - M) o_p / sum_p 2^(c m_p - M) l_p.  One thread per eight
+// columns of a row; parts in order, so the result does not depend on timing.
+template <bool BF16>
+__global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant__ AttnParams p) {
+  using namespace ptx;
+  using namespace attn;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int heads = p.group * p.kv_heads;
+  const int per_row = p.dim / 8;
+  const long long rows = static_cast<long long>(p.tokens) * heads;
+  const long long id = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long r = id / per_row;
+  if (r >= rows) return;
+  const int col = static_cast<int>(id - r * per_row) * 8;
+  const int token = static_cast<int>(r / heads), head = static_cast<int>(r - static_cast<long long>(token) * heads);
+  if (p.op == kAttnPrompt) {
+    // rows that belong to no sequence are left alone
+    if (token < __ldg(p.cu_q) || token >= __ldg(p.cu_q + p.batch)) return;
+  }
+  float big = -INFINITY;
+  for (int s = 0; s < p.parts; ++s) {
+    const float2 ml = p.part_ml[s * rows + r];
+    if (ml.y != 0.0f) big = fmaxf(big, ml.x);
+  }
+  float l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int s = 0; s < p.parts; ++s) {
+    const float2 ml = p.part_ml[s * rows + r];
+    if (ml.y == 0.0f) continue;
+    const float f = ml.x == big ? 1.0f : exp2f(ml.x - big);
+    l += ml.y * f;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + (s * rows + r) * p.dim + col);
+    const float4 u = src[0], v = src[1];
+    o[0] += u.x * f; o[1] += u.y * f; o[2] += u.z * f; o[3] += u.w * f;
+    o[4] += v.x * f; o[5] += v.y * f; o[6] += v.z * f; o[7] += v.w * f;
+  }
+  const float inv = 1.0f / l;
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float x = l == 0.0f ? 0.0f : o[2 * k] * inv, y = l == 0.0f ? 0.0f : o[2 * k + 1] * inv;
+    w[k] = BF16 ? pack_bf16x2(__float_as_uint(x), __float_as_uint(y)) : pack_f16x2(__float_as_uint(x), __float_as_uint(y));
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + token * p.out_row + head * p.out_head + col) =
+      make_uint4(w[0], w[1], w[2], w[3]);
+  if (col == 0 && p.lse)
+    p.lse[token * p.lse_row + head * p.lse_head] =
+        l == 0.0f ? -INFINITY : static_cast<float>((big + log2f(l)) * 0.6931471805599453);
+}
+
+}  // namespace b2b

@@ -1,0 +1,425 @@
+// C entry points of the attention operators (include/b2b.h): prompts and
+// batches that share a prefix.  Host side only: argument checks, tensor maps,
+// how far key ranges are split over CTAs, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "attention_registry.h"
+#include "b2b.h"
+#include "host.h"
+
+using namespace b2b;
+
+struct b2b_attn_plan_s {
+  b2b_dtype_t dtype;
+  int device, sms;
+  int q_heads, kv_heads, dim, group, tile_tokens;
+  float scale;
+  AttnKernels k;
+  int dp;  // 0: padded head size 64, 1: 128
+  int* d_status;
+  uint64_t budget_ns;
+  uint32_t debug;
+};
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+// The registers of the two warp roles (setmaxnreg) are drawn from what the
+// kernel is launched with: a kernel compiled to fewer would wait for them.
+constexpr int kRegsNeeded = 256 * 216 + 128 * 72;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Strides of a tensor of `rows` x `heads` (x `blocks`) rows of `dim` elements:
+// positive multiples of 16 bytes where the extent is above one.
+b2b_status_t check_rows(const b2b_attn_rows_t& t, int64_t rows, int64_t heads, int64_t blocks) {
+  if (rows == 0 || blocks == 0) return B2B_OK;
+  if (!t.data) return B2B_ERR_INVALID_ARG;
+  if (!aligned16(t.data)) return B2B_ERR_ALIGNMENT;
+  const int64_t extent[3] = {rows, heads, blocks}, stride[3] = {t.row_stride, t.head_stride, t.block_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] == 1) continue;
+    if (stride[i] <= 0 || stride[i] >= (int64_t(1) << 38)) return B2B_ERR_INVALID_ARG;
+    if (stride[i] % 8) return B2B_ERR_ALIGNMENT;
+  }
+  return B2B_OK;
+}
+
+size_t span_bytes(const b2b_attn_rows_t& t, int64_t rows, int64_t heads, int64_t blocks, int64_t dim) {
+  if (rows == 0 || blocks == 0) return 0;
+  return 2 * static_cast<size_t>((rows - 1) * t.row_stride + (heads - 1) * t.head_stride +
+                                 (blocks - 1) * t.block_stride + dim);
+}
+
+// 4-D map with boxes of 64 columns (128 bytes, swizzled) by box1 x 1 x box3 or
+// 1 x box2 rows; extents of one take a stride of one dense row.
+b2b_status_t encode(CUtensorMap* map, const b2b_attn_plan_s* p, const void* data, const int64_t (&ext)[3],
+                    const int64_t (&stride)[3], const uint32_t (&box)[3]) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return B2B_ERR_CUDA;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(p->dim), 0, 0, 0}, strides[3];
+  cuuint32_t boxes[4] = {64, box[0], box[1], box[2]};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = static_cast<cuuint64_t>(ext[i]);
+    strides[i] = static_cast<cuuint64_t>(2 * (ext[i] == 1 ? p->dim : stride[i]));
+  }
+  const CUresult r =
+      fn(map, p->dtype == B2B_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+         const_cast<void*>(data), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? B2B_OK : B2B_ERR_CUDA;
+}
+
+// Queries [tokens][kv_heads][group]: one box is `tokens_box` tokens of one key/value head's group.
+b2b_status_t encode_q(CUtensorMap* map, const b2b_attn_plan_s* p, const b2b_attn_rows_t& t, int64_t tokens,
+                      uint32_t tokens_box) {
+  return encode(map, p, t.data, {p->group, p->kv_heads, tokens},
+                {t.head_stride, t.head_stride * p->group, t.row_stride},
+                {static_cast<uint32_t>(p->group), 1, tokens_box});
+}
+// Keys or values [blocks][rows][kv_heads]: one box is `box` rows of one head.
+b2b_status_t encode_kv(CUtensorMap* map, const b2b_attn_plan_s* p, const b2b_attn_rows_t& t, int64_t rows,
+                       int64_t blocks, uint32_t box) {
+  return encode(map, p, t.data, {p->kv_heads, rows, blocks}, {t.head_stride, t.row_stride, t.block_stride}, {1, box, 1});
+}
+
+// How many parts a range of `tiles` key tiles is cut into when `items` CTAs'
+// worth of work share the key range's length: the smallest modelled time, in
+// key tiles, of ceil(items * s / sms) rounds of (tiles / s + 2) plus joining.
+int split_count(int64_t items, int64_t tiles, int sms) {
+  int best = 1;
+  double best_t = 1e30;
+  for (int s = 1; s <= 64 && (s == 1 || tiles >= 3 * s); ++s) {
+    const double rounds = static_cast<double>((items * s + sms - 1) / sms);
+    const double t = rounds * (static_cast<double>((tiles + s - 1) / s) + 2.0) + (s > 1 ? 4.0 + 0.1 * s : 0.0);
+    if (t < best_t - 1e-9) {
+      best_t = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+int prompt_splits(const b2b_attn_plan_s* p, int64_t batch, int64_t tokens, int64_t key_rows) {
+  const int64_t block = 2 * p->tile_tokens;
+  const int64_t blocks = std::max((tokens + block - 1) / block, std::min(batch, tokens));
+  const int64_t tiles = (key_rows / std::max<int64_t>(batch, 1) + kAttnTile - 1) / kAttnTile;
+  return split_count(blocks * p->kv_heads, tiles, p->sms);
+}
+
+struct SharedShape {
+  int64_t row_blocks, block_tokens, own_blocks, prefix_items, own_items;
+  int splits, own_splits;
+};
+SharedShape shared_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t fresh, int64_t prefix, int64_t room) {
+  SharedShape s = {};
+  const int64_t tokens = batch * fresh, block = 2 * p->tile_tokens;
+  s.block_tokens = tokens <= p->tile_tokens ? p->tile_tokens : block;
+  s.row_blocks = (tokens + s.block_tokens - 1) / s.block_tokens;
+  s.own_blocks = (fresh + block - 1) / block;
+  const int64_t tiles = (prefix + kAttnTile - 1) / kAttnTile, own_tiles = (room + kAttnTile - 1) / kAttnTile;
+  s.splits = prefix ? split_count(s.row_blocks * p->kv_heads, tiles, p->sms) : 0;
+  s.own_splits = room ? split_count(batch * s.own_blocks * p->kv_heads, own_tiles, p->sms) : 1;
+  s.prefix_items = s.splits * s.row_blocks * p->kv_heads;
+  s.own_items = s.own_splits * batch * s.own_blocks * p->kv_heads;
+  return s;
+}
+
+size_t part_bytes(const b2b_attn_plan_s* p, int64_t tokens, int64_t parts) {
+  if (parts <= 1) return 0;
+  return static_cast<size_t>(parts * tokens * p->q_heads) * (static_cast<size_t>(p->dim) * 4 + 8);
+}
+
+b2b_status_t check_current_device(const b2b_attn_plan_s* p) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return B2B_ERR_CUDA;
+  }
+  return dev == p->device ? B2B_OK : B2B_ERR_DEVICE;
+}
+
+AttnParams common_params(const b2b_attn_plan_s* p, int64_t tokens, int64_t batch, const b2b_attn_rows_t& out, float* lse,
+                         void* workspace, int parts) {
+  AttnParams a;
+  std::memset(&a, 0, sizeof(a));
+  a.group = p->group;
+  a.kv_heads = p->kv_heads;
+  a.dim = p->dim;
+  a.tile_tokens = p->tile_tokens;
+  a.tokens = static_cast<int>(tokens);
+  a.batch = static_cast<int>(batch);
+  a.scale = p->scale;
+  a.scale_log2 = static_cast<float>(static_cast<double>(p->scale) * 1.4426950408889634);
+  a.out = out.data;
+  a.out_row = out.row_stride;
+  a.out_head = out.head_stride;
+  a.lse = lse;
+  a.lse_row = p->q_heads;
+  a.lse_head = 1;
+  a.wide_stores = p->dim % 16 == 0 && reinterpret_cast<uintptr_t>(out.data) % 32 == 0 && out.row_stride % 16 == 0 &&
+                  out.head_stride % 16 == 0;
+  a.parts = parts;
+  if (parts > 1) {
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(parts) * tokens * p->q_heads * p->dim);
+  }
+  a.q_bytes = static_cast<uint32_t>(p->group * p->tile_tokens) * 128u * (p->dp ? 2u : 1u);
+  a.debug = p->debug;
+  a.status = p->d_status;
+  a.budget_ns = p->budget_ns;
+  return a;
+}
+
+b2b_status_t launch(const b2b_attn_plan_s* p, CUtensorMap (&maps)[6], AttnParams& a, int64_t items, cudaStream_t stream) {
+  void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &maps[4], &maps[5], &a};
+  cudaError_t e = launch_pdl(p->k.main[p->dp], dim3(static_cast<unsigned>(items)), dim3(kAttnThreads), args,
+                             p->k.smem[p->dp], stream);
+  if (e == cudaSuccess && a.parts > 1) {
+    const int64_t threads = static_cast<int64_t>(a.tokens) * p->q_heads * (p->dim / 8);
+    void* cargs[] = {&a};
+    e = launch_pdl(p->k.combine, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), cargs, 0, stream);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return B2B_ERR_CUDA;
+  }
+  return B2B_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+b2b_status_t b2b_attn_plan_create(b2b_attn_plan_t* out, b2b_dtype_t dtype, int64_t q_heads, int64_t kv_heads,
+                                  int64_t head_dim, float scale) {
+  if (!out) return B2B_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (dtype < B2B_F16_F32OUT || dtype > B2B_TF32_BF16) return B2B_ERR_INVALID_ARG;
+  if (q_heads < 1 || kv_heads < 1 || head_dim < 1 || q_heads % kv_heads) return B2B_ERR_INVALID_ARG;
+  if (!(scale >= 0.0f) || std::isinf(scale)) return B2B_ERR_INVALID_ARG;
+  if (dtype != B2B_F16 && dtype != B2B_BF16) return B2B_ERR_UNSUPPORTED;
+  if (head_dim % 8 || head_dim > 128 || q_heads > 65536 || q_heads / kv_heads > kAttnTile) return B2B_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  b2b_status_t st = check_device(&dev, &sms);
+  if (st != B2B_OK) return st;
+  b2b_attn_plan_s* p = new (std::nothrow) b2b_attn_plan_s();
+  if (!p) return B2B_ERR_CUDA;
+  p->dtype = dtype;
+  p->device = dev;
+  p->sms = sms;
+  p->q_heads = static_cast<int>(q_heads);
+  p->kv_heads = static_cast<int>(kv_heads);
+  p->dim = static_cast<int>(head_dim);
+  p->group = p->q_heads / p->kv_heads;
+  p->tile_tokens = kAttnTile / p->group;
+  p->scale = scale > 0.0f ? scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(head_dim)));
+  p->k = dtype == B2B_F16 ? attn_kernels_f16() : attn_kernels_bf16();
+  p->dp = head_dim > 64;
+  p->budget_ns = kDefaultBudgetNs;
+  cudaFuncAttributes fa;
+  if (cudaFuncSetAttribute(p->k.main[p->dp], cudaFuncAttributeMaxDynamicSharedMemorySize, p->k.smem[p->dp]) !=
+          cudaSuccess ||
+      cudaFuncGetAttributes(&fa, p->k.main[p->dp]) != cudaSuccess || fa.numRegs * kAttnThreads < kRegsNeeded ||
+      cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess) {
+    cudaGetLastError();
+    delete p;
+    return B2B_ERR_CUDA;
+  }
+  if (cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) {
+    cudaGetLastError();
+    cudaFree(p->d_status);
+    delete p;
+    return B2B_ERR_CUDA;
+  }
+  *out = p;
+  return B2B_OK;
+}
+
+b2b_status_t b2b_attn_plan_destroy(b2b_attn_plan_t p) {
+  if (!p) return B2B_OK;
+  cudaFree(p->d_status);
+  delete p;
+  return B2B_OK;
+}
+
+b2b_status_t b2b_attn_plan_device_status(b2b_attn_plan_t p, b2b_stream_t stream) {
+  if (!p) return B2B_ERR_INVALID_ARG;
+  int v = 0;
+  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      cudaMemcpy(&v, p->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) {
+    cudaGetLastError();
+    return B2B_ERR_CUDA;
+  }
+  return static_cast<b2b_status_t>(v);
+}
+
+b2b_status_t b2b_attn_plan_set_wait_budget(b2b_attn_plan_t p, uint64_t budget_ns) {
+  if (!p) return B2B_ERR_INVALID_ARG;
+  p->budget_ns = budget_ns ? std::max<uint64_t>(budget_ns, kMinBudgetNs) : kDefaultBudgetNs;
+  return B2B_OK;
+}
+
+b2b_status_t b2b_attn_plan_set_debug(b2b_attn_plan_t p, uint32_t flags) {
+  if (!p) return B2B_ERR_INVALID_ARG;
+  if (flags & ~B2B_DEBUG_DROP_FIRST_LOAD) return B2B_ERR_INVALID_ARG;
+  p->debug = flags;
+  return B2B_OK;
+}
+
+b2b_status_t b2b_prompt_attention_workspace(b2b_attn_plan_t p, int64_t batch, int64_t tokens, int64_t key_rows,
+                                            size_t* bytes) {
+  if (!p || !bytes || batch < 0 || tokens < 0 || key_rows < 0) return B2B_ERR_INVALID_ARG;
+  if (tokens > kMaxRows || key_rows > kMaxRows || batch > kMaxRows) return B2B_ERR_UNSUPPORTED;
+  *bytes = part_bytes(p, tokens, prompt_splits(p, batch, tokens, key_rows));
+  return B2B_OK;
+}
+
+b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attention_t* r, b2b_stream_t stream) {
+  if (!p || !r || r->batch < 0 || r->tokens < 0 || r->key_rows < 0) return B2B_ERR_INVALID_ARG;
+  if (r->tokens > kMaxRows || r->key_rows > kMaxRows || r->batch > kMaxRows) return B2B_ERR_UNSUPPORTED;
+  if (r->tokens == 0 || r->batch == 0) return B2B_OK;
+  if (!r->cu_q || !r->cu_k) return B2B_ERR_INVALID_ARG;
+  const int64_t hq = p->q_heads, hk = p->kv_heads, d = p->dim;
+  b2b_status_t st = check_rows(r->q, r->tokens, hq, 1);
+  if (st == B2B_OK) st = check_rows(r->k, r->key_rows, hk, 1);
+  if (st == B2B_OK) st = check_rows(r->v, r->key_rows, hk, 1);
+  if (st == B2B_OK) st = check_rows(r->out, r->tokens, hq, 1);
+  if (st != B2B_OK) return st;
+  const size_t on = span_bytes(r->out, r->tokens, hq, 1, d);
+  if (overlaps(r->out.data, on, r->q.data, span_bytes(r->q, r->tokens, hq, 1, d)) ||
+      overlaps(r->out.data, on, r->k.data, span_bytes(r->k, r->key_rows, hk, 1, d)) ||
+      overlaps(r->out.data, on, r->v.data, span_bytes(r->v, r->key_rows, hk, 1, d)))
+    return B2B_ERR_ALIAS;
+  const int splits = prompt_splits(p, r->batch, r->tokens, r->key_rows);
+  const size_t need = part_bytes(p, r->tokens, splits);
+  if (need && (!r->workspace || r->workspace_bytes < need)) return B2B_ERR_INVALID_ARG;
+  if (need && reinterpret_cast<uintptr_t>(r->workspace) % 32) return B2B_ERR_ALIGNMENT;
+  const int64_t block = 2 * p->tile_tokens;
+  const int64_t blocks = r->batch == 1 ? (r->tokens + block - 1) / block : r->tokens / block + std::min(r->batch, r->tokens);
+  const int64_t items = blocks * hk * splits;
+  if (items > kMaxRows) return B2B_ERR_UNSUPPORTED;
+  st = check_current_device(p);
+  if (st != B2B_OK) return st;
+
+  AttnParams a = common_params(p, r->tokens, r->batch, r->out, r->lse, r->workspace, splits);
+  a.op = kAttnPrompt;
+  a.causal = r->causal != 0;
+  a.cu_q = r->cu_q;
+  a.cu_k = r->cu_k;
+  a.key_rows = static_cast<int>(r->key_rows);
+  a.splits = splits;
+  a.box_rows = kAttnTile;
+  CUtensorMap maps[6];
+  st = encode_q(&maps[0], p, r->q, r->tokens, static_cast<uint32_t>(p->tile_tokens));
+  // (without keys nothing is loaded through the key and value maps)
+  maps[2] = maps[3] = maps[0];
+  if (st == B2B_OK && r->key_rows) st = encode_kv(&maps[2], p, r->k, r->key_rows, 1, kAttnTile);
+  if (st == B2B_OK && r->key_rows) st = encode_kv(&maps[3], p, r->v, r->key_rows, 1, kAttnTile);
+  maps[1] = maps[0];
+  maps[4] = maps[2];
+  maps[5] = maps[3];
+  return st == B2B_OK ? launch(p, maps, a, items, reinterpret_cast<cudaStream_t>(stream)) : st;
+}
+
+b2b_status_t b2b_shared_attention_workspace(b2b_attn_plan_t p, int64_t batch, int64_t fresh, int64_t prefix, int64_t room,
+                                            size_t* bytes) {
+  if (!p || !bytes || batch < 0 || fresh < 0 || prefix < 0 || room < 0) return B2B_ERR_INVALID_ARG;
+  if (batch > kMaxRows || fresh > kMaxRows || batch * fresh > kMaxRows || prefix > kMaxRows || room > kMaxRows)
+    return B2B_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (batch * fresh == 0) return B2B_OK;
+  const SharedShape s = shared_shape(p, batch, fresh, prefix, room);
+  *bytes = part_bytes(p, batch * fresh, s.splits + s.own_splits);
+  return B2B_OK;
+}
+
+b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t p, const b2b_shared_attention_t* r, b2b_stream_t stream) {
+  if (!p || !r || r->batch < 0 || r->fresh < 0 || r->prefix < 0 || r->cache_rows < 0 || r->cache_blocks < 0 ||
+      r->table_width < 0)
+    return B2B_ERR_INVALID_ARG;
+  const bool paged = r->page_table != nullptr;
+  if (r->batch > kMaxRows || r->fresh > kMaxRows || r->batch * r->fresh > kMaxRows || r->prefix > kMaxRows ||
+      r->cache_rows > kMaxRows || r->cache_blocks > kMaxRows || r->table_width > kMaxRows)
+    return B2B_ERR_UNSUPPORTED;
+  const int64_t tokens = r->batch * r->fresh;
+  if (tokens == 0) return B2B_OK;
+  if (!r->lengths) return B2B_ERR_INVALID_ARG;
+  if (!paged && r->cache_blocks != r->batch) return B2B_ERR_INVALID_ARG;
+  int page_shift = 0;
+  if (paged) {
+    // pages of 16, 32, 64, .. rows: whole boxes of a tile, whole groups of eight swizzled rows
+    if (r->cache_rows < 16 || (r->cache_rows & (r->cache_rows - 1))) return B2B_ERR_UNSUPPORTED;
+    while ((int64_t(1) << page_shift) < r->cache_rows) ++page_shift;
+  }
+  const int64_t room = paged ? (r->cache_blocks ? r->table_width * r->cache_rows : 0) : r->cache_rows;
+  if (room > kMaxRows) return B2B_ERR_UNSUPPORTED;
+  const int64_t hq = p->q_heads, hk = p->kv_heads, d = p->dim;
+  b2b_status_t st = check_rows(r->q, tokens, hq, 1);
+  if (st == B2B_OK) st = check_rows(r->prefix_k, r->prefix, hk, 1);
+  if (st == B2B_OK) st = check_rows(r->prefix_v, r->prefix, hk, 1);
+  if (st == B2B_OK) st = check_rows(r->cache_k, r->cache_rows, hk, r->cache_blocks);
+  if (st == B2B_OK) st = check_rows(r->cache_v, r->cache_rows, hk, r->cache_blocks);
+  if (st == B2B_OK) st = check_rows(r->out, tokens, hq, 1);
+  if (st != B2B_OK) return st;
+  const size_t on = span_bytes(r->out, tokens, hq, 1, d);
+  if (overlaps(r->out.data, on, r->q.data, span_bytes(r->q, tokens, hq, 1, d)) ||
+      overlaps(r->out.data, on, r->prefix_k.data, span_bytes(r->prefix_k, r->prefix, hk, 1, d)) ||
+      overlaps(r->out.data, on, r->prefix_v.data, span_bytes(r->prefix_v, r->prefix, hk, 1, d)) ||
+      overlaps(r->out.data, on, r->cache_k.data, span_bytes(r->cache_k, r->cache_rows, hk, r->cache_blocks, d)) ||
+      overlaps(r->out.data, on, r->cache_v.data, span_bytes(r->cache_v, r->cache_rows, hk, r->cache_blocks, d)))
+    return B2B_ERR_ALIAS;
+  const SharedShape s = shared_shape(p, r->batch, r->fresh, r->prefix, room);
+  const int parts = s.splits + s.own_splits;
+  const size_t need = part_bytes(p, tokens, parts);
+  if (need && (!r->workspace || r->workspace_bytes < need)) return B2B_ERR_INVALID_ARG;
+  if (need && reinterpret_cast<uintptr_t>(r->workspace) % 32) return B2B_ERR_ALIGNMENT;
+  if (s.prefix_items + s.own_items > kMaxRows) return B2B_ERR_UNSUPPORTED;
+  st = check_current_device(p);
+  if (st != B2B_OK) return st;
+
+  AttnParams a = common_params(p, tokens, r->batch, r->out, r->lse, r->workspace, parts);
+  a.op = kAttnShared;
+  a.causal = 1;
+  a.splits = s.splits;
+  a.fresh = static_cast<int>(r->fresh);
+  a.prefix = static_cast<int>(r->prefix);
+  a.prefix_items = static_cast<int>(s.prefix_items);
+  a.row_blocks = static_cast<int>(s.row_blocks);
+  a.block_tokens = static_cast<int>(s.block_tokens);
+  a.own_splits = s.own_splits;
+  a.own_blocks = static_cast<int>(s.own_blocks);
+  a.lengths = r->lengths;
+  a.table = r->page_table;
+  a.table_width = static_cast<int>(r->table_width);
+  a.page_shift = page_shift;
+  a.room = static_cast<int>(room);
+  a.box_rows = kAttnTile;
+  // Own keys in boxes of a page, or of 32 rows, so that little past a
+  // request's length is read.
+  a.own_box_rows = paged ? static_cast<int>(std::min<int64_t>(r->cache_rows, kAttnTile)) : 32;
+  const uint32_t own_tokens = static_cast<uint32_t>(std::min<int64_t>(r->fresh, p->tile_tokens));
+  a.own_q_bytes = static_cast<uint32_t>(p->group) * own_tokens * 128u * (p->dp ? 2u : 1u);
+  CUtensorMap maps[6];
+  st = encode_q(&maps[0], p, r->q, tokens, static_cast<uint32_t>(p->tile_tokens));
+  if (st == B2B_OK) st = encode_q(&maps[1], p, r->q, tokens, own_tokens);
+  maps[2] = maps[3] = maps[4] = maps[5] = maps[0];
+  if (st == B2B_OK && r->prefix) st = encode_kv(&maps[2], p, r->prefix_k, r->prefix, 1, kAttnTile);
+  if (st == B2B_OK && r->prefix) st = encode_kv(&maps[3], p, r->prefix_v, r->prefix, 1, kAttnTile);
+  if (room) {
+    const uint32_t box = static_cast<uint32_t>(a.own_box_rows);
+    if (st == B2B_OK) st = encode_kv(&maps[4], p, r->cache_k, r->cache_rows, r->cache_blocks, box);
+    if (st == B2B_OK) st = encode_kv(&maps[5], p, r->cache_v, r->cache_rows, r->cache_blocks, box);
+  }
+  return st == B2B_OK ? launch(p, maps, a, s.prefix_items + s.own_items, reinterpret_cast<cudaStream_t>(stream)) : st;
+}
+
+}  // extern "C"

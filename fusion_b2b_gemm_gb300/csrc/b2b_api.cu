@@ -20,6 +20,7 @@
 
 #include "b2b.h"
 #include "chain_f64.cuh"
+#include "host.h"
 #include "registry.h"
 #include "transpose.cuh"
 
@@ -29,9 +30,6 @@ static_assert(kMaxStages == B2B_MAX_STAGES, "stage limit of the C interface");
 
 namespace {
 
-constexpr uint64_t kDefaultBudgetNs = 2000000000ull;
-constexpr uint64_t kMinBudgetNs = 1000000ull;  // 1 ms
-constexpr int kSmemOptin = 232448;         // 227 KB per CTA on sm_100 / sm_103
 constexpr int kSmemBudget = kSmemOptin - 1024;  // minus the 1024-byte alignment slack
 
 enum PlanKind : int {
@@ -41,25 +39,6 @@ enum PlanKind : int {
   kPlanGemmF64 = 3,
   kPlanEmpty = 4
 };
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
 
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
@@ -130,25 +109,6 @@ F64Tables f64_tables() {
     }
   });
   return tab;
-}
-
-b2b_status_t check_device(int* dev_out, int* sms_out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return B2B_ERR_DEVICE;
-  }
-  int major = 0, minor = 0, sms = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return B2B_ERR_CUDA;
-  }
-  if (major != 10 || minor != 3) return B2B_ERR_DEVICE;
-  if (dev_out) *dev_out = dev;
-  if (sms_out) *sms_out = sms;
-  return B2B_OK;
 }
 
 }  // namespace
@@ -816,34 +776,6 @@ b2b_status_t encode_w_mn32(CUtensorMap* map, const void* ptr, int64_t n, int64_t
                       CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B);
   return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ptr, n, k, batch, 32, k_rows,
                    CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B);
-}
-
-// Launch with programmatic stream serialization: the kernel may start while
-// the previous kernel in the stream is finishing; it waits (griddepcontrol)
-// before its first global-memory access.
-cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, void** args, size_t smem,
-                       cudaStream_t stream, int cluster = 1) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelExC(&cfg, fn, args);
-}
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
 }
 
 b2b_status_t encode_chain_maps(b2b_plan_s* p, const void* const* W, const void* A, void* D,

@@ -327,6 +327,117 @@ b2b_status_t b2b_run_tf32_noalloc(int64_t batch, int64_t M, int64_t K, int64_t N
                                   const void* A, const void* B, const void* C, void* D,
                                   b2b_stream_t stream);
 
+/* ------------------------------------------------------------ attention
+ * The cascade with a softmax as the step between its two GEMMs (no
+ * counterpart in the patent, whose step is a rearrangement alone):
+ *
+ *   O = softmax(scale * Q.K^T + mask) . V,   LSE = log of the softmax's sums
+ *
+ * for grouped heads: query head h reads key/value head h / (q_heads /
+ * kv_heads).  Scores and probabilities stay on chip.  Products are
+ * accumulated in fp32; the softmax's maxima, sums and exponentials are fp32;
+ * the probabilities are rounded to the operand type for the second GEMM (as
+ * every intermediate of a cascade is), the output to the same type.
+ *
+ *   - A key that is masked takes no part, whatever its key row holds (NaN and
+ *     infinities too), and neither does a value row past its sequence's or
+ *     request's last visible key.  A value row inside the sequence that a
+ *     causal mask hides from some rows is multiplied by zero for these.
+ *   - A row that sees no key gives zeros, and -inf as its LSE.
+ *   - The masks are given by device arrays of row counts, read when the
+ *     kernel runs: a captured run follows their contents.  Counts and
+ *     offsets outside the tensors are clamped to them; pages outside the pool
+ *     read as zeros.
+ *   - Nothing in a run depends on timing: equal inputs give equal bits.
+ */
+typedef struct b2b_attn_plan_s* b2b_attn_plan_t;
+
+/* Rows of head_dim consecutive elements: element (block, row, head, i) lies at
+ * data + block * block_stride + row * row_stride + head * head_stride + i.
+ * Strides are in elements, positive and multiples of 8; those of an extent of
+ * one are not read.  data must be 16-byte aligned. */
+typedef struct {
+  void* data;
+  int64_t row_stride, head_stride, block_stride;
+} b2b_attn_rows_t;
+
+/*
+ * Create a plan for attention with the given heads.
+ *   dtype     B2B_F16 or B2B_BF16 (inputs, probabilities and output).
+ *   q_heads   a multiple of kv_heads, at most 128 times as many.
+ *   head_dim  a multiple of 8, at most 128.
+ *   scale     factor of the scores, positive; 0 for 1 / sqrt(head_dim).
+ * Binds to the current CUDA device (an sm_103 GPU) and allocates a 4-byte
+ * status word.  The plan is not modified by a run: runs on several streams
+ * may overlap.
+ */
+b2b_status_t b2b_attn_plan_create(b2b_attn_plan_t* out, b2b_dtype_t dtype, int64_t q_heads, int64_t kv_heads,
+                                  int64_t head_dim, float scale);
+b2b_status_t b2b_attn_plan_destroy(b2b_attn_plan_t plan);
+/* As b2b_plan_device_status, b2b_plan_set_wait_budget, b2b_plan_set_debug. */
+b2b_status_t b2b_attn_plan_device_status(b2b_attn_plan_t plan, b2b_stream_t stream);
+b2b_status_t b2b_attn_plan_set_wait_budget(b2b_attn_plan_t plan, uint64_t budget_ns);
+b2b_status_t b2b_attn_plan_set_debug(b2b_attn_plan_t plan, uint32_t flags);
+
+/*
+ * Attention over whole prompts, packed one after the other.
+ *   batch       sequences.  Sequence b owns query rows cu_q[b] .. cu_q[b+1] and
+ *               key rows cu_k[b] .. cu_k[b+1] (device arrays of batch + 1
+ *               non-decreasing offsets).  Query rows of no sequence are not
+ *               written.
+ *   tokens      query rows of q, out and lse; key_rows those of k and v.
+ *   causal      0: every row sees all keys of its sequence.  Else row i sees
+ *               keys j <= i + (keys - queries) of its sequence, so that the
+ *               last row sees all: a piece of a prompt can follow keys of
+ *               earlier pieces.
+ *   out         [tokens][q_heads] rows; must not overlap q, k or v.
+ *   lse         [tokens][q_heads] fp32 or NULL.
+ *   workspace   device memory of at least b2b_prompt_attention_workspace bytes
+ *               (may be NULL when that is 0), 32-byte aligned, for this run
+ *               alone until it has finished.  Its contents need not be set.
+ */
+typedef struct {
+  int64_t batch, tokens, key_rows, causal;
+  b2b_attn_rows_t q, k, v, out;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+} b2b_prompt_attention_t;
+b2b_status_t b2b_prompt_attention_workspace(b2b_attn_plan_t plan, int64_t batch, int64_t tokens, int64_t key_rows,
+                                            size_t* bytes);
+b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t plan, const b2b_prompt_attention_t* run, b2b_stream_t stream);
+
+/*
+ * Attention of a batch of requests that share one prefix, for `fresh` new
+ * tokens of each (one, or a few drafted ones).  The prefix's keys and values
+ * are read once for the whole batch.
+ *   q, out, lse  batch * fresh rows, request after request.
+ *   prefix       key rows of prefix_k and prefix_v (0: none).
+ *   cache_k/v    each request's own keys and values, the new tokens' among
+ *                them: dense [batch][cache_rows] rows (cache_blocks = batch), or,
+ *                with page_table, a pool of cache_blocks pages of cache_rows
+ *                rows (a power of two from 16 up); own key j of request b is row
+ *                j % cache_rows of page page_table[b * table_width + j / cache_rows].
+ *   lengths      [batch] own keys of each request (device).  New token t of a
+ *                request sees the prefix and own keys j < length - fresh + 1 + t.
+ *   workspace    as above, sized by b2b_shared_attention_workspace; `room` is
+ *                cache_rows (dense) or table_width * cache_rows (pages).
+ */
+typedef struct {
+  int64_t batch, fresh, prefix, cache_rows, cache_blocks, table_width;
+  b2b_attn_rows_t q, prefix_k, prefix_v, cache_k, cache_v, out;
+  const int32_t* lengths;
+  const int32_t* page_table;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+} b2b_shared_attention_t;
+b2b_status_t b2b_shared_attention_workspace(b2b_attn_plan_t plan, int64_t batch, int64_t fresh, int64_t prefix,
+                                            int64_t room, size_t* bytes);
+b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t plan, const b2b_shared_attention_t* run, b2b_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -280,3 +280,47 @@ def test_operand_checks_refuse_tensors_on_another_gpu():
         args[bad] = OnGpu(args[bad].t, 0)
         with pytest.raises(ValueError, match=bad.replace("[", r"\[").replace("]", r"\]")):
             b2b.check_operands("f16", 2, 100, 48, N, args["A"], [args["W[0]"], args["W[1]"]], args["D"], device=1)
+
+
+@pytest.mark.parametrize("args,code", [
+    ((1, 32, 8, 128, 0.0), 0),        # valid: fails only on the device check below
+    ((2, 7, 7, 8, 0.25), 0),
+    ((1, 0, 8, 128, 0.0), 1),         # no heads
+    ((1, 32, 0, 128, 0.0), 1),
+    ((1, 32, 5, 128, 0.0), 1),        # query heads not a multiple
+    ((1, 32, 8, 0, 0.0), 1),
+    ((1, 32, 8, 128, -1.0), 1),       # negative, infinite, NaN scale
+    ((1, 32, 8, 128, float("inf")), 1),
+    ((1, 32, 8, 128, float("nan")), 1),
+    ((9, 32, 8, 128, 0.0), 1),        # unknown dtype
+    ((0, 32, 8, 128, 0.0), 2),        # fp32 output, tf32, fp64: no kernel
+    ((3, 32, 8, 128, 0.0), 2),
+    ((4, 32, 8, 128, 0.0), 2),
+    ((1, 32, 8, 100, 0.0), 2),        # head size not a multiple of 8, or above 128
+    ((1, 32, 8, 136, 0.0), 2),
+    ((1, 129, 1, 64, 0.0), 2),        # a group that no tile holds
+])
+def test_attn_plan_create_validates_before_device(args, code):
+    h = ctypes.c_void_p()
+    got = b2b.b2b_attn_plan_create(ctypes.byref(h), *args)
+    if code == 0:
+        import torch
+        if torch.cuda.is_available():
+            pytest.skip("a GPU is present")
+        assert got in (5, 6)
+    else:
+        assert got == code
+    assert not h.value
+
+
+def test_attn_calls_refuse_null_plans():
+    n = ctypes.c_size_t()
+    assert b2b.b2b_attn_plan_create(None, 1, 8, 8, 64, 0.0) == 1
+    assert b2b.b2b_attn_plan_destroy(None) == 0
+    assert b2b.b2b_attn_plan_device_status(None, None) == 1
+    assert b2b.b2b_attn_plan_set_wait_budget(None, 0) == 1
+    assert b2b.b2b_attn_plan_set_debug(None, 0) == 1
+    assert b2b.b2b_prompt_attention_workspace(None, 1, 1, 1, ctypes.byref(n)) == 1
+    assert b2b.b2b_shared_attention_workspace(None, 1, 1, 1, 1, ctypes.byref(n)) == 1
+    assert b2b.b2b_prompt_attention_run(None, None, None) == 1
+    assert b2b.b2b_shared_attention_run(None, None, None) == 1
