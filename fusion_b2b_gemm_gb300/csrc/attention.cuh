@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   AttnItem* items = reinterpret_cast<AttnItem*>(gbase + L::kOffItems);
   float2* exchange = reinterpret_cast<float2*>(gbase + L::kOffExchange);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
 
   if (warp == 0) {
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp < 10) {
       // ------------------------------------------------------------ MMA issue
       const int t = warp - 8;
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t d_s = tmem + 128u * static_cast<uint32_t>(t);
         const uint32_t d_o = tmem + kColO + static_cast<uint32_t>(DP * t);
         constexpr uint32_t idesc_qk = make_idesc(kFmt, kAttnTile, 128, false);
