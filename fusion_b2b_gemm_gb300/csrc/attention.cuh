@@ -75,9 +75,9 @@ enum : int {  // barrier slots (8 bytes each)
   kABQFull = 16,      // [2] stream's query tile landed
   kABQEmpty = 18,     // [2] stream's query tile read
   kABSFull = 20,      // [2] stream's scores computed
-  kABPFull = 22,      // [2] stream's probabilities written (and O rescaled)
-  kABOFull = 24,      // [2] stream's O complete
-  kABJoin = 26,       // [2] solo items: stream 1's (m, l) written; both O read
+  kABPFull = 22,      // [2][2] halves of a stream's probabilities written (and O rescaled)
+  kABOFull = 26,      // [2] stream's O complete
+  kABJoin = 45,       // [2] solo items: stream 1's (m, l) written; both O read
   kABItemFull = 28,   // [3] descriptor written
   kABItemEmpty = 31,  // [3] descriptor no longer read
   kABFixed = 34,      // [3] last value tile's tail zeroed (one arrival per item)
@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(bar(kABQFull + t), 1);
       mbar_init(bar(kABQEmpty + t), 1);
       mbar_init(bar(kABSFull + t), 1);
-      mbar_init(bar(kABPFull + t), 4);
+      mbar_init(bar(kABPFull + 2 * t), 4);
+      mbar_init(bar(kABPFull + 2 * t + 1), 4);
       mbar_init(bar(kABOFull + t), 1);
       mbar_init(bar(kABJoin + t), 4);
       mbar_init(bar(kABDrain + t), 1);
@@ -464,26 +465,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         const float mc = m == -INFINITY ? 0.0f : m * sl2;
         const uint64_t mcx2 = pack2(-mc, -mc);
+        // P in two halves of 64 keys, so that the second GEMM starts on the
+        // first while the second is computed; the row's sum afterwards.
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const int e = 2 * k;
             float x0, x1;
-            unpack2(fma2(pack2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), sl2x2, mcx2), x0, x1);
+            unpack2(fma2(pack2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), sl2x2, mcx2), x0, x1);
             x0 = exp2_approx(x0);
             x1 = exp2_approx(x1);
-            l2 = add2(l2, pack2(x0, x1));
-            w[k] = BF16 ? pack_bf16x2(__float_as_uint(x0), __float_as_uint(x1))
-                        : pack_f16x2(__float_as_uint(x0), __float_as_uint(x1));
+            s[c][2 * k] = __float_as_uint(x0);
+            s[c][2 * k + 1] = __float_as_uint(x1);
+            w[k] = BF16 ? pack_bf16x2(s[c][2 * k], s[c][2 * k + 1]) : pack_f16x2(s[c][2 * k], s[c][2 * k + 1]);
           }
           tmem_st16(ts + 16u * c, w);
+          if (c & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kABPFull + 2 * t + c / 2));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kABPFull + t));
+        uint64_t sums[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          sums[c] = pack2(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+          for (int k = 2; k < 32; k += 2)
+            sums[c] = add2(sums[c], pack2(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])));
+        }
+        l2 = add2(l2, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
       }
       if (!ok) break;
       float l;
@@ -629,10 +642,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             return true;
           };
           int left = cnt;  // score tiles still to issue
-          auto scores = [&](int j) -> bool {
-            uint32_t slot;
-            if (!landed(key_pos(j), slot)) return false;
-            tc_fence_after();
+          auto scores = [&](uint32_t slot) {
             const uint64_t kd = k_desc0 + slot * (L::kTileBytes >> 4);
 #pragma unroll
             for (uint32_t kk = 0; kk < DP / 16; ++kk) {
@@ -642,42 +652,52 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tc_commit(bar(kABSFull + t));
             tc_commit(bar(kABEmpty + static_cast<int>(slot)));
             if (--left == 0) tc_commit(bar(kABQEmpty + t));
-            return true;
           };
-          auto outputs = [&](int j, bool first) -> bool {
-            uint32_t slot;
-            if (!landed(value_pos(j, n), slot)) return false;
+          // O += P.V of tile j, then S of this stream's next tile.  All waits
+          // for tiles come before the ones for P, so that the MMAs follow
+          // one another.
+          auto step = [&](int j, int next, bool first) -> bool {
+            uint32_t vslot, kslot = 0;
+            if (!landed(value_pos(j, n), vslot) || (next < n && !landed(key_pos(next), kslot))) return false;
             if (fix && j == n - 1) {
               // (stream 1 has the last tile of every pair item)
               if (solo || t == 1) mbar_arrive(bar(kABTail));
               if (!bw.wait(bar(kABFixed + islot), (it / kAttnItems) & 1u)) return false;
             }
-            if (!bw.wait(bar(kABPFull + t), np & 1u)) return false;
-            ++np;
-            tc_fence_after();
-            const uint64_t vd = v_desc0 + slot * (L::kTileBytes >> 4);
+            const uint64_t vd = v_desc0 + vslot * (L::kTileBytes >> 4);
 #pragma unroll
-            for (uint32_t kk = 0; kk < kAttnTile / 16; ++kk)
-              mma_ts<false>(d_o, d_s + kk * 8u, vd + kk * (16u * 128u >> 4), idesc_pv, (kk || !first) ? 1u : 0u);
-            tc_commit(bar(kABEmpty + static_cast<int>(slot)));
+            for (uint32_t half = 0; half < 2; ++half) {
+              if (!bw.wait(bar(kABPFull + 2 * t + static_cast<int>(half)), np & 1u)) return false;
+              tc_fence_after();
+#pragma unroll
+              for (uint32_t kk = 4 * half; kk < 4 * half + 4; ++kk)
+                mma_ts<false>(d_o, d_s + kk * 8u, vd + kk * (16u * 128u >> 4), idesc_pv, (kk || !first) ? 1u : 0u);
+            }
+            ++np;
+            tc_commit(bar(kABEmpty + static_cast<int>(vslot)));
+            if (next < n) scores(kslot);
             return true;
           };
-          if (cnt > 0) {
-            if (!bw.wait(bar(kABQFull + t), nq & 1u)) break;
+          const int stride = solo ? 2 : 1, j0 = solo ? t : 0, end = solo ? n : cnt;
+          if (solo && t == 1 && n > 0) ok = skip(key_pos(0));
+          if (cnt > 0 && ok) {
+            uint32_t slot;
+            if (!bw.wait(bar(kABQFull + t), nq & 1u) || !landed(key_pos(j0), slot)) break;
             ++nq;
+            tc_fence_after();
+            scores(slot);
+          }
+          for (int j = j0; j < end && ok; j += stride) {
+            if (solo) {  // the other stream's tiles that lie before this one's in the ring
+              if (j >= 1) ok = skip(value_pos(j - 1, n));
+              if (ok && j + 1 < n && (j + 1 >= 2 || t == 0)) ok = skip(key_pos(j + 1));
+              if (!ok) break;
+            }
+            ok = step(j, j + stride < end ? j + stride : n, j == j0);
           }
           if (solo) {
-            RingWalk w(n);
-            for (int pos = 0; pos < 2 * n && ok; ++pos) {
-              const bool is_key = w.next();
-              if ((w.j & 1) != t)
-                ok = skip(static_cast<uint32_t>(pos));
-              else
-                ok = is_key ? scores(w.j) : outputs(w.j, w.j < 2);
-            }
+            if (ok && n > 0 && ((n - 1) & 1) != t) ok = skip(value_pos(n - 1, n));
           } else {
-            if (cnt > 0) ok = scores(0);
-            for (int j = 0; j < cnt && ok; ++j) ok = outputs(j, j == 0) && (j + 1 == cnt || scores(j + 1));
             for (int j = cnt; j < n && ok; ++j) ok = skip(key_pos(j)) && skip(value_pos(j, n));
           }
           if (ok && cnt > 0) tc_commit(bar(kABOFull + t));
