@@ -32,11 +32,12 @@
 // unnormalised O with (c m, l) as one part, and attn_combine_kernel joins the
 // parts in a fixed order.
 //
-// CTA roles (384 threads, one CTA per SM; items handed out by cluster launch
+// CTA roles (512 threads, one CTA per SM; items handed out by cluster launch
 // control, so a CTA that finishes early takes the next unstarted item):
-//   warps 0-3, 4-7  softmax and epilogue of stream 0 and 1 (a row per thread)
+//   warps 0-3, 4-7  softmax of stream 0 and 1 (a row per thread)
 //   warps 8, 9      MMA issue of stream 0 and 1 (one thread each)
 //   warp 10         item decoding and TMA loads
+//   warps 12-15     epilogue of both streams, beside the next item's softmax
 //   warp 11         zeroes the rows of the last value tile past its last key
 //                   (what lies there may be another sequence's, or NaN, and
 //                   0 x NaN is not 0)
@@ -51,7 +52,10 @@
 
 namespace b2b {
 
-constexpr int kAttnThreads = 384;
+constexpr int kAttnThreads = 512;
+// registers of a softmax, an epilogue and another thread: 128 of each thread at launch, shared out anew
+constexpr int kAttnSoftmaxRegs = 176, kAttnEpilogueRegs = 96, kAttnOtherRegs = 64;
+static_assert(256 * kAttnSoftmaxRegs + 128 * kAttnEpilogueRegs + 128 * kAttnOtherRegs <= 65536, "register file");
 constexpr int kAttnTile = 128;        // query rows and keys of a tile
 constexpr int kAttnItems = 3;         // item descriptors in flight
 constexpr float kAttnRescale = 8.0f;  // exponent (base 2) by which a maximum may exceed its reference
@@ -66,7 +70,8 @@ struct AttnShape {
   static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
   static constexpr int kOffItems = kOffBar + 512;
   static constexpr int kOffExchange = kOffItems + kAttnItems * 64;
-  static constexpr int kBytes = kOffExchange + kAttnTile * 8;
+  static constexpr int kBytes = kOffExchange + 2 * kAttnTile * 8;
+  static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
 enum : int {  // barrier slots (8 bytes each)
@@ -77,22 +82,49 @@ enum : int {  // barrier slots (8 bytes each)
   kABSFull = 20,      // [2] stream's scores computed
   kABPFull = 22,      // [2][2] halves of a stream's probabilities written (and O rescaled)
   kABOFull = 26,      // [2] stream's O complete
-  kABJoin = 45,       // [2] solo items: stream 1's (m, l) written; both O read
+  kABMlFull = 45,     // [2] stream's (m, l) written
+  kABMlEmpty = 47,    // [2] stream's (m, l) read
+  kABOEmpty = 49,     // [2] stream's O read
+  kABTail = 51,       // [3] last value tile landed (one arrival per item)
   kABItemFull = 28,   // [3] descriptor written
   kABItemEmpty = 31,  // [3] descriptor no longer read
   kABFixed = 34,      // [3] last value tile's tail zeroed (one arrival per item)
   kABNext = 37,       // next item handed out
   kABDrain = 38,      // [2]
-  kABTail = 40,       // an item's last value tile landed, its tail to be zeroed
   kASlotNext = 42,    // 16 bytes: cluster launch control's answer
   kASlotTmem = 44,    // uint32 tensor-memory base, then the int abort flag
 };
 
 enum : int { kAttnPrompt = 0, kAttnShared = 1 };
 
+// Division of 0 <= x < 2^31 by a number fixed at launch: floor(x mul / 2^32) >> shift
+// with mul = ceil(2^(31 + bits) / d), bits = ceil(log2 d), is exact for such x.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  static FastDiv of(uint32_t d) {
+    uint32_t bits = 0;
+    while ((uint64_t(1) << bits) < d) ++bits;
+    if (bits == 0) return {1, 0, 0};
+    return {d, static_cast<uint32_t>(((uint64_t(1) << (31 + bits)) + d - 1) / d), bits - 1};
+  }
+  // Quotient; x becomes the remainder.
+  __device__ __forceinline__ int split(int& x) const {
+    if (d == 1) {
+      const int q = x;
+      x = 0;
+      return q;
+    }
+    const uint32_t q = __umulhi(static_cast<uint32_t>(x), mul) >> shift;
+    x -= static_cast<int>(q * d);
+    return static_cast<int>(q);
+  }
+  __device__ __forceinline__ int quotient(int x) const { return split(x); }
+};
+
 struct AttnParams {
   int op;
   int group, kv_heads, dim;
+  FastDiv by_group, by_tokens, by_kv_heads, by_block, by_splits, by_row_blocks, by_own_splits, by_own_blocks;  // (by_block: 2 tile_tokens)
   int tile_tokens;     // query tokens of a 128-row tile: 128 / group
   int tokens;          // query rows of the packed query tensor
   int batch;           // sequences or requests
@@ -101,12 +133,10 @@ struct AttnParams {
   const int* cu_q;
   const int* cu_k;
   int key_rows;
-  int splits;          // parts per key range (prompt, or the prefix)
   // shared prefix
   int fresh;           // new tokens per request
   int prefix;          // keys of the prefix
-  int prefix_items, row_blocks, block_tokens;
-  int own_splits, own_blocks;
+  int prefix_items, block_tokens;
   const int* lengths;
   const int* table;    // pages of the requests' own keys, or null (dense)
   int table_width, page_shift, room;
@@ -121,11 +151,13 @@ struct AttnParams {
   long long lse_row, lse_head;
   int wide_stores;     // rows of `out` on 32-byte boundaries: 32-byte stores
   int parts;
-  float* part_o;       // [parts][tokens * heads][dim]
-  float2* part_ml;     // [parts][tokens * heads]: (c m, l)
+  // Rows of the parts are numbered (key/value head, token, head of the group),
+  // as the lanes of a tile hold them: a warp's stores are consecutive.
+  float* part_o;       // [parts][dim / 8][rows][8]
+  float2* part_ml;     // [parts][rows]: (c m, l)
   uint32_t debug;      // bit 0: arm the first ring tile but never fill it
   int* status;
-  unsigned long long budget_ns;
+  uint32_t budget_ns;
 };
 
 struct AttnItem {
@@ -183,6 +215,30 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// As BoundedWait, in fewer instructions (a 32-bit clock, the status word
+// written once at the kernel's end): the roles' code together has to stay in
+// the instruction cache.  With BoundedWait in every wait it was 84 KB, and a
+// fifth of the warps' time on short prompts went by waiting for instructions.
+struct Wait {
+  volatile int* abort_flag;
+  uint32_t budget_ns;
+  __device__ __forceinline__ static uint32_t now() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+  }
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint32_t t0 = now();
+    do {
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+      if (*abort_flag) return false;
+    } while (now() - t0 < budget_ns);
+    *abort_flag = 1;
+    return false;
+  }
+};
+
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 // Keys that token i of the item's block sees.
 __device__ __forceinline__ int visible(const AttnItem& a, int i) {
@@ -214,29 +270,26 @@ __device__ __forceinline__ void packed_range(const int* cu, int b, int rows, int
 // Fill `a` for item number x (whole warp; every lane gets the same).  False: no such item.
 __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane, AttnItem& a) {
   const int block = 2 * p.tile_tokens;
-  int split, splits;
+  const FastDiv* by_splits = &p.by_splits;
   if (p.op == kAttnPrompt) {
-    split = x % p.splits;
-    splits = p.splits;
-    x /= p.splits;
-    a.head = x % p.kv_heads;
-    int u = x / p.kv_heads;
-    // Blocks are numbered sequence after sequence, and taken from the end:
-    // under a causal mask a sequence's last blocks see the most keys, and
-    // the longest items are best begun first.
-    int total = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      int first = 0, len = 0;
-      if (b0 + lane < p.batch) packed_range(p.cu_q, b0 + lane, p.tokens, first, len);
-      total += __reduce_add_sync(0xffffffffu, (len + block - 1) / block);
-    }
-    if (u >= total) return false;
-    u = total - 1 - u;
-    int seq = 0, q0 = 0, qlen = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      int first = 0, len = 0;
-      if (b0 + lane < p.batch) packed_range(p.cu_q, b0 + lane, p.tokens, first, len);
-      int sum = (len + block - 1) / block;
+    int u = p.by_splits.split(x);
+    a.part = x;
+    x = u;
+    u = p.by_kv_heads.split(x);
+    a.head = x;
+    // Blocks are numbered from the end of the last sequence: under a causal
+    // mask a sequence's last blocks see the most keys, and the longest items
+    // are best begun first.
+    int seq = 0, qlen = 0, at = 0, first = 0;
+    bool found = false;
+#pragma unroll 1
+    for (int b0 = (p.batch - 1) & ~31; b0 >= 0; b0 -= 32) {
+      // lane 0 holds the last sequence of the 32
+      const int b = b0 + 31 - lane;
+      int q0 = 0, len = 0;
+      if (b < p.batch) packed_range(p.cu_q, b, p.tokens, q0, len);
+      const int own = p.by_block.quotient(len + block - 1);
+      int sum = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -245,70 +298,66 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
       const uint32_t here = __ballot_sync(0xffffffffu, sum > u);
       if (here) {
         const int l = __ffs(here) - 1;
-        seq = b0 + l;
-        q0 = __shfl_sync(0xffffffffu, first, l);
+        seq = b0 + 31 - l;
+        first = __shfl_sync(0xffffffffu, q0, l);
         qlen = __shfl_sync(0xffffffffu, len, l);
-        const int before = __shfl_sync(0xffffffffu, sum, l) - (qlen + block - 1) / block;
-        u -= before;
+        at = (__shfl_sync(0xffffffffu, sum, l) - 1 - u) * block;  // u counts from the sequence's end
+        found = true;
         break;
       }
       u -= __shfl_sync(0xffffffffu, sum, 31);
     }
+    if (!found) return false;
     int k0, klen;
     packed_range(p.cu_k, seq, p.key_rows, k0, klen);
     a.kind = 0;
-    a.tok0 = q0 + u * block;
-    a.ntok = min(block, qlen - u * block);
+    a.tok0 = first + at;
+    a.ntok = min(block, qlen - at);
     a.causal = p.causal;
-    a.vis0 = klen - qlen + u * block + 1;
+    a.vis0 = klen - qlen + at + 1;
     a.klen = klen;
     a.krow = k0;
-    a.part = split;
   } else if (x < p.prefix_items) {
     // row blocks of the same keys next to each other: they share them in L2
-    const int rb = x % p.row_blocks;
-    x /= p.row_blocks;
-    split = x % p.splits;
-    splits = p.splits;
+    int u = p.by_row_blocks.split(x);
+    a.tok0 = x * p.block_tokens;
+    a.head = p.by_splits.split(u);
+    a.part = u;
     a.kind = 1;
-    a.head = x / p.splits;
-    a.tok0 = rb * p.block_tokens;
     a.ntok = min(p.block_tokens, p.tokens - a.tok0);
     a.causal = 0;
     a.vis0 = 0;
     a.klen = p.prefix;
     a.krow = 0;
-    a.part = split;
   } else {
     x -= p.prefix_items;
-    split = x % p.own_splits;
-    splits = p.own_splits;
-    x /= p.own_splits;
-    a.head = x % p.kv_heads;
-    x /= p.kv_heads;
-    const int tb = x % p.own_blocks;
-    const int b = x / p.own_blocks;
-    if (b >= p.batch) return false;
+    by_splits = &p.by_own_splits;
+    int u = p.by_own_splits.split(x);
+    a.part = x;
+    int v = p.by_kv_heads.split(u);
+    a.head = u;
+    const int b = p.by_own_blocks.split(v);
+    const int at = v * block;
     const int len = clampi(__ldg(p.lengths + b), 0, p.room);
     a.kind = 2;
-    a.tok0 = b * p.fresh + tb * block;
-    a.ntok = min(block, p.fresh - tb * block);
+    a.tok0 = b * p.fresh + at;
+    a.ntok = min(block, p.fresh - at);
     a.causal = 1;
-    a.vis0 = len - p.fresh + tb * block + 1;
+    a.vis0 = len - p.fresh + at + 1;
     a.klen = len;
     a.krow = b;
-    a.part = (p.prefix_items ? p.splits : 0) + split;
   }
   a.solo = a.ntok <= p.tile_tokens;
   const int seen = visible(a, a.ntok - 1);
   const int all = (seen + kAttnTile - 1) / kAttnTile;
-  const int chunk = (all + splits - 1) / splits;
-  a.j0 = split * chunk;
+  const int chunk = by_splits->quotient(all + static_cast<int>(by_splits->d) - 1);
+  a.j0 = a.part * chunk;
   a.n = clampi(all - a.j0, 0, chunk);
   const int all0 = (visible(a, min(a.ntok, p.tile_tokens) - 1) + kAttnTile - 1) / kAttnTile;
   a.n0 = a.solo ? (a.n + 1) / 2 : clampi(all0 - a.j0, 0, a.n);
   a.last = min(seen - a.j0 * kAttnTile, a.n * kAttnTile);
   a.fix = a.n > 0 ? a.last % kAttnTile : 0;
+  if (a.kind == 2 && p.prefix_items) a.part += static_cast<int>(p.by_splits.d);
   a.pad = 0;
   return true;
 }
@@ -335,10 +384,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr uint32_t kFmt = BF16 ? 1u : 0u;
   constexpr uint32_t kColO = 256;  // tensor memory: S0/P0 at 0, S1/P1 at 128, then O0, O1
 
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // (every byte is used: the swizzled tiles need a base on 1024 bytes, which
+  // dynamic shared memory has when a kernel has no other; checked below)
+  const uint32_t base = smem_u32(smem_raw);
+  uint8_t* gbase = smem_raw;
   const uint32_t bar0 = base + L::kOffBar;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * kASlotTmem);
@@ -349,6 +399,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
 
+  if (base & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kTimeoutCode);
+    return;
+  }
   if (warp == 0) {
     if (lane < 8) {
       mbar_init(bar(kABFull + lane), 1);
@@ -361,16 +415,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(bar(kABPFull + 2 * t), 4);
       mbar_init(bar(kABPFull + 2 * t + 1), 4);
       mbar_init(bar(kABOFull + t), 1);
-      mbar_init(bar(kABJoin + t), 4);
+      mbar_init(bar(kABMlFull + t), 4);
+      mbar_init(bar(kABMlEmpty + t), 4);
+      mbar_init(bar(kABOEmpty + t), 4);
       mbar_init(bar(kABDrain + t), 1);
     } else if (lane < 10 + kAttnItems) {
       const int s = lane - 10;
       mbar_init(bar(kABItemFull + s), 1);
-      mbar_init(bar(kABItemEmpty + s), 11);  // 8 softmax warps, 2 MMA threads, warp 11
+      mbar_init(bar(kABItemEmpty + s), 15);  // 8 softmax and 4 epilogue warps, 2 MMA threads, warp 11
       mbar_init(bar(kABFixed + s), 1);
+      mbar_init(bar(kABTail + s), 1);
     } else if (lane == 13) {
       mbar_init(bar(kABNext), 1);
-      mbar_init(bar(kABTail), 1);
       *abort_flag = 0;
     }
     if (lane < 14) fence_barrier_init();
@@ -383,23 +439,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  BoundedWait bw{abort_flag, p.status, p.budget_ns, kTimeoutCode};
+  const Wait bw{abort_flag, p.budget_ns};
   grid_launch_dependents();
 
   if (warp < 8) {
-    // ------------------------------------------------- softmax and epilogue
-    set_max_regs_up<216>();
+    // -------------------------------------------------------------- softmax
+    set_max_regs_up<kAttnSoftmaxRegs>();
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int row_tok = row / p.group;
-    const int row_head = row - row_tok * p.group;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_off + 128u * static_cast<uint32_t>(t);
     const uint32_t to = tmem + lane_off + kColO + static_cast<uint32_t>(DP * t);
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = pack2(sl2, sl2);
-    uint32_t nscore = 0, nout = 0, njoin = 0;
-    grid_dependency_wait();  // (the outputs may still be read by the kernel before)
+    uint32_t nscore = 0, nml = 0;
     for (uint32_t it = 0;; ++it) {
       const uint32_t islot = it % kAttnItems;
       if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
@@ -499,112 +553,142 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         l2 = add2(l2, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
       }
       if (!ok) break;
-      float l;
-      {
+      if (cnt > 0) {
+        if (!bw.wait(bar(kABMlEmpty + t), (nml & 1u) ^ 1u)) break;
+        ++nml;
         float la, lb;
         unpack2(l2, la, lb);
-        l = la + lb;
+        exchange[t * kAttnTile + row] = make_float2(m, la + lb);
       }
-      if (cnt > 0) {
-        if (!bw.wait(bar(kABOFull + t), nout & 1u)) break;
-        ++nout;
+      __syncwarp();
+      if (lane == 0) {
+        if (cnt > 0) mbar_arrive(bar(kABMlFull + t));
+        mbar_arrive(bar(kABItemEmpty + islot));
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------- epilogue
+    set_max_regs_down<kAttnEpilogueRegs>();
+    const int row = (warp & 3) * 32 + lane;
+    const int row_tok = row / p.group;
+    const int row_head = row - row_tok * p.group;
+    const uint32_t to0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO;
+    const float sl2 = p.scale_log2;
+    const long long part_rows = static_cast<long long>(p.tokens) * (p.group * p.kv_heads);
+    uint32_t nout[2] = {0, 0};
+    grid_dependency_wait();  // (the outputs may still be read by the kernel before)
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
+      const uint32_t islot = it % kAttnItems;
+      if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
+      const AttnItem a = items[islot];
+      if (a.kind < 0) break;
+      // (m, l) of stream t's row, once its O is complete
+      auto take = [&](int t, float& m, float& l) -> bool {
+        m = -INFINITY;
+        l = 0.0f;
+        if (stream_tiles(a, t) == 0) return true;
+        if (!bw.wait(bar(kABMlFull + t), nout[t] & 1u)) return false;
+        const float2 ml = exchange[t * kAttnTile + row];
+        m = ml.x;
+        l = ml.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kABMlEmpty + t));
+        if (!bw.wait(bar(kABOFull + t), nout[t] & 1u)) return false;
+        ++nout[t];
         tc_fence_after();
-      }
-      // Solo items with work in both streams: stream 0 joins the two O.
-      const bool join = a.solo && a.n > 1;
-      float f0 = 1.0f, f1 = 0.0f;
-      if (join) {
-        if (t == 1) {
-          exchange[row] = make_float2(m, l);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kABJoin));
-        }
-        if (!bw.wait(bar(kABJoin + t), njoin & 1u)) break;
-        ++njoin;
-        if (t == 0) {
-          tc_fence_after();
-          const float2 other = exchange[row];
-          const float m_new = fmaxf(m, other.x);
+        return true;
+      };
+      auto drained = [&](int t) {  // this warp's rows of stream t's O are read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && stream_tiles(a, t) > 0) mbar_arrive(bar(kABOEmpty + t));
+      };
+      for (int t = 0; t < (a.solo ? 1 : 2) && ok; ++t) {
+        float m, l;
+        ok = take(t, m, l);
+        // Solo items with work in both streams: the two O of a row are joined.
+        const bool join = a.solo && a.n > 1;
+        float f0 = 1.0f, f1 = 0.0f;
+        if (ok && join) {
+          float m1, l1;
+          ok = take(1, m1, l1);
+          const float m_new = fmaxf(m, m1);
           f0 = m == m_new ? 1.0f : exp2_approx((m - m_new) * sl2);
-          f1 = other.x == m_new ? 1.0f : exp2_approx((other.x - m_new) * sl2);
+          f1 = m1 == m_new ? 1.0f : exp2_approx((m1 - m_new) * sl2);
           m = m_new;
-          l = l * f0 + other.y * f1;
+          l = l * f0 + l1 * f1;
         }
-      }
-      if (!(a.solo && t == 1)) {
+        if (!ok) break;
+        const int tile0 = a.solo ? 0 : t * p.tile_tokens;
         const bool valid = row_tok < p.tile_tokens && tile0 + row_tok < a.ntok;
         const int token = a.tok0 + tile0 + row_tok;
         const int head = a.head * p.group + row_head;
-        // 16 columns of the row's O, joined
-        auto fetch = [&](int col, float (&x)[16]) {
-          uint32_t o[16];
-          tmem_ld16(to + static_cast<uint32_t>(col), o);
-          if (join) {
-            uint32_t o1[16];
-            tmem_ld16(to + static_cast<uint32_t>(DP + col), o1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1;
-          } else {
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]);
-          }
-        };
-        if (p.parts > 1) {
-          const long long heads = p.group * p.kv_heads;
-          const long long at = (static_cast<long long>(a.part) * p.tokens + token) * heads + head;
-          if (valid) p.part_ml[at] = make_float2(m * sl2, l);
-          float* dst = p.part_o + at * p.dim;
-          if (cnt > 0) {  // (a part with l = 0 is not read)
-#pragma unroll 1
-            for (int col = 0; col < DP; col += 16) {
-              float x[16];
-              fetch(col, x);
-#pragma unroll
-              for (int k = 0; k < 16; k += 8) {
-                uint32_t v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(x[k + e]);
-                if (valid && col + k < p.dim) st_global_v8(dst + col + k, v);
-              }
-            }
-          }
-        } else {
-          const float inv = 1.0f / l;
-          if (valid && p.lse)
+        const bool some = stream_tiles(a, t) > 0;
+        const bool part = p.parts > 1;
+        const float inv = 1.0f / l;
+        const long long prow = (static_cast<long long>(a.head) * p.tokens + token) * p.group + row_head;
+        float* pdst = p.part_o + (static_cast<long long>(a.part) * (p.dim / 8) * part_rows + prow) * 8;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + token * p.out_row + head * p.out_head;
+        if (valid) {
+          if (part)
+            p.part_ml[a.part * part_rows + prow] = make_float2(m * sl2, l);
+          else if (p.lse)
             p.lse[token * p.lse_row + head * p.lse_head] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
-          uint16_t* dst = static_cast<uint16_t*>(p.out) + token * p.out_row + head * p.out_head;
+        }
+        // 16 columns at a time, in a loop kept short for the instruction cache
+        // (a part with l = 0 is not read)
+        const uint32_t to = to0 + static_cast<uint32_t>(DP * t);
+        if (some || !part) {
 #pragma unroll 1
           for (int col = 0; col < DP; col += 16) {
-            float x[16];
-            fetch(col, x);
-            uint32_t v[8];
+            uint32_t o[16];
+            tmem_ld16(to + static_cast<uint32_t>(col), o);
+            if (join) {
+              uint32_t o1[16];
+              tmem_ld16(to + static_cast<uint32_t>(DP + col), o1);
+              tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float u = l == 0.0f ? 0.0f : x[2 * k] * inv, w = l == 0.0f ? 0.0f : x[2 * k + 1] * inv;
-              v[k] = BF16 ? pack_bf16x2(__float_as_uint(u), __float_as_uint(w))
-                          : pack_f16x2(__float_as_uint(u), __float_as_uint(w));
+              for (int k = 0; k < 16; ++k)
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
+            } else {
+              tmem_wait_ld();
             }
-            if (valid) {
+            if (!valid || col >= p.dim) continue;
+            uint32_t v[8];
+            if (part) {
+              float* d8 = pdst + static_cast<long long>(col / 8) * part_rows * 8;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = o[e];
+              st_global_v8(d8, v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = o[8 + e];
+              if (col + 8 < p.dim) st_global_v8(d8 + part_rows * 8, v);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float x = l == 0.0f ? 0.0f : __uint_as_float(o[2 * e]) * inv;
+                const float y = l == 0.0f ? 0.0f : __uint_as_float(o[2 * e + 1]) * inv;
+                v[e] = BF16 ? pack_bf16x2(__float_as_uint(x), __float_as_uint(y))
+                            : pack_f16x2(__float_as_uint(x), __float_as_uint(y));
+              }
               if (p.wide_stores) {
-                if (col < p.dim) st_global_v8(dst + col, v);
+                st_global_v8(dst + col, v);
               } else {
-                if (col < p.dim) *reinterpret_cast<uint4*>(dst + col) = make_uint4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint4*>(dst + col) = make_uint4(v[0], v[1], v[2], v[3]);
                 if (col + 8 < p.dim) *reinterpret_cast<uint4*>(dst + col + 8) = make_uint4(v[4], v[5], v[6], v[7]);
               }
             }
           }
         }
+        drained(t);
+        if (join) drained(1);
       }
-      tc_fence_before();
       __syncwarp();
-      if (join && t == 0 && lane == 0) mbar_arrive(bar(kABJoin + 1));
-      if (lane == 0) mbar_arrive(bar(kABItemEmpty + islot));
+      if (ok && lane == 0) mbar_arrive(bar(kABItemEmpty + islot));
     }
   } else {
-    set_max_regs_down<72>();
+    set_max_regs_down<kAttnOtherRegs>();
     if (warp < 10) {
       // ------------------------------------------------------------ MMA issue
       const int t = warp - 8;
@@ -616,7 +700,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint64_t q_desc = desc_sw128(base + static_cast<uint32_t>(t) * L::kTileBytes, 16u, 1024u);
         const uint64_t k_desc0 = desc_sw128(base + L::kOffRing, 16u, 1024u);
         const uint64_t v_desc0 = desc_sw128(base + L::kOffRing, kPanelBytes, 1024u);
-        uint32_t ring = 0, nq = 0, np = 0;
+        uint32_t ring = 0, nq = 0, np = 0, no = 0;
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
           const uint32_t islot = it % kAttnItems;
@@ -627,6 +711,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int n = a.n, fix = a.fix;
           const bool solo = a.solo != 0;
           const int cnt = stream_tiles(a, t);
+          // The thread that tells warp 11 when the item's last value tile has
+          // landed (it reads that tile; an item whose tile needs no zeroing
+          // is told of at once).  A barrier per item slot: a stream can be an
+          // item ahead of the other.
+          const bool teller = t == (solo ? (n - 1) & 1 : 1);
+          if (teller && !fix) mbar_arrive(bar(kABTail + islot));
           // Every ring tile is waited for and released by both streams, in
           // order, whether they use it or not: a stream that skipped uses of
           // a slot could not tell their completions from its own by parity.
@@ -641,59 +731,61 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_arrive(bar(kABEmpty + static_cast<int>(slot)));
             return true;
           };
-          int left = cnt;  // score tiles still to issue
-          auto scores = [&](uint32_t slot) {
-            const uint64_t kd = k_desc0 + slot * (L::kTileBytes >> 4);
-#pragma unroll
-            for (uint32_t kk = 0; kk < DP / 16; ++kk) {
-              const uint32_t off = (kk / 4) * (kPanelBytes >> 4) + (kk % 4) * 2;
-              mma_ss<false>(d_s, q_desc + off, kd + off, idesc_qk, kk ? 1u : 0u);
-            }
-            tc_commit(bar(kABSFull + t));
-            tc_commit(bar(kABEmpty + static_cast<int>(slot)));
-            if (--left == 0) tc_commit(bar(kABQEmpty + t));
-          };
-          // O += P.V of tile j, then S of this stream's next tile.  All waits
-          // for tiles come before the ones for P, so that the MMAs follow
-          // one another.
-          auto step = [&](int j, int next, bool first) -> bool {
-            uint32_t vslot, kslot = 0;
-            if (!landed(value_pos(j, n), vslot) || (next < n && !landed(key_pos(next), kslot))) return false;
-            if (fix && j == n - 1) {
-              // (stream 1 has the last tile of every pair item)
-              if (solo || t == 1) mbar_arrive(bar(kABTail));
-              if (!bw.wait(bar(kABFixed + islot), (it / kAttnItems) & 1u)) return false;
-            }
-            const uint64_t vd = v_desc0 + vslot * (L::kTileBytes >> 4);
-#pragma unroll
-            for (uint32_t half = 0; half < 2; ++half) {
-              if (!bw.wait(bar(kABPFull + 2 * t + static_cast<int>(half)), np & 1u)) return false;
-              tc_fence_after();
-#pragma unroll
-              for (uint32_t kk = 4 * half; kk < 4 * half + 4; ++kk)
-                mma_ts<false>(d_o, d_s + kk * 8u, vd + kk * (16u * 128u >> 4), idesc_pv, (kk || !first) ? 1u : 0u);
-            }
-            ++np;
-            tc_commit(bar(kABEmpty + static_cast<int>(vslot)));
-            if (next < n) scores(kslot);
-            return true;
-          };
+          // O += P.V of tile j (none before the first), then S of this stream's
+          // next tile.  All waits for tiles come before the ones for P, so
+          // that the MMAs follow one another.
           const int stride = solo ? 2 : 1, j0 = solo ? t : 0, end = solo ? n : cnt;
           if (solo && t == 1 && n > 0) ok = skip(key_pos(0));
           if (cnt > 0 && ok) {
-            uint32_t slot;
-            if (!bw.wait(bar(kABQFull + t), nq & 1u) || !landed(key_pos(j0), slot)) break;
+            ok = bw.wait(bar(kABQFull + t), nq & 1u);
             ++nq;
-            tc_fence_after();
-            scores(slot);
           }
-          for (int j = j0; j < end && ok; j += stride) {
-            if (solo) {  // the other stream's tiles that lie before this one's in the ring
-              if (j >= 1) ok = skip(value_pos(j - 1, n));
-              if (ok && j + 1 < n && (j + 1 >= 2 || t == 0)) ok = skip(key_pos(j + 1));
-              if (!ok) break;
+          for (int j = j0 - stride; j < end && ok; j += stride) {
+            const int next = j + stride;
+            if (cnt == 0) break;
+            uint32_t vslot = 0, kslot = 0;
+            if (j >= 0) {
+              if (solo) {  // the other stream's tiles that lie before this one's in the ring
+                if (j >= 1) ok = skip(value_pos(j - 1, n));
+                if (ok && j + 1 < n && (j + 1 >= 2 || t == 0)) ok = skip(key_pos(j + 1));
+              }
+              if (!ok || !(ok = landed(value_pos(j, n), vslot))) break;
             }
-            ok = step(j, j + stride < end ? j + stride : n, j == j0);
+            if (next < end && !(ok = landed(key_pos(next), kslot))) break;
+            if (j >= 0) {
+              if (fix && j == n - 1) {
+                if (teller) mbar_arrive(bar(kABTail + islot));
+                if (!(ok = bw.wait(bar(kABFixed + islot), (it / kAttnItems) & 1u))) break;
+              }
+              if (j == j0) {  // the epilogue has read the item before's O
+                if (!(ok = bw.wait(bar(kABOEmpty + t), (no & 1u) ^ 1u))) break;
+                ++no;
+              }
+              const uint64_t vd = v_desc0 + vslot * (L::kTileBytes >> 4);
+#pragma unroll
+              for (uint32_t half = 0; half < 2; ++half) {
+                if (!(ok = bw.wait(bar(kABPFull + 2 * t + static_cast<int>(half)), np & 1u))) break;
+                tc_fence_after();
+#pragma unroll
+                for (uint32_t kk = 4 * half; kk < 4 * half + 4; ++kk)
+                  mma_ts<false>(d_o, d_s + kk * 8u, vd + kk * (16u * 128u >> 4), idesc_pv, (kk || j != j0) ? 1u : 0u);
+              }
+              if (!ok) break;
+              ++np;
+              tc_commit(bar(kABEmpty + static_cast<int>(vslot)));
+            }
+            if (next < end) {
+              tc_fence_after();
+              const uint64_t kd = k_desc0 + kslot * (L::kTileBytes >> 4);
+#pragma unroll
+              for (uint32_t kk = 0; kk < DP / 16; ++kk) {
+                const uint32_t off = (kk / 4) * (kPanelBytes >> 4) + (kk % 4) * 2;
+                mma_ss<false>(d_s, q_desc + off, kd + off, idesc_qk, kk ? 1u : 0u);
+              }
+              tc_commit(bar(kABSFull + t));
+              tc_commit(bar(kABEmpty + static_cast<int>(kslot)));
+              if (next + stride >= end) tc_commit(bar(kABQEmpty + t));
+            }
           }
           if (solo) {
             if (ok && n > 0 && ((n - 1) & 1) != t) ok = skip(value_pos(n - 1, n));
@@ -751,27 +843,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           ++it;
           const bool own = a.kind == 2;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (stream_tiles(a, t) == 0) continue;
-            ok = wait(bar(kABQEmpty + t), (nq[t] & 1u) ^ 1u);
-            if (!ok) break;
-            if (lane == 0) {
-              const uint32_t fb = bar(kABQFull + t);
-              mbar_arrive_expect_tx(fb, own ? p.own_q_bytes : p.q_bytes);
-              const int tok = a.tok0 + (a.solo ? 0 : t * p.tile_tokens);
-#pragma unroll
-              for (int c = 0; c < L::kPanels; ++c)
-                tma_load_4d(base + static_cast<uint32_t>(t) * L::kTileBytes + c * kPanelBytes, own ? &tm_q_own : &tm_q,
-                            fb, c * 64, 0, a.head, tok);
-            }
-            ++nq[t];
-          }
           const int box = own ? p.own_box_rows : p.box_rows;
           const CUtensorMap* km = own ? &tm_k_own : &tm_k;
           const CUtensorMap* vm = own ? &tm_v_own : &tm_v;
           const bool paged = own && p.table != nullptr;
           RingWalk w(a.n);
           for (int pos = 0; pos < 2 * a.n && ok; ++pos) {
+            if (pos == 1) {  // the query tiles, behind the first key tile
+              for (int t = 0; t < 2 && ok; ++t) {
+                if (stream_tiles(a, t) == 0) continue;
+                ok = wait(bar(kABQEmpty + t), (nq[t] & 1u) ^ 1u);
+                if (!ok) break;
+                if (lane == 0) {
+                  const uint32_t fb = bar(kABQFull + t);
+                  mbar_arrive_expect_tx(fb, own ? p.own_q_bytes : p.q_bytes);
+                  const int tok = a.tok0 + (a.solo ? 0 : t * p.tile_tokens);
+#pragma unroll
+                  for (int c = 0; c < L::kPanels; ++c)
+                    tma_load_4d(base + static_cast<uint32_t>(t) * L::kTileBytes + c * kPanelBytes, own ? &tm_q_own : &tm_q,
+                                fb, c * 64, 0, a.head, tok);
+                }
+                ++nq[t];
+              }
+              if (!ok) break;
+            }
             const bool is_k = w.next();
             const int j = w.j;
             const uint32_t g = ring + static_cast<uint32_t>(pos), slot = g % kRing;
@@ -841,17 +936,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     } else {
       // --------------------------------------- tail of the last value tile
-      uint32_t ring = 0, ntail = 0;
+      uint32_t ring = 0;
       for (uint32_t it = 0;; ++it) {
         const uint32_t islot = it % kAttnItems;
         if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
         const int kind = items[islot].kind, n = items[islot].n, fix = items[islot].fix;
         if (kind < 0) break;
+        // (told by the MMA thread that waits for the tile: this warp does not
+        // follow the slot's other uses)
+        if (!bw.wait(bar(kABTail + islot), (it / kAttnItems) & 1u)) break;
         if (fix) {
-          // (told by the MMA thread that waits for the tile: this warp does not
-          // follow the slot's other uses)
-          if (!bw.wait(bar(kABTail), ntail & 1u)) break;
-          ++ntail;
           const uint32_t slot = (ring + value_pos(n - 1, n)) % kRing;
           const uint32_t dst = base + L::kOffRing + slot * L::kTileBytes;
           for (int e = fix * 8 + lane; e < kAttnTile * 8; e += 32)
@@ -874,6 +968,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, 0, kTimeoutCode);
 }
 
 // Joins the parts of every row: with M = max over parts of c m_p,
@@ -885,30 +980,31 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant
   using namespace attn;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int heads = p.group * p.kv_heads;
-  const int per_row = p.dim / 8;
-  const long long rows = static_cast<long long>(p.tokens) * heads;
-  const long long id = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long r = id / per_row;
+  // consecutive threads take consecutive rows of the same eight columns
+  const long long rows = static_cast<long long>(p.tokens) * (p.group * p.kv_heads);
+  const int col = static_cast<int>(blockIdx.y) * 8;
+  int r = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
   if (r >= rows) return;
-  const int col = static_cast<int>(id - r * per_row) * 8;
-  const int token = static_cast<int>(r / heads), head = static_cast<int>(r - static_cast<long long>(token) * heads);
+  const int row = r;
+  int token = p.by_group.split(r);  // r: head of the group
+  const int head = p.by_tokens.split(token) * p.group + r;
   if (p.op == kAttnPrompt) {
     // rows that belong to no sequence are left alone
     if (token < __ldg(p.cu_q) || token >= __ldg(p.cu_q + p.batch)) return;
   }
   float big = -INFINITY;
   for (int s = 0; s < p.parts; ++s) {
-    const float2 ml = p.part_ml[s * rows + r];
+    const float2 ml = p.part_ml[s * rows + row];
     if (ml.y != 0.0f) big = fmaxf(big, ml.x);
   }
   float l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int s = 0; s < p.parts; ++s) {
-    const float2 ml = p.part_ml[s * rows + r];
+    const float2 ml = p.part_ml[s * rows + row];
     if (ml.y == 0.0f) continue;
     const float f = ml.x == big ? 1.0f : exp2f(ml.x - big);
     l += ml.y * f;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + (s * rows + r) * p.dim + col);
+    const float4* src =
+        reinterpret_cast<const float4*>(p.part_o + ((static_cast<long long>(s) * (p.dim / 8) + col / 8) * rows + row) * 8);
     const float4 u = src[0], v = src[1];
     o[0] += u.x * f; o[1] += u.y * f; o[2] += u.z * f; o[3] += u.w * f;
     o[4] += v.x * f; o[5] += v.y * f; o[6] += v.z * f; o[7] += v.w * f;

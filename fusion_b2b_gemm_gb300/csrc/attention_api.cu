@@ -30,9 +30,9 @@ struct b2b_attn_plan_s {
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
-// The registers of the two warp roles (setmaxnreg) are drawn from what the
-// kernel is launched with: a kernel compiled to fewer would wait for them.
-constexpr int kRegsNeeded = 256 * 216 + 128 * 72;
+// The registers of the warp roles (setmaxnreg) are drawn from what the kernel
+// is launched with: a kernel compiled to fewer would wait for them.
+constexpr int kRegsNeeded = 256 * kAttnSoftmaxRegs + 128 * kAttnEpilogueRegs + 128 * kAttnOtherRegs;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -108,6 +108,7 @@ int split_count(int64_t items, int64_t tiles, int sms) {
 }
 
 int prompt_splits(const b2b_attn_plan_s* p, int64_t batch, int64_t tokens, int64_t key_rows) {
+  if (tokens * p->q_heads > kMaxRows) return 1;  // (rows of parts are numbered in 31 bits)
   const int64_t block = 2 * p->tile_tokens;
   const int64_t blocks = std::max((tokens + block - 1) / block, std::min(batch, tokens));
   const int64_t tiles = (key_rows / std::max<int64_t>(batch, 1) + kAttnTile - 1) / kAttnTile;
@@ -154,6 +155,10 @@ AttnParams common_params(const b2b_attn_plan_s* p, int64_t tokens, int64_t batch
   a.kv_heads = p->kv_heads;
   a.dim = p->dim;
   a.tile_tokens = p->tile_tokens;
+  a.by_group = FastDiv::of(static_cast<uint32_t>(p->group));
+  a.by_tokens = FastDiv::of(static_cast<uint32_t>(tokens));
+  a.by_kv_heads = FastDiv::of(static_cast<uint32_t>(p->kv_heads));
+  a.by_block = FastDiv::of(static_cast<uint32_t>(2 * p->tile_tokens));
   a.tokens = static_cast<int>(tokens);
   a.batch = static_cast<int>(batch);
   a.scale = p->scale;
@@ -174,7 +179,7 @@ AttnParams common_params(const b2b_attn_plan_s* p, int64_t tokens, int64_t batch
   a.q_bytes = static_cast<uint32_t>(p->group * p->tile_tokens) * 128u * (p->dp ? 2u : 1u);
   a.debug = p->debug;
   a.status = p->d_status;
-  a.budget_ns = p->budget_ns;
+  a.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(p->budget_ns, 4000000000ull));  // (a 32-bit clock in the kernel)
   return a;
 }
 
@@ -183,9 +188,10 @@ b2b_status_t launch(const b2b_attn_plan_s* p, CUtensorMap (&maps)[6], AttnParams
   cudaError_t e = launch_pdl(p->k.main[p->dp], dim3(static_cast<unsigned>(items)), dim3(kAttnThreads), args,
                              p->k.smem[p->dp], stream);
   if (e == cudaSuccess && a.parts > 1) {
-    const int64_t threads = static_cast<int64_t>(a.tokens) * p->q_heads * (p->dim / 8);
+    const int64_t rows = static_cast<int64_t>(a.tokens) * p->q_heads;
     void* cargs[] = {&a};
-    e = launch_pdl(p->k.combine, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), cargs, 0, stream);
+    e = launch_pdl(p->k.combine, dim3(static_cast<unsigned>((rows + 255) / 256), static_cast<unsigned>(p->dim / 8)),
+                   dim3(256), cargs, 0, stream);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -316,7 +322,7 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attent
   a.cu_q = r->cu_q;
   a.cu_k = r->cu_k;
   a.key_rows = static_cast<int>(r->key_rows);
-  a.splits = splits;
+  a.by_splits = FastDiv::of(static_cast<uint32_t>(splits));
   a.box_rows = kAttnTile;
   CUtensorMap maps[6];
   st = encode_q(&maps[0], p, r->q, r->tokens, static_cast<uint32_t>(p->tile_tokens));
@@ -382,21 +388,21 @@ b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t p, const b2b_shared_attent
   const size_t need = part_bytes(p, tokens, parts);
   if (need && (!r->workspace || r->workspace_bytes < need)) return B2B_ERR_INVALID_ARG;
   if (need && reinterpret_cast<uintptr_t>(r->workspace) % 32) return B2B_ERR_ALIGNMENT;
-  if (s.prefix_items + s.own_items > kMaxRows) return B2B_ERR_UNSUPPORTED;
+  if (s.prefix_items + s.own_items > kMaxRows || tokens * hq > kMaxRows) return B2B_ERR_UNSUPPORTED;
   st = check_current_device(p);
   if (st != B2B_OK) return st;
 
   AttnParams a = common_params(p, tokens, r->batch, r->out, r->lse, r->workspace, parts);
   a.op = kAttnShared;
   a.causal = 1;
-  a.splits = s.splits;
+  a.by_splits = FastDiv::of(static_cast<uint32_t>(std::max(s.splits, 1)));
   a.fresh = static_cast<int>(r->fresh);
   a.prefix = static_cast<int>(r->prefix);
   a.prefix_items = static_cast<int>(s.prefix_items);
-  a.row_blocks = static_cast<int>(s.row_blocks);
+  a.by_row_blocks = FastDiv::of(static_cast<uint32_t>(s.row_blocks));
   a.block_tokens = static_cast<int>(s.block_tokens);
-  a.own_splits = s.own_splits;
-  a.own_blocks = static_cast<int>(s.own_blocks);
+  a.by_own_splits = FastDiv::of(static_cast<uint32_t>(s.own_splits));
+  a.by_own_blocks = FastDiv::of(static_cast<uint32_t>(s.own_blocks));
   a.lengths = r->lengths;
   a.table = r->page_table;
   a.table_width = static_cast<int>(r->table_width);
