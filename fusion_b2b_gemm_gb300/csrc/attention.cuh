@@ -196,6 +196,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -636,49 +641,64 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           else if (p.lse)
             p.lse[token * p.lse_row + head * p.lse_head] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
         }
-        // 16 columns at a time, in a loop kept short for the instruction cache
-        // (a part with l = 0 is not read)
+        // 32 columns of the row: independent work enough for one warp, code
+        // short enough for the instruction cache (16 columns at a time took
+        // 2 us a tile, one instruction after the other).
+        const bool none = __any_sync(0xffffffffu, l == 0.0f);
+        const uint64_t invx2 = pack2(inv, inv);
+        auto emit = [&](int col, uint32_t (&o)[32]) {
+          if (part) {
+            float* d8 = pdst + static_cast<long long>(col / 8) * part_rows * 8;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = o[k + e];
+              if (valid && col + k < p.dim) st_global_v8(d8 + (k / 8) * part_rows * 8, v);
+            }
+            return;
+          }
+          uint32_t v[2][8];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x, y;
+            unpack2(mul2(pack2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), invx2), x, y);
+            v[e / 8][e % 8] = BF16 ? pack_bf16x2(__float_as_uint(x), __float_as_uint(y))
+                                   : pack_f16x2(__float_as_uint(x), __float_as_uint(y));
+          }
+          if (none) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e / 8][e % 8] = l == 0.0f ? 0u : v[e / 8][e % 8];
+          }
+          if (!valid) return;
+          if (p.wide_stores) {
+            if (col < p.dim) st_global_v8(dst + col, v[0]);
+            if (col + 16 < p.dim) st_global_v8(dst + col + 16, v[1]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (col + 8 * q < p.dim)
+                *reinterpret_cast<uint4*>(dst + col + 8 * q) =
+                    make_uint4(v[q / 2][4 * (q % 2)], v[q / 2][4 * (q % 2) + 1], v[q / 2][4 * (q % 2) + 2], v[q / 2][4 * (q % 2) + 3]);
+          }
+        };
         const uint32_t to = to0 + static_cast<uint32_t>(DP * t);
-        if (some || !part) {
+        if (some || !part) {  // (a part with l = 0 is not read)
 #pragma unroll 1
-          for (int col = 0; col < DP; col += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + static_cast<uint32_t>(col), o);
+          for (int col = 0; col < DP; col += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + static_cast<uint32_t>(col), o);
             if (join) {
-              uint32_t o1[16];
-              tmem_ld16(to + static_cast<uint32_t>(DP + col), o1);
+              uint32_t o1[32];
+              tmem_ld32(to + static_cast<uint32_t>(DP + col), o1);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
+              for (int k = 0; k < 32; ++k)
                 o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
             } else {
               tmem_wait_ld();
             }
-            if (!valid || col >= p.dim) continue;
-            uint32_t v[8];
-            if (part) {
-              float* d8 = pdst + static_cast<long long>(col / 8) * part_rows * 8;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = o[e];
-              st_global_v8(d8, v);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = o[8 + e];
-              if (col + 8 < p.dim) st_global_v8(d8 + part_rows * 8, v);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float x = l == 0.0f ? 0.0f : __uint_as_float(o[2 * e]) * inv;
-                const float y = l == 0.0f ? 0.0f : __uint_as_float(o[2 * e + 1]) * inv;
-                v[e] = BF16 ? pack_bf16x2(__float_as_uint(x), __float_as_uint(y))
-                            : pack_f16x2(__float_as_uint(x), __float_as_uint(y));
-              }
-              if (p.wide_stores) {
-                st_global_v8(dst + col, v);
-              } else {
-                *reinterpret_cast<uint4*>(dst + col) = make_uint4(v[0], v[1], v[2], v[3]);
-                if (col + 8 < p.dim) *reinterpret_cast<uint4*>(dst + col + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-              }
-            }
+            emit(col, o);
           }
         }
         drained(t);
@@ -825,14 +845,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         return __shfl_sync(0xffffffffu, r, 0);
       };
       while (ok) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(kABNext), 16);
-          asm volatile(
-              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                  next_slot),
-              "r"(bar(kABNext))
-              : "memory");
-        }
+        // The next item is asked for when this one's loads are nearly all
+        // issued: asked for earlier it would wait here while other CTAs run
+        // out of work (measured: the first CTA done 30 us before the last
+        // instead of the length of an item).
+        bool asked = false;
+        auto ask = [&] {
+          asked = true;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kABNext), 16);
+            asm volatile(
+                "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                    next_slot),
+                "r"(bar(kABNext))
+                : "memory");
+          }
+        };
         AttnItem a;
         if (decode_item(p, x, lane, a)) {
           const uint32_t islot = it % kAttnItems;
@@ -867,6 +895,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
               if (!ok) break;
             }
+            if (!asked && pos >= 2 * a.n - 4) ask();
             const bool is_k = w.next();
             const int j = w.j;
             const uint32_t g = ring + static_cast<uint32_t>(pos), slot = g % kRing;
@@ -900,6 +929,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           ring += 2u * static_cast<uint32_t>(a.n);
         }
+        if (!ok && !asked) break;
+        if (!asked) ask();
         // (waited for even on an abort: the answer is written to shared memory)
         if (lane == 0) drain_wait(bar(kABNext), nnext & 1u, p.budget_ns);
         __syncwarp();
