@@ -35,13 +35,11 @@
 // CTA roles (512 threads, one CTA per SM; items handed out by cluster launch
 // control, so a CTA that finishes early takes the next unstarted item):
 //   warps 0-3, 4-7  softmax of stream 0 and 1 (a row per thread)
-//   warps 8, 9      MMA issue of stream 0 and 1 (one thread each)
-//   warp 10         item decoding and TMA loads
+//   warps 8, 9      MMA issue of stream 0 and 1
+//   warp 10         TMA loads
+//   warp 11         items: asks for them and decodes them ahead of the loads
 //   warps 12-15     epilogue of both streams, beside the next item's softmax
-//   warp 11         zeroes the rows of the last value tile past its last key
-//                   (what lies there may be another sequence's, or NaN, and
-//                   0 x NaN is not 0)
-// Every wait is bounded (ptx::BoundedWait) as in the chain kernels.
+// Every wait is bounded, as in the chain kernels.
 #pragma once
 
 #include <cuda.h>
@@ -85,10 +83,11 @@ enum : int {  // barrier slots (8 bytes each)
   kABMlFull = 45,     // [2] stream's (m, l) written
   kABMlEmpty = 47,    // [2] stream's (m, l) read
   kABOEmpty = 49,     // [2] stream's O read
+  kABAsk = 40,        // an item's loads are nearly all issued
   kABTail = 51,       // [3] last value tile landed (one arrival per item)
   kABItemFull = 28,   // [3] descriptor written
   kABItemEmpty = 31,  // [3] descriptor no longer read
-  kABFixed = 34,      // [3] last value tile's tail zeroed (one arrival per item)
+  kABFixed = 34,      // [3] last value tile's tail zeroed
   kABNext = 37,       // next item handed out
   kABDrain = 38,      // [2]
   kASlotNext = 42,    // 16 bytes: cluster launch control's answer
@@ -232,15 +231,21 @@ struct Wait {
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
     return t;
   }
+  // By one thread.
+  __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity) const {
+    bool done = ptx::mbar_try_wait(bar, parity);
+    if (!done) {
+      const uint32_t t0 = now();
+      while (!(done = ptx::mbar_try_wait(bar, parity)) && !*abort_flag) {
+        if (now() - t0 >= budget_ns) *abort_flag = 1;
+      }
+    }
+    return done;
+  }
+  // By a whole warp; every lane gets the same answer, so that no lane goes on
+  // to a warp-wide instruction without the others.
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const uint32_t t0 = now();
-    do {
-      if (ptx::mbar_try_wait(bar, parity)) return true;
-      if (*abort_flag) return false;
-    } while (now() - t0 < budget_ns);
-    *abort_flag = 1;
-    return false;
+    return __all_sync(0xffffffffu, wait1(bar, parity));
   }
 };
 
@@ -427,11 +432,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else if (lane < 10 + kAttnItems) {
       const int s = lane - 10;
       mbar_init(bar(kABItemFull + s), 1);
-      mbar_init(bar(kABItemEmpty + s), 15);  // 8 softmax and 4 epilogue warps, 2 MMA threads, warp 11
-      mbar_init(bar(kABFixed + s), 1);
+      mbar_init(bar(kABItemEmpty + s), 15);  // 8 softmax and 4 epilogue warps, 2 MMA warps, the loader
+      mbar_init(bar(kABFixed + s), 4);
       mbar_init(bar(kABTail + s), 1);
     } else if (lane == 13) {
       mbar_init(bar(kABNext), 1);
+      mbar_init(bar(kABAsk), 1);
       *abort_flag = 0;
     }
     if (lane < 14) fence_barrier_init();
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t to0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO;
     const float sl2 = p.scale_log2;
     const long long part_rows = static_cast<long long>(p.tokens) * (p.group * p.kv_heads);
-    uint32_t nout[2] = {0, 0};
+    uint32_t nout[2] = {0, 0}, ring = 0;
     grid_dependency_wait();  // (the outputs may still be read by the kernel before)
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
@@ -588,6 +594,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
       const AttnItem a = items[islot];
       if (a.kind < 0) break;
+      // The rows of the last value tile past its last key become zeros: another
+      // sequence's values may lie there, or NaN, and 0 x NaN is not 0.
+      if (!(ok = bw.wait(bar(kABTail + islot), (it / kAttnItems) & 1u))) break;
+      if (a.fix) {
+        const uint32_t dst =
+            base + L::kOffRing + ((ring + value_pos(a.n - 1, a.n)) % kRing) * L::kTileBytes;
+#pragma unroll 1
+        for (int e = a.fix * 8 + static_cast<int>(threadIdx.x & 127u); e < kAttnTile * 8; e += 128)
+#pragma unroll
+          for (int c = 0; c < L::kPanels; ++c)
+            st_shared_v4(dst + c * kPanelBytes + static_cast<uint32_t>(e) * 16u, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kABFixed + islot));
+      ring += 2u * static_cast<uint32_t>(a.n);
       // (m, l) of stream t's row, once its O is complete
       auto take = [&](int t, float& m, float& l) -> bool {
         m = -INFINITY;
@@ -711,6 +733,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     set_max_regs_down<kAttnOtherRegs>();
     if (warp < 10) {
       // ------------------------------------------------------------ MMA issue
+      // One elected thread (measured: a warp-wide walk that elects a thread for
+      // each group of MMAs issues them a fifth slower).
       const int t = warp - 8;
       if (elect_one()) {
         const uint32_t d_s = tmem + 128u * static_cast<uint32_t>(t);
@@ -724,17 +748,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
           const uint32_t islot = it % kAttnItems;
-          if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
-          const int kind = items[islot].kind;
-          if (kind < 0) break;
+          if (!bw.wait1(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
           const AttnItem& a = items[islot];
+          if (a.kind < 0) break;
           const int n = a.n, fix = a.fix;
           const bool solo = a.solo != 0;
           const int cnt = stream_tiles(a, t);
-          // The thread that tells warp 11 when the item's last value tile has
-          // landed (it reads that tile; an item whose tile needs no zeroing
-          // is told of at once).  A barrier per item slot: a stream can be an
-          // item ahead of the other.
+          // The thread that tells the epilogue's warps, which have the time to
+          // zero the tail of the item's last value tile, that it has landed (it
+          // reads that tile itself; a tile that needs nothing is told of at
+          // once).  A barrier per item slot: a stream can be an item ahead of
+          // the other.
           const bool teller = t == (solo ? (n - 1) & 1 : 1);
           if (teller && !fix) mbar_arrive(bar(kABTail + islot));
           // Every ring tile is waited for and released by both streams, in
@@ -743,7 +767,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           auto landed = [&](uint32_t pos, uint32_t& slot) -> bool {
             const uint32_t g = ring + pos;
             slot = g % kRing;
-            return bw.wait(bar(kABFull + static_cast<int>(slot)), (g / kRing) & 1u);
+            return bw.wait1(bar(kABFull + static_cast<int>(slot)), (g / kRing) & 1u);
           };
           auto skip = [&](uint32_t pos) -> bool {
             uint32_t slot;
@@ -757,12 +781,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int stride = solo ? 2 : 1, j0 = solo ? t : 0, end = solo ? n : cnt;
           if (solo && t == 1 && n > 0) ok = skip(key_pos(0));
           if (cnt > 0 && ok) {
-            ok = bw.wait(bar(kABQFull + t), nq & 1u);
+            ok = bw.wait1(bar(kABQFull + t), nq & 1u);
             ++nq;
           }
-          for (int j = j0 - stride; j < end && ok; j += stride) {
+          for (int j = j0 - stride; cnt > 0 && j < end && ok; j += stride) {
             const int next = j + stride;
-            if (cnt == 0) break;
             uint32_t vslot = 0, kslot = 0;
             if (j >= 0) {
               if (solo) {  // the other stream's tiles that lie before this one's in the ring
@@ -775,16 +798,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (j >= 0) {
               if (fix && j == n - 1) {
                 if (teller) mbar_arrive(bar(kABTail + islot));
-                if (!(ok = bw.wait(bar(kABFixed + islot), (it / kAttnItems) & 1u))) break;
+                if (!(ok = bw.wait1(bar(kABFixed + islot), (it / kAttnItems) & 1u))) break;
               }
               if (j == j0) {  // the epilogue has read the item before's O
-                if (!(ok = bw.wait(bar(kABOEmpty + t), (no & 1u) ^ 1u))) break;
+                if (!(ok = bw.wait1(bar(kABOEmpty + t), (no & 1u) ^ 1u))) break;
                 ++no;
               }
               const uint64_t vd = v_desc0 + vslot * (L::kTileBytes >> 4);
 #pragma unroll
               for (uint32_t half = 0; half < 2; ++half) {
-                if (!(ok = bw.wait(bar(kABPFull + 2 * t + static_cast<int>(half)), np & 1u))) break;
+                if (!(ok = bw.wait1(bar(kABPFull + 2 * t + static_cast<int>(half)), np & 1u))) break;
                 tc_fence_after();
 #pragma unroll
                 for (uint32_t kk = 4 * half; kk < 4 * half + 4; ++kk)
@@ -793,6 +816,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               if (!ok) break;
               ++np;
               tc_commit(bar(kABEmpty + static_cast<int>(vslot)));
+              if (next >= end) tc_commit(bar(kABOFull + t));
             }
             if (next < end) {
               tc_fence_after();
@@ -812,7 +836,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           } else {
             for (int j = cnt; j < n && ok; ++j) ok = skip(key_pos(j)) && skip(value_pos(j, n));
           }
-          if (ok && cnt > 0) tc_commit(bar(kABOFull + t));
           if (!ok) break;
           ring += 2u * static_cast<uint32_t>(n);
           mbar_arrive(bar(kABItemEmpty + islot));
@@ -822,7 +845,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         drain_wait(bar(kABDrain + t), 0, p.budget_ns);
       }
     } else if (warp == 10) {
-      // ------------------------------------------------- items and TMA loads
+      // ------------------------------------------------------------ TMA loads
       if (lane == 0) {
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
@@ -834,106 +857,119 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       grid_dependency_wait();
-      const uint32_t next_slot = bar0 + 8u * kASlotNext;
-      uint32_t it = 0, ring = 0, issued = 0, nq[2] = {0, 0}, nnext = 0;
-      int x = static_cast<int>(blockIdx.x);
+      uint32_t ring = 0, issued = 0, nq0 = 0, nq1 = 0;
       bool ok = true;
-      // all lanes: wait on lane 0's behalf
-      auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-        bool r = true;
-        if (lane == 0) r = bw.wait(b, parity);
-        return __shfl_sync(0xffffffffu, r, 0);
-      };
-      while (ok) {
-        // The next item is asked for when this one's loads are nearly all
-        // issued: asked for earlier it would wait here while other CTAs run
-        // out of work (measured: the first CTA done 30 us before the last
-        // instead of the length of an item).
-        bool asked = false;
-        auto ask = [&] {
-          asked = true;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(kABNext), 16);
-            asm volatile(
-                "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                    next_slot),
-                "r"(bar(kABNext))
-                : "memory");
+      const int panel = lane & (L::kPanels - 1), box_at = lane / L::kPanels;  // a lane's share of a tile's boxes
+      for (uint32_t it = 0; ok; ++it) {
+        const uint32_t islot = it % kAttnItems;
+        if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
+        const AttnItem& a = items[islot];
+        if (a.kind < 0) break;
+        const int n = a.n, head = a.head, last = a.last, krow = a.krow;
+        const bool own = a.kind == 2;
+        const bool paged = own && p.table != nullptr;
+        const int box = own ? p.own_box_rows : p.box_rows;
+        const CUtensorMap* km = own ? &tm_k_own : &tm_k;
+        const CUtensorMap* vm = own ? &tm_v_own : &tm_v;
+        const int key0 = a.j0 * kAttnTile + box_at * box;
+        RingWalk w(n);
+        for (int pos = 0; pos < 2 * n; ++pos) {
+          if (pos == 1) {  // the query tiles, behind the first key tile
+            const int tok = a.tok0, cnt0 = stream_tiles(a, 0), cnt1 = stream_tiles(a, 1);
+            const CUtensorMap* qm = own ? &tm_q_own : &tm_q;
+            const uint32_t bytes = own ? p.own_q_bytes : p.q_bytes;
+            if (cnt0 > 0) {
+              if (!(ok = bw.wait(bar(kABQEmpty), (nq0 & 1u) ^ 1u))) break;
+              ++nq0;
+              if (lane == 0) mbar_arrive_expect_tx(bar(kABQFull), bytes);
+              __syncwarp();
+              if (box_at == 0) tma_load_4d(base + panel * kPanelBytes, qm, bar(kABQFull), panel * 64, 0, head, tok);
+            }
+            if (cnt1 > 0) {
+              if (!(ok = bw.wait(bar(kABQEmpty + 1), (nq1 & 1u) ^ 1u))) break;
+              ++nq1;
+              if (lane == 0) mbar_arrive_expect_tx(bar(kABQFull + 1), bytes);
+              __syncwarp();
+              if (box_at == 0)
+                tma_load_4d(base + L::kTileBytes + panel * kPanelBytes, qm, bar(kABQFull + 1), panel * 64, 0, head,
+                            tok + (a.solo ? 0 : p.tile_tokens));
+            }
           }
-        };
+          // Near the end of the item's loads warp 11 asks for the next one.
+          if (pos == max(2 * n - 4, 0) && lane == 0) mbar_arrive(bar(kABAsk));
+          const bool is_k = w.next();
+          const uint32_t g = ring + static_cast<uint32_t>(pos), slot = g % kRing;
+          if (!(ok = bw.wait(bar(kABEmpty + static_cast<int>(slot)), ((g / kRing) & 1u) ^ 1u))) break;
+          const int rows = min(kAttnTile, last - w.j * kAttnTile);  // keys of this tile that are seen
+          const int key = key0 + w.j * kAttnTile;
+          const bool mine = box_at * box < rows;
+          const uint32_t fb = bar(kABFull + static_cast<int>(slot));
+          int r = key, b = krow;
+          if (!own) {
+            r = krow + key;
+            b = 0;
+          } else if (paged && mine) {
+            b = __ldg(p.table + static_cast<long long>(krow) * p.table_width + (key >> p.page_shift));
+            r = key & ((1 << p.page_shift) - 1);
+          }
+          if (lane == 0)
+            mbar_arrive_expect_tx(fb, static_cast<uint32_t>((rows + box - 1) & ~(box - 1)) * 128u * L::kPanels);
+          issued = g + 1;
+          __syncwarp();
+          // test support: the very first ring tile is armed but never filled
+          if (mine && !((p.debug & 1u) && g == 0))
+            tma_load_4d(base + L::kOffRing + slot * L::kTileBytes + panel * kPanelBytes +
+                            static_cast<uint32_t>(box_at * box) * 128u,
+                        is_k ? km : vm, fb, panel * 64, head, r, b);
+        }
+        if (!ok) break;
+        ring += 2u * static_cast<uint32_t>(n);
+        __syncwarp();
+        if (lane == 0) {
+          if (n == 0) mbar_arrive(bar(kABAsk));
+          mbar_arrive(bar(kABItemEmpty + islot));
+        }
+      }
+      __syncwarp();
+      // copies still in flight must land before the CTA exits
+      if (nq0 > 0) drain_wait(bar(kABQFull), (nq0 - 1) & 1u, p.budget_ns);
+      if (nq1 > 0) drain_wait(bar(kABQFull + 1), (nq1 - 1) & 1u, p.budget_ns);
+      for (uint32_t k = 1; k <= kRing && k <= issued; ++k)
+        drain_wait(bar(kABFull + static_cast<int>((issued - k) % kRing)), ((issued - k) / kRing) & 1u, p.budget_ns);
+    } else {
+      // ---------------------------------------------------------------- items
+      grid_dependency_wait();
+      const uint32_t next_slot = bar0 + 8u * kASlotNext;
+      int x = static_cast<int>(blockIdx.x);
+      uint32_t it = 0, nnext = 0;
+      while (true) {
         AttnItem a;
-        if (decode_item(p, x, lane, a)) {
+        const bool some = decode_item(p, x, lane, a);
+        if (some) {
           const uint32_t islot = it % kAttnItems;
-          ok = wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u);
-          if (ok && lane == 0) {
+          if (!bw.wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u)) break;
+          if (lane == 0) {
             items[islot] = a;
             mbar_arrive(bar(kABItemFull + islot));
           }
+          // The next item is asked for when this one's loads are nearly all
+          // issued: asked for earlier it would wait here while other CTAs run
+          // out of work (measured: the first CTA done 30 us before the last
+          // instead of the length of an item).
+          if (!bw.wait(bar(kABAsk), it & 1u)) break;
           ++it;
-          const bool own = a.kind == 2;
-          const int box = own ? p.own_box_rows : p.box_rows;
-          const CUtensorMap* km = own ? &tm_k_own : &tm_k;
-          const CUtensorMap* vm = own ? &tm_v_own : &tm_v;
-          const bool paged = own && p.table != nullptr;
-          RingWalk w(a.n);
-          for (int pos = 0; pos < 2 * a.n && ok; ++pos) {
-            if (pos == 1) {  // the query tiles, behind the first key tile
-              for (int t = 0; t < 2 && ok; ++t) {
-                if (stream_tiles(a, t) == 0) continue;
-                ok = wait(bar(kABQEmpty + t), (nq[t] & 1u) ^ 1u);
-                if (!ok) break;
-                if (lane == 0) {
-                  const uint32_t fb = bar(kABQFull + t);
-                  mbar_arrive_expect_tx(fb, own ? p.own_q_bytes : p.q_bytes);
-                  const int tok = a.tok0 + (a.solo ? 0 : t * p.tile_tokens);
-#pragma unroll
-                  for (int c = 0; c < L::kPanels; ++c)
-                    tma_load_4d(base + static_cast<uint32_t>(t) * L::kTileBytes + c * kPanelBytes, own ? &tm_q_own : &tm_q,
-                                fb, c * 64, 0, a.head, tok);
-                }
-                ++nq[t];
-              }
-              if (!ok) break;
-            }
-            if (!asked && pos >= 2 * a.n - 4) ask();
-            const bool is_k = w.next();
-            const int j = w.j;
-            const uint32_t g = ring + static_cast<uint32_t>(pos), slot = g % kRing;
-            ok = wait(bar(kABEmpty + static_cast<int>(slot)), ((g / kRing) & 1u) ^ 1u);
-            if (!ok) break;
-            const int rows = min(kAttnTile, a.last - j * kAttnTile);  // keys of this tile that are seen
-            const int boxes = (rows + box - 1) / box;
-            const int key0 = (a.j0 + j) * kAttnTile;
-            const uint32_t fb = bar(kABFull + static_cast<int>(slot));
-            const uint32_t dst = base + L::kOffRing + slot * L::kTileBytes;
-            if (lane == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(boxes * box) * 128u * L::kPanels);
-            issued = g + 1;
-            __syncwarp();
-            // test support: the very first ring tile is armed but never filled
-            if (!((p.debug & 1u) && g == 0) && lane < boxes) {
-              const int key = key0 + lane * box;
-              int r = key, b = a.krow;
-              if (!own) {
-                r = a.krow + key;
-                b = 0;
-              } else if (paged) {
-                b = __ldg(p.table + static_cast<long long>(a.krow) * p.table_width + (key >> p.page_shift));
-                r = key & ((1 << p.page_shift) - 1);
-              }
-#pragma unroll
-              for (int c = 0; c < L::kPanels; ++c)
-                tma_load_4d(dst + c * kPanelBytes + static_cast<uint32_t>(lane * box) * 128u, is_k ? km : vm, fb, c * 64,
-                            a.head, r, b);
-            }
-            __syncwarp();
-          }
-          ring += 2u * static_cast<uint32_t>(a.n);
         }
-        if (!ok && !asked) break;
-        if (!asked) ask();
-        // (waited for even on an abort: the answer is written to shared memory)
-        if (lane == 0) drain_wait(bar(kABNext), nnext & 1u, p.budget_ns);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kABNext), 16);
+          asm volatile(
+              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                  next_slot),
+              "r"(bar(kABNext))
+              : "memory");
+        }
         __syncwarp();
+        // (waited for even on an abort: the answer is written to shared memory)
+        drain_wait(bar(kABNext), nnext & 1u, p.budget_ns);
         ++nnext;
         uint32_t got, nx;
         asm volatile(
@@ -948,49 +984,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             : "memory");
         fence_proxy_async_smem();
         __syncwarp();
-        if (!got) break;
+        if (!got) {
+          const uint32_t islot = it % kAttnItems;
+          if (bw.wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u) && lane == 0) {
+            items[islot].kind = -1;
+            mbar_arrive(bar(kABItemFull + islot));
+          }
+          break;
+        }
         x = static_cast<int>(nx);
-      }
-      if (ok) {
-        const uint32_t islot = it % kAttnItems;
-        if (wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u) && lane == 0) {
-          items[islot].kind = -1;
-          mbar_arrive(bar(kABItemFull + islot));
-        }
-      }
-      // copies still in flight must land before the CTA exits
-      if (lane == 0) {
-        for (int t = 0; t < 2; ++t)
-          if (nq[t] > 0) drain_wait(bar(kABQFull + t), (nq[t] - 1) & 1u, p.budget_ns);
-        for (uint32_t k = 1; k <= kRing && k <= issued; ++k)
-          drain_wait(bar(kABFull + static_cast<int>((issued - k) % kRing)), ((issued - k) / kRing) & 1u, p.budget_ns);
-      }
-    } else {
-      // --------------------------------------- tail of the last value tile
-      uint32_t ring = 0;
-      for (uint32_t it = 0;; ++it) {
-        const uint32_t islot = it % kAttnItems;
-        if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
-        const int kind = items[islot].kind, n = items[islot].n, fix = items[islot].fix;
-        if (kind < 0) break;
-        // (told by the MMA thread that waits for the tile: this warp does not
-        // follow the slot's other uses)
-        if (!bw.wait(bar(kABTail + islot), (it / kAttnItems) & 1u)) break;
-        if (fix) {
-          const uint32_t slot = (ring + value_pos(n - 1, n)) % kRing;
-          const uint32_t dst = base + L::kOffRing + slot * L::kTileBytes;
-          for (int e = fix * 8 + lane; e < kAttnTile * 8; e += 32)
-#pragma unroll
-            for (int c = 0; c < L::kPanels; ++c)
-              st_shared_v4(dst + c * kPanelBytes + static_cast<uint32_t>(e) * 16u, 0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kABFixed + islot));
-          mbar_arrive(bar(kABItemEmpty + islot));
-        }
-        ring += 2u * static_cast<uint32_t>(n);
       }
     }
   }
