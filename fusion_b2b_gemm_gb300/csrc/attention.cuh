@@ -233,14 +233,12 @@ struct Wait {
   }
   // By one thread.
   __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity) const {
-    bool done = ptx::mbar_try_wait(bar, parity);
-    if (!done) {
-      const uint32_t t0 = now();
-      while (!(done = ptx::mbar_try_wait(bar, parity)) && !*abort_flag) {
-        if (now() - t0 >= budget_ns) *abort_flag = 1;
-      }
+    const uint32_t t0 = now();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+      if (*abort_flag) return false;
+      if (now() - t0 >= budget_ns) *abort_flag = 1;
     }
-    return done;
+    return true;
   }
   // By a whole warp; every lane gets the same answer, so that no lane goes on
   // to a warp-wide instruction without the others.
@@ -667,7 +665,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // short enough for the instruction cache (16 columns at a time took
         // 2 us a tile, one instruction after the other).
         const bool none = __any_sync(0xffffffffu, l == 0.0f);
-        const uint64_t invx2 = pack2(inv, inv);
+        const uint64_t invx2 = pack2(inv, inv), f0x2 = pack2(f0, f0), f1x2 = pack2(f1, f1);
         auto emit = [&](int col, uint32_t (&o)[32]) {
           if (part) {
             float* d8 = pdst + static_cast<long long>(col / 8) * part_rows * 8;
@@ -715,8 +713,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               tmem_ld32(to + static_cast<uint32_t>(DP + col), o1);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
+              for (int k = 0; k < 32; k += 2) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(o1[k]), __uint_as_float(o1[k + 1])), f1x2,
+                             mul2(pack2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), f0x2)), x, y);
+                o[k] = __float_as_uint(x);
+                o[k + 1] = __float_as_uint(y);
+              }
             } else {
               tmem_wait_ld();
             }
@@ -747,8 +750,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         uint32_t ring = 0, nq = 0, np = 0, no = 0;
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
-          const uint32_t islot = it % kAttnItems;
-          if (!bw.wait1(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
+          const uint32_t islot = it % kAttnItems, iphase = (it / kAttnItems) & 1u;
+          if (!bw.wait1(bar(kABItemFull + islot), iphase)) break;
           const AttnItem& a = items[islot];
           if (a.kind < 0) break;
           const int n = a.n, fix = a.fix;
@@ -764,43 +767,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // Every ring tile is waited for and released by both streams, in
           // order, whether they use it or not: a stream that skipped uses of
           // a slot could not tell their completions from its own by parity.
-          auto landed = [&](uint32_t pos, uint32_t& slot) -> bool {
-            const uint32_t g = ring + pos;
-            slot = g % kRing;
-            return bw.wait1(bar(kABFull + static_cast<int>(slot)), (g / kRing) & 1u);
-          };
-          auto skip = [&](uint32_t pos) -> bool {
-            uint32_t slot;
-            if (!landed(pos, slot)) return false;
-            mbar_arrive(bar(kABEmpty + static_cast<int>(slot)));
-            return true;
-          };
-          // O += P.V of tile j (none before the first), then S of this stream's
-          // next tile.  All waits for tiles come before the ones for P, so
-          // that the MMAs follow one another.
-          const int stride = solo ? 2 : 1, j0 = solo ? t : 0, end = solo ? n : cnt;
-          if (solo && t == 1 && n > 0) ok = skip(key_pos(0));
-          if (cnt > 0 && ok) {
-            ok = bw.wait1(bar(kABQFull + t), nq & 1u);
-            ++nq;
-          }
-          for (int j = j0 - stride; cnt > 0 && j < end && ok; j += stride) {
-            const int next = j + stride;
-            uint32_t vslot = 0, kslot = 0;
-            if (j >= 0) {
-              if (solo) {  // the other stream's tiles that lie before this one's in the ring
-                if (j >= 1) ok = skip(value_pos(j - 1, n));
-                if (ok && j + 1 < n && (j + 1 >= 2 || t == 0)) ok = skip(key_pos(j + 1));
-              }
-              if (!ok || !(ok = landed(value_pos(j, n), vslot))) break;
+          // Each of this stream's value tiles is held until its next key tile
+          // (if there is one) has landed too, so that O += P.V and the next S
+          // are issued without a wait between them.
+          RingWalk w(n);
+          int keys = 0, vtile = -1;  // key tiles seen; value tile held
+          uint32_t vslot = 0, kslot = 0;
+          bool key = false;          // key tile held
+          for (int pos = 0; pos < 2 * n; ++pos) {
+            const bool is_key = w.next();
+            const uint32_t g = ring + static_cast<uint32_t>(pos), slot = g % kRing;
+            if (!(ok = bw.wait1(bar(kABFull + static_cast<int>(slot)), (g / kRing) & 1u))) break;
+            if (solo ? (w.j & 1) != t : w.j >= cnt) {
+              mbar_arrive(bar(kABEmpty + static_cast<int>(slot)));
+              continue;
             }
-            if (next < end && !(ok = landed(key_pos(next), kslot))) break;
-            if (j >= 0) {
-              if (fix && j == n - 1) {
+            if (is_key) {
+              kslot = slot;
+              key = true;
+              ++keys;
+            } else {
+              vslot = slot;
+              vtile = w.j;
+            }
+            if (vtile < 0 ? keys != 1 : !key && keys < cnt) continue;
+            if (vtile < 0) {
+              if (!(ok = bw.wait1(bar(kABQFull + t), nq & 1u))) break;
+              ++nq;
+            } else {
+              if (fix && vtile == n - 1) {
                 if (teller) mbar_arrive(bar(kABTail + islot));
-                if (!(ok = bw.wait1(bar(kABFixed + islot), (it / kAttnItems) & 1u))) break;
+                if (!(ok = bw.wait1(bar(kABFixed + islot), iphase))) break;
               }
-              if (j == j0) {  // the epilogue has read the item before's O
+              const bool first = vtile < (solo ? 2 : 1);
+              if (first) {  // the epilogue has read the item before's O
                 if (!(ok = bw.wait1(bar(kABOEmpty + t), (no & 1u) ^ 1u))) break;
                 ++no;
               }
@@ -811,14 +811,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (uint32_t kk = 4 * half; kk < 4 * half + 4; ++kk)
-                  mma_ts<false>(d_o, d_s + kk * 8u, vd + kk * (16u * 128u >> 4), idesc_pv, (kk || j != j0) ? 1u : 0u);
+                  mma_ts<false>(d_o, d_s + kk * 8u, vd + kk * (16u * 128u >> 4), idesc_pv, (kk || !first) ? 1u : 0u);
               }
               if (!ok) break;
               ++np;
               tc_commit(bar(kABEmpty + static_cast<int>(vslot)));
-              if (next >= end) tc_commit(bar(kABOFull + t));
+              if (!key) tc_commit(bar(kABOFull + t));
+              vtile = -1;
             }
-            if (next < end) {
+            if (key) {
+              key = false;
               tc_fence_after();
               const uint64_t kd = k_desc0 + kslot * (L::kTileBytes >> 4);
 #pragma unroll
@@ -828,13 +830,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
               tc_commit(bar(kABSFull + t));
               tc_commit(bar(kABEmpty + static_cast<int>(kslot)));
-              if (next + stride >= end) tc_commit(bar(kABQEmpty + t));
+              if (keys == cnt) tc_commit(bar(kABQEmpty + t));
             }
-          }
-          if (solo) {
-            if (ok && n > 0 && ((n - 1) & 1) != t) ok = skip(value_pos(n - 1, n));
-          } else {
-            for (int j = cnt; j < n && ok; ++j) ok = skip(key_pos(j)) && skip(value_pos(j, n));
           }
           if (!ok) break;
           ring += 2u * static_cast<uint32_t>(n);
@@ -857,7 +854,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       grid_dependency_wait();
-      uint32_t ring = 0, issued = 0, nq0 = 0, nq1 = 0;
+      uint32_t ring = 0, issued = 0;
+      uint32_t nq = 0, used = 0;  // bit t: parity of stream t's query loads, whether it had any
       bool ok = true;
       const int panel = lane & (L::kPanels - 1), box_at = lane / L::kPanels;  // a lane's share of a tile's boxes
       for (uint32_t it = 0; ok; ++it) {
@@ -875,25 +873,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         RingWalk w(n);
         for (int pos = 0; pos < 2 * n; ++pos) {
           if (pos == 1) {  // the query tiles, behind the first key tile
-            const int tok = a.tok0, cnt0 = stream_tiles(a, 0), cnt1 = stream_tiles(a, 1);
             const CUtensorMap* qm = own ? &tm_q_own : &tm_q;
-            const uint32_t bytes = own ? p.own_q_bytes : p.q_bytes;
-            if (cnt0 > 0) {
-              if (!(ok = bw.wait(bar(kABQEmpty), (nq0 & 1u) ^ 1u))) break;
-              ++nq0;
-              if (lane == 0) mbar_arrive_expect_tx(bar(kABQFull), bytes);
-              __syncwarp();
-              if (box_at == 0) tma_load_4d(base + panel * kPanelBytes, qm, bar(kABQFull), panel * 64, 0, head, tok);
-            }
-            if (cnt1 > 0) {
-              if (!(ok = bw.wait(bar(kABQEmpty + 1), (nq1 & 1u) ^ 1u))) break;
-              ++nq1;
-              if (lane == 0) mbar_arrive_expect_tx(bar(kABQFull + 1), bytes);
+#pragma unroll 1
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (stream_tiles(a, t) == 0) continue;
+              if (!(ok = bw.wait(bar(kABQEmpty + t), ((nq >> t) & 1u) ^ 1u))) break;
+              nq ^= 1u << t;
+              used |= 1u << t;
+              if (lane == 0) mbar_arrive_expect_tx(bar(kABQFull + t), own ? p.own_q_bytes : p.q_bytes);
               __syncwarp();
               if (box_at == 0)
-                tma_load_4d(base + L::kTileBytes + panel * kPanelBytes, qm, bar(kABQFull + 1), panel * 64, 0, head,
-                            tok + (a.solo ? 0 : p.tile_tokens));
+                tma_load_4d(base + static_cast<uint32_t>(t) * L::kTileBytes + panel * kPanelBytes, qm, bar(kABQFull + t),
+                            panel * 64, 0, head, a.tok0 + (a.solo ? 0 : t * p.tile_tokens));
             }
+            if (!ok) break;
           }
           // Near the end of the item's loads warp 11 asks for the next one.
           if (pos == max(2 * n - 4, 0) && lane == 0) mbar_arrive(bar(kABAsk));
@@ -932,8 +925,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       __syncwarp();
       // copies still in flight must land before the CTA exits
-      if (nq0 > 0) drain_wait(bar(kABQFull), (nq0 - 1) & 1u, p.budget_ns);
-      if (nq1 > 0) drain_wait(bar(kABQFull + 1), (nq1 - 1) & 1u, p.budget_ns);
+      for (int t = 0; t < 2; ++t)
+        if ((used >> t) & 1u) drain_wait(bar(kABQFull + t), ((nq >> t) & 1u) ^ 1u, p.budget_ns);
       for (uint32_t k = 1; k <= kRing && k <= issued; ++k)
         drain_wait(bar(kABFull + static_cast<int>((issued - k) % kRing)), ((issued - k) / kRing) & 1u, p.budget_ns);
     } else {
