@@ -10,45 +10,23 @@ last one is 1.  Inference only.  There is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
-from . import DTYPES, _check, _current_device, _lib
+from . import DTYPES, _check, _current_device, _lib, _stream_handle
 
 __all__ = ["PromptAttentionPlan", "SharedPrefixAttentionPlan"]
 
 _TORCH = {"f16": torch.float16, "bf16": torch.bfloat16}
-_P, _I = ctypes.c_void_p, ctypes.c_int64
 
-
-def _rows(*names):
-    """Fields of one b2b_attn_rows_t for each name."""
-    return [(f"{n}_{f}", t) for n in names
-            for f, t in (("data", _P), ("row_stride", _I), ("head_stride", _I), ("block_stride", _I))]
-
-
-class _PromptRun(ctypes.Structure):  # b2b_prompt_attention_t
-    _fields_ = ([(n, _I) for n in ("batch", "tokens", "key_rows", "causal")] + _rows("q", "k", "v", "out") +
-                [(n, _P) for n in ("cu_q", "cu_k", "lse", "workspace")] + [("workspace_bytes", ctypes.c_size_t)])
-
-
-class _SharedRun(ctypes.Structure):  # b2b_shared_attention_t
-    _fields_ = ([(n, _I) for n in ("batch", "fresh", "prefix", "cache_rows", "cache_blocks", "table_width")] +
-                _rows("q", "prefix_k", "prefix_v", "cache_k", "cache_v", "out") +
-                [(n, _P) for n in ("lengths", "page_table", "lse", "workspace")] +
-                [("workspace_bytes", ctypes.c_size_t)])
-
-
-def _packed(t):
-    """Arguments of a [rows][heads][dim] tensor."""
-    s = t.stride()
-    return t.data_ptr(), s[0], s[1], 0
-
-
-def _blocks(t):
-    """Arguments of a [blocks][rows][heads][dim] tensor."""
-    s = t.stride()
-    return t.data_ptr(), s[1], s[2], s[0]
+# The argument structures, whose members all take eight bytes (b2b_attn_rows_t:
+# data, row_stride, head_stride, block_stride), as the C functions read them.
+# b2b_prompt_attention_t: batch, tokens, key_rows, causal; q, k, v, out; cu_q, cu_k, lse, workspace, workspace_bytes
+_prompt_run = struct.Struct("25q").pack
+# b2b_shared_attention_t: batch, fresh, prefix, cache_rows, cache_blocks, table_width; q, prefix_k, prefix_v,
+# cache_k, cache_v, out; lengths, page_table, lse, workspace, workspace_bytes
+_shared_run = struct.Struct("35q").pack
 
 
 class _AttentionPlan:
@@ -74,39 +52,60 @@ class _AttentionPlan:
         self._workspace_sizes = {}
 
     # -- checks ------------------------------------------------------------
-    def _tensor(self, name, t, heads, dims):
+    # The runs test a tensor's type, layout and device in one expression and
+    # come here only to say what is wrong: a call's checks cost about as much
+    # as its launch.
+    def _refuse(self, name, t, heads, dims):
         if t.dtype is not self._torch_dtype:
             raise TypeError(f"{name}: {t.dtype} given, {self._torch_dtype} expected")
         shape = t.shape
         if len(shape) != dims or shape[-2] != heads or shape[-1] != self.head_dim:
             raise ValueError(f"{name}: shape {tuple(shape)} given, {'[blocks, ' if dims == 4 else '['}rows, {heads}, "
                              f"{self.head_dim}] expected")
-        if t.stride(-1) != 1:
-            raise ValueError(f"{name}: the elements of a head must be consecutive (last stride {t.stride(-1)})")
         self._placed(name, t)
+        raise ValueError(f"{name}: the elements of a head must be consecutive (last stride {t.stride(-1)})")
+
+    def _packed(self, name, t, heads):
+        """Rows and arguments of a [rows][heads][dim] tensor."""
+        shape, stride = t.shape, t.stride()
+        if (t.dtype is not self._torch_dtype or len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim
+                or stride[2] != 1 or t.get_device() != self.device_index):
+            self._refuse(name, t, heads, 3)
+        return shape[0], t.data_ptr(), stride[0], stride[1]
+
+    def _blocks(self, name, t):
+        """Blocks, rows and arguments of a [blocks][rows][heads][dim] tensor."""
+        shape, stride = t.shape, t.stride()
+        if (t.dtype is not self._torch_dtype or len(shape) != 4 or shape[2] != self.kv_heads or shape[3] != self.head_dim
+                or stride[3] != 1 or t.get_device() != self.device_index):
+            self._refuse(name, t, self.kv_heads, 4)
+        return shape[0], shape[1], t.data_ptr(), stride[1], stride[2], stride[0]
 
     def _placed(self, name, t):
         if t.get_device() != self.device_index:  # (-1 for a CPU tensor)
             raise ValueError(f"{name} is on {t.device}, the plan on cuda:{self.device_index}")
 
-    def _counts(self, name, t, n, width=None):
-        """A dense int32 array of n entries (or n rows of any width)."""
+    def _counts(self, name, t, n, dims=1):
+        """A dense int32 array of n entries (or n rows of any width); returns its extent and address."""
+        shape = t.shape
         if t.dtype is not torch.int32:
             raise TypeError(f"{name}: {t.dtype} given, torch.int32 expected")
-        if t.dim() != (1 if width is None else 2) or (n is not None and t.shape[0] != n) or not t.is_contiguous():
-            raise ValueError(f"{name}: shape {tuple(t.shape)} given, a contiguous array of "
-                             f"{n if width is None else f'{n} rows'} expected")
-        self._placed(name, t)
+        if len(shape) != dims or (n is not None and shape[0] != n) or not t.is_contiguous():
+            raise ValueError(f"{name}: shape {tuple(shape)} given, a contiguous array of "
+                             f"{n if dims == 1 else f'{n} rows'} expected")
+        if t.get_device() != self.device_index:
+            self._placed(name, t)
+        return shape[-1], t.data_ptr()
 
-    def _results(self, q, out, lse, return_lse, sizes, query):
-        """Output, LSE and workspace of one run, in the pool of the current stream."""
-        tokens = q.shape[0]
+    def _results(self, q, tokens, out, lse, return_lse):
+        """Output and LSE of one run with the output's arguments and the LSE's address."""
         if out is None:
             out = torch.empty((tokens, self.q_heads, self.head_dim), dtype=self._torch_dtype, device=q.device)
+            args = out.data_ptr(), self.q_heads * self.head_dim, self.head_dim
         else:
-            self._tensor("out", out, self.q_heads, 3)
-            if out.shape[0] != tokens:
-                raise ValueError(f"out: {out.shape[0]} rows given, {tokens} expected")
+            rows, *args = self._packed("out", out, self.q_heads)
+            if rows != tokens:
+                raise ValueError(f"out: {rows} rows given, {tokens} expected")
         if lse is not None:
             if lse.dtype is not torch.float32:
                 raise TypeError(f"lse: {lse.dtype} given, torch.float32 expected")
@@ -115,6 +114,10 @@ class _AttentionPlan:
             self._placed("lse", lse)
         elif return_lse:
             lse = torch.empty((tokens, self.q_heads), dtype=torch.float32, device=q.device)
+        return out, lse, args, 0 if lse is None else lse.data_ptr()
+
+    def _workspace(self, q, sizes, query):
+        """Workspace of one run, from the pool of the current stream, and its size."""
         need = self._workspace_sizes.get(sizes)
         if need is None:
             n = ctypes.c_size_t()
@@ -122,14 +125,16 @@ class _AttentionPlan:
             if len(self._workspace_sizes) >= 4096:
                 self._workspace_sizes.clear()
             need = self._workspace_sizes[sizes] = n.value
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        return out, lse, ws, need
+        return (torch.empty(need, dtype=torch.uint8, device=q.device) if need else None), need
+
+    def _stream(self):
+        # (the public torch.cuda.current_stream() builds an object each time, 3 us)
+        return torch._C._cuda_getCurrentRawStream(self.device_index) or None
 
     # -- as the chain plans ------------------------------------------------
     def status(self, stream=None) -> int:
         """Synchronise and return the device status word (0 = OK)."""
-        stream = torch.cuda.current_stream() if stream is None else stream
-        return int(_lib.b2b_attn_plan_device_status(self._h, stream.cuda_stream or None))
+        return int(_lib.b2b_attn_plan_device_status(self._h, _stream_handle(stream)))
 
     def set_wait_budget(self, ns: int) -> None:
         _check(_lib.b2b_attn_plan_set_wait_budget(self._h, int(ns)), "b2b_attn_plan_set_wait_budget")
@@ -167,26 +172,23 @@ class PromptAttentionPlan(_AttentionPlan):
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.run(q, k, v, cu_q, cu_k, causal, out, lse, return_lse)
-        if cu_k is None:
-            cu_k = cu_q
-        self._tensor("q", q, self.q_heads, 3)
-        self._tensor("k", k, self.kv_heads, 3)
-        self._tensor("v", v, self.kv_heads, 3)
-        tokens, key_rows = q.shape[0], k.shape[0]
-        if v.shape[0] != key_rows:
-            raise ValueError(f"v: {v.shape[0]} rows given, {key_rows} expected as k has")
-        self._counts("cu_q", cu_q, None)
-        batch = cu_q.shape[0] - 1
-        if batch < 0:
+        tokens, *qa = self._packed("q", q, self.q_heads)
+        key_rows, *ka = self._packed("k", k, self.kv_heads)
+        rows, *va = self._packed("v", v, self.kv_heads)
+        if rows != key_rows:
+            raise ValueError(f"v: {rows} rows given, {key_rows} expected as k has")
+        offsets, cu_qp = self._counts("cu_q", cu_q, None)
+        if offsets < 1:
             raise ValueError("cu_q: at least one offset is expected")
-        self._counts("cu_k", cu_k, batch + 1)
-        out, lse, ws, need = self._results(q, out, lse, return_lse, (batch, tokens, key_rows),
-                                           _lib.b2b_prompt_attention_workspace)
-        r = _PromptRun(batch, tokens, key_rows, bool(causal), *_packed(q), *_packed(k), *_packed(v), *_packed(out),
-                       cu_q.data_ptr(), cu_k.data_ptr(), None if lse is None else lse.data_ptr(),
-                       None if ws is None else ws.data_ptr(), need)
-        _check(_lib.b2b_prompt_attention_run(self._h, ctypes.byref(r), torch.cuda.current_stream().cuda_stream or None),
-               "b2b_prompt_attention_run")
+        cu_kp = cu_qp if cu_k is None else self._counts("cu_k", cu_k, offsets)[1]
+        batch = offsets - 1
+        out, lse, oa, lsep = self._results(q, tokens, out, lse, return_lse)
+        ws, need = self._workspace(q, (batch, tokens, key_rows), _lib.b2b_prompt_attention_workspace)
+        r = _prompt_run(batch, tokens, key_rows, bool(causal), *qa, 0, *ka, 0, *va, 0, *oa, 0, cu_qp, cu_kp, lsep,
+                        0 if ws is None else ws.data_ptr(), need)
+        code = _lib.b2b_prompt_attention_run(self._h, r, self._stream())
+        if code:
+            _check(code, "b2b_prompt_attention_run")
         return out if lse is None else (out, lse)
 
 
@@ -210,35 +212,31 @@ class SharedPrefixAttentionPlan(_AttentionPlan):
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.run(q, prefix_k, prefix_v, cache_k, cache_v, lengths, page_table, out, lse, return_lse)
-        self._tensor("q", q, self.q_heads, 3)
-        self._tensor("prefix_k", prefix_k, self.kv_heads, 3)
-        self._tensor("prefix_v", prefix_v, self.kv_heads, 3)
-        self._tensor("cache_k", cache_k, self.kv_heads, 4)
-        self._tensor("cache_v", cache_v, self.kv_heads, 4)
-        if prefix_v.shape[0] != prefix_k.shape[0]:
-            raise ValueError(f"prefix_v: {prefix_v.shape[0]} rows given, {prefix_k.shape[0]} expected as prefix_k has")
-        if cache_v.shape != cache_k.shape:
+        tokens, *qa = self._packed("q", q, self.q_heads)
+        prefix, *pka = self._packed("prefix_k", prefix_k, self.kv_heads)
+        rows, *pva = self._packed("prefix_v", prefix_v, self.kv_heads)
+        if rows != prefix:
+            raise ValueError(f"prefix_v: {rows} rows given, {prefix} expected as prefix_k has")
+        blocks, rows, *cka = self._blocks("cache_k", cache_k)
+        vblocks, vrows, *cva = self._blocks("cache_v", cache_v)
+        if vblocks != blocks or vrows != rows:
             raise ValueError(f"cache_v: shape {tuple(cache_v.shape)} given, {tuple(cache_k.shape)} expected as cache_k has")
-        self._counts("lengths", lengths, None)
-        batch, tokens = lengths.shape[0], q.shape[0]
+        batch, lengthsp = self._counts("lengths", lengths, None)
         if tokens % batch if batch else tokens:
             raise ValueError(f"q: {tokens} rows given, a multiple of the {batch} requests expected")
         fresh = tokens // batch if batch else 0
-        blocks, rows = cache_k.shape[:2]
-        width = 0
-        if page_table is not None:
-            self._counts("page_table", page_table, batch, "any")
-            width = page_table.shape[1]
-        elif blocks != batch:
-            raise ValueError(f"cache_k: {blocks} requests given, {batch} expected as lengths has")
-        prefix = prefix_k.shape[0]
-        room = (width * rows if blocks else 0) if page_table is not None else rows
-        out, lse, ws, need = self._results(q, out, lse, return_lse, (batch, fresh, prefix, room),
-                                           _lib.b2b_shared_attention_workspace)
-        r = _SharedRun(batch, fresh, prefix, rows, blocks, width, *_packed(q), *_packed(prefix_k), *_packed(prefix_v),
-                       *_blocks(cache_k), *_blocks(cache_v), *_packed(out), lengths.data_ptr(),
-                       None if page_table is None else page_table.data_ptr(), None if lse is None else lse.data_ptr(),
-                       None if ws is None else ws.data_ptr(), need)
-        _check(_lib.b2b_shared_attention_run(self._h, ctypes.byref(r), torch.cuda.current_stream().cuda_stream or None),
-               "b2b_shared_attention_run")
+        if page_table is None:
+            width, tablep, room = 0, 0, rows
+            if blocks != batch:
+                raise ValueError(f"cache_k: {blocks} requests given, {batch} expected as lengths has")
+        else:
+            width, tablep = self._counts("page_table", page_table, batch, 2)
+            room = width * rows if blocks else 0
+        out, lse, oa, lsep = self._results(q, tokens, out, lse, return_lse)
+        ws, need = self._workspace(q, (batch, fresh, prefix, room), _lib.b2b_shared_attention_workspace)
+        r = _shared_run(batch, fresh, prefix, rows, blocks, width, *qa, 0, *pka, 0, *pva, 0, *cka, *cva, *oa, 0, lengthsp,
+                        tablep, lsep, 0 if ws is None else ws.data_ptr(), need)
+        code = _lib.b2b_shared_attention_run(self._h, r, self._stream())
+        if code:
+            _check(code, "b2b_shared_attention_run")
         return out if lse is None else (out, lse)

@@ -83,6 +83,7 @@ enum : int {  // barrier slots (8 bytes each)
   kABMlFull = 45,     // [2] stream's (m, l) written
   kABMlEmpty = 47,    // [2] stream's (m, l) read
   kABOEmpty = 49,     // [2] stream's O read
+  kABTurn = 54,       // [2] the stream may compute its next exponentials
   kABAsk = 40,        // an item's loads are nearly all issued
   kABTail = 51,       // [3] last value tile landed (one arrival per item)
   kABItemFull = 28,   // [3] descriptor written
@@ -426,6 +427,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(bar(kABMlFull + t), 4);
       mbar_init(bar(kABMlEmpty + t), 4);
       mbar_init(bar(kABOEmpty + t), 4);
+      mbar_init(bar(kABTurn + t), 4);
       mbar_init(bar(kABDrain + t), 1);
     } else if (lane < 10 + kAttnItems) {
       const int s = lane - 10;
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t to = tmem + lane_off + kColO + static_cast<uint32_t>(DP * t);
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = pack2(sl2, sl2);
-    uint32_t nscore = 0, nml = 0;
+    uint32_t nscore = 0, nml = 0, nturn = 0;
     for (uint32_t it = 0;; ++it) {
       const uint32_t islot = it % kAttnItems;
       if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
@@ -470,6 +472,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (a.kind < 0) break;
       const int cnt = stream_tiles(a, t);
       const int tile0 = a.solo ? 0 : t * p.tile_tokens;  // first token of this stream's tile
+      // In the tiles that both streams of a pair item have (stream 0 has no
+      // more than stream 1) they take turns at the exponentials, which keeps
+      // them half a tile apart, one in its MMAs while the other has the
+      // exponential unit: 128-wide heads, 8192 tokens: 375 -> 358 us.  64-wide
+      // ones, bound by the softmax, lose by it (284 -> 297 us).
+      const int common = DP < 128 || a.solo ? 0 : a.n0;
       const int vis = visible(a, tile0 + row_tok);
       const int vis_min = visible(a, tile0);
       float m = -INFINITY;
@@ -528,6 +536,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         const float mc = m == -INFINITY ? 0.0f : m * sl2;
         const uint64_t mcx2 = pack2(-mc, -mc);
+        if (i < common) {
+          if (!(ok = bw.wait(bar(kABTurn + t), (nturn & 1u) ^ (t == 0)))) break;
+          ++nturn;
+        }
         // P in two halves of 64 keys, so that the second GEMM starts on the
         // first while the second is computed; the row's sum afterwards.
 #pragma unroll
@@ -548,7 +560,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kABPFull + 2 * t + c / 2));
+            if (lane == 0) {
+              mbar_arrive(bar(kABPFull + 2 * t + c / 2));
+              if (c == 3 && i < common) mbar_arrive(bar(kABTurn + 1 - t));
+            }
           }
         }
         uint64_t sums[4];
@@ -998,55 +1013,96 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // Joins the parts of every row: with M = max over parts of c m_p,
-// o = sum_p 2^(c m_p - M) o_p / sum_p 2^(c m_p - M) l_p.  One thread per eight
-// columns of a row; parts in order, so the result does not depend on timing.
+// o = sum_p 2^(c m_p - M) o_p / sum_p 2^(c m_p - M) l_p.
+// A block takes 32 rows and eight of their columns.  Each of its eight warps
+// reads every eighth part, four of them in flight (one thread walking all
+// parts of a row took 16 us for 17 parts: a memory latency for each), and the
+// warps' results are joined through shared memory.  The order is fixed, so
+// the result does not depend on timing.
+constexpr int kJoinWarps = 8;
+
+struct AttnPart {
+  float m, l, o[8];  // (m = -inf, l = 0, o = 0: nothing yet)
+  __device__ __forceinline__ void add(float pm, float pl, const float* po) {
+    if (pl == 0.0f) return;  // (a part without keys; its o was not written)
+    const float big = fmaxf(m, pm);
+    const float f = m == big ? 1.0f : exp2f(m - big), g = pm == big ? 1.0f : exp2f(pm - big);
+    m = big;
+    l = l * f + pl * g;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = o[k] * f + po[k] * g;
+  }
+};
+
 template <bool BF16>
-__global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __grid_constant__ AttnParams p) {
   using namespace ptx;
   using namespace attn;
+  __shared__ float joined[kJoinWarps][10][32];
   grid_launch_dependents();
   grid_dependency_wait();
-  // consecutive threads take consecutive rows of the same eight columns
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long rows = static_cast<long long>(p.tokens) * (p.group * p.kv_heads);
-  const int col = static_cast<int>(blockIdx.y) * 8;
-  int r = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
-  if (r >= rows) return;
-  const int row = r;
-  int token = p.by_group.split(r);  // r: head of the group
-  const int head = p.by_tokens.split(token) * p.group + r;
+  const int col8 = static_cast<int>(blockIdx.y);
+  const int row = static_cast<int>(blockIdx.x) * 32 + lane;
+  const bool valid = row < rows;
+  AttnPart a = {-INFINITY, 0.0f, {0, 0, 0, 0, 0, 0, 0, 0}};
+  if (valid) {
+    constexpr int kBatch = 4;
+    for (int s0 = warp; s0 < p.parts; s0 += kBatch * kJoinWarps) {
+      float2 ml[kBatch];
+      float4 u[kBatch], v[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int s = s0 + b * kJoinWarps;
+        ml[b] = make_float2(0.0f, 0.0f);
+        if (s < p.parts) {
+          const float4* src =
+              reinterpret_cast<const float4*>(p.part_o + ((static_cast<long long>(s) * (p.dim / 8) + col8) * rows + row) * 8);
+          ml[b] = p.part_ml[s * rows + row];
+          u[b] = src[0];
+          v[b] = src[1];
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (s0 + b * kJoinWarps >= p.parts) break;
+        const float po[8] = {u[b].x, u[b].y, u[b].z, u[b].w, v[b].x, v[b].y, v[b].z, v[b].w};
+        a.add(ml[b].x, ml[b].y, po);
+      }
+    }
+  }
+  joined[warp][8][lane] = a.m;
+  joined[warp][9][lane] = a.l;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) joined[warp][k][lane] = a.o[k];
+  __syncthreads();
+  if (warp != 0 || !valid) return;
+  for (int w = 1; w < kJoinWarps; ++w) {
+    float po[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) po[k] = joined[w][k][lane];
+    a.add(joined[w][8][lane], joined[w][9][lane], po);
+  }
+  int head = row, token;
+  token = p.by_group.split(head);  // head: of the group
+  head += p.by_tokens.split(token) * p.group;
   if (p.op == kAttnPrompt) {
     // rows that belong to no sequence are left alone
     if (token < __ldg(p.cu_q) || token >= __ldg(p.cu_q + p.batch)) return;
   }
-  float big = -INFINITY;
-  for (int s = 0; s < p.parts; ++s) {
-    const float2 ml = p.part_ml[s * rows + row];
-    if (ml.y != 0.0f) big = fmaxf(big, ml.x);
-  }
-  float l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int s = 0; s < p.parts; ++s) {
-    const float2 ml = p.part_ml[s * rows + row];
-    if (ml.y == 0.0f) continue;
-    const float f = ml.x == big ? 1.0f : exp2f(ml.x - big);
-    l += ml.y * f;
-    const float4* src =
-        reinterpret_cast<const float4*>(p.part_o + ((static_cast<long long>(s) * (p.dim / 8) + col / 8) * rows + row) * 8);
-    const float4 u = src[0], v = src[1];
-    o[0] += u.x * f; o[1] += u.y * f; o[2] += u.z * f; o[3] += u.w * f;
-    o[4] += v.x * f; o[5] += v.y * f; o[6] += v.z * f; o[7] += v.w * f;
-  }
-  const float inv = 1.0f / l;
+  const float inv = 1.0f / a.l;
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float x = l == 0.0f ? 0.0f : o[2 * k] * inv, y = l == 0.0f ? 0.0f : o[2 * k + 1] * inv;
+    const float x = a.l == 0.0f ? 0.0f : a.o[2 * k] * inv, y = a.l == 0.0f ? 0.0f : a.o[2 * k + 1] * inv;
     w[k] = BF16 ? pack_bf16x2(__float_as_uint(x), __float_as_uint(y)) : pack_f16x2(__float_as_uint(x), __float_as_uint(y));
   }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + token * p.out_row + head * p.out_head + col) =
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + token * p.out_row + head * p.out_head + col8 * 8) =
       make_uint4(w[0], w[1], w[2], w[3]);
-  if (col == 0 && p.lse)
+  if (col8 == 0 && p.lse)
     p.lse[token * p.lse_row + head * p.lse_head] =
-        l == 0.0f ? -INFINITY : static_cast<float>((big + log2f(l)) * 0.6931471805599453);
+        a.l == 0.0f ? -INFINITY : static_cast<float>((a.m + log2f(a.l)) * 0.6931471805599453);
 }
 
 }  // namespace b2b

@@ -190,8 +190,8 @@ b2b_status_t launch(const b2b_attn_plan_s* p, CUtensorMap (&maps)[6], AttnParams
   if (e == cudaSuccess && a.parts > 1) {
     const int64_t rows = static_cast<int64_t>(a.tokens) * p->q_heads;
     void* cargs[] = {&a};
-    e = launch_pdl(p->k.combine, dim3(static_cast<unsigned>((rows + 255) / 256), static_cast<unsigned>(p->dim / 8)),
-                   dim3(256), cargs, 0, stream);
+    e = launch_pdl(p->k.combine, dim3(static_cast<unsigned>((rows + 31) / 32), static_cast<unsigned>(p->dim / 8)),
+                   dim3(32 * kJoinWarps), cargs, 0, stream);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
