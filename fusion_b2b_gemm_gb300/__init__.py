@@ -82,7 +82,7 @@ def _load() -> ctypes.CDLL:
         "b2b_attn_plan_device_status": [P, P],
         "b2b_attn_plan_set_wait_budget": [P, u64],
         "b2b_attn_plan_set_debug": [P, ctypes.c_uint32],
-        "b2b_prompt_attention_workspace": [P, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "b2b_prompt_attention_workspace": [P, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
         "b2b_prompt_attention_run": [P, P, P],
         "b2b_shared_attention_workspace": [P, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
         "b2b_shared_attention_run": [P, P, P],

@@ -183,8 +183,9 @@ class PromptAttentionPlan(_AttentionPlan):
         cu_kp = cu_qp if cu_k is None else self._counts("cu_k", cu_k, offsets)[1]
         batch = offsets - 1
         out, lse, oa, lsep = self._results(q, tokens, out, lse, return_lse)
-        ws, need = self._workspace(q, (batch, tokens, key_rows), _lib.b2b_prompt_attention_workspace)
-        r = _prompt_run(batch, tokens, key_rows, bool(causal), *qa, 0, *ka, 0, *va, 0, *oa, 0, cu_qp, cu_kp, lsep,
+        causal = bool(causal)
+        ws, need = self._workspace(q, (batch, tokens, key_rows, causal), _lib.b2b_prompt_attention_workspace)
+        r = _prompt_run(batch, tokens, key_rows, causal, *qa, 0, *ka, 0, *va, 0, *oa, 0, cu_qp, cu_kp, lsep,
                         0 if ws is None else ws.data_ptr(), need)
         code = _lib.b2b_prompt_attention_run(self._h, r, self._stream())
         if code:

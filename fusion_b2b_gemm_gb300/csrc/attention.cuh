@@ -52,7 +52,7 @@ namespace b2b {
 
 constexpr int kAttnThreads = 512;
 // registers of a softmax, an epilogue and another thread: 128 of each thread at launch, shared out anew
-constexpr int kAttnSoftmaxRegs = 176, kAttnEpilogueRegs = 96, kAttnOtherRegs = 64;
+constexpr int kAttnSoftmaxRegs = 160, kAttnEpilogueRegs = 96, kAttnOtherRegs = 96;
 static_assert(256 * kAttnSoftmaxRegs + 128 * kAttnEpilogueRegs + 128 * kAttnOtherRegs <= 65536, "register file");
 constexpr int kAttnTile = 128;        // query rows and keys of a tile
 constexpr int kAttnItems = 3;         // item descriptors in flight
@@ -124,7 +124,7 @@ struct FastDiv {
 struct AttnParams {
   int op;
   int group, kv_heads, dim;
-  FastDiv by_group, by_tokens, by_kv_heads, by_block, by_splits, by_row_blocks, by_own_splits, by_own_blocks;  // (by_block: 2 tile_tokens)
+  FastDiv by_group, by_tokens, by_kv_heads, by_block, by_splits, by_row_blocks, by_own_splits, by_own_blocks;  // (by_block: tokens of an item)
   int tile_tokens;     // query tokens of a 128-row tile: 128 / group
   int tokens;          // query rows of the packed query tensor
   int batch;           // sequences or requests
@@ -133,6 +133,7 @@ struct AttnParams {
   const int* cu_q;
   const int* cu_k;
   int key_rows;
+  int most_blocks;     // no sequence has more blocks
   // shared prefix
   int fresh;           // new tokens per request
   int prefix;          // keys of the prefix
@@ -151,6 +152,7 @@ struct AttnParams {
   long long lse_row, lse_head;
   int wide_stores;     // rows of `out` on 32-byte boundaries: 32-byte stores
   int parts;
+  int join_warps;      // warps that share a row's parts when they are joined (1, 2, 4 or 8)
   // Rows of the parts are numbered (key/value head, token, head of the group),
   // as the lanes of a tile hold them: a warp's stores are consecutive.
   float* part_o;       // [parts][dim / 8][rows][8]
@@ -270,15 +272,27 @@ struct RingWalk {
   }
 };
 
-// Sequence b's first packed row and row count, inside the tensor whatever the table says.
-__device__ __forceinline__ void packed_range(const int* cu, int b, int rows, int& first, int& len) {
-  first = clampi(__ldg(cu + b), 0, rows);
-  len = clampi(__ldg(cu + b + 1), first, rows) - first;
+// A sequence's query and key rows, inside the tensors whatever the offsets say.
+struct AttnSeq {
+  int q0, qlen, k0, klen, blocks;
+};
+__device__ __forceinline__ AttnSeq load_seq(const AttnParams& p, int b) {
+  AttnSeq s = {0, 0, 0, 0, 0};
+  if (p.op == kAttnPrompt && b < p.batch) {
+    const int q = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1), k = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+    s.q0 = clampi(q, 0, p.tokens);
+    s.qlen = clampi(q1, s.q0, p.tokens) - s.q0;
+    s.k0 = clampi(k, 0, p.key_rows);
+    s.klen = clampi(k1, s.k0, p.key_rows) - s.k0;
+    s.blocks = p.by_block.quotient(s.qlen + static_cast<int>(p.by_block.d) - 1);
+  }
+  return s;
 }
 
 // Fill `a` for item number x (whole warp; every lane gets the same).  False: no such item.
-__device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane, AttnItem& a) {
-  const int block = 2 * p.tile_tokens;
+// mine: the lane's sequence, load_seq(p, lane), of a prompt.
+__device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane, const AttnSeq& mine, AttnItem& a) {
+  const int block = static_cast<int>(p.by_block.d);
   const FastDiv* by_splits = &p.by_splits;
   if (p.op == kAttnPrompt) {
     int u = p.by_splits.split(x);
@@ -286,46 +300,54 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
     x = u;
     u = p.by_kv_heads.split(x);
     a.head = x;
-    // Blocks are numbered from the end of the last sequence: under a causal
-    // mask a sequence's last blocks see the most keys, and the longest items
-    // are best begun first.
-    int seq = 0, qlen = 0, at = 0, first = 0;
-    bool found = false;
+    // Blocks in the order of their place in their sequences, the furthest
+    // first: under a causal mask they see the most keys, and the longest items
+    // are best begun first.  The blocks at place k or further of all
+    // sequences number sum max(0, blocks - k); the item's place is the
+    // largest k for which that exceeds u.
+    auto further = [&](int k) -> int {
+      int n = 0;
 #pragma unroll 1
-    for (int b0 = (p.batch - 1) & ~31; b0 >= 0; b0 -= 32) {
-      // lane 0 holds the last sequence of the 32
-      const int b = b0 + 31 - lane;
-      int q0 = 0, len = 0;
-      if (b < p.batch) packed_range(p.cu_q, b, p.tokens, q0, len);
-      const int own = p.by_block.quotient(len + block - 1);
-      int sum = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
+      for (int b0 = 0; b0 < p.batch; b0 += 32)
+        n += __reduce_add_sync(0xffffffffu, max(0, (b0 ? load_seq(p, b0 + lane) : mine).blocks - k));
+      return n;
+    };
+    int lo = 0, hi = p.most_blocks, after = 0;  // further(lo) > u >= further(hi) = after
+    if (further(0) <= u) return false;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2, n = further(mid);
+      if (n > u) {
+        lo = mid;
+      } else {
+        hi = mid;
+        after = n;
       }
-      const uint32_t here = __ballot_sync(0xffffffffu, sum > u);
-      if (here) {
-        const int l = __ffs(here) - 1;
-        seq = b0 + 31 - l;
-        first = __shfl_sync(0xffffffffu, q0, l);
-        qlen = __shfl_sync(0xffffffffu, len, l);
-        at = (__shfl_sync(0xffffffffu, sum, l) - 1 - u) * block;  // u counts from the sequence's end
-        found = true;
+    }
+    u -= after;  // among the sequences that have a block at that place
+    AttnSeq q = mine;
+#pragma unroll 1
+    for (int b0 = 0;; b0 += 32) {
+      if (b0) q = load_seq(p, b0 + lane);
+      const uint32_t has = __ballot_sync(0xffffffffu, q.blocks > lo);
+      if (u < __popc(has) || b0 + 32 >= p.batch) {
+        const bool it = ((has >> lane) & 1u) && __popc(has & ((1u << lane) - 1u)) == u;
+        const int l = max(__ffs(__ballot_sync(0xffffffffu, it)) - 1, 0);
+        q.q0 = __shfl_sync(0xffffffffu, q.q0, l);
+        q.qlen = __shfl_sync(0xffffffffu, q.qlen, l);
+        q.k0 = __shfl_sync(0xffffffffu, q.k0, l);
+        q.klen = __shfl_sync(0xffffffffu, q.klen, l);
         break;
       }
-      u -= __shfl_sync(0xffffffffu, sum, 31);
+      u -= __popc(has);
     }
-    if (!found) return false;
-    int k0, klen;
-    packed_range(p.cu_k, seq, p.key_rows, k0, klen);
+    const int at = lo * block;
     a.kind = 0;
-    a.tok0 = first + at;
-    a.ntok = min(block, qlen - at);
+    a.tok0 = q.q0 + at;
+    a.ntok = min(block, q.qlen - at);
     a.causal = p.causal;
-    a.vis0 = klen - qlen + at + 1;
-    a.klen = klen;
-    a.krow = k0;
+    a.vis0 = q.klen - q.qlen + at + 1;
+    a.klen = q.klen;
+    a.krow = q.k0;
   } else if (x < p.prefix_items) {
     // row blocks of the same keys next to each other: they share them in L2
     int u = p.by_row_blocks.split(x);
@@ -949,10 +971,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       grid_dependency_wait();
       const uint32_t next_slot = bar0 + 8u * kASlotNext;
       int x = static_cast<int>(blockIdx.x);
+      const AttnSeq mine = load_seq(p, lane);
       uint32_t it = 0, nnext = 0;
       while (true) {
         AttnItem a;
-        const bool some = decode_item(p, x, lane, a);
+        const bool some = decode_item(p, x, lane, mine, a);
         if (some) {
           const uint32_t islot = it % kAttnItems;
           if (!bw.wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u)) break;
@@ -1014,11 +1037,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 // Joins the parts of every row: with M = max over parts of c m_p,
 // o = sum_p 2^(c m_p - M) o_p / sum_p 2^(c m_p - M) l_p.
-// A block takes 32 rows and eight of their columns.  Each of its eight warps
-// reads every eighth part, four of them in flight (one thread walking all
-// parts of a row took 16 us for 17 parts: a memory latency for each), and the
-// warps' results are joined through shared memory.  The order is fixed, so
-// the result does not depend on timing.
+// A block takes 32 rows and eight of their columns for each group of
+// join_warps warps.  Each warp of a group reads every join_warps-th part, four
+// of them in flight (one thread walking all parts of a row took 16 us for 17
+// parts: a memory latency for each), and the group's results are joined
+// through shared memory.  The order is fixed, so the result does not depend
+// on timing.
 constexpr int kJoinWarps = 8;
 
 struct AttnPart {
@@ -1043,18 +1067,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long rows = static_cast<long long>(p.tokens) * (p.group * p.kv_heads);
-  const int col8 = static_cast<int>(blockIdx.y);
+  const int across = p.join_warps, first = warp & ~(across - 1);
+  const int col8 = static_cast<int>(blockIdx.y) * (kJoinWarps / across) + warp / across;
   const int row = static_cast<int>(blockIdx.x) * 32 + lane;
-  const bool valid = row < rows;
+  const bool valid = row < rows && col8 < p.dim / 8;
   AttnPart a = {-INFINITY, 0.0f, {0, 0, 0, 0, 0, 0, 0, 0}};
   if (valid) {
     constexpr int kBatch = 4;
-    for (int s0 = warp; s0 < p.parts; s0 += kBatch * kJoinWarps) {
+    for (int s0 = warp - first; s0 < p.parts; s0 += kBatch * across) {
       float2 ml[kBatch];
       float4 u[kBatch], v[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int s = s0 + b * kJoinWarps;
+        const int s = s0 + b * across;
         ml[b] = make_float2(0.0f, 0.0f);
         if (s < p.parts) {
           const float4* src =
@@ -1066,7 +1091,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        if (s0 + b * kJoinWarps >= p.parts) break;
+        if (s0 + b * across >= p.parts) break;
         const float po[8] = {u[b].x, u[b].y, u[b].z, u[b].w, v[b].x, v[b].y, v[b].z, v[b].w};
         a.add(ml[b].x, ml[b].y, po);
       }
@@ -1077,8 +1102,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
 #pragma unroll
   for (int k = 0; k < 8; ++k) joined[warp][k][lane] = a.o[k];
   __syncthreads();
-  if (warp != 0 || !valid) return;
-  for (int w = 1; w < kJoinWarps; ++w) {
+  if (warp != first || !valid) return;
+  for (int w = first + 1; w < first + across; ++w) {
     float po[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) po[k] = joined[w][k][lane];

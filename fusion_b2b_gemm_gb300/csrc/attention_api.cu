@@ -90,29 +90,54 @@ b2b_status_t encode_kv(CUtensorMap* map, const b2b_attn_plan_s* p, const b2b_att
   return encode(map, p, t.data, {p->kv_heads, rows, blocks}, {t.head_stride, t.row_stride, t.block_stride}, {1, box, 1});
 }
 
-// How many parts a range of `tiles` key tiles is cut into when `items` CTAs'
-// worth of work share the key range's length: the smallest modelled time, in
-// key tiles, of ceil(items * s / sms) rounds of (tiles / s + 2) plus joining.
-int split_count(int64_t items, int64_t tiles, int sms) {
-  int best = 1;
-  double best_t = 1e30;
-  for (int s = 1; s <= 64 && (s == 1 || tiles >= 3 * s); ++s) {
-    const double rounds = static_cast<double>((items * s + sms - 1) / sms);
-    const double t = rounds * (static_cast<double>((tiles + s - 1) / s) + 2.0) + (s > 1 ? 4.0 + 0.1 * s : 0.0);
-    if (t < best_t - 1e-9) {
-      best_t = t;
-      best = s;
-    }
-  }
-  return best;
+// ---------------------------------------------------------------- shapes
+// How work is cut into items is chosen by a model of the time, in units of a
+// key tile of a pair item (about 1.45 us for 128-wide heads): a tile of a solo
+// item takes 0.55, an item's beginning and end 1.2 more (traces of both).
+constexpr double kSoloTile = 0.55, kItemCost = 1.2;
+
+// Launch and latencies of joining parts, and their traffic (written and read
+// once, in fp32, at some 4 TB/s).
+double join_cost(const b2b_attn_plan_s* p, double tokens, int parts) {
+  return parts <= 1 ? 0.0 : 3.0 + parts * tokens * p->q_heads * p->dim * 8.0 / 5.8e6;
 }
 
-int prompt_splits(const b2b_attn_plan_s* p, int64_t batch, int64_t tokens, int64_t key_rows) {
-  if (tokens * p->q_heads > kMaxRows) return 1;  // (rows of parts are numbered in 31 bits)
-  const int64_t block = 2 * p->tile_tokens;
-  const int64_t blocks = std::max((tokens + block - 1) / block, std::min(batch, tokens));
-  const int64_t tiles = (key_rows / std::max<int64_t>(batch, 1) + kAttnTile - 1) / kAttnTile;
-  return split_count(blocks * p->kv_heads, tiles, p->sms);
+struct PromptShape {
+  int tiles;   // query tiles of an item: 2 (pair) or 1 (solo)
+  int splits;  // parts of the key range
+  int64_t blocks;  // at most so many blocks of queries
+};
+// Few rows over many keys are cut along the keys, and blocks that would fill
+// the GPU's SMs a little more than a whole number of times are halved (six
+// pieces of 200-256 tokens over 1000-6000 keys: 164 items of two tiles took
+// 77 us, 320 of one tile XX us).
+PromptShape prompt_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t tokens, int64_t key_rows, bool causal) {
+  PromptShape best = {2, 1, 0};
+  double best_t = 1e300;
+  const double b = static_cast<double>(std::max<int64_t>(1, std::min(batch, tokens)));
+  const double most = static_cast<double>(key_rows) / b / kAttnTile;  // key tiles of a sequence
+  const double seen = std::max(causal ? most - 0.5 * tokens / b / kAttnTile : most, 0.0);
+  for (int tiles = 1; tiles <= 2; ++tiles) {
+    const int64_t block = tiles * p->tile_tokens;
+    const double tile = tiles == 2 ? 1.0 : kSoloTile;
+    // (a sequence's last block is half empty on average)
+    const double blocks = batch == 1 ? static_cast<double>((tokens + block - 1) / block) : static_cast<double>(tokens) / block + 0.5 * b;
+    for (int s = 1; s <= 64 && (s == 1 || most >= 4.0 * s); ++s) {
+      // (rows of parts are numbered in 31 bits)
+      if (s > 1 && tokens * p->q_heads > kMaxRows) break;
+      const double items = std::max(blocks, b) * p->kv_heads * s, rounds = items / p->sms;
+      const double item = std::ceil(seen / s + 0.5) * tile + kItemCost, longest = (most / s + 0.5) * tile + kItemCost;
+      const double t = std::max((rounds < 4.0 ? std::ceil(rounds) : rounds + 0.5) * item, longest) +
+                       join_cost(p, static_cast<double>(tokens), s);
+      if (t < best_t * 0.999) {
+        best_t = t;
+        best = {tiles, s, 0};
+      }
+    }
+  }
+  const int64_t block = best.tiles * p->tile_tokens;
+  best.blocks = batch == 1 ? (tokens + block - 1) / block : tokens / block + std::min(batch, tokens);
+  return best;
 }
 
 struct SharedShape {
@@ -125,9 +150,30 @@ SharedShape shared_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t fresh,
   s.block_tokens = tokens <= p->tile_tokens ? p->tile_tokens : block;
   s.row_blocks = (tokens + s.block_tokens - 1) / s.block_tokens;
   s.own_blocks = (fresh + block - 1) / block;
-  const int64_t tiles = (prefix + kAttnTile - 1) / kAttnTile, own_tiles = (room + kAttnTile - 1) / kAttnTile;
-  s.splits = prefix ? split_count(s.row_blocks * p->kv_heads, tiles, p->sms) : 0;
-  s.own_splits = room ? split_count(batch * s.own_blocks * p->kv_heads, own_tiles, p->sms) : 1;
+  // lengths are known to the device only: half the room on average
+  const double pre_tiles = static_cast<double>((prefix + kAttnTile - 1) / kAttnTile);
+  const double own_tiles = std::ceil(0.5 * static_cast<double>(room) / kAttnTile);
+  const double pre_tile = s.block_tokens == block ? 1.0 : kSoloTile, own_tile = fresh > p->tile_tokens ? 1.0 : kSoloTile;
+  const double pre = static_cast<double>(s.row_blocks * p->kv_heads), own = static_cast<double>(batch * s.own_blocks * p->kv_heads);
+  double best_t = 1e300;
+  s.splits = prefix ? 1 : 0;
+  s.own_splits = 1;
+  for (int so = 1; so <= 64 && (so == 1 || (own * so <= 2.0 * p->sms && own_tiles >= 2.0 * so)); ++so) {
+    for (int sp = prefix ? 1 : 0; sp <= 64 && (sp <= 1 || pre_tiles >= 2.0 * sp); ++sp) {
+      const double pre_item = sp ? std::ceil(pre_tiles / sp) * pre_tile + kItemCost : 0.0;
+      const double own_item = std::ceil(own_tiles / so) * own_tile + kItemCost;
+      // prefix items are begun first, own ones fill the gaps they leave
+      const double total = (pre * sp * pre_item + own * so * own_item) / p->sms;
+      const double t = std::max(total, std::max(pre_item, own_item)) + (pre * sp + own * so > p->sms ? 0.5 * own_item : 0.0) +
+                       join_cost(p, static_cast<double>(tokens), sp + so);
+      if (t < best_t * 0.999) {
+        best_t = t;
+        s.splits = sp;
+        s.own_splits = so;
+      }
+      if (!prefix) break;
+    }
+  }
   s.prefix_items = s.splits * s.row_blocks * p->kv_heads;
   s.own_items = s.own_splits * batch * s.own_blocks * p->kv_heads;
   return s;
@@ -172,6 +218,8 @@ AttnParams common_params(const b2b_attn_plan_s* p, int64_t tokens, int64_t batch
   a.wide_stores = p->dim % 16 == 0 && reinterpret_cast<uintptr_t>(out.data) % 32 == 0 && out.row_stride % 16 == 0 &&
                   out.head_stride % 16 == 0;
   a.parts = parts;
+  a.join_warps = 1;
+  while (a.join_warps < kJoinWarps && a.join_warps < parts) a.join_warps *= 2;
   if (parts > 1) {
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(parts) * tokens * p->q_heads * p->dim);
@@ -189,8 +237,9 @@ b2b_status_t launch(const b2b_attn_plan_s* p, CUtensorMap (&maps)[6], AttnParams
                              p->k.smem[p->dp], stream);
   if (e == cudaSuccess && a.parts > 1) {
     const int64_t rows = static_cast<int64_t>(a.tokens) * p->q_heads;
+    const int columns = kJoinWarps / a.join_warps;
     void* cargs[] = {&a};
-    e = launch_pdl(p->k.combine, dim3(static_cast<unsigned>((rows + 31) / 32), static_cast<unsigned>(p->dim / 8)),
+    e = launch_pdl(p->k.combine, dim3(static_cast<unsigned>((rows + 31) / 32), static_cast<unsigned>((p->dim / 8 + columns - 1) / columns)),
                    dim3(32 * kJoinWarps), cargs, 0, stream);
   }
   if (e != cudaSuccess) {
@@ -282,10 +331,12 @@ b2b_status_t b2b_attn_plan_set_debug(b2b_attn_plan_t p, uint32_t flags) {
 }
 
 b2b_status_t b2b_prompt_attention_workspace(b2b_attn_plan_t p, int64_t batch, int64_t tokens, int64_t key_rows,
-                                            size_t* bytes) {
+                                            int64_t causal, size_t* bytes) {
   if (!p || !bytes || batch < 0 || tokens < 0 || key_rows < 0) return B2B_ERR_INVALID_ARG;
   if (tokens > kMaxRows || key_rows > kMaxRows || batch > kMaxRows) return B2B_ERR_UNSUPPORTED;
-  *bytes = part_bytes(p, tokens, prompt_splits(p, batch, tokens, key_rows));
+  *bytes = 0;
+  if (batch == 0 || tokens == 0) return B2B_OK;
+  *bytes = part_bytes(p, tokens, prompt_shape(p, batch, tokens, key_rows, causal != 0).splits);
   return B2B_OK;
 }
 
@@ -305,13 +356,12 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attent
       overlaps(r->out.data, on, r->k.data, span_bytes(r->k, r->key_rows, hk, 1, d)) ||
       overlaps(r->out.data, on, r->v.data, span_bytes(r->v, r->key_rows, hk, 1, d)))
     return B2B_ERR_ALIAS;
-  const int splits = prompt_splits(p, r->batch, r->tokens, r->key_rows);
+  const PromptShape shape = prompt_shape(p, r->batch, r->tokens, r->key_rows, r->causal != 0);
+  const int splits = shape.splits;
   const size_t need = part_bytes(p, r->tokens, splits);
   if (need && (!r->workspace || r->workspace_bytes < need)) return B2B_ERR_INVALID_ARG;
   if (need && reinterpret_cast<uintptr_t>(r->workspace) % 32) return B2B_ERR_ALIGNMENT;
-  const int64_t block = 2 * p->tile_tokens;
-  const int64_t blocks = r->batch == 1 ? (r->tokens + block - 1) / block : r->tokens / block + std::min(r->batch, r->tokens);
-  const int64_t items = blocks * hk * splits;
+  const int64_t items = shape.blocks * hk * splits;
   if (items > kMaxRows) return B2B_ERR_UNSUPPORTED;
   st = check_current_device(p);
   if (st != B2B_OK) return st;
@@ -323,6 +373,8 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attent
   a.cu_k = r->cu_k;
   a.key_rows = static_cast<int>(r->key_rows);
   a.by_splits = FastDiv::of(static_cast<uint32_t>(splits));
+  a.by_block = FastDiv::of(static_cast<uint32_t>(shape.tiles * p->tile_tokens));
+  a.most_blocks = static_cast<int>((r->tokens + a.by_block.d - 1) / a.by_block.d);
   a.box_rows = kAttnTile;
   CUtensorMap maps[6];
   st = encode_q(&maps[0], p, r->q, r->tokens, static_cast<uint32_t>(p->tile_tokens));

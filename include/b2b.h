@@ -406,7 +406,7 @@ typedef struct {
   size_t workspace_bytes;
 } b2b_prompt_attention_t;
 b2b_status_t b2b_prompt_attention_workspace(b2b_attn_plan_t plan, int64_t batch, int64_t tokens, int64_t key_rows,
-                                            size_t* bytes);
+                                            int64_t causal, size_t* bytes);
 b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t plan, const b2b_prompt_attention_t* run, b2b_stream_t stream);
 
 /*

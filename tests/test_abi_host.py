@@ -320,7 +320,7 @@ def test_attn_calls_refuse_null_plans():
     assert b2b.b2b_attn_plan_device_status(None, None) == 1
     assert b2b.b2b_attn_plan_set_wait_budget(None, 0) == 1
     assert b2b.b2b_attn_plan_set_debug(None, 0) == 1
-    assert b2b.b2b_prompt_attention_workspace(None, 1, 1, 1, ctypes.byref(n)) == 1
+    assert b2b.b2b_prompt_attention_workspace(None, 1, 1, 1, 1, ctypes.byref(n)) == 1
     assert b2b.b2b_shared_attention_workspace(None, 1, 1, 1, 1, ctypes.byref(n)) == 1
     assert b2b.b2b_prompt_attention_run(None, None, None) == 1
     assert b2b.b2b_shared_attention_run(None, None, None) == 1
