@@ -133,7 +133,7 @@ struct AttnParams {
   const int* cu_q;
   const int* cu_k;
   int key_rows;
-  int most_blocks;     // no sequence has more blocks
+  int most_tiles;      // no sequence has more key tiles
   // shared prefix
   int fresh;           // new tokens per request
   int prefix;          // keys of the prefix
@@ -300,47 +300,62 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
     x = u;
     u = p.by_kv_heads.split(x);
     a.head = x;
-    // Blocks in the order of their place in their sequences, the furthest
-    // first: under a causal mask they see the most keys, and the longest items
-    // are best begun first.  The blocks at place k or further of all
-    // sequences number sum max(0, blocks - k); the item's place is the
-    // largest k for which that exceeds u.
-    auto further = [&](int k) -> int {
-      int n = 0;
+    // Blocks in the order of the key tiles they see, the most first: the
+    // longest items are best begun first.  count(s, n) of a sequence's blocks
+    // see n tiles or more, its last ones under a causal mask, where block k sees
+    // klen - qlen + min((k + 1) block, qlen) keys.  The item's n is the largest
+    // for which the sequences' counts together exceed u.
+    auto count = [&](const AttnSeq& s, int n) -> int {
+      const int keys = (n - 1) * kAttnTile + 1;  // n tiles from so many keys on
+      if (n == 0) return s.blocks;
+      if (s.klen < keys) return 0;
+      if (!p.causal) return s.blocks;
+      const int rows = max(keys - (s.klen - s.qlen), 0);  // rows of the sequence before its blocks see that many
+      return s.blocks - max(p.by_block.quotient(rows + block - 1) - 1, 0);
+    };
+    auto counts = [&](int n) -> int {
+      int sum = 0;
 #pragma unroll 1
       for (int b0 = 0; b0 < p.batch; b0 += 32)
-        n += __reduce_add_sync(0xffffffffu, max(0, (b0 ? load_seq(p, b0 + lane) : mine).blocks - k));
-      return n;
+        sum += __reduce_add_sync(0xffffffffu, count(b0 ? load_seq(p, b0 + lane) : mine, n));
+      return sum;
     };
-    int lo = 0, hi = p.most_blocks, after = 0;  // further(lo) > u >= further(hi) = after
-    if (further(0) <= u) return false;
+    if (counts(0) <= u) return false;
+    int lo = 0, hi = p.most_tiles + 1, more = 0;  // counts(lo) > u >= counts(hi) = more
     while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2, n = further(mid);
+      const int mid = (lo + hi) / 2, n = counts(mid);
       if (n > u) {
         lo = mid;
       } else {
         hi = mid;
-        after = n;
+        more = n;
       }
     }
-    u -= after;  // among the sequences that have a block at that place
+    u -= more;  // among the blocks that see just that many
     AttnSeq q = mine;
+    int at = 0;
 #pragma unroll 1
-    for (int b0 = 0;; b0 += 32) {
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
       if (b0) q = load_seq(p, b0 + lane);
-      const uint32_t has = __ballot_sync(0xffffffffu, q.blocks > lo);
-      if (u < __popc(has) || b0 + 32 >= p.batch) {
-        const bool it = ((has >> lane) & 1u) && __popc(has & ((1u << lane) - 1u)) == u;
-        const int l = max(__ffs(__ballot_sync(0xffffffffu, it)) - 1, 0);
+      const int from = count(q, lo), here = from - count(q, lo + 1);
+      int sum = here;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, sum > u);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        at = __shfl_sync(0xffffffffu, q.blocks - from + u - (sum - here), l) * block;
         q.q0 = __shfl_sync(0xffffffffu, q.q0, l);
         q.qlen = __shfl_sync(0xffffffffu, q.qlen, l);
         q.k0 = __shfl_sync(0xffffffffu, q.k0, l);
         q.klen = __shfl_sync(0xffffffffu, q.klen, l);
         break;
       }
-      u -= __popc(has);
+      u -= __shfl_sync(0xffffffffu, sum, 31);
     }
-    const int at = lo * block;
     a.kind = 0;
     a.tok0 = q.q0 + at;
     a.ntok = min(block, q.qlen - at);

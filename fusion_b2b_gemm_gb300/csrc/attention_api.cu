@@ -374,7 +374,7 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attent
   a.key_rows = static_cast<int>(r->key_rows);
   a.by_splits = FastDiv::of(static_cast<uint32_t>(splits));
   a.by_block = FastDiv::of(static_cast<uint32_t>(shape.tiles * p->tile_tokens));
-  a.most_blocks = static_cast<int>((r->tokens + a.by_block.d - 1) / a.by_block.d);
+  a.most_tiles = static_cast<int>((r->key_rows + kAttnTile - 1) / kAttnTile);
   a.box_rows = kAttnTile;
   CUtensorMap maps[6];
   st = encode_q(&maps[0], p, r->q, r->tokens, static_cast<uint32_t>(p->tile_tokens));
