@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // ones, bound by the softmax, lose by it (284 -> 297 us).
       const int common = DP < 128 || a.solo ? 0 : a.n0;
       const int vis = visible(a, tile0 + row_tok);
-      const int vis_min = visible(a, tile0);
+      const int vis_min = __shfl_sync(0xffffffffu, vis, 0);  // the warp's first row sees the fewest
       float m = -INFINITY;
       uint64_t l2 = 0;
       bool ok = true;
@@ -533,12 +533,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32u * c, s[c]);
         tmem_wait_ld();
         if ((j + 1) * kAttnTile > vis_min) {
-          const int lim = vis - j * kAttnTile;
+          const int lim = vis - j * kAttnTile, lim_min = vis_min - j * kAttnTile;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
+            if (c * 32 + 32 > lim_min) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c * 32 + k >= lim) s[c][k] = 0xff800000u;  // -inf
+              for (int k = 0; k < 32; ++k)
+                if (c * 32 + k >= lim) s[c][k] = 0xff800000u;  // -inf
+            }
         }
         float mx[4];
 #pragma unroll
