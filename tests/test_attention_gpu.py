@@ -521,3 +521,40 @@ def test_debug_flags_are_validated():
     with pytest.raises(b2b.B2BError) as e:
         plan.set_debug(2)
     assert e.value.code == INVALID
+
+
+# ------------------------------------------------------------------- together
+def test_the_example_runs_both_and_they_agree():
+    """Both paths round P and the output to bf16, differently where they cut the keys: each to 2^-8 of the output's
+    size at most, so together within 4 x 2^-8 in norm."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    try:
+        import shared_prompt
+    finally:
+        sys.path.pop(0)
+    assert shared_prompt.main(["--prompt", "333", "--answers", "5", "--tokens", "20"]) <= 4 * U["bf16"]
+
+
+def test_many_short_prompts_and_requests_at_once():
+    """More sequences than a warp has lanes, some empty; more requests than SMs."""
+    prompt_case("bf16", 2, 1, 128, [(5 * i) % 37 for i in range(70)], [(11 * i) % 53 for i in range(70)], seed=11)
+    shared_case("f16", 2, 1, 64, 70, [1 + (17 * i) % 140 for i in range(200)], page=32, seed=12)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_shapes(seed):
+    import random
+    r = random.Random(seed)
+    hq, hk = r.choice([(4, 4), (6, 2), (8, 1), (7, 1)])
+    dtype, dim = r.choice(["f16", "bf16"]), r.choice([40, 64, 80, 128])
+    if seed % 2:
+        nq = [r.choice([0, 1, r.randint(1, 300)]) for _ in range(r.randint(1, 9))]
+        nk = [max(0, n + r.randint(-3, 400)) for n in nq]
+        prompt_case(dtype, hq, hk, dim, nq, nk, causal=r.random() < 0.7, seed=seed)
+    else:
+        fresh = r.choice([1, 1, 2, 7])
+        lengths = [r.randint(0, 400) for _ in range(r.randint(1, 20))]
+        shared_case(dtype, hq, hk, dim, r.choice([0, 1, 130, 900]), lengths, fresh=fresh, page=r.choice([0, 16, 64]),
+                    seed=seed, fill=math.nan)
