@@ -138,6 +138,7 @@ struct AttnParams {
   int fresh;           // new tokens per request
   int prefix;          // keys of the prefix
   int prefix_items, block_tokens;
+  int whole;           // an item of own keys begins with the prefix's: one part, nothing to join
   const int* lengths;
   const int* table;    // pages of the requests' own keys, or null (dense)
   int table_width, page_shift, room;
@@ -171,10 +172,10 @@ struct AttnItem {
   int causal;     // token i sees clamp(vis0 + i, 0, klen) keys, else klen
   int krow;       // first row of the sequence's keys, or the request
   int j0, n, n0;  // first key tile, tiles of stream 1 (solo: of both), tiles of stream 0
-  int last;       // keys from the item's first tile on that any row sees
+  int last;       // keys from the first of these tiles (past the prefix's) on that any row sees
   int fix;        // rows of the last tile that hold keys (0: all of them)
   int part;
-  int pad;
+  int pre;        // tiles of the prefix in front of the request's own (items of whole requests)
 };
 static_assert(sizeof(AttnItem) == 64, "descriptor slot");
 
@@ -394,17 +395,20 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
     a.krow = b;
   }
   a.solo = a.ntok <= p.tile_tokens;
+  a.pre = a.kind == 2 && p.whole ? (p.prefix + kAttnTile - 1) / kAttnTile : 0;
   const int seen = visible(a, a.ntok - 1);
   const int all = (seen + kAttnTile - 1) / kAttnTile;
   const int chunk = by_splits->quotient(all + static_cast<int>(by_splits->d) - 1);
   a.j0 = a.part * chunk;
-  a.n = clampi(all - a.j0, 0, chunk);
+  const int n = clampi(all - a.j0, 0, chunk);
   const int all0 = (visible(a, min(a.ntok, p.tile_tokens) - 1) + kAttnTile - 1) / kAttnTile;
-  a.n0 = a.solo ? (a.n + 1) / 2 : clampi(all0 - a.j0, 0, a.n);
-  a.last = min(seen - a.j0 * kAttnTile, a.n * kAttnTile);
-  a.fix = a.n > 0 ? a.last % kAttnTile : 0;
+  a.n = a.pre + n;
+  a.n0 = a.solo ? (a.n + 1) / 2 : a.pre + clampi(all0 - a.j0, 0, n);
+  a.last = min(seen - a.j0 * kAttnTile, n * kAttnTile);
+  // (a prefix's last tile needs no zeroing: its tensor ends there, and TMA
+  // fills what lies past it with zeros)
+  a.fix = n > 0 && a.kind != 1 ? a.last % kAttnTile : 0;
   if (a.kind == 2 && p.prefix_items) a.part += static_cast<int>(p.by_splits.d);
-  a.pad = 0;
   return true;
 }
 
@@ -521,7 +525,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       uint64_t l2 = 0;
       bool ok = true;
       for (int i = 0; i < cnt; ++i) {
-        const int j = a.j0 + (a.solo ? 2 * i + t : i);
+        const int j = a.solo ? 2 * i + t : i;
+        const int key = (j < a.pre ? j : a.j0 + j - a.pre) * kAttnTile;  // the tile's first
         if (!bw.wait(bar(kABSFull + t), nscore & 1u)) {
           ok = false;
           break;
@@ -532,8 +537,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32u * c, s[c]);
         tmem_wait_ld();
-        if ((j + 1) * kAttnTile > vis_min) {
-          const int lim = vis - j * kAttnTile, lim_min = vis_min - j * kAttnTile;
+        const int lim_min = (j < a.pre ? p.prefix : vis_min) - key;
+        if (lim_min < kAttnTile) {
+          const int lim = (j < a.pre ? p.prefix : vis) - key;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             if (c * 32 + 32 > lim_min) {
@@ -919,11 +925,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (a.kind < 0) break;
         const int n = a.n, head = a.head, last = a.last, krow = a.krow;
         const bool own = a.kind == 2;
-        const bool paged = own && p.table != nullptr;
-        const int box = own ? p.own_box_rows : p.box_rows;
-        const CUtensorMap* km = own ? &tm_k_own : &tm_k;
-        const CUtensorMap* vm = own ? &tm_v_own : &tm_v;
-        const int key0 = a.j0 * kAttnTile + box_at * box;
+        const bool paged = p.table != nullptr;
+        const int pre = a.pre, j0 = a.j0;
         RingWalk w(n);
         for (int pos = 0; pos < 2 * n; ++pos) {
           if (pos == 1) {  // the query tiles, behind the first key tile
@@ -947,13 +950,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const bool is_k = w.next();
           const uint32_t g = ring + static_cast<uint32_t>(pos), slot = g % kRing;
           if (!(ok = bw.wait(bar(kABEmpty + static_cast<int>(slot)), ((g / kRing) & 1u) ^ 1u))) break;
-          const int rows = min(kAttnTile, last - w.j * kAttnTile);  // keys of this tile that are seen
-          const int key = key0 + w.j * kAttnTile;
+          const bool from_own = own && w.j >= pre;  // a tile of the requests' own tensors
+          const int box = from_own ? p.own_box_rows : p.box_rows;
+          // keys of this tile that are seen, and this lane's first
+          const int rows = min(kAttnTile, w.j < pre ? p.prefix - w.j * kAttnTile : last - (w.j - pre) * kAttnTile);
+          const int key = (w.j < pre ? w.j : j0 + w.j - pre) * kAttnTile + box_at * box;
           const bool mine = box_at * box < rows;
           const uint32_t fb = bar(kABFull + static_cast<int>(slot));
           int r = key, b = krow;
-          if (!own) {
-            r = krow + key;
+          if (!from_own) {
+            r = own ? key : krow + key;
             b = 0;
           } else if (paged && mine) {
             b = __ldg(p.table + static_cast<long long>(krow) * p.table_width + (key >> p.page_shift));
@@ -967,7 +973,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (mine && !((p.debug & 1u) && g == 0))
             tma_load_4d(base + L::kOffRing + slot * L::kTileBytes + panel * kPanelBytes +
                             static_cast<uint32_t>(box_at * box) * 128u,
-                        is_k ? km : vm, fb, panel * 64, head, r, b);
+                        from_own ? (is_k ? &tm_k_own : &tm_v_own) : (is_k ? &tm_k : &tm_v), fb, panel * 64, head, r, b);
         }
         if (!ok) break;
         ring += 2u * static_cast<uint32_t>(n);

@@ -96,10 +96,11 @@ b2b_status_t encode_kv(CUtensorMap* map, const b2b_attn_plan_s* p, const b2b_att
 // item takes 0.55, an item's beginning and end 1.2 more (traces of both).
 constexpr double kSoloTile = 0.55, kItemCost = 1.2;
 
-// Launch and latencies of joining parts, and their traffic (written and read
-// once, in fp32, at some 4 TB/s).
+// Joining parts: a second launch (and, where the host sets the pace, its
+// share of the call) and memory latencies, some 8 us, and the parts' traffic,
+// written and read once in fp32 at some 4 TB/s.
 double join_cost(const b2b_attn_plan_s* p, double tokens, int parts) {
-  return parts <= 1 ? 0.0 : 3.0 + parts * tokens * p->q_heads * p->dim * 8.0 / 5.8e6;
+  return parts <= 1 ? 0.0 : 5.5 + parts * tokens * p->q_heads * p->dim * 8.0 / 5.8e6;
 }
 
 struct PromptShape {
@@ -143,6 +144,7 @@ PromptShape prompt_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t tokens
 struct SharedShape {
   int64_t row_blocks, block_tokens, own_blocks, prefix_items, own_items;
   int splits, own_splits;
+  bool whole;  // items of whole requests, prefix and own keys: nothing is shared, and nothing to join
 };
 SharedShape shared_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t fresh, int64_t prefix, int64_t room) {
   SharedShape s = {};
@@ -172,6 +174,18 @@ SharedShape shared_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t fresh,
         s.own_splits = so;
       }
       if (!prefix) break;
+    }
+  }
+  // Small batches on short prefixes: every request reads the prefix itself (from
+  // L2, at some 8 TB/s), which saves the join.
+  if (prefix) {
+    const double item = (pre_tiles + own_tiles) * own_tile + kItemCost, rounds = own / p->sms;
+    const double t = std::max((rounds < 4.0 ? std::ceil(rounds) : rounds + 0.5) * item,
+                              own * static_cast<double>(prefix) * p->dim * 4.0 / 11.6e6);
+    s.whole = t < best_t;
+    if (s.whole) {
+      s.splits = 0;
+      s.own_splits = 1;
     }
   }
   s.prefix_items = s.splits * s.row_blocks * p->kv_heads;
@@ -453,6 +467,7 @@ b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t p, const b2b_shared_attent
   a.prefix_items = static_cast<int>(s.prefix_items);
   a.by_row_blocks = FastDiv::of(static_cast<uint32_t>(s.row_blocks));
   a.block_tokens = static_cast<int>(s.block_tokens);
+  a.whole = s.whole;
   a.by_own_splits = FastDiv::of(static_cast<uint32_t>(s.own_splits));
   a.by_own_blocks = FastDiv::of(static_cast<uint32_t>(s.own_blocks));
   a.lengths = r->lengths;
@@ -467,9 +482,11 @@ b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t p, const b2b_shared_attent
   const uint32_t own_tokens = static_cast<uint32_t>(std::min<int64_t>(r->fresh, p->tile_tokens));
   a.own_q_bytes = static_cast<uint32_t>(p->group) * own_tokens * 128u * (p->dp ? 2u : 1u);
   CUtensorMap maps[6];
-  st = encode_q(&maps[0], p, r->q, tokens, static_cast<uint32_t>(p->tile_tokens));
-  if (st == B2B_OK) st = encode_q(&maps[1], p, r->q, tokens, own_tokens);
-  maps[2] = maps[3] = maps[4] = maps[5] = maps[0];
+  // (maps that no item uses are copies)
+  st = encode_q(&maps[1], p, r->q, tokens, own_tokens);
+  maps[0] = maps[2] = maps[3] = maps[4] = maps[5] = maps[1];
+  if (st == B2B_OK && s.prefix_items && own_tokens != static_cast<uint32_t>(p->tile_tokens))
+    st = encode_q(&maps[0], p, r->q, tokens, static_cast<uint32_t>(p->tile_tokens));
   if (st == B2B_OK && r->prefix) st = encode_kv(&maps[2], p, r->prefix_k, r->prefix, 1, kAttnTile);
   if (st == B2B_OK && r->prefix) st = encode_kv(&maps[3], p, r->prefix_v, r->prefix, 1, kAttnTile);
   if (room) {
