@@ -521,6 +521,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int common = DP < 128 || a.solo ? 0 : a.n0;
       const int vis = visible(a, tile0 + row_tok);
       const int vis_min = __shfl_sync(0xffffffffu, vis, 0);  // the warp's first row sees the fewest
+      // Rows that hold no query of the item (other queries, or what lay there
+      // before) have no say in when the warp's rows are rescaled.
+      const bool query = row_tok < p.tile_tokens && tile0 + row_tok < a.ntok;
       float m = -INFINITY;
       uint64_t l2 = 0;
       bool ok = true;
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (i == 0) {
           m = tile_max;
-        } else if (__any_sync(0xffffffffu, (tile_max - m) * sl2 > kAttnRescale)) {
+        } else if (__any_sync(0xffffffffu, query && (tile_max - m) * sl2 > kAttnRescale)) {
           // S complete implies the MMAs before it: O holds every earlier tile
           // and nothing writes it until this tile's P is handed over.
           const float m_new = fmaxf(m, tile_max);

@@ -261,6 +261,26 @@ def test_equal_inputs_give_equal_bits():
         assert torch.equal(first, plan.run(q, k, v, ints([0, 100, 600])))
 
 
+@pytest.mark.parametrize("heads", [(7, 1), (3, 1), (28, 4)], ids=str)
+def test_equal_bits_whatever_ran_before(heads):
+    """Groups that leave rows of a tile without a query, and one-token requests: what an earlier launch left in shared
+    memory must not show, not even in the rounding."""
+    hq, hk = heads
+    q, k, v = normal(1, 300, hq, 128, scale=4.0), normal(2, 900, hk, 128), normal(3, 900, hk, 128)
+    prompt, shared = b2b.PromptAttentionPlan("f16", hq, hk, 128), b2b.SharedPrefixAttentionPlan("f16", hq, hk, 128)
+    cache = normal(4, 20, 400, hk, 128)
+    n = ints([1 + 19 * i for i in range(20)])
+    calls = [lambda: prompt.run(q, k, v, ints([0, 300]), ints([0, 900])),
+             lambda: shared.run(q[:20], k, v, cache, cache, n),
+             lambda: shared.run(q[:40], k[:70], v[:70], cache, cache, n)]
+    first = [f() for f in calls]
+    for i in range(30):
+        noise = normal(10 + i, 2000, hq, 128, scale=30.0)
+        prompt.run(noise, noise[:, :hk], noise[:, :hk], ints([0, 2000]))
+        j = i % 3
+        assert torch.equal(first[j], calls[j]())
+
+
 def test_side_streams_and_capture():
     """Runs on streams of their own, and a captured run that follows the offsets' contents."""
     q, k, v = normal(1, 300, 4, 64), normal(2, 300, 2, 64), normal(3, 300, 2, 64)
