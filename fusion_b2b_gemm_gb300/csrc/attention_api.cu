@@ -110,8 +110,9 @@ struct PromptShape {
 };
 // Few rows over many keys are cut along the keys, and blocks that would fill
 // the GPU's SMs a little more than a whole number of times are halved (six
-// pieces of 200-256 tokens over 1000-6000 keys: 164 items of two tiles took
-// 77 us, 320 of one tile XX us).
+// pieces of 200-256 tokens over 1000-6000 keys, 28/4 heads of 128: 172 items
+// of two tiles 76 us, 320 of one tile 65 us; 16 passages of 100-512 tokens, 12
+// heads of 96, the other way round, 22.0 against 22.9 us).
 PromptShape prompt_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t tokens, int64_t key_rows, bool causal) {
   PromptShape best = {2, 1, 0};
   double best_t = 1e300;
@@ -177,7 +178,8 @@ SharedShape shared_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t fresh,
     }
   }
   // Small batches on short prefixes: every request reads the prefix itself (from
-  // L2, at some 8 TB/s), which saves the join.
+  // L2, at some 8 TB/s), which saves the join (four requests, 133 shared keys:
+  // 23.4 us a call with two parts, 16.9 us whole).
   if (prefix) {
     const double item = (pre_tiles + own_tiles) * own_tile + kItemCost, rounds = own / p->sms;
     const double t = std::max((rounds < 4.0 ? std::ceil(rounds) : rounds + 0.5) * item,
