@@ -290,9 +290,17 @@ __device__ __forceinline__ AttnSeq load_seq(const AttnParams& p, int b) {
   return s;
 }
 
+// Where the last item of a prompt was found.  The blocks that see n key tiles
+// have the numbers first .. end - 1; `before` of these belong to the sequences
+// before seq0, a multiple of 32.
+struct AttnCursor {
+  int n = 0, first = 0, end = 0, seq0 = 0, before = 0;
+};
+
 // Fill `a` for item number x (whole warp; every lane gets the same).  False: no such item.
 // mine: the lane's sequence, load_seq(p, lane), of a prompt.
-__device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane, const AttnSeq& mine, AttnItem& a) {
+__device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane, const AttnSeq& mine, AttnCursor& c,
+                                            AttnItem& a) {
   const int block = static_cast<int>(p.by_block.d);
   const FastDiv* by_splits = &p.by_splits;
   if (p.op == kAttnPrompt) {
@@ -321,24 +329,37 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
         sum += __reduce_add_sync(0xffffffffu, count(b0 ? load_seq(p, b0 + lane) : mine, n));
       return sum;
     };
-    if (counts(0) <= u) return false;
-    int lo = 0, hi = p.most_tiles + 1, more = 0;  // counts(lo) > u >= counts(hi) = more
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2, n = counts(mid);
-      if (n > u) {
-        lo = mid;
-      } else {
-        hi = mid;
-        more = n;
+    // A search reads every sequence up to ten times, so a CTA's next item, whose
+    // number is mostly a little higher, is looked for from the last one on (200
+    // prompts of 20-200 tokens, 32/8 heads: 273 -> 126 us; 1000: 6,120 -> 660).
+    if (u < c.first || u >= c.end) {
+      int lo = 0, hi = p.most_tiles + 1, more = 0, all;  // counts(lo) = all > u >= counts(hi) = more
+      if (c.end > 0 && u >= c.end) {
+        hi = c.n;
+        more = c.end;
       }
+      if (hi == 0 || (all = counts(0)) <= u) return false;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2, n = counts(mid);
+        if (n > u) {
+          lo = mid;
+          all = n;
+        } else {
+          hi = mid;
+          more = n;
+        }
+      }
+      c = {lo, more, all, 0, 0};
+    } else if (u < c.first + c.before) {
+      c.seq0 = c.before = 0;
     }
-    u -= more;  // among the blocks that see just that many
+    u -= c.first + c.before;  // among the blocks that see just that many, of the sequences from seq0 on
     AttnSeq q = mine;
     int at = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      if (b0) q = load_seq(p, b0 + lane);
-      const int from = count(q, lo), here = from - count(q, lo + 1);
+    for (; c.seq0 < p.batch; c.seq0 += 32) {
+      if (c.seq0) q = load_seq(p, c.seq0 + lane);
+      const int from = count(q, c.n), here = from - count(q, c.n + 1);
       int sum = here;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -355,7 +376,9 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
         q.klen = __shfl_sync(0xffffffffu, q.klen, l);
         break;
       }
-      u -= __shfl_sync(0xffffffffu, sum, 31);
+      const int skipped = __shfl_sync(0xffffffffu, sum, 31);
+      u -= skipped;
+      c.before += skipped;
     }
     a.kind = 0;
     a.tok0 = q.q0 + at;
@@ -998,10 +1021,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint32_t next_slot = bar0 + 8u * kASlotNext;
       int x = static_cast<int>(blockIdx.x);
       const AttnSeq mine = load_seq(p, lane);
+      AttnCursor cursor;
       uint32_t it = 0, nnext = 0;
       while (true) {
         AttnItem a;
-        const bool some = decode_item(p, x, lane, mine, a);
+        const bool some = decode_item(p, x, lane, mine, cursor, a);
         if (some) {
           const uint32_t islot = it % kAttnItems;
           if (!bw.wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u)) break;

@@ -164,6 +164,14 @@ def test_many_sequences():
     prompt_case("f16", 2, 1, 64, [(7 * i) % 23 for i in range(100)], seed=5)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_sequences_of_short_and_long_keys(causal):
+    """Several items of every CTA, found from where the one before was, in sequences of one to twelve key tiles."""
+    lens = [(37 * i) % 90 + (700 if i % 61 == 0 else 0) for i in range(300)]
+    keys = [n + (800 if i % 53 == 0 else (11 * i) % 200) for i, n in enumerate(lens)]
+    prompt_case("bf16", 4, 2, 64, lens, keys, causal=causal, seed=6)
+
+
 @pytest.mark.parametrize("spread", [1e-3, 8.0, 40.0])
 def test_flat_and_peaked_scores(spread):
     """Scores far apart move the running maximum by far more than the rescaling threshold."""
