@@ -11,7 +11,7 @@
 // Online softmax (c = scale * log2 e): a row keeps a reference m and
 // l = sum_j 2^(c s_j - c m); O accumulates sum_j 2^(c s_j - c m) v_j in
 // tensor memory.  m is the first tile's maximum and is moved only when a
-// later maximum exceeds it by more than 8 in the exponent (kRescale), so P
+// later maximum exceeds it by more than 8 in the exponent (kAttnRescale), so P
 // stays below 2^8 (exact powers apart, the relative rounding of P and the
 // fp32 sums do not depend on m) and O is rarely rescaled.  A masked score
 // counts as -inf whatever it holds; a row that has seen no key keeps
@@ -36,7 +36,7 @@
 // control, so a CTA that finishes early takes the next unstarted item):
 //   warps 0-3, 4-7  softmax of stream 0 and 1 (a row per thread)
 //   warps 8, 9      MMA issue of stream 0 and 1
-//   warp 10         TMA loads
+//   warp 10         TMA loads of keys, values and queries
 //   warp 11         items: asks for them and decodes them ahead of the loads
 //   warps 12-15     epilogue of both streams, beside the next item's softmax
 // Every wait is bounded, as in the chain kernels.
@@ -88,7 +88,7 @@ enum : int {  // barrier slots (8 bytes each)
   kABTail = 51,       // [3] last value tile landed (one arrival per item)
   kABItemFull = 28,   // [3] descriptor written
   kABItemEmpty = 31,  // [3] descriptor no longer read
-  kABFixed = 34,      // [3] last value tile's tail zeroed
+  kABFixed = 34,      // [3] last value tile's rows past its last key zeroed
   kABNext = 37,       // next item handed out
   kABDrain = 38,      // [2]
   kASlotNext = 42,    // 16 bytes: cluster launch control's answer
@@ -292,9 +292,9 @@ __device__ __forceinline__ AttnSeq load_seq(const AttnParams& p, int b) {
 
 // Where the last item of a prompt was found.  The blocks that see n key tiles
 // have the numbers first .. end - 1; `before` of these belong to the sequences
-// before seq0, a multiple of 32.
+// before seq0, a multiple of 32; `all` counts every block (-1: not known yet).
 struct AttnCursor {
-  int n = 0, first = 0, end = 0, seq0 = 0, before = 0;
+  int n = 0, first = 0, end = 0, seq0 = 0, before = 0, all = -1;
 };
 
 // Fill `a` for item number x (whole warp; every lane gets the same).  False: no such item.
@@ -325,20 +325,33 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
     auto counts = [&](int n) -> int {
       int sum = 0;
 #pragma unroll 1
-      for (int b0 = 0; b0 < p.batch; b0 += 32)
-        sum += __reduce_add_sync(0xffffffffu, count(b0 ? load_seq(p, b0 + lane) : mine, n));
-      return sum;
+      for (int b0 = 0; b0 < p.batch; b0 += 32) sum += count(b0 ? load_seq(p, b0 + lane) : mine, n);
+      return __reduce_add_sync(0xffffffffu, sum);
     };
-    // A search reads every sequence up to ten times, so a CTA's next item, whose
+    // A search reads every sequence once a step, so a CTA's next item, whose
     // number is mostly a little higher, is looked for from the last one on (200
-    // prompts of 20-200 tokens, 32/8 heads: 273 -> 126 us; 1000: 6,120 -> 660).
+    // prompts of 20-200 tokens, 32/8 heads: 273 -> 126 us; 1000: 6,120 -> 660 us).
     if (u < c.first || u >= c.end) {
-      int lo = 0, hi = p.most_tiles + 1, more = 0, all;  // counts(lo) = all > u >= counts(hi) = more
-      if (c.end > 0 && u >= c.end) {
-        hi = c.n;
-        more = c.end;
+      if (c.all < 0) {
+        // No block sees more tiles than the longest sequence has, which spares
+        // steps of the first search, the one the kernel's start waits for (24
+        // prompts of 1-700 tokens 55.6 -> 55.1 us, 1000 of 20-200 660 -> 535 us).
+        int sum = 0, keys = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+          const AttnSeq s = b0 ? load_seq(p, b0 + lane) : mine;
+          sum += s.blocks;
+          keys = max(keys, s.klen);
+        }
+        c.all = __reduce_add_sync(0xffffffffu, sum);
+        c.n = (__reduce_max_sync(0xffffffffu, keys) + kAttnTile - 1) / kAttnTile + 1;
       }
-      if (hi == 0 || (all = counts(0)) <= u) return false;
+      if (u >= c.all) return false;
+      int lo = 0, hi = c.n, more = c.end, all = c.all;  // counts(lo) = all > u >= counts(hi) = more
+      if (u < c.first) {
+        hi = p.most_tiles + 1;
+        more = 0;
+      }
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2, n = counts(mid);
         if (n > u) {
@@ -349,7 +362,7 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
           more = n;
         }
       }
-      c = {lo, more, all, 0, 0};
+      c = {lo, more, all, 0, 0, c.all};
     } else if (u < c.first + c.before) {
       c.seq0 = c.before = 0;
     }

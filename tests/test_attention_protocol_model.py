@@ -267,43 +267,89 @@ def test_the_model_notices_planted_mistakes(planted):
 
 
 # ------------------------------------------------------------ order of items --
-def enumerate_items(seqs, block, causal, tile=128):
-    """The kernel's search for item number u (decode_item), for every u."""
-    def blocks(q):
-        return -(-q // block)
+class Search:
+    """The kernel's search for an item number (decode_item), with the cursor that a CTA keeps."""
 
-    def count(s, n):
+    def __init__(self, seqs, block, causal, tile=128):
+        self.seqs, self.block, self.causal, self.tile = seqs, block, causal, tile
+        self.most = -(-sum(k for _, k in seqs) // tile)
+        self.reset()
+
+    def reset(self):
+        self.n = self.first = self.end = self.seq0 = self.before = 0
+        self.all = -1
+
+    def blocks(self, q):
+        return -(-q // self.block)
+
+    def count(self, s, n):
         q, k = s
-        keys = (n - 1) * tile + 1
+        keys = (n - 1) * self.tile + 1
         if n == 0:
-            return blocks(q)
+            return self.blocks(q)
         if k < keys:
             return 0
-        if not causal:
-            return blocks(q)
-        return blocks(q) - max(-(-max(keys - (k - q), 0) // block) - 1, 0)
+        if not self.causal:
+            return self.blocks(q)
+        return self.blocks(q) - max(self.blocks(max(keys - (k - q), 0)) - 1, 0)
 
-    def counts(n):
-        return sum(count(s, n) for s in seqs)
+    def counts(self, n):
+        return sum(self.count(s, n) for s in self.seqs)
 
-    out, most = [], -(-sum(k for _, k in seqs) // tile)
-    for u in range(counts(0)):
-        lo, hi, more = 0, most + 1, 0
-        while hi - lo > 1:
-            mid = (lo + hi) // 2
-            n = counts(mid)
-            if n > u:
-                lo = mid
-            else:
-                hi, more = mid, n
-        u -= more
-        for b, s in enumerate(seqs):
-            here = count(s, lo) - count(s, lo + 1)
-            if u < here:
-                out.append((b, blocks(s[0]) - count(s, lo) + u))
-                break
-            u -= here
+    def find(self, u):
+        """(sequence, block) of item u, or None."""
+        if u < self.first or u >= self.end:
+            if self.all < 0:
+                self.all = self.counts(0)
+                self.n = -(-max(k for _, k in self.seqs) // self.tile) + 1
+            if u >= self.all:
+                return None
+            lo, hi, more, whole = 0, self.n, self.end, self.all
+            if u < self.first:
+                hi, more = self.most + 1, 0
+            while hi - lo > 1:
+                mid = (lo + hi) // 2
+                n = self.counts(mid)
+                if n > u:
+                    lo, whole = mid, n
+                else:
+                    hi, more = mid, n
+            self.n, self.first, self.end, self.seq0, self.before = lo, more, whole, 0, 0
+        elif u < self.first + self.before:
+            self.seq0 = self.before = 0
+        u -= self.first + self.before
+        while self.seq0 < len(self.seqs):
+            for b, s in enumerate(self.seqs[self.seq0:self.seq0 + 32], self.seq0):
+                here = self.count(s, self.n) - self.count(s, self.n + 1)
+                if u < here:
+                    return b, self.blocks(s[0]) - self.count(s, self.n) + u
+                u -= here
+            self.before += sum(self.count(s, self.n) - self.count(s, self.n + 1) for s in self.seqs[self.seq0:self.seq0 + 32])
+            self.seq0 += 32
+        raise AssertionError("no sequence holds the item")
+
+
+def enumerate_items(seqs, block, causal):
+    """Every item, each searched for from the beginning."""
+    out, search = [], Search(seqs, block, causal)
+    while (item := search.find(len(out))) is not None:
+        out.append(item)
+        search.reset()
     return out
+
+
+def test_items_found_from_the_one_before():
+    """A CTA's numbers mostly rise, by any step; whatever they do, it finds what a fresh search finds."""
+    rng = random.Random(5)
+    for _ in range(200):
+        seqs = [(rng.choice((0, 1, rng.randint(0, 500))), rng.choice((0, 1, rng.randint(0, 900))))
+                for _ in range(rng.choice((1, 5, 31, 32, 33, 64, 100)))]
+        block, causal = rng.choice((18, 32, 64, 256)), rng.random() < 0.7
+        want = enumerate_items(seqs, block, causal)
+        search, u = Search(seqs, block, causal), rng.randint(0, 20)
+        for _ in range(60):
+            assert search.find(u) == (want[u] if u < len(want) else None)
+            u = max(0, u + rng.choice((0, 1, 1, 3, 19, 40, -1, -7, -len(want))))
 
 
 def test_every_block_is_an_item_and_the_longest_come_first():
