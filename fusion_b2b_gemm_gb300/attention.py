@@ -100,7 +100,7 @@ class _AttentionPlan:
     def _results(self, q, tokens, out, lse, return_lse):
         """Output and LSE of one run with the output's arguments and the LSE's address."""
         if out is None:
-            out = torch.empty((tokens, self.q_heads, self.head_dim), dtype=self._torch_dtype, device=q.device)
+            out = q.new_empty((tokens, self.q_heads, self.head_dim))
             args = out.data_ptr(), self.q_heads * self.head_dim, self.head_dim
         else:
             rows, *args = self._packed("out", out, self.q_heads)
