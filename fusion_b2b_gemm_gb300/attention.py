@@ -10,15 +10,21 @@ last one is 1.  Inference only.  There is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
 
 import torch
 
-from . import DTYPES, _check, _current_device, _lib, _stream_handle
+from . import DTYPES, _check, _current_device, _lib, _stream_handle, library_path
 
 __all__ = ["PromptAttentionPlan", "SharedPrefixAttentionPlan"]
 
 _TORCH = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+# (the public torch.cuda.current_stream() builds an object each time, 3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 # The argument structures, whose members all take eight bytes (b2b_attn_rows_t:
 # data, row_stride, head_stride, block_stride), as the C functions read them.
@@ -27,6 +33,25 @@ _prompt_run = struct.Struct("25q").pack
 # b2b_shared_attention_t: batch, fresh, prefix, cache_rows, cache_blocks, table_width; q, prefix_k, prefix_v,
 # cache_k, cache_v, out; lengths, page_table, lse, workspace, workspace_bytes
 _shared_run = struct.Struct("35q").pack
+
+
+
+
+def _load_binding():
+    """The module that passes tensors to the C functions (binding/attention.cpp)."""
+    path = os.path.join(os.path.dirname(library_path()), "attn_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it first (python fusion_b2b_gemm_gb300/_build.py)")
+    loader = importlib.machinery.ExtensionFileLoader("attn_binding", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("attn_binding", loader))
+    loader.exec_module(module)
+    module.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        _lib.b2b_prompt_attention_workspace, _lib.b2b_prompt_attention_run,
+        _lib.b2b_shared_attention_workspace, _lib.b2b_shared_attention_run)))
+    return module
+
+
+_binding = _load_binding()
 
 
 class _AttentionPlan:
@@ -50,6 +75,11 @@ class _AttentionPlan:
         self._torch_dtype = _TORCH[dtype]
         self.device_index = _current_device()
         self._workspace_sizes = {}
+        # What the binding's calls need to know of the plan.  They take the
+        # common call, with no tensors for the results and no stream, and return
+        # None where anything is not as they want it: the same in Python below
+        # finds out what.
+        self._bound = _binding.bind(h.value, dtype == "bf16", q_heads, kv_heads, head_dim, self.device_index)
 
     # -- checks ------------------------------------------------------------
     # The runs test a tensor's type, layout and device in one expression and
@@ -128,8 +158,7 @@ class _AttentionPlan:
         return (torch.empty(need, dtype=torch.uint8, device=q.device) if need else None), need
 
     def _stream(self):
-        # (the public torch.cuda.current_stream() builds an object each time, 3 us)
-        return torch._C._cuda_getCurrentRawStream(self.device_index) or None
+        return _raw_stream(self.device_index) or None
 
     # -- as the chain plans ------------------------------------------------
     def status(self, stream=None) -> int:
@@ -144,6 +173,7 @@ class _AttentionPlan:
         _check(_lib.b2b_attn_plan_set_debug(self._h, int(flags)), "b2b_attn_plan_set_debug")
 
     def close(self) -> None:
+        self._bound = None
         h = getattr(self, "_h", None)
         if h is not None and h.value:
             _lib.b2b_attn_plan_destroy(h)
@@ -172,6 +202,10 @@ class PromptAttentionPlan(_AttentionPlan):
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.run(q, k, v, cu_q, cu_k, causal, out, lse, return_lse)
+        if out is None and lse is None:
+            done = _binding.prompt(self._bound, _raw_stream(self.device_index), q, k, v, cu_q, cu_k, causal, return_lse)
+            if done is not None:
+                return done
         tokens, *qa = self._packed("q", q, self.q_heads)
         key_rows, *ka = self._packed("k", k, self.kv_heads)
         rows, *va = self._packed("v", v, self.kv_heads)
@@ -213,6 +247,11 @@ class SharedPrefixAttentionPlan(_AttentionPlan):
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.run(q, prefix_k, prefix_v, cache_k, cache_v, lengths, page_table, out, lse, return_lse)
+        if out is None and lse is None:
+            done = _binding.shared(self._bound, _raw_stream(self.device_index), q, prefix_k, prefix_v, cache_k, cache_v,
+                                   lengths, page_table, return_lse)
+            if done is not None:
+                return done
         tokens, *qa = self._packed("q", q, self.q_heads)
         prefix, *pka = self._packed("prefix_k", prefix_k, self.kv_heads)
         rows, *pva = self._packed("prefix_v", prefix_v, self.kv_heads)

@@ -468,6 +468,35 @@ def test_a_prompt_and_its_answers():
 
 
 # ------------------------------------------------------------ failure, refusals
+def test_results_given_or_made_are_the_same():
+    """Calls with tensors for the results are marshalled in Python, the others by the compiled module."""
+    q, k, v = (normal(i, 150, h, 72, dtype="bf16") for i, h in ((1, 6), (2, 2), (3, 2)))
+    cu = cumulative([40, 0, 110])
+    plan = b2b.PromptAttentionPlan("bf16", 6, 2, 72)
+    for causal in (True, False):
+        made = plan.run(q, k, v, cu, causal=causal, return_lse=True)
+        out, lse = torch.empty_like(q), torch.empty(150, 6, device="cuda")
+        given = plan.run(q, k, v, cu, cu, causal, out=out, lse=lse)
+        assert given[0] is out and given[1] is lse
+        assert torch.equal(made[0], out) and torch.equal(made[1], lse)
+        assert torch.equal(plan.run(q, k, v, cu, causal=causal), out)
+    shared = b2b.SharedPrefixAttentionPlan("bf16", 6, 2, 72)
+    pool = normal(4, 12, 16, 2, 72, dtype="bf16")
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4)
+    lengths = torch.tensor([3, 64, 20], dtype=torch.int32, device="cuda")
+    for prefix in (0, 150):
+        args = (q[:6], k[:prefix], v[:prefix], pool, pool, lengths, table)
+        made = shared.run(*args, return_lse=True)
+        out, lse = torch.empty_like(q[:6]), torch.empty(6, 6, device="cuda")
+        shared.run(*args, out=out, lse=lse)
+        assert torch.equal(made[0], out) and torch.equal(made[1], lse)
+        assert torch.equal(shared.run(*args), out)
+    assert plan.status() == 0 and shared.status() == 0
+    plan.close()
+    with pytest.raises(b2b.B2BError):
+        plan.run(q, k, v, cu)
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_timeout_is_reported_and_the_plan_recovers(dim):
     q, k, v = normal(1, 200, 4, dim), normal(2, 200, 2, dim), normal(3, 200, 2, dim)
