@@ -96,11 +96,12 @@ b2b_status_t encode_kv(CUtensorMap* map, const b2b_attn_plan_s* p, const b2b_att
 // item takes 0.55, an item's beginning and end 1.2 more (traces of both).
 constexpr double kSoloTile = 0.55, kItemCost = 1.2;
 
-// Joining parts: a second launch (and, where the host sets the pace, its
-// share of the call) and memory latencies, some 8 us, and the parts' traffic,
-// written and read once in fp32 at some 4 TB/s.
+// Joining parts: a second launch and memory latencies, some 4.5 us, and the
+// parts' traffic, written and read once in fp32 at some 4 TB/s.  (Nine requests
+// on 1,222 shared keys, which parts make quicker: 12.3 us a call counted as 8
+// us, 9.3 as 4.5; three of five tokens on 207, whole either way: 7.9, in parts 11.4.)
 double join_cost(const b2b_attn_plan_s* p, double tokens, int parts) {
-  return parts <= 1 ? 0.0 : 5.5 + parts * tokens * p->q_heads * p->dim * 8.0 / 5.8e6;
+  return parts <= 1 ? 0.0 : 3.0 + parts * tokens * p->q_heads * p->dim * 8.0 / 5.8e6;
 }
 
 struct PromptShape {
@@ -179,7 +180,7 @@ SharedShape shared_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t fresh,
   }
   // Small batches on short prefixes: every request reads the prefix itself (from
   // L2, at some 8 TB/s), which saves the join (four requests, 133 shared keys:
-  // 23.4 us a call with two parts, 16.9 us whole).
+  // 10.1 us a call with two parts, 7.0 us whole).
   if (prefix) {
     const double item = (pre_tiles + own_tiles) * own_tile + kItemCost, rounds = own / p->sms;
     const double t = std::max((rounds < 4.0 ? std::ceil(rounds) : rounds + 0.5) * item,
