@@ -271,6 +271,7 @@ class SharedPrefixAttentionPlan(_AttentionPlan):
                 raise ValueError(f"cache_k: {blocks} requests given, {batch} expected as lengths has")
         else:
             width, tablep = self._counts("page_table", page_table, batch, 2)
+            tablep = tablep or lengthsp  # (null means no table, and is the address of one without columns)
             room = width * rows if blocks else 0
         out, lse, oa, lsep = self._results(q, tokens, out, lse, return_lse)
         ws, need = self._workspace(q, (batch, fresh, prefix, room), _lib.b2b_shared_attention_workspace)

@@ -51,11 +51,13 @@ const at::Tensor* rows(const Bound& p, PyObject* o, int64_t dims, int64_t heads,
   return t;
 }
 
-const int32_t* counts(const Bound& p, PyObject* o, int64_t n, int64_t dims, int64_t& width) {
+// False: not a dense array of n counts (or n rows of any width).  The address of an array without entries is null.
+bool counts(const Bound& p, PyObject* o, int64_t n, int64_t dims, const int32_t*& data, int64_t& width) {
   const at::Tensor* t = tensor(p, o, c10::kInt, dims);
-  if (!t || (n >= 0 && t->size(0) != n) || !t->is_contiguous()) return nullptr;
+  if (!t || (n >= 0 && t->size(0) != n) || !t->is_contiguous()) return false;
   width = t->size(dims - 1);
-  return static_cast<const int32_t*>(t->data_ptr());
+  data = static_cast<const int32_t*>(t->data_ptr());
+  return true;
 }
 
 // The result's tensors, the workspace, and the launch.
@@ -100,9 +102,9 @@ PyObject* prompt(Bound& p, PyObject* const* arg) {
   const at::Tensor* k = rows(p, arg[3], 3, p.kv_heads, a.k);
   const at::Tensor* v = rows(p, arg[4], 3, p.kv_heads, a.v);
   int64_t offsets = 0, n = 0;
-  if (!q || !k || !v || k->size(0) != v->size(0) || !(a.cu_q = counts(p, arg[5], -1, 1, offsets)) || offsets < 1) return nullptr;
-  a.cu_k = arg[6] == Py_None ? a.cu_q : counts(p, arg[6], offsets, 1, n);
-  if (!a.cu_k) return nullptr;
+  if (!q || !k || !v || k->size(0) != v->size(0) || !counts(p, arg[5], -1, 1, a.cu_q, offsets) || offsets < 1) return nullptr;
+  a.cu_k = a.cu_q;
+  if (arg[6] != Py_None && !counts(p, arg[6], offsets, 1, a.cu_k, n)) return nullptr;
   a.batch = offsets - 1;
   a.tokens = q->size(0);
   a.key_rows = k->size(0);
@@ -121,7 +123,7 @@ PyObject* shared(Bound& p, PyObject* const* arg) {
   const at::Tensor* ck = rows(p, arg[5], 4, p.kv_heads, a.cache_k);
   const at::Tensor* cv = rows(p, arg[6], 4, p.kv_heads, a.cache_v);
   if (!q || !pk || !pv || !ck || !cv || pk->size(0) != pv->size(0) || ck->size(0) != cv->size(0) || ck->size(1) != cv->size(1) ||
-      !(a.lengths = counts(p, arg[7], -1, 1, a.batch)) || a.batch < 1 || q->size(0) % a.batch)
+      !counts(p, arg[7], -1, 1, a.lengths, a.batch) || a.batch < 1 || q->size(0) % a.batch)
     return nullptr;
   a.fresh = q->size(0) / a.batch;
   a.prefix = pk->size(0);
@@ -131,7 +133,8 @@ PyObject* shared(Bound& p, PyObject* const* arg) {
   if (arg[8] == Py_None) {
     if (a.cache_blocks != a.batch) return nullptr;
   } else {
-    if (!(a.page_table = counts(p, arg[8], a.batch, 2, a.table_width))) return nullptr;
+    if (!counts(p, arg[8], a.batch, 2, a.page_table, a.table_width)) return nullptr;
+    if (!a.page_table) a.page_table = a.lengths;  // (a table without columns, which is not read; null means none)
     room = a.cache_blocks ? a.table_width * a.cache_rows : 0;
   }
   return finish(p, *q, want_lse, a, {a.batch, a.fresh, a.prefix, room}, abi.shared_workspace, abi.shared_run, stream);

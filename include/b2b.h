@@ -421,6 +421,8 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t plan, const b2b_prompt_att
  *                with page_table, a pool of cache_blocks pages of cache_rows
  *                rows (a power of two from 16 up); own key j of request b is row
  *                j % cache_rows of page page_table[b * table_width + j / cache_rows].
+ *   page_table   NULL: dense.  A table of width 0 (no request has a page, so
+ *                none has a key of its own) is any other address.
  *   lengths      [batch] own keys of each request (device).  New token t of a
  *                request sees the prefix and own keys j < length - fresh + 1 + t.
  *   workspace    as above, sized by b2b_shared_attention_workspace; `room` is
