@@ -76,7 +76,8 @@ struct AttnShape {
   static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
   static constexpr int kOffItems = kOffBar + 512;
   static constexpr int kOffExchange = kOffItems + kAttnItems * 64;
-  static constexpr int kBytes = kOffExchange + 2 * kAttnTile * 8;
+  static constexpr int kOffClaimed = kOffExchange + 2 * kAttnTile * 8;  // an item claimed but handed to no role
+  static constexpr int kBytes = kOffClaimed + 64;
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -456,6 +457,20 @@ __device__ __forceinline__ bool decode_item(const AttnParams& p, int x, int lane
   return true;
 }
 
+// Marks the rows of parts that a CTA has claimed and may not have written (no
+// healthy part has l < 0), so that they are not joined: the workspace holds
+// whatever was there before, an earlier run's parts perhaps.  A call of its
+// own, which leaves the code of the roles' loops as it is.
+inline __device__ __noinline__ void give_up_parts(float2* part_ml, const AttnItem* items, const AttnItem* claimed,
+                                                  int kv_heads, int tokens, int group) {
+  for (int s = 0; s <= kAttnItems; ++s) {
+    const AttnItem& a = s < kAttnItems ? items[s] : *claimed;
+    if (a.kind < 0) continue;
+    float2* rows = part_ml + ((static_cast<long long>(a.part) * kv_heads + a.head) * tokens + a.tok0) * group;
+    for (int i = static_cast<int>(threadIdx.x); i < a.ntok * group; i += kAttnThreads) rows[i] = make_float2(0.0f, -1.0f);
+  }
+}
+
 // Key tiles of stream t.
 __device__ __forceinline__ int stream_tiles(const AttnItem& a, int t) {
   return t == 0 ? a.n0 : (a.solo ? a.n / 2 : a.n);
@@ -488,6 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * kASlotTmem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   AttnItem* items = reinterpret_cast<AttnItem*>(gbase + L::kOffItems);
+  AttnItem* claimed = reinterpret_cast<AttnItem*>(gbase + L::kOffClaimed);
   float2* exchange = reinterpret_cast<float2*>(gbase + L::kOffExchange);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -524,6 +540,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(bar(kABNext), 1);
       mbar_init(bar(kABAsk), 1);
       *abort_flag = 0;
+    } else if (lane < 14 + kAttnItems) {
+      items[lane - 14].kind = -1;
+    } else if (lane == 14 + kAttnItems) {
+      claimed->kind = -1;
     }
     if (lane < 14) fence_barrier_init();
   }
@@ -1049,7 +1069,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool some = decode_item(p, x, lane, mine, cursor, a);
         if (some) {
           const uint32_t islot = it % kAttnItems;
-          if (!bw.wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u)) break;
+          if (!bw.wait(bar(kABItemEmpty + islot), ((it / kAttnItems) & 1u) ^ 1u)) {
+            if (lane == 0) *claimed = a;
+            break;
+          }
           if (lane == 0) {
             items[islot] = a;
             mbar_arrive(bar(kABItemFull + islot));
@@ -1103,7 +1126,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
-  if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, 0, kTimeoutCode);
+  if (*abort_flag) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kTimeoutCode);
+    if (p.parts > 1) give_up_parts(p.part_ml, items, claimed, p.kv_heads, p.tokens, p.group);
+  }
 }
 
 // Joins the parts of every row: with M = max over parts of c m_p,
@@ -1113,7 +1139,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // of them in flight (one thread walking all parts of a row took 16 us for 17
 // parts: a memory latency for each), and the group's results are joined
 // through shared memory.  The order is fixed, so the result does not depend
-// on timing.
+// on timing.  A row with a part that was given up (l < 0) is not written.
 constexpr int kJoinWarps = 8;
 
 struct AttnPart {
@@ -1143,6 +1169,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
   const int row = static_cast<int>(blockIdx.x) * 32 + lane;
   const bool valid = row < rows && col8 < p.dim / 8;
   AttnPart a = {-INFINITY, 0.0f, {0, 0, 0, 0, 0, 0, 0, 0}};
+  bool lost = false;
   if (valid) {
     constexpr int kBatch = 4;
     for (int s0 = warp - first; s0 < p.parts; s0 += kBatch * across) {
@@ -1164,12 +1191,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
       for (int b = 0; b < kBatch; ++b) {
         if (s0 + b * across >= p.parts) break;
         const float po[8] = {u[b].x, u[b].y, u[b].z, u[b].w, v[b].x, v[b].y, v[b].z, v[b].w};
+        lost = lost || ml[b].y < 0.0f;
         a.add(ml[b].x, ml[b].y, po);
       }
     }
   }
   joined[warp][8][lane] = a.m;
-  joined[warp][9][lane] = a.l;
+  joined[warp][9][lane] = lost ? -1.0f : a.l;
 #pragma unroll
   for (int k = 0; k < 8; ++k) joined[warp][k][lane] = a.o[k];
   __syncthreads();
@@ -1178,8 +1206,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
     float po[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) po[k] = joined[w][k][lane];
+    lost = lost || joined[w][9][lane] < 0.0f;
     a.add(joined[w][8][lane], joined[w][9][lane], po);
   }
+  if (lost) return;
   int head = row, token;
   token = p.by_group.split(head);  // head: of the group
   head += p.by_tokens.split(token) * p.group;

@@ -2,11 +2,12 @@
 
 Inputs, results in 64 bits and their tolerances are those of test_attention_gpu.py.
 """
+import ctypes
 
 import pytest
 import torch
 
-from test_attention_gpu import Want, b2b, ints, normal
+from test_attention_gpu import TIMEOUT, Want, b2b, ints, normal, want_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -34,4 +35,60 @@ def test_a_page_table_without_columns_holds_no_keys(prefix, pages):
         want.check(*plan.run(q, k, v, pool, pool, lengths, table, return_lse=True))
         out, lse = torch.full_like(q, 7.0), torch.full((2, 4), 7.0, device="cuda")
         want.check(*plan.run(q, k, v, pool, pool, lengths, table, out=out, lse=lse))
+    assert plan.status() == 0
+
+
+# -------------------------------------------------------------------- timeouts
+def split_prompt():
+    """One query over many keys, which are cut into parts: plan, arguments of a run."""
+    q, k, v = normal(1, 1, 4, 64), normal(2, 5000, 2, 64), normal(3, 5000, 2, 64)
+    plan = b2b.PromptAttentionPlan("f16", 4, 2, 64)
+    n = ctypes.c_size_t()
+    assert b2b.b2b_prompt_attention_workspace(plan._h, 1, 1, 5000, 1, ctypes.byref(n)) == 0 and n.value > 0
+    want = want_prompt(q, k, v, [1], [5000], True, None, "f16")
+    return plan, (q, k, v, ints([0, 1]), ints([0, 5000])), want
+
+
+def split_shared():
+    q, k, v = normal(1, 3, 4, 64), normal(2, 5000, 2, 64), normal(3, 5000, 2, 64)
+    cache, lengths = normal(4, 3, 300, 2, 64), [300, 0, 17]
+    plan = b2b.SharedPrefixAttentionPlan("f16", 4, 2, 64)
+    n = ctypes.c_size_t()
+    assert b2b.b2b_shared_attention_workspace(plan._h, 3, 1, 5000, 300, ctypes.byref(n)) == 0 and n.value > 0
+    want = Want(3, 4, 64)
+    for b, m in enumerate(lengths):
+        want.rows(b, q[b:b + 1], torch.cat([k, cache[b, :m]]), torch.cat([v, cache[b, :m]]), [5000 + m], 1 / 8, "f16")
+    return plan, (q, k, v, cache, cache, ints(lengths)), want
+
+
+def split_many():
+    """More short items than CTAs: some are claimed ahead of the one that stops."""
+    q, k, v = normal(1, 300, 8, 64), normal(2, 4000, 4, 64), normal(3, 4000, 4, 64)
+    cache, lengths = normal(4, 300, 64, 4, 64), [(7 * b) % 65 for b in range(300)]
+    plan = b2b.SharedPrefixAttentionPlan("f16", 8, 4, 64)
+    n = ctypes.c_size_t()
+    assert b2b.b2b_shared_attention_workspace(plan._h, 300, 1, 4000, 64, ctypes.byref(n)) == 0 and n.value > 0
+    want = Want(300, 8, 64)
+    for b, m in enumerate(lengths):
+        want.rows(b, q[b:b + 1], torch.cat([k, cache[b, :m]]), torch.cat([v, cache[b, :m]]), [4000 + m], 1 / 8, "f16")
+    return plan, (q, k, v, cache, cache, ints(lengths)), want
+
+
+@pytest.mark.parametrize("case", [split_prompt, split_shared, split_many])
+def test_a_timeout_leaves_results_of_joined_parts_alone(case):
+    """Parts that were not written are not joined, neither another run's that lie in the same workspace."""
+    plan, args, want = case()
+    first = plan.run(*args, return_lse=True)  # its parts stay in the allocator's memory
+    want.check(*first)
+    assert plan.status() == 0
+    out, lse = torch.full_like(first[0], 7.0), torch.full_like(first[1], 7.0)
+    plan.set_wait_budget(20_000_000)
+    plan.set_debug(1)
+    plan.run(*args, out=out, lse=lse)
+    plan.set_debug(0)
+    plan.set_wait_budget(0)
+    good = plan.run(*args, return_lse=True)  # (before the status is read: a run of its own)
+    assert plan.status() == TIMEOUT
+    assert (out == 7).all() and (lse == 7).all()
+    assert torch.equal(good[0], first[0]) and torch.equal(good[1], first[1])
     assert plan.status() == 0
