@@ -70,9 +70,12 @@ def _current(path: str, stamp: str, digest: str) -> bool:
         return f.read().strip() == digest
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile attn_binding.so if its source, b2b.h or torch changed; return its path."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+def build_binding(force: bool = False) -> str | None:
+    """Compile attn_binding.so if its source, b2b.h or torch changed; return its path (None without torch)."""
+    torch_spec = importlib.util.find_spec("torch")
+    if torch_spec is None:
+        return None
+    torch_dir = torch_spec.submodule_search_locations[0]
     inc = os.path.join(torch_dir, "include")
     flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-I" + INCLUDE, "-I" + inc,
              "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), "-I" + sysconfig.get_paths()["include"]]

@@ -14,17 +14,16 @@ import importlib.machinery
 import importlib.util
 import os
 import struct
-
-import torch
+import warnings
 
 from . import DTYPES, _check, _current_device, _lib, _stream_handle, library_path
 
 __all__ = ["PromptAttentionPlan", "SharedPrefixAttentionPlan"]
 
-_TORCH = {"f16": torch.float16, "bf16": torch.bfloat16}
+_TYPES = {"f16": "float16", "bf16": "bfloat16"}
 
-# (the public torch.cuda.current_stream() builds an object each time, 3 us)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# Set when the first plan is made (_load): the package's other parts need neither torch nor the compiled module.
+torch = _raw_stream = _binding = None
 
 # The argument structures, whose members all take eight bytes (b2b_attn_rows_t:
 # data, row_stride, head_stride, block_stride), as the C functions read them.
@@ -35,23 +34,42 @@ _prompt_run = struct.Struct("25q").pack
 _shared_run = struct.Struct("35q").pack
 
 
+class _NoBinding:
+    """In the compiled module's place where there is none: every call takes the way through Python."""
+
+    @staticmethod
+    def bind(*_):
+        return None
+
+    prompt = shared = bind
 
 
 def _load_binding():
-    """The module that passes tensors to the C functions (binding/attention.cpp)."""
+    """The module that passes tensors to the C functions (binding/attention.cpp), if it is there for this torch."""
     path = os.path.join(os.path.dirname(library_path()), "attn_binding.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it first (python fusion_b2b_gemm_gb300/_build.py)")
-    loader = importlib.machinery.ExtensionFileLoader("attn_binding", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("attn_binding", loader))
-    loader.exec_module(module)
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("attn_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("attn_binding", loader))
+        loader.exec_module(module)
+        if not torch.__version__.startswith(module.torch_version):
+            raise ImportError(f"built for torch {module.torch_version}, this is {torch.__version__}")
+    except ImportError as e:
+        warnings.warn(f"{path}: {e}; attention calls take some microseconds longer without it "
+                      "(python fusion_b2b_gemm_gb300/_build.py)", RuntimeWarning, stacklevel=5)
+        return _NoBinding
     module.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         _lib.b2b_prompt_attention_workspace, _lib.b2b_prompt_attention_run,
         _lib.b2b_shared_attention_workspace, _lib.b2b_shared_attention_run)))
     return module
 
 
-_binding = _load_binding()
+def _load():
+    global torch, _raw_stream, _binding
+    if _binding is None:
+        import torch
+        # (the public torch.cuda.current_stream() builds an object each time, 3 us)
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _binding = _load_binding()
 
 
 class _AttentionPlan:
@@ -64,15 +82,16 @@ class _AttentionPlan:
 
     def __init__(self, dtype: str, q_heads: int, kv_heads: int, head_dim: int, scale: float | None = None):
         if dtype not in DTYPES:
-            raise ValueError(f"unknown dtype {dtype!r}; one of {sorted(_TORCH)}")
+            raise ValueError(f"unknown dtype {dtype!r}; one of {sorted(_TYPES)}")
         if scale is not None and not scale > 0:
             raise ValueError(f"scale {scale!r}: a positive number is expected")
+        _load()
         self.dtype, self.q_heads, self.kv_heads, self.head_dim = dtype, q_heads, kv_heads, head_dim
         h = ctypes.c_void_p()
         _check(_lib.b2b_attn_plan_create(ctypes.byref(h), DTYPES[dtype], q_heads, kv_heads, head_dim, scale or 0.0),
                "b2b_attn_plan_create")
         self._h = h
-        self._torch_dtype = _TORCH[dtype]
+        self._torch_dtype = getattr(torch, _TYPES[dtype])
         self.device_index = _current_device()
         self._workspace_sizes = {}
         # What the binding's calls need to know of the plan.  They take the

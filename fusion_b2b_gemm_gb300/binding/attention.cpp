@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <torch/version.h>
 
 #include <array>
 #include <map>
@@ -189,4 +190,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "attn_binding", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_attn_binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit_attn_binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -92,3 +92,22 @@ def test_a_timeout_leaves_results_of_joined_parts_alone(case):
     assert (out == 7).all() and (lse == 7).all()
     assert torch.equal(good[0], first[0]) and torch.equal(good[1], first[1])
     assert plan.status() == 0
+
+
+# ------------------------------------------------------- the compiled module
+def test_calls_without_the_compiled_module(monkeypatch):
+    """The way through Python gives the same bits."""
+    from fusion_b2b_gemm_gb300 import attention
+    q, k, v, cu = normal(1, 90, 4, 64), normal(2, 90, 2, 64), normal(3, 90, 2, 64), ints([0, 31, 90])
+    cache, lengths = normal(4, 9, 16, 2, 64), ints([5, 16, 0])
+    calls = [("PromptAttentionPlan", (q, k, v, cu)), ("SharedPrefixAttentionPlan", (q[:9], k, v, cache[:3], cache[:3], lengths)),
+             ("SharedPrefixAttentionPlan", (q[:9], k, v, cache, cache, lengths, ints([[8], [3], [-1]])))]
+    want = [getattr(b2b, kind)("f16", 4, 2, 64).run(*args, return_lse=True) for kind, args in calls]
+    assert attention._binding is not attention._NoBinding
+    monkeypatch.setattr(attention, "_binding", attention._NoBinding)
+    for (kind, args), w in zip(calls, want):
+        plan = getattr(b2b, kind)("f16", 4, 2, 64)
+        got = plan.run(*args, return_lse=True)
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+        assert torch.equal(plan.run(*args, stream=torch.cuda.current_stream()), w[0])
+        assert plan.status() == 0
