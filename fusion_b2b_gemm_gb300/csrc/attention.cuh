@@ -570,6 +570,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = pack2(sl2, sl2);
     uint32_t nscore = 0, nml = 0, nturn = 0;
+    grid_dependency_wait();  // (the waits below are for this run's work, not for the kernel before)
     for (uint32_t it = 0;; ++it) {
       const uint32_t islot = it % kAttnItems;
       if (!bw.wait(bar(kABItemFull + islot), (it / kAttnItems) & 1u)) break;
@@ -866,6 +867,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // One elected thread (measured: a warp-wide walk that elects a thread for
       // each group of MMAs issues them a fifth slower).
       const int t = warp - 8;
+      grid_dependency_wait();  // (as in the softmax)
       if (elect_one()) {
         const uint32_t d_s = tmem + 128u * static_cast<uint32_t>(t);
         const uint32_t d_o = tmem + kColO + static_cast<uint32_t>(DP * t);

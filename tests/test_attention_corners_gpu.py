@@ -7,7 +7,7 @@ import ctypes
 import pytest
 import torch
 
-from test_attention_gpu import TIMEOUT, Want, b2b, ints, normal, want_prompt
+from test_attention_gpu import TIMEOUT, Want, b2b, cumulative, ints, normal, want_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,36 @@ def test_calls_without_the_compiled_module(monkeypatch):
         assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
         assert torch.equal(plan.run(*args, stream=torch.cuda.current_stream()), w[0])
         assert plan.status() == 0
+
+
+def one_long_item(queries):
+    """2000 sequences of which one has 600,000 keys: its item alone takes several milliseconds."""
+    n = 600_000
+    nq, nk = [1] * 1999 + [queries], [1] * 1999 + [n]
+    q, k, v = normal(1, sum(nq), 1, 64), normal(2, sum(nk), 1, 64), normal(3, sum(nk), 1, 64)
+    plan = b2b.PromptAttentionPlan("f16", 1, 1, 64)
+    size = ctypes.c_size_t()
+    assert b2b.b2b_prompt_attention_workspace(plan._h, 2000, sum(nq), sum(nk), 0, ctypes.byref(size)) == 0
+    assert size.value == 0  # (not cut into parts)
+    args = q, k, v, cumulative(nq), cumulative(nk), False
+    return plan, args
+
+
+def test_a_short_budget_does_not_count_the_kernel_before():
+    """A run starts while the kernel before it in the stream is finishing, and its waits count from that one's end."""
+    long, args = one_long_item(128)
+    q, k, v, cu = normal(4, 150, 4, 64), normal(5, 150, 2, 64), normal(6, 150, 2, 64), ints([0, 150])
+    plan = b2b.PromptAttentionPlan("f16", 4, 2, 64)
+    plan.set_wait_budget(1_000_000)
+    plan.run(q, k, v, cu)
+    assert plan.status() == 0
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    long.run(*args)
+    assert long.status() == 0
+    start.record()
+    long.run(*args)
+    out = plan.run(q, k, v, cu)  # (nothing between the two, which would keep them apart)
+    end.record()
+    assert plan.status() == 0 and long.status() == 0
+    assert start.elapsed_time(end) > 1.5  # (the budget had time to run out)
+    want_prompt(q, k, v, [150], [150], True, None, "f16").check(out)
