@@ -210,8 +210,21 @@ b2b_status_t check_current_device(const b2b_attn_plan_s* p) {
   return dev == p->device ? B2B_OK : B2B_ERR_DEVICE;
 }
 
+// Some waits last as long as an item does (the epilogue's for its last tile,
+// the item warp's for its loads), and the first of all as long as the search
+// for an item, which reads `searched` sequences once for every halving of the
+// tiles.  A budget counts as no less than these take with some ten times to
+// spare: 20 us a tile of the longest item, 0.3 us a sequence and step.
+uint64_t wait_budget(const b2b_attn_plan_s* p, int64_t tiles, int64_t searched) {
+  uint64_t steps = 4;
+  while ((int64_t(1) << (steps - 4)) < tiles) ++steps;
+  return std::max(p->budget_ns, 20000 * static_cast<uint64_t>(tiles) + 300 * steps * static_cast<uint64_t>(searched));
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 AttnParams common_params(const b2b_attn_plan_s* p, int64_t tokens, int64_t batch, const b2b_attn_rows_t& out, float* lse,
-                         void* workspace, int parts) {
+                         void* workspace, int parts, uint64_t budget_ns) {
   AttnParams a;
   std::memset(&a, 0, sizeof(a));
   a.group = p->group;
@@ -244,7 +257,7 @@ AttnParams common_params(const b2b_attn_plan_s* p, int64_t tokens, int64_t batch
   a.q_bytes = static_cast<uint32_t>(p->group * p->tile_tokens) * 128u * (p->dp ? 2u : 1u);
   a.debug = p->debug;
   a.status = p->d_status;
-  a.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(p->budget_ns, 4000000000ull));  // (a 32-bit clock in the kernel)
+  a.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(budget_ns, 4000000000ull));  // (a 32-bit clock in the kernel)
   return a;
 }
 
@@ -383,7 +396,9 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attent
   st = check_current_device(p);
   if (st != B2B_OK) return st;
 
-  AttnParams a = common_params(p, r->tokens, r->batch, r->out, r->lse, r->workspace, splits);
+  const int64_t most_tiles = ceil_div(r->key_rows, kAttnTile);
+  AttnParams a = common_params(p, r->tokens, r->batch, r->out, r->lse, r->workspace, splits,
+                               wait_budget(p, ceil_div(most_tiles, splits), r->batch));
   a.op = kAttnPrompt;
   a.causal = r->causal != 0;
   a.cu_q = r->cu_q;
@@ -391,7 +406,7 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attent
   a.key_rows = static_cast<int>(r->key_rows);
   a.by_splits = FastDiv::of(static_cast<uint32_t>(splits));
   a.by_block = FastDiv::of(static_cast<uint32_t>(shape.tiles * p->tile_tokens));
-  a.most_tiles = static_cast<int>((r->key_rows + kAttnTile - 1) / kAttnTile);
+  a.most_tiles = static_cast<int>(most_tiles);
   a.box_rows = kAttnTile;
   CUtensorMap maps[6];
   st = encode_q(&maps[0], p, r->q, r->tokens, static_cast<uint32_t>(p->tile_tokens));
@@ -461,7 +476,9 @@ b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t p, const b2b_shared_attent
   st = check_current_device(p);
   if (st != B2B_OK) return st;
 
-  AttnParams a = common_params(p, tokens, r->batch, r->out, r->lse, r->workspace, parts);
+  const int64_t pre_tiles = ceil_div(r->prefix, kAttnTile), own_tiles = ceil_div(ceil_div(room, kAttnTile), s.own_splits);
+  const int64_t item_tiles = std::max(s.splits ? ceil_div(pre_tiles, s.splits) : 0, own_tiles + (s.whole ? pre_tiles : 0));
+  AttnParams a = common_params(p, tokens, r->batch, r->out, r->lse, r->workspace, parts, wait_budget(p, item_tiles, 0));
   a.op = kAttnShared;
   a.causal = 1;
   a.by_splits = FastDiv::of(static_cast<uint32_t>(std::max(s.splits, 1)));

@@ -375,7 +375,9 @@ b2b_status_t b2b_attn_plan_create(b2b_attn_plan_t* out, b2b_dtype_t dtype, int64
                                   int64_t head_dim, float scale);
 b2b_status_t b2b_attn_plan_destroy(b2b_attn_plan_t plan);
 /* As b2b_plan_device_status, b2b_plan_set_wait_budget (budgets above 4 s count
- * as 4 s: the kernel's clock has 32 bits), b2b_plan_set_debug. */
+ * as 4 s: the kernel's clock has 32 bits; one shorter than a run's longest
+ * wait may be, 20 us for each 128 keys that a CTA reads in a row and for
+ * prompts some microseconds a sequence, counts as that), b2b_plan_set_debug. */
 b2b_status_t b2b_attn_plan_device_status(b2b_attn_plan_t plan, b2b_stream_t stream);
 b2b_status_t b2b_attn_plan_set_wait_budget(b2b_attn_plan_t plan, uint64_t budget_ns);
 b2b_status_t b2b_attn_plan_set_debug(b2b_attn_plan_t plan, uint32_t flags);

@@ -144,3 +144,15 @@ def test_a_short_budget_does_not_count_the_kernel_before():
     assert plan.status() == 0 and long.status() == 0
     assert start.elapsed_time(end) > 1.5  # (the budget had time to run out)
     want_prompt(q, k, v, [150], [150], True, None, "f16").check(out)
+
+
+@pytest.mark.parametrize("queries", [100, 200])
+def test_a_short_budget_covers_a_long_item(queries):
+    """Some waits last as long as an item does, in which every single hand-over is quick."""
+    plan, args = one_long_item(queries)
+    want = plan.run(*args)
+    assert plan.status() == 0
+    plan.set_wait_budget(1_000_000)
+    out = plan.run(*args)
+    assert plan.status() == 0
+    assert torch.equal(out, want)
