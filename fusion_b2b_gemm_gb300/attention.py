@@ -5,7 +5,8 @@ The cascade softmax(scale * Q K^T + mask) V in one kernel, for grouped heads
 whole prompts of different lengths, :class:`SharedPrefixAttentionPlan` for the
 new tokens of a batch of requests that share one long prefix.  A plan holds
 the head layout; a run takes tensors of any length, with any strides whose
-last one is 1.  Inference only.  There is no CPU path.
+last one is 1.  Inference only: inputs that require a gradient are refused
+where gradients are recorded.  There is no CPU path.
 """
 from __future__ import annotations
 
@@ -130,6 +131,11 @@ class _AttentionPlan:
             self._refuse(name, t, self.kv_heads, 4)
         return shape[0], shape[1], t.data_ptr(), stride[1], stride[2], stride[0]
 
+    def _no_gradient(self, *inputs):
+        if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+            raise RuntimeError(f"{type(self).__name__} is inference-only: its output has no gradient "
+                               "(run it under torch.no_grad())")
+
     def _placed(self, name, t):
         if t.get_device() != self.device_index:  # (-1 for a CPU tensor)
             raise ValueError(f"{name} is on {t.device}, the plan on cuda:{self.device_index}")
@@ -225,6 +231,7 @@ class PromptAttentionPlan(_AttentionPlan):
             done = _binding.prompt(self._bound, _raw_stream(self.device_index), q, k, v, cu_q, cu_k, causal, return_lse)
             if done is not None:
                 return done
+        self._no_gradient(q, k, v)
         tokens, *qa = self._packed("q", q, self.q_heads)
         key_rows, *ka = self._packed("k", k, self.kv_heads)
         rows, *va = self._packed("v", v, self.kv_heads)
@@ -271,6 +278,7 @@ class SharedPrefixAttentionPlan(_AttentionPlan):
                                    lengths, page_table, return_lse)
             if done is not None:
                 return done
+        self._no_gradient(q, prefix_k, prefix_v, cache_k, cache_v)
         tokens, *qa = self._packed("q", q, self.q_heads)
         prefix, *pka = self._packed("prefix_k", prefix_k, self.kv_heads)
         rows, *pva = self._packed("prefix_v", prefix_v, self.kv_heads)

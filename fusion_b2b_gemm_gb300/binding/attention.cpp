@@ -8,6 +8,7 @@
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <torch/version.h>
 
@@ -44,10 +45,13 @@ const at::Tensor* tensor(const Bound& p, PyObject* o, c10::ScalarType type, int6
              : nullptr;
 }
 
+// Whether a gradient would have to be recorded, which no run does.
+bool recorded(const at::Tensor& t) { return t.requires_grad() && at::GradMode::is_enabled(); }
+
 // [rows][heads][dim], or [blocks][rows][heads][dim]
 const at::Tensor* rows(const Bound& p, PyObject* o, int64_t dims, int64_t heads, b2b_attn_rows_t& r) {
   const at::Tensor* t = tensor(p, o, p.type, dims);
-  if (!t || t->size(dims - 2) != heads || t->size(dims - 1) != p.dim || t->stride(dims - 1) != 1) return nullptr;
+  if (!t || t->size(dims - 2) != heads || t->size(dims - 1) != p.dim || t->stride(dims - 1) != 1 || recorded(*t)) return nullptr;
   r = {t->data_ptr(), t->stride(dims - 3), t->stride(dims - 2), dims == 4 ? t->stride(0) : 0};
   return t;
 }

@@ -156,3 +156,21 @@ def test_a_short_budget_covers_a_long_item(queries):
     out = plan.run(*args)
     assert plan.status() == 0
     assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------- gradients
+def test_inputs_that_require_a_gradient_are_refused():
+    """The results have none; without grad mode the inputs may be parameters."""
+    q, k, v, cu = normal(1, 9, 4, 64), normal(2, 9, 2, 64), normal(3, 9, 2, 64), ints([0, 9])
+    cache, lengths = normal(4, 3, 16, 2, 64), ints([1, 2, 3])
+    prompt, shared = b2b.PromptAttentionPlan("f16", 4, 2, 64), b2b.SharedPrefixAttentionPlan("f16", 4, 2, 64)
+    for plan, args, floats in ((prompt, (q, k, v, cu), 3), (shared, (q, k, v, cache, cache.clone(), lengths), 5)):
+        want = plan.run(*args)
+        for i in range(floats):
+            leaf = args[:i] + (args[i].clone().requires_grad_(),) + args[i + 1:]
+            for kw in ({}, {"out": torch.empty_like(q)}, {"stream": torch.cuda.Stream()}):
+                with pytest.raises(RuntimeError, match="no_grad"):
+                    plan.run(*leaf, **kw)
+            with torch.no_grad():
+                assert torch.equal(plan.run(*leaf), want)
+        assert plan.status() == 0
