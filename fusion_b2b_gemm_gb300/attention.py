@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import math
 import os
 import struct
 import warnings
@@ -21,6 +22,7 @@ from . import DTYPES, _check, _current_device, _lib, _stream_handle, library_pat
 
 __all__ = ["PromptAttentionPlan", "SharedPrefixAttentionPlan"]
 
+_LOG2E = 1 / math.log(2)
 _TYPES = {"f16": "float16", "bf16": "bfloat16"}
 
 # Set when the first plan is made (_load): the package's other parts need neither torch nor the compiled module.
@@ -84,8 +86,9 @@ class _AttentionPlan:
     def __init__(self, dtype: str, q_heads: int, kv_heads: int, head_dim: int, scale: float | None = None):
         if dtype not in DTYPES:
             raise ValueError(f"unknown dtype {dtype!r}; one of {sorted(_TYPES)}")
-        if scale is not None and not scale > 0:
-            raise ValueError(f"scale {scale!r}: a positive number is expected")
+        # (in 32 bits, where the kernel also takes it times log2(e); there 0 would mean the default)
+        if scale is not None and not (ctypes.c_float(scale).value > 0 and ctypes.c_float(scale * _LOG2E).value < math.inf):
+            raise ValueError(f"scale {scale!r}: a positive number is expected that fp32 holds, also times log2(e)")
         _load()
         self.dtype, self.q_heads, self.kv_heads, self.head_dim = dtype, q_heads, kv_heads, head_dim
         h = ctypes.c_void_p()

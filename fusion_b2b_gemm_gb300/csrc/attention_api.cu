@@ -34,6 +34,8 @@ constexpr int64_t kMaxRows = int64_t(1) << 30;
 // is launched with: a kernel compiled to fewer would wait for them.
 constexpr int kRegsNeeded = 256 * kAttnSoftmaxRegs + 128 * kAttnEpilogueRegs + 128 * kAttnOtherRegs;
 
+float times_log2e(float scale) { return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634); }
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Strides of a tensor of `rows` x `heads` (x `blocks`) rows of `dim` elements:
@@ -238,7 +240,7 @@ AttnParams common_params(const b2b_attn_plan_s* p, int64_t tokens, int64_t batch
   a.tokens = static_cast<int>(tokens);
   a.batch = static_cast<int>(batch);
   a.scale = p->scale;
-  a.scale_log2 = static_cast<float>(static_cast<double>(p->scale) * 1.4426950408889634);
+  a.scale_log2 = times_log2e(p->scale);
   a.out = out.data;
   a.out_row = out.row_stride;
   a.out_head = out.head_stride;
@@ -289,7 +291,7 @@ b2b_status_t b2b_attn_plan_create(b2b_attn_plan_t* out, b2b_dtype_t dtype, int64
   *out = nullptr;
   if (dtype < B2B_F16_F32OUT || dtype > B2B_TF32_BF16) return B2B_ERR_INVALID_ARG;
   if (q_heads < 1 || kv_heads < 1 || head_dim < 1 || q_heads % kv_heads) return B2B_ERR_INVALID_ARG;
-  if (!(scale >= 0.0f) || std::isinf(scale)) return B2B_ERR_INVALID_ARG;
+  if (!(scale >= 0.0f) || std::isinf(times_log2e(scale))) return B2B_ERR_INVALID_ARG;
   if (dtype != B2B_F16 && dtype != B2B_BF16) return B2B_ERR_UNSUPPORTED;
   if (head_dim % 8 || head_dim > 128 || q_heads > 65536 || q_heads / kv_heads > kAttnTile) return B2B_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;

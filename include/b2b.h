@@ -366,7 +366,8 @@ typedef struct {
  *   dtype     B2B_F16 or B2B_BF16 (inputs, probabilities and output).
  *   q_heads   a multiple of kv_heads, at most 128 times as many.
  *   head_dim  a multiple of 8, at most 128.
- *   scale     factor of the scores, positive; 0 for 1 / sqrt(head_dim).
+ *   scale     factor of the scores, positive, and finite also times log2(e);
+ *             0 for 1 / sqrt(head_dim).
  * Binds to the current CUDA device (an sm_103 GPU) and allocates a 4-byte
  * status word.  The plan is not modified by a run: runs on several streams
  * may overlap.

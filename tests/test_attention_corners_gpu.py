@@ -7,7 +7,7 @@ import ctypes
 import pytest
 import torch
 
-from test_attention_gpu import TIMEOUT, Want, b2b, cumulative, ints, normal, want_prompt
+from test_attention_gpu import TIMEOUT, Want, b2b, cumulative, ints, normal, prompt_case, want_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -174,3 +174,9 @@ def test_inputs_that_require_a_gradient_are_refused():
             with torch.no_grad():
                 assert torch.equal(plan.run(*leaf), want)
         assert plan.status() == 0
+
+
+# --------------------------------------------------------------------- scales
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 20.0])
+def test_small_and_large_scales(scale):
+    prompt_case("f16", 4, 2, 64, [150], scale=scale)
