@@ -36,6 +36,7 @@ constexpr int kRegsNeeded = 256 * kAttnSoftmaxRegs + 128 * kAttnEpilogueRegs + 1
 
 float times_log2e(float scale) { return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634); }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Strides of a tensor of `rows` x `heads` (x `blocks`) rows of `dim` elements:
@@ -377,6 +378,7 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attent
   if (r->tokens > kMaxRows || r->key_rows > kMaxRows || r->batch > kMaxRows) return B2B_ERR_UNSUPPORTED;
   if (r->tokens == 0 || r->batch == 0) return B2B_OK;
   if (!r->cu_q || !r->cu_k) return B2B_ERR_INVALID_ARG;
+  if (!aligned4(r->cu_q) || !aligned4(r->cu_k) || !aligned4(r->lse)) return B2B_ERR_ALIGNMENT;
   const int64_t hq = p->q_heads, hk = p->kv_heads, d = p->dim;
   b2b_status_t st = check_rows(r->q, r->tokens, hq, 1);
   if (st == B2B_OK) st = check_rows(r->k, r->key_rows, hk, 1);
@@ -445,6 +447,7 @@ b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t p, const b2b_shared_attent
   const int64_t tokens = r->batch * r->fresh;
   if (tokens == 0) return B2B_OK;
   if (!r->lengths) return B2B_ERR_INVALID_ARG;
+  if (!aligned4(r->lengths) || !aligned4(r->page_table) || !aligned4(r->lse)) return B2B_ERR_ALIGNMENT;
   if (!paged && r->cache_blocks != r->batch) return B2B_ERR_INVALID_ARG;
   int page_shift = 0;
   if (paged) {

@@ -348,6 +348,8 @@ b2b_status_t b2b_run_tf32_noalloc(int64_t batch, int64_t M, int64_t K, int64_t N
  *     kernel runs: a captured run follows their contents.  Counts and
  *     offsets outside the tensors are clamped to them; pages outside the pool
  *     read as zeros.
+ *   - Arrays of counts, offsets and pages and the LSE lie on 4-byte boundaries
+ *     (else B2B_ERR_ALIGNMENT).
  *   - Nothing in a run depends on timing: equal inputs give equal bits.
  */
 typedef struct b2b_attn_plan_s* b2b_attn_plan_t;

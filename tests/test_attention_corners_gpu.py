@@ -7,7 +7,7 @@ import ctypes
 import pytest
 import torch
 
-from test_attention_gpu import TIMEOUT, Want, b2b, cumulative, ints, normal, prompt_case, want_prompt
+from test_attention_gpu import ALIGNMENT, TIMEOUT, Want, b2b, cumulative, ints, normal, prompt_case, want_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -180,3 +180,28 @@ def test_inputs_that_require_a_gradient_are_refused():
 @pytest.mark.parametrize("scale", [1e-30, 1e-3, 20.0])
 def test_small_and_large_scales(scale):
     prompt_case("f16", 4, 2, 64, [150], scale=scale)
+
+
+# ------------------------------------------------- the C functions' own checks
+def test_counts_and_lse_off_their_alignment_are_refused():
+    """Arrays of 32-bit values at odd addresses: refused before anything is launched."""
+    q, k, v, cu = normal(1, 9, 4, 64), normal(2, 9, 2, 64), normal(3, 9, 2, 64), ints([0, 9, 9])
+    out, lse, cache = torch.empty_like(q), torch.empty(10, 4, device="cuda"), normal(4, 9, 16, 2, 64)
+    lengths, table = ints([1] * 10), ints([[0]] * 10)
+
+    def rows(t):
+        return t.data_ptr(), t.stride(-3), t.stride(-2), t.stride(0) if t.dim() == 4 else 0
+
+    prompt, shared = b2b.PromptAttentionPlan("f16", 4, 2, 64), b2b.SharedPrefixAttentionPlan("f16", 4, 2, 64)
+    for at in range(3):
+        for off in (1, 2, 3):
+            p = [cu.data_ptr(), cu.data_ptr(), lse.data_ptr()]
+            p[at] += off
+            run = (ctypes.c_int64 * 25)(1, 9, 9, 1, *rows(q), *rows(k), *rows(v), *rows(out), *p, 0, 0)
+            assert b2b.b2b_prompt_attention_run(prompt._h, run, None) == ALIGNMENT
+            p = [lengths.data_ptr(), table.data_ptr(), lse.data_ptr()]
+            p[at] += off
+            run = (ctypes.c_int64 * 35)(9, 1, 9, 16, 9, 1, *rows(q), *rows(k), *rows(v), *rows(cache), *rows(cache),
+                                        *rows(out), *p, 0, 0)
+            assert b2b.b2b_shared_attention_run(shared._h, run, None) == ALIGNMENT
+    assert prompt.status() == 0 and shared.status() == 0
