@@ -60,6 +60,23 @@ size_t span_bytes(const b2b_attn_rows_t& t, int64_t rows, int64_t heads, int64_t
                                  (blocks - 1) * t.block_stride + dim);
 }
 
+// Whether the output's rows share bytes with an input's.  Tensors whose rows
+// alternate, as column ranges of one buffer do, have overlapping spans but no
+// byte in common: with rows an equal stride apart, and each in a window no
+// wider than it, the windows repeat with that stride and have to be disjoint
+// in one period.  Other strides are judged by the spans.
+bool rows_overlap(const b2b_attn_rows_t& out, int64_t out_rows, int64_t out_heads, const b2b_attn_rows_t& in, int64_t rows,
+                  int64_t heads, int64_t blocks, int64_t dim) {
+  if (!overlaps(out.data, span_bytes(out, out_rows, out_heads, 1, dim), in.data, span_bytes(in, rows, heads, blocks, dim)))
+    return false;
+  if (blocks != 1 || out_rows == 1 || rows == 1 || out.row_stride != in.row_stride) return true;
+  const int64_t period = 2 * out.row_stride;
+  const int64_t a = static_cast<int64_t>(span_bytes(out, 1, out_heads, 1, dim)), b = static_cast<int64_t>(span_bytes(in, 1, heads, 1, dim));
+  int64_t apart = (reinterpret_cast<intptr_t>(in.data) - reinterpret_cast<intptr_t>(out.data)) % period;
+  if (apart < 0) apart += period;
+  return apart < a || apart + b > period;  // (a window wider than the period is caught by one or the other)
+}
+
 // 4-D map with boxes of 64 columns (128 bytes, swizzled) by box1 x 1 x box3 or
 // 1 x box2 rows; extents of one take a stride of one dense row.
 b2b_status_t encode(CUtensorMap* map, const b2b_attn_plan_s* p, const void* data, const int64_t (&ext)[3],
@@ -385,10 +402,8 @@ b2b_status_t b2b_prompt_attention_run(b2b_attn_plan_t p, const b2b_prompt_attent
   if (st == B2B_OK) st = check_rows(r->v, r->key_rows, hk, 1);
   if (st == B2B_OK) st = check_rows(r->out, r->tokens, hq, 1);
   if (st != B2B_OK) return st;
-  const size_t on = span_bytes(r->out, r->tokens, hq, 1, d);
-  if (overlaps(r->out.data, on, r->q.data, span_bytes(r->q, r->tokens, hq, 1, d)) ||
-      overlaps(r->out.data, on, r->k.data, span_bytes(r->k, r->key_rows, hk, 1, d)) ||
-      overlaps(r->out.data, on, r->v.data, span_bytes(r->v, r->key_rows, hk, 1, d)))
+  if (rows_overlap(r->out, r->tokens, hq, r->q, r->tokens, hq, 1, d) || rows_overlap(r->out, r->tokens, hq, r->k, r->key_rows, hk, 1, d) ||
+      rows_overlap(r->out, r->tokens, hq, r->v, r->key_rows, hk, 1, d))
     return B2B_ERR_ALIAS;
   const PromptShape shape = prompt_shape(p, r->batch, r->tokens, r->key_rows, r->causal != 0);
   const int splits = shape.splits;
@@ -465,12 +480,10 @@ b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t p, const b2b_shared_attent
   if (st == B2B_OK) st = check_rows(r->cache_v, r->cache_rows, hk, r->cache_blocks);
   if (st == B2B_OK) st = check_rows(r->out, tokens, hq, 1);
   if (st != B2B_OK) return st;
-  const size_t on = span_bytes(r->out, tokens, hq, 1, d);
-  if (overlaps(r->out.data, on, r->q.data, span_bytes(r->q, tokens, hq, 1, d)) ||
-      overlaps(r->out.data, on, r->prefix_k.data, span_bytes(r->prefix_k, r->prefix, hk, 1, d)) ||
-      overlaps(r->out.data, on, r->prefix_v.data, span_bytes(r->prefix_v, r->prefix, hk, 1, d)) ||
-      overlaps(r->out.data, on, r->cache_k.data, span_bytes(r->cache_k, r->cache_rows, hk, r->cache_blocks, d)) ||
-      overlaps(r->out.data, on, r->cache_v.data, span_bytes(r->cache_v, r->cache_rows, hk, r->cache_blocks, d)))
+  if (rows_overlap(r->out, tokens, hq, r->q, tokens, hq, 1, d) || rows_overlap(r->out, tokens, hq, r->prefix_k, r->prefix, hk, 1, d) ||
+      rows_overlap(r->out, tokens, hq, r->prefix_v, r->prefix, hk, 1, d) ||
+      rows_overlap(r->out, tokens, hq, r->cache_k, r->cache_rows, hk, r->cache_blocks, d) ||
+      rows_overlap(r->out, tokens, hq, r->cache_v, r->cache_rows, hk, r->cache_blocks, d))
     return B2B_ERR_ALIAS;
   const SharedShape s = shared_shape(p, r->batch, r->fresh, r->prefix, room);
   const int parts = s.splits + s.own_splits;

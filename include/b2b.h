@@ -396,7 +396,8 @@ b2b_status_t b2b_attn_plan_set_debug(b2b_attn_plan_t plan, uint32_t flags);
  *               keys j <= i + (keys - queries) of its sequence, so that the
  *               last row sees all: a piece of a prompt can follow keys of
  *               earlier pieces.
- *   out         [tokens][q_heads] rows; must not overlap q, k or v.
+ *   out         [tokens][q_heads] rows; must not overlap q, k or v.  (It may lie
+ *               between their rows in one buffer if its row stride is theirs.)
  *   lse         [tokens][q_heads] fp32 or NULL.
  *   workspace   device memory of at least b2b_prompt_attention_workspace bytes
  *               (may be NULL when that is 0), 32-byte aligned, for this run

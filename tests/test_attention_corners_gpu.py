@@ -7,7 +7,7 @@ import ctypes
 import pytest
 import torch
 
-from test_attention_gpu import ALIGNMENT, TIMEOUT, Want, b2b, cumulative, ints, normal, prompt_case, want_prompt
+from test_attention_gpu import ALIAS, ALIGNMENT, TIMEOUT, Want, b2b, cumulative, ints, normal, prompt_case, want_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -205,3 +205,59 @@ def test_counts_and_lse_off_their_alignment_are_refused():
                                         *rows(out), *p, 0, 0)
             assert b2b.b2b_shared_attention_run(shared._h, run, None) == ALIGNMENT
     assert prompt.status() == 0 and shared.status() == 0
+
+
+# ------------------------------------------------------------------- outputs
+def test_an_output_between_the_inputs_columns():
+    """Output and inputs as column ranges of one buffer, in any order: their rows alternate and do not overlap."""
+    n, hq, hk, d = 150, 4, 2, 64
+    widths = {"q": hq, "k": hk, "v": hk, "out": hq}
+    plan = b2b.PromptAttentionPlan("bf16", hq, hk, d)
+    for order in ("q k v out", "out q k v", "q out k v"):
+        names = order.split()
+        both = normal(5, n, sum(widths.values()) * d, dtype="bf16")
+        t = dict(zip(names, (x.unflatten(1, (-1, d)) for x in both.split([widths[x] * d for x in names], 1))))
+        want = want_prompt(t["q"], t["k"], t["v"], [n], [n], True, None, "bf16")
+        keep = {x: t[x].clone() for x in "qkv"}
+        want.check(plan.run(t["q"], t["k"], t["v"], ints([0, n]), out=t["out"]))
+        assert all(torch.equal(keep[x], t[x]) for x in "qkv")
+
+
+def test_outputs_that_overlap_an_input_are_refused():
+    n, d = 20, 64
+    both = normal(6, n + 2, 16, d)
+    plan = b2b.PromptAttentionPlan("f16", 4, 2, d)
+    k, v = normal(2, n, 2, d), normal(3, n, 2, d)
+    q = both[1:n + 1, 4:8]
+    for out in (q, both[:n, 4:8], both[2:, 4:8], both[1:n + 1, 3:7], both[1:n + 1, 5:9], both[1:n + 1, 1:5],
+                both[:n, 7:11], both[2:, 1:5]):
+        with pytest.raises(b2b.B2BError) as e:
+            plan.run(q, k, v, ints([0, n]), out=out)
+        assert e.value.code == ALIAS
+
+
+def test_overlaps_by_their_elements():
+    """Outputs and queries anywhere in one buffer: refused where an element is in both, run where rows an equal stride
+    apart have none in common."""
+    import random
+    r, n, hq, d = random.Random(0), 5, 2, 8
+    plan = b2b.PromptAttentionPlan("f16", hq, 1, d)
+    k, v, cu = normal(2, n, 1, d), normal(3, n, 1, d), ints([0, n])
+    buffer, at = normal(6, 60 * d), torch.arange(60 * d)
+    seen = {True: 0, False: 0}
+    for _ in range(300):
+        step = [r.choice([2, 3, 4, 5, 6]) for _ in range(2)]
+        if r.random() < 0.7:
+            step[1] = step[0]
+        where = [(r.randrange(60 - (n - 1) * s - hq), s) for s in step]
+        out, q = (buffer.as_strided((n, hq, d), (s * d, d, 1), o * d) for o, s in where)
+        both = set.intersection(*(set(at.as_strided((n, hq, d), (s * d, d, 1), o * d).flatten().tolist()) for o, s in where))
+        if both:
+            with pytest.raises(b2b.B2BError) as e:
+                plan.run(q, k, v, cu, out=out)
+            assert e.value.code == ALIAS
+        elif step[0] == step[1]:
+            want = want_prompt(q.clone(), k, v, [n], [n], True, None, "f16")
+            want.check(plan.run(q, k, v, cu, out=out))
+        seen[bool(both)] += 1
+    assert min(seen.values()) > 50
