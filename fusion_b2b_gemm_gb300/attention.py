@@ -185,6 +185,19 @@ class _AttentionPlan:
             need = self._workspace_sizes[sizes] = n.value
         return (torch.empty(need, dtype=torch.uint8, device=q.device) if need else None), need
 
+    def _kept(self, stream, done, given):
+        """Results of a run on `stream`, which is told of the tensors it uses: their memory may belong to another stream,
+        and is not handed out anew before `stream` is done with it, even if the caller lets go of them at once.  The
+        caller's stream likewise of the results made on `stream`."""
+        current = torch.cuda.current_stream(self.device_index)
+        if current != stream:
+            for t in given:
+                if t is not None:
+                    t.record_stream(stream)
+            for t in done if isinstance(done, tuple) else (done,):
+                t.record_stream(current)
+        return done
+
     def _stream(self):
         return _raw_stream(self.device_index) or None
 
@@ -229,7 +242,8 @@ class PromptAttentionPlan(_AttentionPlan):
         """
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.run(q, k, v, cu_q, cu_k, causal, out, lse, return_lse)
+                done = self.run(q, k, v, cu_q, cu_k, causal, out, lse, return_lse)
+            return self._kept(stream, done, (q, k, v, cu_q, cu_k, out, lse))
         if out is None and lse is None:
             done = _binding.prompt(self._bound, _raw_stream(self.device_index), q, k, v, cu_q, cu_k, causal, return_lse)
             if done is not None:
@@ -275,7 +289,8 @@ class SharedPrefixAttentionPlan(_AttentionPlan):
         """
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.run(q, prefix_k, prefix_v, cache_k, cache_v, lengths, page_table, out, lse, return_lse)
+                done = self.run(q, prefix_k, prefix_v, cache_k, cache_v, lengths, page_table, out, lse, return_lse)
+            return self._kept(stream, done, (q, prefix_k, prefix_v, cache_k, cache_v, lengths, page_table, out, lse))
         if out is None and lse is None:
             done = _binding.shared(self._bound, _raw_stream(self.device_index), q, prefix_k, prefix_v, cache_k, cache_v,
                                    lengths, page_table, return_lse)

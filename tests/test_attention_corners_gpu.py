@@ -3,6 +3,7 @@
 Inputs, results in 64 bits and their tolerances are those of test_attention_gpu.py.
 """
 import ctypes
+import math
 
 import pytest
 import torch
@@ -261,3 +262,54 @@ def test_overlaps_by_their_elements():
             want.check(plan.run(q, k, v, cu, out=out))
         seen[bool(both)] += 1
     assert min(seen.values()) > 50
+
+
+# --------------------------------------------------------------------- streams
+@pytest.mark.parametrize("given", [False, True])
+def test_inputs_freed_after_a_call_on_another_stream(given):
+    """Memory of a call's inputs is not handed out anew before the call's stream has read it."""
+    q, k, v, cu = normal(1, 4000, 4, 64), normal(2, 4000, 2, 64), normal(3, 4000, 2, 64), ints([0, 4000])
+    cache, lengths = normal(4, 4000, 16, 2, 64), ints([16] * 4000)
+    prompt, shared = b2b.PromptAttentionPlan("f16", 4, 2, 64), b2b.SharedPrefixAttentionPlan("f16", 4, 2, 64)
+    side, busy = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    for plan, args in ((prompt, (q, k, v, cu)), (shared, (q, k, v, cache, cache, lengths))):
+        want = plan.run(*args)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(40):
+                busy @ busy  # some tens of milliseconds
+        kw = {"out": torch.empty_like(q)} if given else {}
+        copies = [x.clone() for x in args]
+        side.wait_stream(torch.cuda.current_stream())
+        out = plan.run(*copies, stream=side, **kw)
+        del copies
+        for x in args:  # what the allocator hands out now
+            y = torch.empty_like(x)
+            y.fill_(math.nan if x.is_floating_point() else 0)
+            del y
+        fresh = [torch.empty_like(x).fill_(math.nan if x.is_floating_point() else 0) for x in args]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del fresh
+        assert plan.status() == 0
+
+
+def test_another_stream_within_a_capture():
+    q, k, v, cu = normal(1, 300, 4, 64), normal(2, 300, 2, 64), normal(3, 300, 2, 64), ints([0, 120, 300])
+    plan, side = b2b.PromptAttentionPlan("f16", 4, 2, 64), torch.cuda.Stream()
+    want = plan.run(q, k, v, cu)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        inside = q * 1
+        side.wait_stream(torch.cuda.current_stream())
+        first = plan.run(inside, k, v, cu, stream=side)
+        del inside
+        torch.cuda.current_stream().wait_stream(side)
+        second = plan.run(q, k, v, cu)
+    for _ in range(3):
+        first.zero_(), second.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, want) and torch.equal(second, want)
+    assert plan.status() == 0
