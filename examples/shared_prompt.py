@@ -76,8 +76,9 @@ def answer(layer, prompt, answers, steps):
         outputs.append(shared_plan.run(nq, k, v, pages_k, pages_v, lengths, page_table=table))
         token = layer.next_token(outputs[-1])
     for plan in (prompt_plan, shared_plan):
-        if plan.status() != 0:
-            raise RuntimeError(f"device status {plan.status()}")
+        status = plan.status()  # (cleared by reading it)
+        if status != 0:
+            raise RuntimeError(f"device status {status}")
     return torch.stack(tokens, 1), torch.stack(outputs, 1)
 
 

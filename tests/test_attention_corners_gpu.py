@@ -313,3 +313,17 @@ def test_another_stream_within_a_capture():
         torch.cuda.synchronize()
         assert torch.equal(first, want) and torch.equal(second, want)
     assert plan.status() == 0
+
+
+def test_the_example_tells_the_status_that_it_saw(monkeypatch):
+    """Reading the status clears it."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "shared_prompt.py")
+    spec = importlib.util.spec_from_file_location("shared_prompt_status", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    answers = iter([TIMEOUT])
+    monkeypatch.setattr(b2b.PromptAttentionPlan, "status", lambda self: next(answers, 0))
+    with pytest.raises(RuntimeError, match=f"status {TIMEOUT}"):
+        example.main(["--prompt", "50", "--answers", "2", "--tokens", "3"])
