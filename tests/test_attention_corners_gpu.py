@@ -315,6 +315,20 @@ def test_another_stream_within_a_capture():
     assert plan.status() == 0
 
 
+def test_rows_outside_every_sequence_are_left_alone_where_parts_are_joined():
+    q, k, v = normal(1, 9, 4, 64), normal(2, 6000, 2, 64), normal(3, 6000, 2, 64)
+    plan = b2b.PromptAttentionPlan("f16", 4, 2, 64)
+    n = ctypes.c_size_t()
+    assert b2b.b2b_prompt_attention_workspace(plan._h, 2, 9, 6000, 1, ctypes.byref(n)) == 0 and n.value > 0
+    out, lse = torch.full_like(q, 5.0), torch.full((9, 4), 5.0, device="cuda")
+    plan.run(q, k, v, ints([3, 5, 6]), ints([10, 3000, 5990]), out=out, lse=lse)
+    assert plan.status() == 0
+    for t in (out, lse):
+        assert (t[:3] == 5).all() and (t[6:] == 5).all()
+    want = want_prompt(q[3:6], k[10:5990], v[10:5990], [2, 1], [2990, 2990], True, None, "f16")
+    want.check(out[3:6], lse[3:6])
+
+
 def test_the_example_tells_the_status_that_it_saw(monkeypatch):
     """Reading the status clears it."""
     import importlib.util
