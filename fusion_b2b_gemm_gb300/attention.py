@@ -4,8 +4,9 @@ The cascade softmax(scale * Q K^T + mask) V in one kernel, for grouped heads
 (``include/b2b.h``, section "attention"): :class:`PromptAttentionPlan` for
 whole prompts of different lengths, :class:`SharedPrefixAttentionPlan` for the
 new tokens of a batch of requests that share one long prefix.  A plan holds
-the head layout; a run takes tensors of any length, with any strides whose
-last one is 1.  Inference only: inputs that require a gradient are refused
+the head layout; a run takes tensors of any length on 16-byte boundaries, with
+any positive strides that are multiples of 8 elements, the last one 1 (a stride
+of 0, as of keys expanded over heads, is refused).  Inference only: inputs that require a gradient are refused
 where gradients are recorded.  There is no CPU path.
 """
 from __future__ import annotations
@@ -238,6 +239,8 @@ class PromptAttentionPlan(_AttentionPlan):
         head_dim]; ``cu_q``, ``cu_k`` int32 [sequences + 1] on the GPU, the
         offsets of each sequence's rows (``cu_k`` defaults to ``cu_q``).  With
         ``causal`` row i of a sequence sees keys j <= i + (keys - queries).
+        Rows of no sequence are not computed: they stay as they are in a given
+        ``out`` and are unset in a new one.
         Returns ``out``, or ``(out, lse)`` when ``lse`` is given or asked for.
         """
         if stream is not None:

@@ -1,9 +1,9 @@
 // The common call of an attention plan's run(), from torch's tensors to the C
 // ABI (include/b2b.h): checks, output and workspace, launch.  In Python these
 // take longer than the kernels of a small call (a prompt of 19 tokens: 11.1 us
-// a call in Python, 5.6 here; the kernel takes 5.1).  Whatever is not as the call wants it makes a function
-// here return None, and attention.py, which does the same in Python, finds out
-// what and says it.
+// a call in Python, 5.6 here; the kernel takes 5.1).  Whatever is not as the
+// call wants it makes a function here return None, and attention.py, which does
+// the same in Python, finds out what and says it.
 #include <Python.h>
 
 #include <torch/csrc/autograd/python_variable.h>

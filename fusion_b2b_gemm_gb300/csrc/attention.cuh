@@ -41,13 +41,14 @@
 //   warps 12-15     epilogue of both streams, beside the next item's softmax
 // Every wait is bounded, as in the chain kernels.
 //
-// What bounds it (one GB300, a call among others): long 128-wide prompts the
-// tensor pipe under the power cap (8192 tokens, 32/8 heads, bf16: 352 us, 1.56
-// PFLOP/s, pipe 72 % busy); long 64-wide ones the softmax's chain from scores
-// to P (12001 tokens, 16/4 heads, fp16: 277 us, 1.07 PFLOP/s); batches on a
-// long prefix memory (32 requests on 65,521 keys: 58 us, 5.5 TB/s; 200 requests
-// with keys of their own: 143 us, 5.8 TB/s); short prompts the latencies of an
-// item (24 prompts of 1-700 tokens: 55 us against 26 at the measured rates).
+// What bounds it (on a GB300, a call among others): long 128-wide prompts the
+// tensor pipe under the power cap (8192 tokens, 32/8 heads, bf16: 352-364 us on
+// several GPUs, 1.51-1.56 PFLOP/s, pipe 72 % busy); long 64-wide ones the
+// softmax's chain from scores to P (12001 tokens, 16/4 heads, fp16: 276-282 us,
+// 1.05-1.07 PFLOP/s); batches on a long prefix memory (32 requests on 65,521
+// keys: 58 us, 5.5 TB/s; 200 requests with keys of their own: 144 us, 5.8
+// TB/s); short prompts the latencies of an item (24 prompts of 1-700 tokens:
+// 55 us against 26 at the measured rates).
 #pragma once
 
 #include <cuda.h>

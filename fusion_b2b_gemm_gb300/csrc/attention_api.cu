@@ -112,8 +112,9 @@ b2b_status_t encode_kv(CUtensorMap* map, const b2b_attn_plan_s* p, const b2b_att
 
 // ---------------------------------------------------------------- shapes
 // How work is cut into items is chosen by a model of the time, in units of a
-// key tile of a pair item (about 1.45 us for 128-wide heads): a tile of a solo
-// item takes 0.55, an item's beginning and end 1.2 more (traces of both).
+// key tile of a pair item (about 1.45 us for 128-wide heads; 64-wide ones, whose
+// tiles take some 1.2 us, are counted in the same units): a tile of a solo item
+// takes 0.55, an item's beginning and end 1.2 more (traces of both).
 constexpr double kSoloTile = 0.55, kItemCost = 1.2;
 
 // Joining parts: a second launch and memory latencies, some 4.5 us, and the
@@ -132,8 +133,11 @@ struct PromptShape {
 // Few rows over many keys are cut along the keys, and blocks that would fill
 // the GPU's SMs a little more than a whole number of times are halved (six
 // pieces of 200-256 tokens over 1000-6000 keys, 28/4 heads of 128: 172 items
-// of two tiles 76 us, 320 of one tile 65 us; 16 passages of 100-512 tokens, 12
-// heads of 96, the other way round, 22.0 against 22.9 us).
+// of two tiles 76 us, 320 of one tile 66 us; 24 prompts of 1-700 tokens keep
+// two, 55 us against 61).  Between two and four rounds of the SMs the model
+// counts whole ones, which short items of different lengths do not take: 16
+// passages of 100-512 tokens, 12 heads of 96, get one tile (22.6 us) and would
+// be quicker with two (21.5 us).
 PromptShape prompt_shape(const b2b_attn_plan_s* p, int64_t batch, int64_t tokens, int64_t key_rows, bool causal) {
   PromptShape best = {2, 1, 0};
   double best_t = 1e300;
