@@ -6,8 +6,9 @@ whole prompts of different lengths, :class:`SharedPrefixAttentionPlan` for the
 new tokens of a batch of requests that share one long prefix.  A plan holds
 the head layout; a run takes tensors of any length on 16-byte boundaries, with
 any positive strides that are multiples of 8 elements, the last one 1 (a stride
-of 0, as of keys expanded over heads, is refused).  Inference only: inputs that require a gradient are refused
-where gradients are recorded.  There is no CPU path.
+of 0, as of keys expanded over heads, is refused).  Inference only: inputs that
+require a gradient are refused where gradients are recorded.  There is no CPU
+path.
 """
 from __future__ import annotations
 
