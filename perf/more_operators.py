@@ -170,6 +170,11 @@ def prepare(case, seed):
 
 
 # -------------------------------------------------------------- plain forms
+def _power(e):
+    """2^e for -126 <= e <= 127, by its bits."""
+    return ((e.int() + 127) << 23).view(torch.float32)
+
+
 def _quantized(x):
     """Values on the e4m3 grid (in x's type) and the power-of-two scale of each 128 of a row."""
     rows, k = x.shape
@@ -178,9 +183,9 @@ def _quantized(x):
     padded[:, :k] = x
     tiles = padded.view(rows, kb, BLOCK)
     m, e = torch.frexp(tiles.abs().amax(2))  # m * 2^e, m in [1/2, 1); 448 = 7/8 * 2^9
-    scale = torch.ldexp(torch.ones_like(m), (e - 9 + (m > 0.875)).clamp(min=-126))
+    scale = _power((e - 9 + (m > 0.875)).clamp(min=-126))
     q = (tiles / scale[..., None]).to(E4M3).to(x.dtype)
-    return q.view(rows, kb * BLOCK)[:, :k], scale.float()
+    return q.view(rows, kb * BLOCK)[:, :k], scale
 
 
 def _widened(q, scale, rows_of_block, dtype=torch.float32):
@@ -249,7 +254,7 @@ def run(s):
 # ---------------------------------------------------------------- in 64 bits
 def _grid(v):
     """v rounded to the nearest e4m3 value, ties to even: steps of 2^-9 up to 2^-6, then of an eighth of the power below."""
-    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    step = _power(torch.frexp(v.abs().clamp(min=2.0 ** -6))[1] - 4).double()
     return torch.round(v / step) * step
 
 
@@ -258,7 +263,8 @@ def _exact_quantized(x):
     for k in range(0, x.shape[1], BLOCK):
         part = x[:, k:k + BLOCK]
         top = part.abs().amax(1, keepdim=True)
-        scale = torch.exp2(torch.ceil(torch.log2(top.clamp(min=448 * 2.0 ** -126) / 448)))
+        m, e = torch.frexp(top.clamp(min=448 * 2.0 ** -126) / 448)
+        scale = _power(e - (m == 0.5).int()).double()
         out[:, k:k + BLOCK] = _grid(part / scale) * scale
     return out
 
