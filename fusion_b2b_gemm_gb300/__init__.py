@@ -7,8 +7,11 @@ this module raises on import, telling how to build it.
 
 Low-level functions carry the C names (``b2b_plan_create``, ``b2b_run``,
 ...); :class:`Plan`, :class:`ChainPlan` and :class:`GemmPlan` wrap them for
-torch tensors, and :class:`PromptAttentionPlan` and
-:class:`SharedPrefixAttentionPlan` (``attention.py``) the attention operators.
+torch tensors, :class:`PromptAttentionPlan` and
+:class:`SharedPrefixAttentionPlan` (``attention.py``) the attention operators,
+:class:`GatedFeedForwardPlan`, :class:`ScaledFeedForwardPlan`,
+:class:`ScaledGemmPlan` and :func:`quantize_blocks` (``feedforward.py``) the
+feed-forward ones.
 """
 from __future__ import annotations
 
@@ -27,6 +30,10 @@ __all__ = [
     "b2b_attn_plan_device_status", "b2b_attn_plan_set_wait_budget", "b2b_attn_plan_set_debug",
     "b2b_prompt_attention_workspace", "b2b_prompt_attention_run", "b2b_shared_attention_workspace",
     "b2b_shared_attention_run",
+    "GatedFeedForwardPlan", "ScaledFeedForwardPlan", "ScaledGemmPlan", "quantize_blocks", "b2b_ffn_plan_create",
+    "b2b_scaled_ffn_plan_create", "b2b_scaled_gemm_plan_create", "b2b_ffn_plan_destroy", "b2b_ffn_plan_device_status",
+    "b2b_ffn_plan_set_wait_budget", "b2b_ffn_plan_set_debug", "b2b_ffn_workspace", "b2b_ffn_forward", "b2b_ffn_backward",
+    "b2b_scaled_ffn_run", "b2b_scaled_gemm_run", "b2b_quantize_blocks",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -86,6 +93,19 @@ def _load() -> ctypes.CDLL:
         "b2b_prompt_attention_run": [P, P, P],
         "b2b_shared_attention_workspace": [P, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
         "b2b_shared_attention_run": [P, P, P],
+        "b2b_ffn_plan_create": [ctypes.POINTER(P), i32, i64, i64, i64, i32],
+        "b2b_scaled_ffn_plan_create": [ctypes.POINTER(P), i32, i64, i64, i64, i32],
+        "b2b_scaled_gemm_plan_create": [ctypes.POINTER(P), i32, i64, i64],
+        "b2b_ffn_plan_destroy": [P],
+        "b2b_ffn_plan_device_status": [P, P],
+        "b2b_ffn_plan_set_wait_budget": [P, u64],
+        "b2b_ffn_plan_set_debug": [P, ctypes.c_uint32],
+        "b2b_ffn_workspace": [P, i64, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "b2b_ffn_forward": [P, P, P],
+        "b2b_ffn_backward": [P, P, P],
+        "b2b_scaled_ffn_run": [P, P, P],
+        "b2b_scaled_gemm_run": [P, P, P],
+        "b2b_quantize_blocks": [i32, i64, i64, i32, P, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -125,6 +145,19 @@ b2b_prompt_attention_workspace = _lib.b2b_prompt_attention_workspace
 b2b_prompt_attention_run = _lib.b2b_prompt_attention_run
 b2b_shared_attention_workspace = _lib.b2b_shared_attention_workspace
 b2b_shared_attention_run = _lib.b2b_shared_attention_run
+b2b_ffn_plan_create = _lib.b2b_ffn_plan_create
+b2b_scaled_ffn_plan_create = _lib.b2b_scaled_ffn_plan_create
+b2b_scaled_gemm_plan_create = _lib.b2b_scaled_gemm_plan_create
+b2b_ffn_plan_destroy = _lib.b2b_ffn_plan_destroy
+b2b_ffn_plan_device_status = _lib.b2b_ffn_plan_device_status
+b2b_ffn_plan_set_wait_budget = _lib.b2b_ffn_plan_set_wait_budget
+b2b_ffn_plan_set_debug = _lib.b2b_ffn_plan_set_debug
+b2b_ffn_workspace = _lib.b2b_ffn_workspace
+b2b_ffn_forward = _lib.b2b_ffn_forward
+b2b_ffn_backward = _lib.b2b_ffn_backward
+b2b_scaled_ffn_run = _lib.b2b_scaled_ffn_run
+b2b_scaled_gemm_run = _lib.b2b_scaled_gemm_run
+b2b_quantize_blocks = _lib.b2b_quantize_blocks
 
 
 def _check(code: int, where: str) -> None:
@@ -523,3 +556,4 @@ def probe_f64_rearrange(cfrag):
 
 
 from .attention import PromptAttentionPlan, SharedPrefixAttentionPlan  # noqa: E402  (uses the names above)
+from .feedforward import GatedFeedForwardPlan, ScaledFeedForwardPlan, ScaledGemmPlan, quantize_blocks  # noqa: E402

@@ -1,0 +1,859 @@
+// GEMMs of the feed-forward operators on pairs of SMs (tcgen05, cta_group::2,
+// sm_103a), each with the step that follows it in its epilogue:
+//
+//   kEpiStore      D = A.B
+//   kEpiAdd        D += A.B                       (fp32 D)
+//   kEpiGate       H = act(A.Bg) * (A.Bu)         (and, kept for the backward pass, A.Bg and A.Bu)
+//   kEpiGateGrad   dU = (A.B) act(G), dG = (A.B) U act'(G)
+//   kEpiGateQuant  as kEpiGate, brought to e4m3 with a scale for each 128 of a row
+//
+// act(g) = g s(u(g)), s(u) = 1 / (1 + e^-u), u = g (silu) or 2 sqrt(2/pi) (g +
+// 0.044715 g^3) (gelu, tanh form: (1 + tanh z) / 2 = s(2 z)), and act'(g) =
+// s + g s (1 - s) u'(g).
+//
+// A pair of CTAs computes a tile of 256 rows by 256 columns: each CTA holds 128
+// rows of A and of the accumulator, and half of B's columns.  In kEpiGate the
+// even CTA's half are 128 columns of Bg, the odd CTA's the same columns of Bu,
+// so one accumulator row has the gate in its first 128 columns and the other
+// projection in its last 128: both products with one read of A, and the epilogue
+// finds a pair of values in one thread.  16-bit operands are read as stored,
+// K-major or MN-major (AMN, BMN); 64 of them, or 128 e4m3 values, are a 128-byte
+// K panel, the ring's unit.  Tensor memory holds two accumulators, so that a
+// tile's epilogue runs beside the next tile's MMAs.
+//
+// e4m3 operands carry a scale for each 128 of k: every K panel's product is an
+// accumulator of its own, which the epilogue's warps multiply by its scales and
+// add up in registers in fp32 (128 columns of a row for each thread) while the
+// next panel's MMAs run.
+//
+// Work units.  A unit is a tile, or, of the last tiles, which would fill the
+// SMs a fraction of a time only, a range of the tile's K panels: such a unit
+// writes its accumulator as one part in fp32, and gemm_combine_kernel adds
+// the parts of a tile in a fixed order and takes the epilogue's step.
+//
+// Roles (384 threads, one CTA per SM, persistent over units):
+//   warp 0      TMA loads of this CTA's half of each panel
+//   warp 1      the even CTA's elected thread issues the MMAs
+//   warp 2      tensor-memory allocation
+//   warps 4-11  epilogue, two warps for each quadrant of 32 rows: columns [0, 128)
+//               and [128, 256), or the halves of the gate's and the other projection's 128
+// Every wait is bounded, as in the chain kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cstdint>
+
+#include "chain_tc.cuh"
+#include "ptx.cuh"
+
+namespace b2b {
+
+constexpr int kGemmThreads = 384;
+constexpr int kGemmTile = 256;     // rows and columns of a pair's tile
+constexpr int kGemmRing = 6;       // panels in flight
+constexpr int kGemmSlot = 2 * kPanelBytes;  // a panel of A and one of B, 128 rows or columns of 128 bytes each
+constexpr int kGemmStage = 4096;   // output box of a warp: 32 rows of 128 bytes
+constexpr int kGemmOffStage = kGemmRing * kGemmSlot;
+constexpr int kGemmOffTop = kGemmOffStage;  // kEpiGateQuant (no boxes): [2][2][128] largest magnitudes
+constexpr int kGemmOffBar = kGemmOffStage + 8 * kGemmStage;
+constexpr int kGemmSmem = kGemmOffBar + 256 + 1024;  // (the ring begins on a 1024-byte boundary)
+static_assert(kGemmSmem <= 232448, "shared memory of a CTA");
+// e4m3: registers of an epilogue thread and of another; 168 of each thread at launch, shared out anew
+constexpr int kGemmEpilogueRegs = 224, kGemmOtherRegs = 56;
+static_assert(256 * kGemmEpilogueRegs + 128 * kGemmOtherRegs <= 168 * kGemmThreads, "register file");
+constexpr int kGemmPartFloats = 2 * 128 * kGemmTile;  // a unit's part, both CTAs
+constexpr int kGemmMaxProblems = 3;
+
+enum : int { kGemmF16 = 0, kGemmBF16 = 1, kGemmE4M3 = 2 };  // operands (outputs: the first two)
+enum : int { kEpiStore = 0, kEpiAdd = 1, kEpiGate = 2, kEpiGateGrad = 3, kEpiGateQuant = 4 };
+
+enum : int {  // barrier slots (8 bytes each)
+  kGBFull = 0,       // [8] panel landed in both CTAs (even CTA's)
+  kGBEmpty = 8,      // [8] panel read
+  kGBAccFull = 16,   // [2] accumulator complete
+  kGBAccEmpty = 18,  // [2] accumulator read in both CTAs (even CTA's)
+  kGBDrain = 20,
+  kGBTop = 21,       // [4] both warps of a quadrant have written their rows' largest magnitudes
+  kGSlotTmem = 25,   // uint32 tensor-memory base, then the int abort flag
+};
+
+// One product of a launch: D [M][N].  Tiles are numbered problem after problem.
+struct GemmProblem {
+  int first;             // first tile
+  int m_tiles, n_tiles;  // of 256 rows; of 256 columns (gate: of 128)
+  int M, N;
+};
+
+struct GemmParams {
+  GemmProblem prob[kGemmMaxProblems];
+  int problems;
+  int tiles, whole;   // in all; computed as one unit each
+  int splits;         // units of each of the others
+  int units;
+  int kpan;           // K panels of a product (all segments)
+  int kseg;           // K panels of the first segment (then A and B go on in the second maps)
+  int a_box_rows;     // rows of A's boxes (fewer than 128 for few rows: the others are never looked at)
+  int group;          // 256-row tiles that share a pass over the columns
+  int act;            // activation: 0 silu, 1 gelu
+  int keep;           // kEpiGate: store gate and up as well
+  // kEpiGateGrad: rows of the gate's and the other projection's values
+  const void* gate;
+  const void* up;
+  long long gate_ld, up_ld;
+  // e4m3: scales of A's rows and of B's blocks of 128 columns ([0]; [1]: the other projection's)
+  const float* a_scale;
+  long long a_scale_row, a_scale_k;
+  const float* b_scale[2];
+  long long b_scale_row[2], b_scale_k[2];
+  // kEpiGateQuant: values and scales (scale of row r and block b at q_scale[b * q_scale_ld + r])
+  uint8_t* q;
+  long long q_ld;
+  float* q_scale;
+  long long q_scale_ld;
+  // parts, and the outputs as gemm_combine_kernel writes them
+  float* part;
+  void* out[kGemmMaxProblems];
+  long long out_ld[kGemmMaxProblems];
+  uint32_t debug;     // bit 0: arm the first panel but never fill it
+  int* status;
+  uint32_t budget_ns;
+};
+
+struct GemmMaps {
+  CUtensorMap a[kGemmMaxProblems], b[kGemmMaxProblems], out[kGemmMaxProblems];
+};
+
+struct GemmUnit {
+  int prob, mt, nt;
+  int k0, k1;   // K panels
+  int part;     // number of its part, or -1
+};
+
+// Rows of the tiles go fastest within groups of p.group row tiles, so that the
+// units that run side by side share few panels of A and of B.
+__host__ __device__ __forceinline__ void gemm_tile(const GemmParams& p, int t, GemmUnit& c) {
+  c.prob = 0;
+  while (c.prob + 1 < p.problems && t >= p.prob[c.prob + 1].first) ++c.prob;
+  const GemmProblem& q = p.prob[c.prob];
+  t -= q.first;
+  const int per_group = p.group * q.n_tiles;
+  const int g = t / per_group, rem = t - g * per_group;
+  const int left = q.m_tiles - g * p.group, rows = left < p.group ? left : p.group;
+  c.nt = rem / rows;
+  c.mt = g * p.group + rem - c.nt * rows;
+}
+__host__ __device__ __forceinline__ GemmUnit gemm_unit(const GemmParams& p, int u) {
+  GemmUnit c;
+  c.k0 = 0;
+  c.k1 = p.kpan;
+  c.part = -1;
+  int t = u;
+  if (u >= p.whole) {
+    c.part = u - p.whole;
+    const int i = c.part / p.splits, j = c.part - i * p.splits;
+    t = p.whole + i;
+    c.k0 = static_cast<int>(static_cast<long long>(p.kpan) * j / p.splits);
+    c.k1 = static_cast<int>(static_cast<long long>(p.kpan) * (j + 1) / p.splits);
+  }
+  gemm_tile(p, t, c);
+  return c;
+}
+// Element (row of the pair's tile, column) of a part: groups of four columns,
+// then rows, so that the 32 rows of a warp are consecutive.
+__host__ __device__ __forceinline__ long long gemm_part_at(int part, int row, int col4) {
+  return ((static_cast<long long>(part) * 2 + (row >> 7)) * (kGemmTile / 4) + col4) * 512 + (row & 127) * 4;
+}
+
+namespace gemm {
+
+// As ptx::BoundedWait with a 32-bit clock; the status word is written once at the end.
+struct Wait {
+  volatile int* abort_flag;
+  uint32_t budget_ns;
+  __device__ __forceinline__ static uint32_t now() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+  }
+  // By one thread.
+  __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity) const {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint32_t t0 = now();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+      if (*abort_flag) return false;
+      if (now() - t0 >= budget_ns) *abort_flag = 1;
+    }
+    return true;
+  }
+  // By a whole warp: every lane gets the same answer.
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, wait1(bar, parity));
+  }
+};
+
+__device__ __forceinline__ float sigmoid(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
+constexpr float kGelu = 1.5957691216057308f, kGelu3 = 0.044715f;  // 2 sqrt(2 / pi)
+
+// act(g)
+__device__ __forceinline__ float activation(int act, float g) {
+  const float u = act ? kGelu * (g + kGelu3 * g * g * g) : g;
+  return g * sigmoid(u);
+}
+// act(g) and its slope.  Far out s (1 - s) is 0, times a slope of u that has to stay finite.
+__device__ __forceinline__ void activation_slope(int act, float g, float& a, float& slope) {
+  const float s = sigmoid(act ? kGelu * (g + kGelu3 * g * g * g) : g);
+  const float du = act ? kGelu * (1.0f + 3.0f * kGelu3 * fminf(g * g, 1e30f)) : 1.0f;
+  a = g * s;
+  slope = s + a * (1.0f - s) * du;
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  return T == kGemmF16 ? ptx::pack_f16x2(__float_as_uint(lo), __float_as_uint(hi))
+                       : ptx::pack_bf16x2(__float_as_uint(lo), __float_as_uint(hi));
+}
+template <int T>
+__device__ __forceinline__ void unpack16(uint32_t w, float& lo, float& hi) {
+  if constexpr (T == kGemmF16) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(w));
+  } else {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+  }
+}
+
+// Scale of a block whose largest magnitude has the bits `top`, and its inverse:
+// the smallest power of two that leaves nothing above 448 = 1.75 * 2^8, at least
+// 2^-126.  A power of two, so that scaling rounds nothing.  A block that holds an
+// infinity or a NaN gets NaN as its scale, and with it as each of its values.
+__device__ __forceinline__ float block_scale(uint32_t top, float& inverse) {
+  if (top >= 0x7f800000u) {
+    inverse = __uint_as_float(0x7fffffffu);
+    return inverse;
+  }
+  int e = static_cast<int>(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(e, 1);
+  inverse = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+  return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+// Four values to e4m3, round to nearest even, the first in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// One warp's boxes on their way out: 32 rows of 128 bytes, swizzled.
+struct Stage {
+  uint32_t addr;
+  int lane;
+  // The box before has been read.
+  __device__ __forceinline__ void ready() const {
+    if (lane == 0) ptx::bulk_wait_read<0>();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void store(const CUtensorMap* m, int col, int row, bool inside) const {
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && inside) {
+      ptx::tma_store_2d(m, addr, col, row);
+      ptx::bulk_commit();
+    }
+  }
+  __device__ __forceinline__ void add(const CUtensorMap* m, int col, int row, bool inside) const {
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && inside) {
+      ptx::tma_add_2d(m, addr, col, row);
+      ptx::bulk_commit();
+    }
+  }
+  // 32 packed 16-bit pairs: the row's 64 columns
+  __device__ __forceinline__ void put(const uint32_t (&w)[32]) const {
+    const uint32_t sw = static_cast<uint32_t>(lane & 7), row = addr + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+    for (uint32_t u = 0; u < 8; ++u)
+      ptx::st_shared_v4(row + ((u ^ sw) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  }
+};
+
+}  // namespace gemm
+
+template <int IN, bool AMN, bool BMN, int EPI, int OUT>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams p) {
+  using namespace ptx;
+  constexpr bool F8 = IN == kGemmE4M3;
+  constexpr bool GATE = EPI == kEpiGate || EPI == kEpiGateQuant;
+  constexpr int CK = F8 ? 128 : 64;  // K elements of a panel
+  static_assert(!F8 || (!AMN && !BMN && (EPI == kEpiStore || EPI == kEpiGateQuant)), "e4m3 operands are K-major");
+  static_assert(F8 || (EPI != kEpiGateQuant && OUT == IN), "16-bit operands and outputs have one type");
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bar0 = base + kGemmOffBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kGemmOffBar + 8 * kGSlotTmem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool leader = rank == 0;
+  const int cid = static_cast<int>(blockIdx.x >> 1), ncl = static_cast<int>(gridDim.x >> 1);
+
+  if (warp == 0) {
+    if (lane < 8) {
+      mbar_init(bar(kGBFull + lane), 1);
+      mbar_init(bar(kGBEmpty + lane), 1);
+    } else if (lane < 10) {
+      mbar_init(bar(kGBAccFull + lane - 8), 1);
+      mbar_init(bar(kGBAccEmpty + lane - 8), 16);  // epilogue warps of both CTAs
+    } else if (lane == 10) {
+      mbar_init(bar(kGBDrain), 1);
+      *abort_flag = 0;
+    } else if (lane < 15) {
+      mbar_init(bar(kGBTop + lane - 11), 2);
+    }
+    fence_barrier_init();
+  } else if (warp == 2) {
+    tmem_alloc<2>(smem_u32(tmem_slot), 512);
+    tmem_relinquish<2>();
+  } else if (warp == 3 && lane == 0) {
+    prefetch_tmap(&maps.a[0]);
+    prefetch_tmap(&maps.b[0]);
+    if (EPI != kEpiGateQuant) prefetch_tmap(&maps.out[0]);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  const gemm::Wait bw{abort_flag, p.budget_ns};
+
+  if (warp < 4) {
+    if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGemmOtherRegs));
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ loads
+      uint32_t slot = 0, phase = 0;
+      unsigned long long issued = 0;
+      bool ok = true;
+      const uint32_t a_bytes = AMN ? kPanelBytes : static_cast<uint32_t>(p.a_box_rows) * 128u;
+      for (int u = cid; u < p.units && ok; u += ncl) {
+        const GemmUnit c = gemm_unit(p, u);
+        const GemmProblem& q = p.prob[c.prob];
+        const int m0 = c.mt * kGemmTile + rank * 128;
+        const int n0 = GATE ? c.nt * 128 : c.nt * kGemmTile + rank * 128;
+        // halves past the last row or column are not loaded: what the MMAs make of
+        // the panel's old contents is never looked at
+        const bool a_odd = c.mt * kGemmTile + 128 < q.M, b_odd = GATE || c.nt * kGemmTile + 128 < q.N;
+        const bool has_a = leader || a_odd, has_b = leader || b_odd;
+        const uint32_t bytes = a_bytes * (a_odd ? 2u : 1u) + static_cast<uint32_t>(kPanelBytes) * (b_odd ? 2u : 1u);
+        for (int k = c.k0; k < c.k1; ++k) {
+          ok = bw.wait1(bar(kGBEmpty + slot), phase ^ 1u);
+          if (!ok) break;
+          const uint32_t full = mapa_shared(bar(kGBFull + slot), 0);
+          // The even CTA arms its barrier for both CTAs' copies; the odd CTA's
+          // may land first (the count then dips below zero, which is allowed).
+          if (leader) mbar_arrive_expect_tx(bar(kGBFull + slot), bytes);
+          const int seg = k >= p.kseg ? 1 : 0, kc = (k - (seg ? p.kseg : 0)) * CK;
+          const CUtensorMap* ma = &maps.a[c.prob + seg];
+          const CUtensorMap* mb = &maps.b[c.prob + seg + (GATE ? rank : 0)];
+          const uint32_t sa = base + slot * static_cast<uint32_t>(kGemmSlot), sb = sa + kPanelBytes;
+          if (!((p.debug & 1u) && issued == 0)) {  // (test support: the first panel is armed but never filled)
+            if (has_a) {
+              if constexpr (AMN) {
+                tma_load_2d_pair(sa, ma, full, m0, kc);
+                tma_load_2d_pair(sa + kPanelBytes / 2, ma, full, m0 + 64, kc);
+              } else {
+                tma_load_2d_pair(sa, ma, full, kc, m0);
+              }
+            }
+            if (has_b) {
+              if constexpr (BMN) {
+                tma_load_2d_pair(sb, mb, full, n0, kc);
+                tma_load_2d_pair(sb + kPanelBytes / 2, mb, full, n0 + 64, kc);
+              } else {
+                tma_load_2d_pair(sb, mb, full, kc, n0);
+              }
+            }
+          }
+          ++issued;
+          if (++slot == kGemmRing) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Copies in flight land before exit (the even CTA's barriers count both CTAs').
+      const unsigned long long tail = !leader ? 0 : (issued < kGemmRing ? issued : kGemmRing);
+      for (unsigned long long j = 0; j < tail; ++j) {
+        const unsigned long long idx = issued - 1 - j;
+        drain_wait(bar(kGBFull + static_cast<int>(idx % kGemmRing)), static_cast<uint32_t>((idx / kGemmRing) & 1u),
+                   p.budget_ns);
+      }
+    } else if (warp == 1 && leader) {
+      // ------------------------------------------------------------- MMAs
+      if (elect_one()) {
+        constexpr uint32_t kFmt = IN == kGemmBF16 ? 1u : 0u;  // (0: f16, or e4m3 of the 8-bit kind)
+        constexpr uint32_t idesc = make_idesc(kFmt, 256, 256, BMN) | (AMN ? 1u << 15 : 0u);
+        // a K step (16 elements, 32 bytes) along a row, or 16 rows of 128 bytes
+        constexpr uint32_t a_step = AMN ? 128 : 2, b_step = BMN ? 128 : 2;
+        const uint64_t a0 = desc_sw128(base, AMN ? kPanelBytes / 2 : 16u, 1024u);
+        const uint64_t b0 = desc_sw128(base + kPanelBytes, BMN ? kPanelBytes / 2 : 16u, 1024u);
+        uint32_t slot = 0, phase = 0, acc = 0, acc_phase = 0;
+        bool ok = true;
+        for (int u = cid; u < p.units && ok; u += ncl) {
+          const GemmUnit c = gemm_unit(p, u);
+          for (int k = c.k0; k < c.k1; ++k) {
+            if (F8 || k == c.k0) {
+              ok = bw.wait1(bar(kGBAccEmpty + acc), acc_phase ^ 1u);
+              if (!ok) break;
+            }
+            ok = bw.wait1(bar(kGBFull + slot), phase);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem_base + acc * 256u;
+            const uint64_t a = a0 + slot * (kGemmSlot / 16), b = b0 + slot * (kGemmSlot / 16);
+#pragma unroll
+            for (uint32_t s = 0; s < 4; ++s) {
+              const uint32_t more = s || (!F8 && k != c.k0) ? 1u : 0u;
+              if constexpr (F8)
+                mma_ss_f8_pair(d, a + s * a_step, b + s * b_step, idesc, more);
+              else
+                mma_ss<false, 2>(d, a + s * a_step, b + s * b_step, idesc, more);
+            }
+            tc_commit<2>(bar(kGBEmpty + slot));
+            if (++slot == kGemmRing) {
+              slot = 0;
+              phase ^= 1u;
+            }
+            if (F8 || k + 1 == c.k1) {
+              tc_commit<2>(bar(kGBAccFull + acc));
+              acc ^= 1u;
+              if (acc == 0) acc_phase ^= 1u;
+            }
+          }
+        }
+        tc_commit<2>(bar(kGBDrain));
+        drain_wait(bar(kGBDrain), 0, p.budget_ns);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGemmEpilogueRegs));
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int row = quad * 32 + lane;  // of this CTA's 128
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    const gemm::Stage stage{base + kGemmOffStage + static_cast<uint32_t>(warp - 4) * kGemmStage, lane};
+    const uint32_t empty0 = mapa_shared(bar(kGBAccEmpty), 0);
+    auto release = [&](uint32_t acc) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(empty0 + 8u * acc);
+    };
+    // first column, in the accumulator, of this warp's 32-column chunk i of four
+    auto column = [&](int i) -> int { return GATE ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * 128 + i * 32; };
+    uint32_t acc = 0, acc_phase = 0, tops = 0;
+    bool ok = true;
+    for (int u = cid; u < p.units && ok; u += ncl) {
+      const GemmUnit c = gemm_unit(p, u);
+      const GemmProblem& q = p.prob[c.prob];
+      const int m0 = c.mt * kGemmTile + rank * 128;
+      const int mw = m0 + quad * 32;  // this warp's first row
+      const bool rows = mw < q.M;     // it has some
+      float* part = c.part < 0 ? nullptr : p.part + gemm_part_at(c.part, rank * 128 + row, 0);
+      const bool mine = m0 + row < q.M;
+      if constexpr (F8) {
+        // Scales of this thread's row and of the columns' block(s), four panels ahead of their use.
+        const float* sa = p.a_scale + (mine ? m0 + row : 0) * p.a_scale_row;
+        const int nb = GATE ? c.nt : 2 * c.nt + half;
+        const float* s0 = p.b_scale[0] + (nb * 128 < q.N ? nb : 0) * p.b_scale_row[0];
+        const float* s1 = GATE ? p.b_scale[1] + c.nt * p.b_scale_row[1] : nullptr;
+        uint64_t sum[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) sum[i] = 0;
+        float f0[4], f1[4];
+        auto fetch = [&](int j, int k) {
+          if (k < c.k1) {
+            const float a = __ldg(sa + k * p.a_scale_k);
+            f0[j] = a * __ldg(s0 + k * p.b_scale_k[0]);
+            if constexpr (GATE) f1[j] = a * __ldg(s1 + k * p.b_scale_k[1]);
+          }
+        };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fetch(j, c.k0 + j);
+        for (int k0 = c.k0; k0 < c.k1 && ok; k0 += 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (k0 + j < c.k1 && ok) {
+              ok = bw.wait(bar(kGBAccFull + acc), acc_phase);
+              if (ok) {
+                tc_fence_after();
+                if (rows) {
+                  const uint64_t g = gemm::pack2(f0[j], f0[j]), h = GATE ? gemm::pack2(f1[j], f1[j]) : g;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    uint32_t v[32];
+                    tmem_ld32(lanes + acc * 256u + static_cast<uint32_t>(column(i)), v);
+                    tmem_wait_ld();
+                    if (i == 3) release(acc);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                      sum[i * 16 + e] = gemm::fma2(gemm::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                                                   i < 2 ? g : h, sum[i * 16 + e]);
+                  }
+                } else {
+                  release(acc);
+                }
+                acc ^= 1u;
+                if (acc == 0) acc_phase ^= 1u;
+                fetch(j, k0 + j + 4);
+              }
+            }
+          }
+        }
+        if (!ok) break;
+        if (part) {
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float4 v;
+                gemm::unpack2(sum[i * 16 + 2 * e], v.x, v.y);
+                gemm::unpack2(sum[i * 16 + 2 * e + 1], v.z, v.w);
+                *reinterpret_cast<float4*>(part + (column(i) / 4 + e) * 512) = v;
+              }
+          }
+        } else if constexpr (EPI == kEpiStore) {
+          if (rows) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                float x, y;
+                gemm::unpack2(sum[b * 32 + e], x, y);
+                w[e] = gemm::pack16<OUT>(x, y);
+              }
+              stage.ready();
+              stage.put(w);
+              const int col = c.nt * kGemmTile + half * 128 + b * 64;
+              stage.store(&maps.out[0], col, mw, col < q.N);
+            }
+          }
+        } else {
+          // h of 64 columns, the row's largest magnitude over both warps' halves, values and scale
+          float h[64];
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float g0, g1, u0, u1;
+            gemm::unpack2(sum[e], g0, g1);
+            gemm::unpack2(sum[32 + e], u0, u1);
+            h[2 * e] = gemm::activation(p.act, g0) * u0;
+            h[2 * e + 1] = gemm::activation(p.act, g1) * u1;
+            top = max(top, max(__float_as_uint(h[2 * e]) & 0x7fffffffu, __float_as_uint(h[2 * e + 1]) & 0x7fffffffu));
+          }
+          volatile uint32_t* tops_row = reinterpret_cast<volatile uint32_t*>(gbase + kGemmOffTop) + (tops & 1u) * 256u + row;
+          tops_row[half * 128] = top;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kGBTop + quad));
+          ok = bw.wait(bar(kGBTop + quad), tops & 1u);
+          if (!ok) break;
+          top = max(top, tops_row[(half ^ 1) * 128]);
+          ++tops;
+          float inv;
+          const float scale = gemm::block_scale(top, inv);
+          if (mine) {
+            const int col = c.nt * 128 + half * 64;
+            uint8_t* dst = p.q + (m0 + row) * p.q_ld + col;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 w;
+              w.x = gemm::pack_e4m3(h[16 * e] * inv, h[16 * e + 1] * inv, h[16 * e + 2] * inv, h[16 * e + 3] * inv);
+              w.y = gemm::pack_e4m3(h[16 * e + 4] * inv, h[16 * e + 5] * inv, h[16 * e + 6] * inv, h[16 * e + 7] * inv);
+              w.z = gemm::pack_e4m3(h[16 * e + 8] * inv, h[16 * e + 9] * inv, h[16 * e + 10] * inv, h[16 * e + 11] * inv);
+              w.w = gemm::pack_e4m3(h[16 * e + 12] * inv, h[16 * e + 13] * inv, h[16 * e + 14] * inv, h[16 * e + 15] * inv);
+              if (col + 16 * e < q.N) *reinterpret_cast<uint4*>(dst + 16 * e) = w;
+            }
+            if (half == 0) p.q_scale[c.nt * p.q_scale_ld + m0 + row] = scale;
+          }
+        }
+      } else {
+        ok = bw.wait(bar(kGBAccFull + acc), acc_phase);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t src = lanes + acc * 256u;
+        if (!rows) {
+          release(acc);
+        } else if (part) {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[32];
+            tmem_ld32(src + static_cast<uint32_t>(column(i)), v);
+            tmem_wait_ld();
+            if (i == 3) release(acc);
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(part + (column(i) / 4 + e) * 512) =
+                    make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+          }
+        } else if constexpr (EPI == kEpiStore) {
+#pragma unroll 1
+          for (int b = 0; b < 2; ++b) {
+            uint32_t v0[32], v1[32];
+            tmem_ld32(src + static_cast<uint32_t>(half * 128 + b * 64), v0);
+            tmem_ld32(src + static_cast<uint32_t>(half * 128 + b * 64 + 32), v1);
+            tmem_wait_ld();
+            if (b == 1) release(acc);
+            stage.ready();
+            store_output_row<OUT == kGemmF16 ? kOutF16 : kOutBF16>(stage.addr, lane, 0, v0);
+            store_output_row<OUT == kGemmF16 ? kOutF16 : kOutBF16>(stage.addr, lane, 32, v1);
+            const int col = c.nt * kGemmTile + half * 128 + b * 64;
+            stage.store(&maps.out[c.prob], col, mw, col < q.N);
+          }
+        } else if constexpr (EPI == kEpiAdd) {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[32];
+            tmem_ld32(src + static_cast<uint32_t>(column(i)), v);
+            tmem_wait_ld();
+            if (i == 3) release(acc);
+            stage.ready();
+            store_output_row<kOutF32>(stage.addr, lane, 0, v);
+            const int col = c.nt * kGemmTile + column(i);
+            stage.add(&maps.out[c.prob], col, mw, col < q.N);
+          }
+        } else if constexpr (EPI == kEpiGate) {
+          const int col = c.nt * 128 + half * 64;
+          const bool inside = col < q.N;
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t g[32], v[32];
+            tmem_ld32(src + static_cast<uint32_t>(column(i)), g);
+            tmem_ld32(src + static_cast<uint32_t>(column(i + 2)), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[i * 16 + e] = gemm::pack16<OUT>(
+                  gemm::activation(p.act, __uint_as_float(g[2 * e])) * __uint_as_float(v[2 * e]),
+                  gemm::activation(p.act, __uint_as_float(g[2 * e + 1])) * __uint_as_float(v[2 * e + 1]));
+          }
+          if (!p.keep) release(acc);
+          stage.ready();
+          stage.put(w);
+          stage.store(&maps.out[0], col, mw, inside);
+          if (p.keep) {
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+              uint32_t v0[32], v1[32];
+              tmem_ld32(src + static_cast<uint32_t>(column(2 * b)), v0);
+              tmem_ld32(src + static_cast<uint32_t>(column(2 * b + 1)), v1);
+              tmem_wait_ld();
+              if (b == 1) release(acc);
+              stage.ready();
+              store_output_row<OUT == kGemmF16 ? kOutF16 : kOutBF16>(stage.addr, lane, 0, v0);
+              store_output_row<OUT == kGemmF16 ? kOutF16 : kOutBF16>(stage.addr, lane, 32, v1);
+              stage.store(&maps.out[1 + b], col, mw, inside);
+            }
+          }
+        } else {
+          const int row0 = mine ? m0 + row : 0;
+          const uint16_t* gate = static_cast<const uint16_t*>(p.gate) + row0 * p.gate_ld;
+          const uint16_t* up = static_cast<const uint16_t*>(p.up) + row0 * p.up_ld;
+#pragma unroll 1
+          for (int b = 0; b < 2; ++b) {
+            const int col = c.nt * kGemmTile + half * 128 + b * 64;
+            uint32_t dg[32], du[32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t v[32];
+              tmem_ld32(src + static_cast<uint32_t>(half * 128 + b * 64 + i * 32), v);
+              uint4 g4[4], u4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int at = col + i * 32 + e * 8;
+                const bool in = mine && at < q.N;
+                g4[e] = in ? __ldg(reinterpret_cast<const uint4*>(gate + at)) : make_uint4(0, 0, 0, 0);
+                u4[e] = in ? __ldg(reinterpret_cast<const uint4*>(up + at)) : make_uint4(0, 0, 0, 0);
+              }
+              tmem_wait_ld();
+              if (b == 1 && i == 1) release(acc);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t gw = (&g4[e >> 2].x)[e & 3], uw = (&u4[e >> 2].x)[e & 3];
+                float g0, g1, u0, u1, a0, a1, s0, s1;
+                gemm::unpack16<IN>(gw, g0, g1);
+                gemm::unpack16<IN>(uw, u0, u1);
+                gemm::activation_slope(p.act, g0, a0, s0);
+                gemm::activation_slope(p.act, g1, a1, s1);
+                const float d0 = __uint_as_float(v[2 * e]), d1 = __uint_as_float(v[2 * e + 1]);
+                dg[i * 16 + e] = gemm::pack16<OUT>(d0 * u0 * s0, d1 * u1 * s1);
+                du[i * 16 + e] = gemm::pack16<OUT>(d0 * a0, d1 * a1);
+              }
+            }
+            stage.ready();
+            stage.put(dg);
+            stage.store(&maps.out[0], col, mw, col < q.N);
+            stage.ready();
+            stage.put(du);
+            stage.store(&maps.out[1], col, mw, col < q.N);
+          }
+        }
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  __syncthreads();
+  // Neither CTA leaves, or frees tensor memory, while the other may still
+  // arrive on its barriers or the even CTA's MMAs may still write it.
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc<2>(tmem_base, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag && p.status) atomicCAS(p.status, 0, kTimeoutCode);
+}
+
+// Adds the parts of the tiles that were cut along k, in order, and takes the
+// epilogue's step.  blockIdx.x: 32 rows of such a tile; a warp takes 8 columns
+// (of both projections for the gate), a row to a lane.
+template <int EPI, int OUT>
+__global__ void __launch_bounds__(512) gemm_combine_kernel(const __grid_constant__ GemmParams p) {
+  constexpr bool GATE = EPI == kEpiGate || EPI == kEpiGateQuant;
+  __shared__ uint32_t tops[16][32];
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x >> 3, row = (blockIdx.x & 7) * 32 + lane;
+  GemmUnit c;
+  gemm_tile(p, p.whole + t, c);
+  const GemmProblem& q = p.prob[c.prob];
+  const int m = c.mt * kGemmTile + row;
+  if (c.mt * kGemmTile + (blockIdx.x & 7) * 32 >= q.M) return;
+  const bool mine = m < q.M;
+  // columns [8 col8, +8) of the tile, of both halves of it for the gate
+  const int col8 = GATE ? warp : blockIdx.y * 16 + warp;
+  float v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+  if (mine) {
+    for (int j = 0; j < p.splits; ++j) {
+#pragma unroll
+      for (int h = 0; h < (GATE ? 4 : 2); ++h) {
+        const int col4 = 2 * col8 + (h & 1) + (h >> 1) * 32;
+        const float4 x = *reinterpret_cast<const float4*>(p.part + gemm_part_at(t * p.splits + j, row, col4));
+        v[4 * h] += x.x;
+        v[4 * h + 1] += x.y;
+        v[4 * h + 2] += x.z;
+        v[4 * h + 3] += x.w;
+      }
+    }
+  }
+  const int col = c.nt * (GATE ? 128 : kGemmTile) + 8 * col8;
+  const bool in = mine && col < q.N;
+  auto store16 = [&](int o, const float* x) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[o]) + m * p.out_ld[o] + col) =
+        make_uint4(gemm::pack16<OUT>(x[0], x[1]), gemm::pack16<OUT>(x[2], x[3]), gemm::pack16<OUT>(x[4], x[5]),
+                   gemm::pack16<OUT>(x[6], x[7]));
+  };
+  if constexpr (EPI == kEpiStore) {
+    if (in) store16(c.prob, v);
+  } else if constexpr (EPI == kEpiAdd) {
+    if (in) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out[c.prob]) + m * p.out_ld[c.prob] + col);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float4 x = dst[h];
+        x.x += v[4 * h];
+        x.y += v[4 * h + 1];
+        x.z += v[4 * h + 2];
+        x.w += v[4 * h + 3];
+        dst[h] = x;
+      }
+    }
+  } else if constexpr (EPI == kEpiGateGrad) {
+    if (in) {
+      const uint4 gw = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.gate) + m * p.gate_ld + col));
+      const uint4 uw = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.up) + m * p.up_ld + col));
+      float dg[8], du[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float g[2], w[2];
+        gemm::unpack16<OUT>((&gw.x)[e], g[0], g[1]);
+        gemm::unpack16<OUT>((&uw.x)[e], w[0], w[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float a, s;
+          gemm::activation_slope(p.act, g[k], a, s);
+          dg[2 * e + k] = v[2 * e + k] * w[k] * s;
+          du[2 * e + k] = v[2 * e + k] * a;
+        }
+      }
+      store16(0, dg);
+      store16(1, du);
+    }
+  } else {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = gemm::activation(p.act, v[e]) * v[8 + e];
+    if constexpr (EPI == kEpiGate) {
+      if (in) {
+        store16(0, h);
+        if (p.keep) {
+          store16(1, v);
+          store16(2, v + 8);
+        }
+      }
+    } else {
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(h[e]) & 0x7fffffffu);
+      tops[warp][lane] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < 16; ++w) top = max(top, tops[w][lane]);
+      float inv;
+      const float scale = gemm::block_scale(top, inv);
+      if (in)
+        *reinterpret_cast<uint2*>(p.q + m * p.q_ld + col) =
+            make_uint2(gemm::pack_e4m3(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv),
+                       gemm::pack_e4m3(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv));
+      if (warp == 0 && mine) p.q_scale[c.nt * p.q_scale_ld + m] = scale;
+    }
+  }
+}
+
+}  // namespace b2b

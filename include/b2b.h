@@ -447,6 +447,159 @@ b2b_status_t b2b_shared_attention_workspace(b2b_attn_plan_t plan, int64_t batch,
                                             int64_t room, size_t* bytes);
 b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t plan, const b2b_shared_attention_t* run, b2b_stream_t stream);
 
+/* --------------------------------------------------------- feed-forward
+ * The gated feed-forward block, a cascade with an activation and a product of
+ * two projections between its GEMMs (no counterpart in the patent):
+ *
+ *   H = act(X.Wg) * (X.Wu)      Y = H.Wd
+ *
+ * act(g) = g / (1 + exp(-u)), u = g (B2B_SILU) or 2 sqrt(2/pi) (g + 0.044715 g^3)
+ * (B2B_GELU_TANH: gelu in its tanh form).  Both projections, the activation and
+ * the product are one kernel; X is read once for both.
+ *
+ * Three kinds of plans, which share b2b_ffn_workspace, _destroy, _device_status,
+ * _set_wait_budget and _set_debug:
+ *   b2b_ffn_plan_create          16-bit operands; with the backward pass
+ *   b2b_scaled_ffn_plan_create   e4m3 operands with a scale for each block of 128
+ *   b2b_scaled_gemm_plan_create  one product of such operands
+ *
+ *   - Products are accumulated in fp32; activations and their slopes are fp32
+ *     functions of fp32 sums (in the backward pass: of the kept 16-bit values).
+ *     Intermediates that a GEMM reads are rounded to its operand type, results
+ *     once to theirs.
+ *   - Where few tiles would leave SMs idle, products are cut along k and the
+ *     parts joined in fp32 in a fixed order: equal inputs give equal bits.
+ *   - A plan is not modified by a run: runs on several streams may overlap, each
+ *     with a workspace of its own.
+ *   - A run that gives up a bounded wait reports B2B_ERR_TIMEOUT in the status
+ *     word; what its outputs hold is undefined.
+ */
+typedef struct b2b_ffn_plan_s* b2b_ffn_plan_t;
+typedef enum { B2B_SILU = 0, B2B_GELU_TANH = 1 } b2b_activation_t;
+
+/* Rows of consecutive elements: element (r, c) lies at data + r * row_stride + c.
+ * The stride is in elements, at least the columns, a multiple of 16 bytes; that
+ * of a single row is not read.  data must be 16-byte aligned. */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+} b2b_matrix_t;
+/* Scales of the blocks of a matrix, fp32: that of row (or block of 128 rows) r
+ * and block b of 128 columns lies at data[r * row_stride + b * block_stride].
+ * Strides in elements, not negative. */
+typedef struct {
+  float* data;
+  int64_t row_stride, block_stride;
+} b2b_scales_t;
+
+/*
+ * Create a plan for the block with weights Wg, Wu [width][hidden] and Wd
+ * [hidden][out_width], each read as stored.
+ *   dtype   B2B_F16 or B2B_BF16, of every matrix but fp32 weight gradients.
+ *   width, hidden, out_width   multiples of 8, at most 2^20.
+ * Binds to the current CUDA device (an sm_103 GPU) and allocates a 4-byte
+ * status word.
+ */
+b2b_status_t b2b_ffn_plan_create(b2b_ffn_plan_t* out, b2b_dtype_t dtype, int64_t width, int64_t hidden,
+                                 int64_t out_width, b2b_activation_t activation);
+/* With e4m3 weights as [columns][k], Wg and Wu [hidden][width], Wd
+ * [out_width][hidden], each with scales of its blocks of 128 x 128; dtype
+ * (B2B_F16 or B2B_BF16) is that of X and Y.  Extents are multiples of 16. */
+b2b_status_t b2b_scaled_ffn_plan_create(b2b_ffn_plan_t* out, b2b_dtype_t dtype, int64_t width, int64_t hidden,
+                                        int64_t out_width, b2b_activation_t activation);
+/* D [rows][n] = A.B^T of e4m3 matrices A [rows][k] and B [n][k]; dtype (B2B_F16
+ * or B2B_BF16) is that of D.  k is a multiple of 16, n of 8, at most 2^20. */
+b2b_status_t b2b_scaled_gemm_plan_create(b2b_ffn_plan_t* out, b2b_dtype_t dtype, int64_t k, int64_t n);
+b2b_status_t b2b_ffn_plan_destroy(b2b_ffn_plan_t plan);
+/* As b2b_plan_device_status, b2b_plan_set_wait_budget (budgets above 4 s count
+ * as 4 s, and one shorter than 5 us for each 64 of a product's k (128 for
+ * e4m3) as that), b2b_plan_set_debug. */
+b2b_status_t b2b_ffn_plan_device_status(b2b_ffn_plan_t plan, b2b_stream_t stream);
+b2b_status_t b2b_ffn_plan_set_wait_budget(b2b_ffn_plan_t plan, uint64_t budget_ns);
+b2b_status_t b2b_ffn_plan_set_debug(b2b_ffn_plan_t plan, uint32_t flags);
+
+/* Bytes of workspace of one run on `rows` tokens or rows: device memory for this
+ * run alone until it has finished, 256-byte aligned, of any contents.  pass is
+ * one of these (B2B_FFN_INFERENCE for the scaled plans). */
+#define B2B_FFN_INFERENCE 0 /* b2b_ffn_forward that keeps nothing */
+#define B2B_FFN_TRAINING 1  /* b2b_ffn_forward that keeps gate, up and hidden */
+#define B2B_FFN_BACKWARD 2
+b2b_status_t b2b_ffn_workspace(b2b_ffn_plan_t plan, int64_t rows, int pass, size_t* bytes);
+
+/*
+ * Y of `tokens` rows of X.
+ *   gate, up, hidden   NULL data, or [tokens][hidden] matrices that receive X.Wg,
+ *                      X.Wu and H, rounded to the plan's type, for the backward
+ *                      pass: all three or none.
+ * Outputs must overlap neither inputs nor each other.
+ */
+typedef struct {
+  int64_t tokens;
+  b2b_matrix_t x, w_gate, w_up, w_down, out;
+  b2b_matrix_t gate, up, hidden;
+  void* workspace;
+  size_t workspace_bytes;
+} b2b_ffn_forward_t;
+b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t plan, const b2b_ffn_forward_t* run, b2b_stream_t stream);
+
+/*
+ * Gradients of the block for dy, the gradient of its Y:
+ *   dU = dH * act(G), dG = dH * U * act'(G), with dH = dY.Wd^T;
+ *   dX = dG.Wg^T + dU.Wu^T; dWg = X^T.dG; dWu = X^T.dU; dWd = H^T.dY.
+ *   x, weights, gate, up, hidden   what the forward pass read and kept.
+ *   accumulate   0: weight gradients in the plan's type.  Else fp32 matrices to
+ *                which they are added.
+ * dx, and any of the weight gradients, may have NULL data: not computed.  dG and
+ * dU are rounded to the plan's type.
+ */
+typedef struct {
+  int64_t tokens, accumulate;
+  b2b_matrix_t dy, x, w_gate, w_up, w_down, gate, up, hidden;
+  b2b_matrix_t dx, dw_gate, dw_up, dw_down;
+  void* workspace;
+  size_t workspace_bytes;
+} b2b_ffn_backward_t;
+b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t plan, const b2b_ffn_backward_t* run, b2b_stream_t stream);
+
+/*
+ * The block with e4m3 weights.  X and H are brought to e4m3 as
+ * b2b_quantize_blocks does, for each 128 columns of a row.
+ */
+typedef struct {
+  int64_t tokens;
+  b2b_matrix_t x, w_gate, w_up, w_down, out;
+  b2b_scales_t gate_scale, up_scale, down_scale;
+  void* workspace;
+  size_t workspace_bytes;
+} b2b_scaled_ffn_t;
+b2b_status_t b2b_scaled_ffn_run(b2b_ffn_plan_t plan, const b2b_scaled_ffn_t* run, b2b_stream_t stream);
+
+/*
+ * D[r][c] = sum over blocks b of 128 of k:  a_scale(r, b) b_scale(c / 128, b) sum_j a[r][j] b[c][j],
+ * the inner sums and the outer one in fp32.  A NaN among a block's values or in
+ * its scale makes the results that it takes part in NaN.
+ */
+typedef struct {
+  int64_t rows;
+  b2b_matrix_t a, b, out;
+  b2b_scales_t a_scale, b_scale; /* of rows; of blocks of 128 rows */
+  void* workspace;
+  size_t workspace_bytes;
+} b2b_scaled_gemm_t;
+b2b_status_t b2b_scaled_gemm_run(b2b_ffn_plan_t plan, const b2b_scaled_gemm_t* run, b2b_stream_t stream);
+
+/*
+ * Bring a 16-bit matrix x [rows][cols] (dtype B2B_F16 or B2B_BF16, cols a
+ * multiple of 8) to e4m3 with a scale for each block of block_rows (1 or 128) by
+ * 128: the smallest power of two that leaves no magnitude above 448 (at least
+ * 2^-126), so that scaling itself rounds nothing; values are rounded to nearest
+ * even.  A block that holds an infinity or a NaN gets NaN as its scale and in
+ * each value.  q's rows lie on 8-byte boundaries.  Works on the current device;
+ * asynchronous on `stream`, without waits.
+ */
+b2b_status_t b2b_quantize_blocks(b2b_dtype_t dtype, int64_t rows, int64_t cols, int block_rows, const b2b_matrix_t* x,
+                                 const b2b_matrix_t* q, const b2b_scales_t* scale, b2b_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
