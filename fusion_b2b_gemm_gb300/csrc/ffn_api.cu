@@ -233,6 +233,51 @@ struct Launch {
   }
 };
 
+// A product for few rows in the making.
+struct FewRows {
+  const b2b_ffn_plan_s* plan;
+  const SkinnyKernels& k;
+  bool e4m3;
+  SkinnyMaps maps;
+  SkinnyParams p;
+  b2b_status_t st = B2B_OK;
+
+  FewRows(const b2b_ffn_plan_s* plan_, const SkinnyKernels& k_, bool e4m3_, const Matrix& x) : plan(plan_), k(k_), e4m3(e4m3_) {
+    std::memset(&p, 0, sizeof(p));
+    p.rows = static_cast<int>(x.rows);
+    p.slots = static_cast<int>(ceil_div(x.cols, k.depth));
+    p.x_box_rows = static_cast<int>((x.rows + 7) & ~int64_t(7));
+    p.act = plan->act;
+    p.debug = plan->debug;
+    p.status = plan->d_status;
+    st = encode(&maps.x, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(plan), x, e4m3 ? 128 : 64, static_cast<uint32_t>(p.x_box_rows));
+  }
+  // 16 bits [k][columns], e4m3 [columns][k]
+  void weight(int i, const Matrix& w) {
+    if (st != B2B_OK) return;
+    p.N = static_cast<int>(e4m3 ? w.rows : w.cols);
+    st = e4m3 ? encode(&maps.w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w, 128, 128)
+              : encode(&maps.w[i], type16(plan), w, 64, 64);
+  }
+  b2b_status_t run(cudaStream_t stream) {
+    if (st != B2B_OK) return st;
+    int size = 0;
+    while (p.rows > 16 << size) ++size;
+    const int slices = static_cast<int>(ceil_div(p.N, k.columns)), room = 2 * plan->sms;
+    // As many CTAs as are resident at once, two slots each at least.
+    p.splits = 1;
+    while (p.splits < kSkinnyMaxSplits && 2 * p.splits * slices <= room && p.slots >= 4 * p.splits) p.splits *= 2;
+    p.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(plan->budget_ns, 5000ull * p.slots), 4000000000ull));
+    void* args[] = {&maps, &p};
+    if (launch_pdl(k.main[size], dim3(static_cast<unsigned>(slices * p.splits)), dim3(kSkinnyThreads), args, k.smem[size], stream, p.splits) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return B2B_ERR_CUDA;
+    }
+    return B2B_OK;
+  }
+};
+
 size_t part_bytes(const b2b_ffn_plan_s* p, int64_t tiles, int kpan) { return cut(tiles, kpan, p->sms / 2).part_bytes(); }
 constexpr int64_t kMaxTiles = int64_t(1) << 28;
 
@@ -245,11 +290,17 @@ struct Pieces {
   size_t total() const { return rounded(hidden) + rounded(second) + rounded(x_scale) + rounded(h_scale) + parts; }
 };
 
+// Up to so many rows the products of a plan (but the backward pass's) take the kernel for few rows.
+int few_rows(const b2b_ffn_plan_s* p) { return (p->kind == kFfn ? p->k.gate_few : p->s.gate_few).most_rows(); }
+
 Pieces pieces(const b2b_ffn_plan_s* p, int64_t rows, int pass) {
   Pieces w;
   const int64_t d = p->width, f = p->hidden, o = p->out_width;
   const size_t t = static_cast<size_t>(rows);
-  auto part = [&](int64_t tiles, int kpan) { w.parts = std::max(w.parts, part_bytes(p, tiles, kpan)); };
+  const bool few = rows <= few_rows(p) && pass != B2B_FFN_BACKWARD;
+  auto part = [&](int64_t tiles, int kpan) {
+    if (!few) w.parts = std::max(w.parts, part_bytes(p, tiles, kpan));
+  };
   if (p->kind == kScaledGemm) {
     part(tile_count(rows, o, false), panels(d, true));
   } else if (p->kind == kScaledFfn) {
@@ -303,6 +354,9 @@ b2b_status_t create(b2b_ffn_plan_t* out, FfnKind kind, b2b_dtype_t dtype, int64_
   const GemmKernel all[] = {p->k.gate, p->k.down, p->k.gate_grad, p->k.dx, p->k.dw, p->k.dw_add,
                             p->s.gate, p->s.product[0], p->s.product[1]};
   bool ok = true;
+  for (const SkinnyKernels& k : {p->k.gate_few, p->k.down_few, p->s.gate_few, p->s.product_few[0], p->s.product_few[1]})
+    for (int i = 0; i < k.sizes; ++i)
+      ok = ok && cudaFuncSetAttribute(k.main[i], cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem[i]) == cudaSuccess;
   for (const GemmKernel& k : all)
     ok = ok && cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem) == cudaSuccess;
   // The registers of the e4m3 kernels' roles (setmaxnreg) are drawn from what
@@ -324,6 +378,21 @@ b2b_status_t create(b2b_ffn_plan_t* out, FfnKind kind, b2b_dtype_t dtype, int64_
   }
   *out = p;
   return B2B_OK;
+}
+
+b2b_status_t scaled_few(const b2b_ffn_plan_s* p, const Matrix& a, const b2b_scales_t& a_scale, const Matrix& b, const b2b_scales_t& b_scale,
+                        const Matrix& out, cudaStream_t stream) {
+  FewRows l(p, p->s.product_few[p->dtype == B2B_BF16], true, a);
+  l.weight(0, b);
+  l.p.out = out.m->data;
+  l.p.out_ld = out.m->row_stride;
+  l.p.a_scale = a_scale.data;
+  l.p.a_scale_row = a_scale.row_stride;
+  l.p.a_scale_k = a_scale.block_stride;
+  l.p.b_scale[0] = b_scale.data;
+  l.p.b_scale_row[0] = b_scale.row_stride;
+  l.p.b_scale_k[0] = b_scale.block_stride;
+  return l.run(stream);
 }
 
 // The 16-bit quantiser's launch.
@@ -433,6 +502,25 @@ b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t p, const b2b_ffn_forward_t* r, b2b_s
   const b2b_matrix_t scratch = {ws, f};
   void* parts = ws + rounded(w.hidden);
   const Matrix h = keep ? out[3] : Matrix{&scratch, t, f, 2};
+  if (t <= few_rows(p)) {
+    FewRows up(p, p->k.gate_few, false, in[0]);
+    up.weight(0, in[1]);
+    up.weight(1, in[2]);
+    up.p.out = h.m->data;
+    up.p.out_ld = h.m->row_stride;
+    up.p.keep = keep;
+    up.p.gate = r->gate.data;
+    up.p.gate_ld = r->gate.row_stride;
+    up.p.up = r->up.data;
+    up.p.up_ld = r->up.row_stride;
+    st = up.run(stream);
+    if (st != B2B_OK) return st;
+    FewRows down(p, p->k.down_few, false, h);
+    down.weight(0, in[3]);
+    down.p.out = r->out.data;
+    down.p.out_ld = r->out.row_stride;
+    return down.run(stream);
+  }
   {
     Launch l(p, true, false);
     l.a_rows(0, in[0]);
@@ -555,6 +643,25 @@ b2b_status_t b2b_scaled_ffn_run(b2b_ffn_plan_t p, const b2b_scaled_ffn_t* r, b2b
   void* parts = hs + rounded(w.h_scale) / 4;
   st = quantize(p->k, t, d, 1, r->x, xq, {xs, 1, t}, stream);
   if (st != B2B_OK) return st;
+  if (t <= few_rows(p)) {
+    FewRows up(p, p->s.gate_few, true, {&xq, t, d, 1});
+    up.weight(0, in[1]);
+    up.weight(1, in[2]);
+    up.p.out = ws;
+    up.p.out_ld = f;
+    up.p.a_scale = xs;
+    up.p.a_scale_row = 1;
+    up.p.a_scale_k = t;
+    for (int i = 0; i < 2; ++i) {
+      up.p.b_scale[i] = scales[i]->data;
+      up.p.b_scale_row[i] = scales[i]->row_stride;
+      up.p.b_scale_k[i] = scales[i]->block_stride;
+    }
+    up.p.q_scale = hs;
+    up.p.q_scale_ld = t;
+    st = up.run(stream);
+    return st == B2B_OK ? scaled_few(p, {&hq, t, f, 1}, {hs, 1, t}, in[3], r->down_scale, out[0], stream) : st;
+  }
   {
     Launch l(p, true, true);
     l.a_rows(0, {&xq, t, d, 1});
@@ -607,6 +714,7 @@ b2b_status_t b2b_scaled_gemm_run(b2b_ffn_plan_t p, const b2b_scaled_gemm_t* r, b
   if (st == B2B_OK) st = check_workspace(r->workspace, r->workspace_bytes, w.total());
   if (st == B2B_OK) st = check_current_device(p);
   if (st != B2B_OK) return st;
+  if (m <= few_rows(p)) return scaled_few(p, in[0], r->a_scale, in[1], r->b_scale, out[0], reinterpret_cast<cudaStream_t>(stream_));
   Launch l(p, false, true);
   l.a_rows(0, in[0]);
   l.b_rows(0, in[1]);

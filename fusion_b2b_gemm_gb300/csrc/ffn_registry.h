@@ -3,6 +3,7 @@
 
 #include "gemm.cuh"
 #include "quantize.cuh"
+#include "skinny.cuh"
 
 namespace b2b {
 
@@ -18,6 +19,29 @@ GemmKernel gemm_kernel_pair() {
           reinterpret_cast<const void*>(&gemm_combine_kernel<EPI, OUT>)};
 }
 
+// The kernels for at most 16, 32, 64 and (16-bit operands) 128 rows.
+struct SkinnyKernels {
+  const void* main[4];
+  int smem[4], sizes, columns, depth;
+  int most_rows() const { return 8 << sizes; }
+};
+template <int IN, int OUT, bool GATE>
+SkinnyKernels skinny_kernels() {
+  constexpr bool F8 = IN == kGemmE4M3;
+  SkinnyKernels k = {{reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, GATE, 16>), reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, GATE, 32>),
+                      reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, GATE, 64>), nullptr},
+                     {SkinnyShape<F8, GATE, 16>::kBytes, SkinnyShape<F8, GATE, 32>::kBytes, SkinnyShape<F8, GATE, 64>::kBytes, 0},
+                     3,
+                     SkinnyShape<F8, GATE, 16>::kColumns,
+                     SkinnyShape<F8, GATE, 16>::kDepth};
+  if constexpr (!F8) {
+    k.main[3] = reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, GATE, 128>);
+    k.smem[3] = SkinnyShape<F8, GATE, 128>::kBytes;
+    k.sizes = 4;
+  }
+  return k;
+}
+
 // By operand type: the products of the block and of its backward pass.
 struct FfnKernels {
   GemmKernel gate;       // H = act(X.Wg) * (X.Wu)
@@ -26,6 +50,7 @@ struct FfnKernels {
   GemmKernel dx;         // dG.Wg^T + dU.Wu^T
   GemmKernel dw;         // X^T.dG, X^T.dU, H^T.dY
   GemmKernel dw_add;     // the same, added to fp32
+  SkinnyKernels gate_few, down_few;
   const void* quantize_rows;
   const void* quantize_tiles;
 };
@@ -38,6 +63,8 @@ FfnKernels ffn_kernels() {
           gemm_kernel_pair<T, false, false, kEpiStore, T>(),
           gemm_kernel_pair<T, true, true, kEpiStore, T>(),
           gemm_kernel_pair<T, true, true, kEpiAdd, T>(),
+          skinny_kernels<T, T, true>(),
+          skinny_kernels<T, T, false>(),
           reinterpret_cast<const void*>(&quantize_rows_kernel<T>),
           reinterpret_cast<const void*>(&quantize_tiles_kernel<T>)};
 }
@@ -48,6 +75,7 @@ FfnKernels ffn_kernels_bf16();
 struct ScaledKernels {
   GemmKernel gate;        // quantised H
   GemmKernel product[2];  // f16, bf16
+  SkinnyKernels gate_few, product_few[2];
 };
 ScaledKernels scaled_kernels();
 

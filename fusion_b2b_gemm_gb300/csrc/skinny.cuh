@@ -1,0 +1,393 @@
+// The feed-forward operators' products for few rows (16-bit operands: at most
+// 128, e4m3: 64): the weights' bytes are what they cost, so every weight is read
+// once, by many CTAs at a time, and nothing is written but the result.
+//
+// The product is taken transposed: the weights' columns are the 128 rows of
+// tcgen05.mma's A, the tokens the N columns of its B, so that a token more costs
+// 1/128 of the tile and not a tile's row of 256.  (The same with mma.sync, the
+// operands zipped in registers, was as quick up to 16 tokens, but its rate on
+// this GPU bounds it from there on: a block of 4096/14336/4096, bf16, 59, 77 and
+// 111 us for 16, 32 and 64 tokens, against 56, 58 and 61 us; the pair kernel,
+// whose tile of 256 rows is mostly empty, takes 72 us for one token, this one 54.)
+//
+// A CTA takes a slice of the columns and, where slices alone are too few to keep
+// the memory busy, a range of k; the CTAs of a slice are a cluster and add
+// their sums up through each other's shared memory in a fixed order, so there is
+// no second launch and no workspace.  TMA brings panels of the weight(s) and of
+// the rows into a ring; two CTAs share an SM, some 160 KB in flight.
+//
+//   16 bits: weights as stored, [k][column], an MN-major A of 128 columns by 64 k
+//            a slot; the gate takes 64 columns of either weight as the two halves
+//            of one A.  The sums stay in tensor memory to the end.
+//   e4m3:    weights [column][k], 128 columns (whole blocks of scales) by 128 k, of
+//            both weights for the gate.  Each slot's product is an accumulator of
+//            its own, multiplied by its scales and added up in registers.
+//
+// Warp 0 loads, warp 1 multiplies (one elected thread), warps 2-5 read tensor
+// memory.  Every wait is bounded.
+#pragma once
+
+#include "gemm.cuh"
+
+namespace b2b {
+
+constexpr int kSkinnyThreads = 192;
+constexpr int kSkinnyMaxSplits = 8;  // CTAs of a cluster
+
+struct SkinnyParams {
+  int rows, N;
+  int slots;          // panels of the whole of k
+  int splits;         // CTAs of a slice
+  int x_box_rows;
+  int act, keep;
+  void* out;          // h (or, e4m3 gate, its values), or the product
+  long long out_ld;
+  void* gate;         // kept
+  void* up;
+  long long gate_ld, up_ld;
+  const float* a_scale;
+  long long a_scale_row, a_scale_k;
+  const float* b_scale[2];
+  long long b_scale_row[2], b_scale_k[2];
+  float* q_scale;
+  long long q_scale_ld;
+  uint32_t debug;
+  int* status;
+  uint32_t budget_ns;
+};
+
+struct SkinnyMaps {
+  CUtensorMap x, w[2];
+};
+
+enum : int {  // barrier slots (8 bytes each)
+  kSBFull = 0,       // [8] slot landed
+  kSBEmpty = 8,      // [8] slot read
+  kSBAccFull = 16,   // [2] accumulator complete (16 bits: [0], all of k)
+  kSBAccEmpty = 18,  // [2] accumulator read
+  kSBDrain = 20,
+  kSSlotTmem = 21,   // uint32 tensor-memory base, then the int abort flag
+};
+
+template <bool F8, bool GATE, int NT>
+struct SkinnyShape {
+  static constexpr int kColumns = F8 || !GATE ? 128 : 64;  // of a slice
+  static constexpr int kDepth = F8 ? 128 : 64;             // k of a slot
+  static constexpr int kWeight = F8 && GATE ? 32768 : 16384;
+  static constexpr int kSlot = kWeight + NT * 128;
+  static constexpr int kRing = 104 * 1024 / kSlot;
+  static constexpr int kSumLd = GATE ? 2 * kColumns : kColumns;
+  static constexpr int kOffScales = kRing * kSlot;          // e4m3: [4 warps][2 weights][NT]
+  static constexpr int kOffBar = kOffScales + (F8 ? 4 * 2 * NT * 4 : 0);
+  static constexpr int kBytes = kOffBar + 256 + 1024;
+  // columns of tensor memory: an accumulator, or two (of both weights)
+  static constexpr int kTmemCols = F8 ? 2 * NT * (GATE ? 2 : 1) : (NT < 32 ? 32 : NT);
+  static_assert(kRing <= 8 && kRing >= 2 && NT * kSumLd * 4 <= kRing * kSlot, "the sums take the ring's place");
+  static_assert(2 * (kBytes + 1024) <= 233472 && 2 * kTmemCols <= 512, "two CTAs on an SM");
+};
+
+namespace skinny {
+
+// V consecutive floats of a CTA of the cluster
+template <int V>
+__device__ __forceinline__ void add_remote(float (&sum)[V], uint32_t addr) {
+  if constexpr (V == 2) {
+    float x, y;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(addr));
+    sum[0] += x;
+    sum[1] += y;
+  } else {
+    float x, y, z, w;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x), "=f"(y), "=f"(z), "=f"(w) : "r"(addr));
+    sum[0] += x;
+    sum[1] += y;
+    sum[2] += z;
+    sum[3] += w;
+  }
+}
+// C columns of this warp's lanes, C = 16 or 32
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[C]) {
+  if constexpr (C == 16)
+    ptx::tmem_ld16(addr, v);
+  else
+    ptx::tmem_ld32(addr, v);
+}
+
+}  // namespace skinny
+
+// IN: operands; OUT: 16-bit type of the result (not of the e4m3 gate, which is quantised).  NT: 16, 32, 64 or 128 tokens.
+template <int IN, int OUT, bool GATE, int NT>
+__global__ void __launch_bounds__(kSkinnyThreads, 2)
+    skinny_kernel(const __grid_constant__ SkinnyMaps maps, const __grid_constant__ SkinnyParams p) {
+  using namespace ptx;
+  constexpr bool F8 = IN == kGemmE4M3;
+  using L = SkinnyShape<F8, GATE, NT>;
+  constexpr int W = F8 && GATE ? 2 : 1;      // accumulators of a slot
+  constexpr int C = NT < 32 ? NT : 32;       // columns read at a time
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bar0 = base + L::kOffBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * kSSlotTmem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = static_cast<int>(blockIdx.x) % p.splits, col0 = static_cast<int>(blockIdx.x) / p.splits * L::kColumns;
+  const int s0 = static_cast<int>(static_cast<long long>(p.slots) * part / p.splits);
+  const int s1 = static_cast<int>(static_cast<long long>(p.slots) * (part + 1) / p.splits);
+  // 16 bits: columns of a row are consecutive, two blocks of 64 a slot; e4m3: k
+  auto weights = [&](int s, auto&& each) {
+    if constexpr (F8) {
+      each(0, &maps.w[0], s * 128, col0);
+      if constexpr (GATE) each(16384, &maps.w[1], s * 128, col0);
+    } else {
+      each(0, &maps.w[0], col0, s * 64);
+      each(8192, &maps.w[GATE ? 1 : 0], GATE ? col0 : col0 + 64, s * 64);
+    }
+  };
+  if (warp == 0) {
+    if (elect_one()) {
+      // The first slots into L2, before anything is waited for (a prefetch reads no value).
+      for (int s = s0; s < s1 && s < s0 + L::kRing; ++s)
+        weights(s, [&](int, const CUtensorMap* m, int x, int y) { tma_prefetch_l2_2d(m, x, y); });
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
+    tmem_relinquish();
+  } else if (warp == 2) {
+    if (lane < L::kRing) {
+      mbar_init(bar(kSBFull + lane), 1);
+      mbar_init(bar(kSBEmpty + lane), 1);
+    } else if (lane < 10 && lane >= 8) {
+      mbar_init(bar(kSBAccFull + lane - 8), 1);
+      mbar_init(bar(kSBAccEmpty + lane - 8), 4);
+    } else if (lane == 10) {
+      mbar_init(bar(kSBDrain), 1);
+      *abort_flag = 0;
+    }
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  // (after the allocation: a kernel that starts behind this one waits for it with
+  // tensor memory in hand, and must not hold what a CTA of this one still asks for)
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const gemm::Wait bw{abort_flag, p.budget_ns};
+  float* sum = reinterpret_cast<float*>(gbase);  // [token][column], in the ring's place
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t slot = 0, phase = 0;
+      int issued = 0;
+      const uint32_t bytes = L::kWeight + static_cast<uint32_t>(p.x_box_rows) * 128u;
+      for (int s = s0; s < s1; ++s) {
+        if (!bw.wait1(bar(kSBEmpty + slot), phase ^ 1u)) break;
+        const uint32_t full = bar(kSBFull + slot), dst = base + slot * static_cast<uint32_t>(L::kSlot);
+        mbar_arrive_expect_tx(full, bytes);
+        if (!((p.debug & 1u) && issued == 0)) {  // (test support: the first slot is armed but never filled)
+          weights(s, [&](int off, const CUtensorMap* m, int x, int y) { tma_load_2d(dst + off, m, full, x, y); });
+          tma_load_2d(dst + L::kWeight, &maps.x, full, s * L::kDepth, 0);
+        }
+        ++issued;
+        if (++slot == L::kRing) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+      // copies in flight land before exit
+      for (int j = 0; j < issued && j < L::kRing; ++j) {
+        const int i = issued - 1 - j;
+        drain_wait(bar(kSBFull + i % L::kRing), static_cast<uint32_t>(i / L::kRing) & 1u, p.budget_ns);
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      constexpr uint32_t kFmt = IN == kGemmBF16 ? 1u : 0u;
+      constexpr uint32_t idesc = make_idesc(kFmt, NT, 128, false) | (F8 ? 0u : 1u << 15);
+      constexpr uint32_t a_step = F8 ? 2 : 128;
+      uint32_t slot = 0, phase = 0, acc = 0, acc_phase = 0;
+      for (int s = s0; s < s1; ++s) {
+        if (F8 && !bw.wait1(bar(kSBAccEmpty + acc), acc_phase ^ 1u)) break;
+        if (!bw.wait1(bar(kSBFull + slot), phase)) break;
+        tc_fence_after();
+        const uint32_t src = base + slot * static_cast<uint32_t>(L::kSlot);
+        const uint64_t b = desc_sw128(src + L::kWeight, 16u, 1024u);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const uint64_t a = desc_sw128(src + w * 16384u, F8 ? 16u : 8192u, 1024u);
+          const uint32_t d = tmem_base + (F8 ? (acc * W + w) * NT : 0u);
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            if constexpr (F8)
+              mma_ss_f8(d, a + i * a_step, b + i * 2u, idesc, i ? 1u : 0u);
+            else
+              mma_ss<false>(d, a + i * a_step, b + i * 2u, idesc, i || s != s0 ? 1u : 0u);
+          }
+        }
+        tc_commit(bar(kSBEmpty + slot));
+        if (++slot == L::kRing) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        if (F8 || s + 1 == s1) {
+          tc_commit(bar(kSBAccFull + acc));
+          acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+      }
+      tc_commit(bar(kSBDrain));
+      drain_wait(bar(kSBDrain), 0, p.budget_ns);
+    }
+  } else {
+    const int quad = warp & 3;
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    const int column = quad * 32 + lane;  // of A's 128: of the slice, or of both weights' 64
+    bool ok = true;
+    if constexpr (!F8) {
+      ok = bw.wait(bar(kSBAccFull), 0);
+      tc_fence_after();
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < NT; c += C) {
+          if (c < p.rows) {
+            uint32_t v[C];
+            skinny::tmem_ld<C>(lanes + static_cast<uint32_t>(c), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < C; ++e) sum[(c + e) * L::kSumLd + column] = __uint_as_float(v[e]);
+          }
+        }
+      }
+    } else {
+      float acc_sum[W][NT];
+#pragma unroll
+      for (auto& a : acc_sum)
+#pragma unroll
+        for (float& x : a) x = 0.0f;
+      // Scales of the tokens times that of the weights' block, a slot ahead of their use.
+      constexpr int R = NT < 32 ? 1 : NT / 32;
+      float next[W][R];
+      const int nb = col0 / 128;
+      auto fetch = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int r = i * 32 + lane;
+          const float a = r < p.rows ? __ldg(p.a_scale + r * p.a_scale_row + s * p.a_scale_k) : 0.0f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) next[w][i] = a * __ldg(p.b_scale[w] + nb * p.b_scale_row[w] + s * p.b_scale_k[w]);
+        }
+      };
+      float* scales = reinterpret_cast<float*>(gbase + L::kOffScales) + quad * 2 * NT;
+      if (s0 < s1) fetch(s0);
+      uint32_t acc = 0, acc_phase = 0;
+      for (int s = s0; s < s1; ++s) {
+        __syncwarp();
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+            if (i * 32 + lane < NT) scales[w * NT + i * 32 + lane] = next[w][i];
+        __syncwarp();
+        if (s + 1 < s1) fetch(s + 1);
+        ok = bw.wait(bar(kSBAccFull + acc), acc_phase);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int c = 0; c < NT; c += C) {
+            uint32_t v[C];
+            skinny::tmem_ld<C>(lanes + (acc * W + w) * NT + static_cast<uint32_t>(c), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < C; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(scales + w * NT + c + e);
+              acc_sum[w][c + e] += __uint_as_float(v[e]) * f.x;
+              acc_sum[w][c + e + 1] += __uint_as_float(v[e + 1]) * f.y;
+              acc_sum[w][c + e + 2] += __uint_as_float(v[e + 2]) * f.z;
+              acc_sum[w][c + e + 3] += __uint_as_float(v[e + 3]) * f.w;
+            }
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSBAccEmpty + acc));
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      // every copy into the ring has been waited for by the MMAs that these sums came from
+      if (ok) {
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int e = 0; e < NT; ++e) sum[e * L::kSumLd + w * 128 + column] = acc_sum[w][e];
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (p.splits > 1) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, L::kTmemCols);
+  }
+
+  // Rows are shared out over the slice's CTAs, a warp to a row, V columns to a lane.
+  if (!*abort_flag) {
+    constexpr int V = L::kColumns / 32;
+    const int col = col0 + lane * V;
+    for (int r = part + warp * p.splits; r < p.rows; r += kSkinnyThreads / 32 * p.splits) {
+      float v[GATE ? 2 : 1][V];
+#pragma unroll
+      for (auto& a : v)
+#pragma unroll
+        for (float& b : a) b = 0.0f;
+      const uint32_t at = base + static_cast<uint32_t>(r * L::kSumLd + lane * V) * 4u;
+#pragma unroll 4
+      for (int c = 0; c < p.splits; ++c) {
+        const uint32_t from = mapa_shared(at, static_cast<uint32_t>(c));
+        skinny::add_remote<V>(v[0], from);
+        if constexpr (GATE) skinny::add_remote<V>(v[GATE ? 1 : 0], from + L::kColumns * 4u);
+      }
+      const bool in = col < p.N;  // (N is a multiple of V)
+      if constexpr (!GATE) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col);
+        if (in) {
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) dst[e] = gemm::pack16<OUT>(v[0][2 * e], v[0][2 * e + 1]);
+        }
+      } else {
+        float h[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[e] = gemm::activation(p.act, v[0][e]) * v[1][e];
+        if constexpr (F8) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(h[e]) & 0x7fffffffu);
+          top = __reduce_max_sync(0xffffffffu, top);
+          float inv;
+          const float scale = gemm::block_scale(top, inv);
+          if (in)
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + r * p.out_ld + col) =
+                gemm::pack_e4m3(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+          if (lane == 0) p.q_scale[col0 / 128 * p.q_scale_ld + r] = scale;
+        } else if (in) {
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) = gemm::pack16<OUT>(h[0], h[1]);
+          if (p.keep) {
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.gate) + r * p.gate_ld + col) = gemm::pack16<OUT>(v[0][0], v[0][1]);
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.up) + r * p.up_ld + col) = gemm::pack16<OUT>(v[1][0], v[1][1]);
+          }
+        }
+      }
+    }
+  }
+  if (threadIdx.x == 0 && *abort_flag && p.status) atomicCAS(p.status, 0, kTimeoutCode);
+  if (p.splits > 1) cluster_sync();  // (the sums have been read)
+}
+
+}  // namespace b2b
