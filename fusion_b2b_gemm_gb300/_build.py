@@ -1,6 +1,7 @@
 """Build the in-tree CUDA library ``fusion_b2b_gemm_gb300/_lib/libb2b.so`` and
-the module ``_lib/attn_binding.so`` (``binding/attention.cpp``, host code against
-torch's headers) that passes tensors to its attention calls.
+the modules ``_lib/attn_binding.so`` and ``_lib/ffn_binding.so``
+(``binding/attention.cpp``, ``binding/feedforward.cpp``, host code against torch's
+headers) that pass tensors to its attention and feed-forward calls.
 
 Every translation unit under ``csrc/`` is compiled for sm_103a only
 (``-gencode arch=compute_103a,code=sm_103a``) in parallel, then linked with
@@ -26,8 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libb2b.so")
 OBJ_DIR = os.path.join(HERE, "_build")
-BINDING_SRC = os.path.join(HERE, "binding", "attention.cpp")
-BINDING = os.path.join(OUT_DIR, "attn_binding.so")
+BINDINGS = {"attn_binding": "attention.cpp", "ffn_binding": "feedforward.cpp"}  # module: source under binding/
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -70,8 +70,8 @@ def _current(path: str, stamp: str, digest: str) -> bool:
         return f.read().strip() == digest
 
 
-def build_binding(force: bool = False) -> str | None:
-    """Compile attn_binding.so if its source, b2b.h or torch changed; return its path (None without torch)."""
+def build_binding(force: bool = False) -> list[str] | None:
+    """Compile each binding if its source, b2b.h or torch changed; return their paths (None without torch)."""
     torch_spec = importlib.util.find_spec("torch")
     if torch_spec is None:
         return None
@@ -80,26 +80,32 @@ def build_binding(force: bool = False) -> str | None:
     flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-I" + INCLUDE, "-I" + inc,
              "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), "-I" + sysconfig.get_paths()["include"]]
     libs = ["-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
-    h = hashlib.sha256(" ".join(flags + libs).encode())
-    for path in (BINDING_SRC, os.path.join(INCLUDE, "b2b.h"), os.path.join(torch_dir, "version.py")):
-        with open(path, "rb") as f:
-            h.update(f.read())
-    stamp = os.path.join(OUT_DIR, "attn_binding.sha256")
-    if not force and _current(BINDING, stamp, h.hexdigest()):
-        return BINDING
     os.makedirs(OUT_DIR, exist_ok=True)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    r = subprocess.run(["g++"] + flags + [BINDING_SRC, "-o", tmp] + libs, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    with open(stamp, "w") as f:
-        f.write(h.hexdigest() + "\n")
-    return BINDING
+
+    def compile_one(name: str) -> str:
+        src, out = os.path.join(HERE, "binding", BINDINGS[name]), os.path.join(OUT_DIR, name + ".so")
+        h = hashlib.sha256(" ".join(flags + libs).encode())
+        for path in (src, os.path.join(INCLUDE, "b2b.h"), os.path.join(torch_dir, "version.py")):
+            with open(path, "rb") as f:
+                h.update(f.read())
+        stamp = os.path.join(OUT_DIR, name + ".sha256")
+        if not force and _current(out, stamp, h.hexdigest()):
+            return out
+        tmp = out + f".tmp{os.getpid()}"
+        r = subprocess.run(["g++"] + flags + [src, "-o", tmp] + libs, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, out)
+        with open(stamp, "w") as f:
+            f.write(h.hexdigest() + "\n")
+        return out
+
+    with cf.ThreadPoolExecutor(len(BINDINGS)) as ex:
+        return list(ex.map(compile_one, BINDINGS))
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    """Compile and link libb2b.so and attn_binding.so if any source changed; return the first's path."""
+    """Compile and link libb2b.so and the bindings if any source changed; return the library's path."""
     with cf.ThreadPoolExecutor(1) as ex:
         binding = ex.submit(build_binding, force)
         lib = _build_library(force, verbose, jobs)

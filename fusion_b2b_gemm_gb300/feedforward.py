@@ -15,10 +15,14 @@ refused where gradients are recorded.  There is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
+import warnings
 from typing import NamedTuple
 
-from . import DTYPES, _check, _current_device, _lib, _stream_handle
+from . import DTYPES, _check, _current_device, _lib, _stream_handle, library_path
 
 __all__ = ["GatedFeedForwardPlan", "ScaledFeedForwardPlan", "ScaledGemmPlan", "quantize_blocks", "KeptActivations", "ACTIVATIONS"]
 
@@ -27,8 +31,8 @@ BLOCK = 128
 _TYPES = {"f16": "float16", "bf16": "bfloat16"}
 _INFERENCE, _TRAINING, _BACKWARD = 0, 1, 2  # B2B_FFN_*
 
-# Set when the first plan is made: the package's other parts do not need torch.
-torch = _raw_stream = None
+# Set when the first plan is made (_load): the package's other parts need neither torch nor the compiled module.
+torch = _raw_stream = _binding = None
 
 # The argument structures, whose members all take eight bytes (b2b_matrix_t: data, row_stride; b2b_scales_t: data,
 # row_stride, block_stride), as the C functions read them.
@@ -49,12 +53,41 @@ class KeptActivations(NamedTuple):
     hidden: "torch.Tensor"
 
 
+class _NoBinding:
+    """In the compiled module's place where there is none: every call takes the way through Python."""
+
+    @staticmethod
+    def bind(*_):
+        return None
+
+    run = forward = backward = scaled_ffn = scaled_gemm = bind
+
+
+def _load_binding():
+    """The module that passes tensors to the C functions (binding/feedforward.cpp), if it is there for this torch."""
+    path = os.path.join(os.path.dirname(library_path()), "ffn_binding.so")
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("ffn_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("ffn_binding", loader))
+        loader.exec_module(module)
+        if not torch.__version__.startswith(module.torch_version):
+            raise ImportError(f"built for torch {module.torch_version}, this is {torch.__version__}")
+    except ImportError as e:
+        warnings.warn(f"{path}: {e}; feed-forward calls take some microseconds longer without it "
+                      "(python fusion_b2b_gemm_gb300/_build.py)", RuntimeWarning, stacklevel=5)
+        return _NoBinding
+    module.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        _lib.b2b_ffn_workspace, _lib.b2b_ffn_forward, _lib.b2b_ffn_backward, _lib.b2b_scaled_ffn_run, _lib.b2b_scaled_gemm_run)))
+    return module
+
+
 def _load():
-    global torch, _raw_stream
-    if torch is None:
+    global torch, _raw_stream, _binding
+    if _binding is None:
         import torch
         # (the public torch.cuda.current_stream() builds an object each time, 3 us)
         _raw_stream = torch._C._cuda_getCurrentRawStream
+        _binding = _load_binding()
 
 
 def _refuse(name, t, dtype, rows, cols, device):
@@ -113,19 +146,22 @@ def _blocks(n):
 class _Plan:
     """Widths and status word of one kind of operator.  Bound to the GPU that is current now."""
 
-    _passes = (_INFERENCE,)
-
-    def __init__(self, dtype, create, *args):
+    def __init__(self, dtype, create, sizes, *args):
         if dtype not in _TYPES:
             raise ValueError(f"unknown dtype {dtype!r}; one of {sorted(_TYPES)}")
         _load()
         self.dtype = dtype
         h = ctypes.c_void_p()
-        _check(create(ctypes.byref(h), DTYPES[dtype], *args), create.__name__)
+        _check(create(ctypes.byref(h), DTYPES[dtype], *(n for n in sizes if n is not None), *args), create.__name__)
         self._h = h
         self._torch_dtype = getattr(torch, _TYPES[dtype])
         self.device_index = _current_device()
         self._workspace_sizes = {}
+        # What the binding's calls need to know of the plan.  They take the
+        # common call, with no tensors for the results and no stream, and return
+        # None where anything is not as they want it: the same in Python below
+        # finds out what.
+        self._bound = _binding.bind(h.value, dtype == "bf16", *(n or 0 for n in sizes), self.device_index)
 
     def _no_gradient(self, *inputs):
         if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
@@ -164,6 +200,7 @@ class _Plan:
         _check(_lib.b2b_ffn_plan_set_debug(self._h, int(flags)), "b2b_ffn_plan_set_debug")
 
     def close(self) -> None:
+        self._bound = None
         h = getattr(self, "_h", None)
         if h is not None and h.value:
             _lib.b2b_ffn_plan_destroy(h)
@@ -192,7 +229,7 @@ class GatedFeedForwardPlan(_Plan):
 
     def __init__(self, dtype: str, width: int, hidden: int, out_width: int | None = None, activation: str = "silu"):
         out_width = width if out_width is None else out_width
-        super().__init__(dtype, _lib.b2b_ffn_plan_create, width, hidden, out_width, _activation(activation))
+        super().__init__(dtype, _lib.b2b_ffn_plan_create, (width, hidden, out_width), _activation(activation))
         self.width, self.hidden, self.out_width, self.activation = width, hidden, out_width, activation
 
     def _operands(self, x, w_gate, w_up, w_down):
@@ -214,6 +251,10 @@ class GatedFeedForwardPlan(_Plan):
                 done = self.run(x, w_gate, w_up, w_down, out)
             _kept(stream, self.device_index, (done,), (x, w_gate, w_up, w_down, out))
             return done
+        if out is None:
+            done = _binding.run(self._bound, _raw_stream(self.device_index), x, w_gate, w_up, w_down)
+            if done is not None:
+                return done
         tokens, operands = self._operands(x, w_gate, w_up, w_down)
         self._no_gradient(x, w_gate, w_up, w_down)
         out, oa = self._result(x, tokens, out)
@@ -229,6 +270,10 @@ class GatedFeedForwardPlan(_Plan):
                 done = self.forward(x, w_gate, w_up, w_down, out, kept)
             _kept(stream, self.device_index, (done[0], *done[1]), (x, w_gate, w_up, w_down, out, *(kept or ())))
             return done
+        if out is None and kept is None:
+            done = _binding.forward(self._bound, _raw_stream(self.device_index), x, w_gate, w_up, w_down)
+            if done is not None:
+                return done[0], KeptActivations(*done[1:])
         tokens, operands = self._operands(x, w_gate, w_up, w_down)
         self._no_gradient(x, w_gate, w_up, w_down)
         out, oa = self._result(x, tokens, out)
@@ -262,6 +307,10 @@ class GatedFeedForwardPlan(_Plan):
                 done = self.backward(dy, x, w_gate, w_up, w_down, kept, input_grad, weight_grads)
             _kept(stream, self.device_index, done, (dy, x, w_gate, w_up, w_down, *kept))
             return done
+        if weight_grads is True:
+            done = _binding.backward(self._bound, _raw_stream(self.device_index), dy, x, w_gate, w_up, w_down, *kept, input_grad)
+            if done is not None:
+                return done
         tokens, (xp, xs, *weights) = self._operands(x, w_gate, w_up, w_down)
         dya = _rows("dy", dy, self._torch_dtype, tokens, self.out_width, self.device_index)[1:]
         kept = KeptActivations(*kept)
@@ -298,7 +347,7 @@ class ScaledFeedForwardPlan(_Plan):
 
     def __init__(self, dtype: str, width: int, hidden: int, out_width: int | None = None, activation: str = "silu"):
         out_width = width if out_width is None else out_width
-        super().__init__(dtype, _lib.b2b_scaled_ffn_plan_create, width, hidden, out_width, _activation(activation))
+        super().__init__(dtype, _lib.b2b_scaled_ffn_plan_create, (width, hidden, out_width), _activation(activation))
         self.width, self.hidden, self.out_width, self.activation = width, hidden, out_width, activation
 
     def run(self, x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, out=None, stream=None):
@@ -315,6 +364,11 @@ class ScaledFeedForwardPlan(_Plan):
                 done = self.run(x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, out)
             _kept(stream, self.device_index, (done,), (x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, out))
             return done
+        if out is None:
+            done = _binding.scaled_ffn(self._bound, _raw_stream(self.device_index), x, w_gate, gate_scale, w_up, up_scale, w_down,
+                                       down_scale)
+            if done is not None:
+                return done
         dev, f8 = self.device_index, torch.float8_e4m3fn
         d, f, o = self.width, self.hidden, self.out_width
         tokens, *xa = _rows("x", x, self._torch_dtype, None, d, dev)
@@ -337,7 +391,7 @@ class ScaledGemmPlan(_Plan):
     of 128 x 128.  ``dtype`` ("f16" or "bf16") is that of the result; ``k`` is a multiple of 16, ``n`` of 8."""
 
     def __init__(self, dtype: str, k: int, n: int):
-        super().__init__(dtype, _lib.b2b_scaled_gemm_plan_create, k, n)
+        super().__init__(dtype, _lib.b2b_scaled_gemm_plan_create, (k, None, n))
         self.k, self.n = k, n
 
     def run(self, a, a_scale, b, b_scale, out=None, stream=None):
@@ -349,6 +403,10 @@ class ScaledGemmPlan(_Plan):
                 done = self.run(a, a_scale, b, b_scale, out)
             _kept(stream, self.device_index, (done,), (a, a_scale, b, b_scale, out))
             return done
+        if out is None:
+            done = _binding.scaled_gemm(self._bound, _raw_stream(self.device_index), a, a_scale, b, b_scale)
+            if done is not None:
+                return done
         dev, f8 = self.device_index, torch.float8_e4m3fn
         rows, *aa = _rows("a", a, f8, None, self.k, dev)
         ba = _rows("b", b, f8, self.n, self.k, dev)[1:]
