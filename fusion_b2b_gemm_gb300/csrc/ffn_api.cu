@@ -219,7 +219,7 @@ struct Launch {
     p.group = 8;
     p.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(plan->budget_ns, 5000ull * kpan), 4000000000ull));
     void* args[] = {&maps, &p};
-    cudaError_t e = launch_pdl(kernel.main, dim3(2 * static_cast<unsigned>(std::min(p.units, clusters))), dim3(kGemmThreads), args,
+    cudaError_t e = launch_pdl(kernel.main, dim3(2 * static_cast<unsigned>(std::min(p.units, clusters))), dim3(gemm_threads(e4m3)), args,
                                kGemmSmem, stream, 2);
     if (e == cudaSuccess && p.whole < p.tiles) {
       void* cargs[] = {&p};
@@ -364,7 +364,7 @@ b2b_status_t create(b2b_ffn_plan_t* out, FfnKind kind, b2b_dtype_t dtype, int64_
   for (const GemmKernel& k : {p->s.gate, p->s.product[0], p->s.product[1]}) {
     cudaFuncAttributes fa;
     ok = ok && cudaFuncGetAttributes(&fa, k.main) == cudaSuccess &&
-         fa.numRegs * kGemmThreads >= 256 * kGemmEpilogueRegs + 128 * kGemmOtherRegs;
+         fa.numRegs * gemm_threads(true) >= 512 * kGemmEpilogueRegs + 128 * kGemmOtherRegs;
   }
   ok = ok && cudaMalloc(&p->d_status, sizeof(int)) == cudaSuccess;
   if (ok && cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) {

@@ -23,8 +23,14 @@
 //
 // e4m3 operands carry a scale for each 128 of k: every K panel's product is an
 // accumulator of its own, which the epilogue's warps multiply by its scales and
-// add up in registers in fp32 (128 columns of a row for each thread) while the
-// next panel's MMAs run.
+// add up in registers in fp32 while the next panel's MMAs run.  A warp's wait for
+// a panel, its loads and its release are some 500 cycles of latencies, as long
+// as the MMAs take, so that sixteen warps of 64 columns share the work, 16 columns
+// at a time, which also keeps the sums in registers: 8192 x 4096 x 14336 takes 385 us;
+// with eight warps of 128 columns 450, with 32 columns at a time, where three
+// values are spilled, 491 us; without the additions 283 us.  Two more warps hand
+// the epilogue its scales, four panels ahead (each warp's own loads, one panel
+// ahead: 505 us); the barrier that announces a panel's product announces these too.
 //
 // Work units.  A unit is a tile, or, of the last tiles, which would fill the
 // SMs a fraction of a time only, a range of the tile's K panels: such a unit
@@ -35,8 +41,10 @@
 //   warp 0      TMA loads of this CTA's half of each panel
 //   warp 1      the even CTA's elected thread issues the MMAs
 //   warp 2      tensor-memory allocation
+//   warps 2, 3  e4m3: scales of 64 rows each, and of the columns, for every panel
 //   warps 4-11  epilogue, two warps for each quadrant of 32 rows: columns [0, 128)
 //               and [128, 256), or the halves of the gate's and the other projection's 128
+//   warps 4-19  the same for e4m3, four warps for each quadrant, a quarter each
 // Every wait is bounded, as in the chain kernels.
 #pragma once
 
@@ -48,19 +56,22 @@
 
 namespace b2b {
 
-constexpr int kGemmThreads = 384;
+// epilogue warps and threads of a CTA, panels in its ring
+__host__ __device__ constexpr int gemm_warps(bool e4m3) { return e4m3 ? 16 : 8; }
+__host__ __device__ constexpr int gemm_threads(bool e4m3) { return 128 + 32 * gemm_warps(e4m3); }
+__host__ __device__ constexpr int gemm_ring(bool e4m3) { return e4m3 ? 5 : 6; }
 constexpr int kGemmTile = 256;     // rows and columns of a pair's tile
-constexpr int kGemmRing = 6;       // panels in flight
 constexpr int kGemmSlot = 2 * kPanelBytes;  // a panel of A and one of B, 128 rows or columns of 128 bytes each
 constexpr int kGemmStage = 4096;   // output box of a warp: 32 rows of 128 bytes
-constexpr int kGemmOffStage = kGemmRing * kGemmSlot;
-constexpr int kGemmOffTop = kGemmOffStage;  // kEpiGateQuant (no boxes): [2][2][128] largest magnitudes
-constexpr int kGemmOffBar = kGemmOffStage + 8 * kGemmStage;
-constexpr int kGemmSmem = kGemmOffBar + 256 + 1024;  // (the ring begins on a 1024-byte boundary)
+__host__ __device__ constexpr int gemm_off_stage(bool e4m3) { return gemm_ring(e4m3) * kGemmSlot; }
+constexpr int kGemmOffScales = 6 * kGemmSlot + 8 * kGemmStage;  // e4m3: [3][128] scales of rows, [3][2] of columns
+static_assert(gemm_off_stage(false) + 8 * kGemmStage == kGemmOffScales && gemm_off_stage(true) + 16 * kGemmStage == kGemmOffScales, "");
+constexpr int kGemmOffBar = kGemmOffScales + 1536 + 32;
+constexpr int kGemmSmem = kGemmOffBar + 224 + 1024;  // (the ring begins on a 1024-byte boundary)
 static_assert(kGemmSmem <= 232448, "shared memory of a CTA");
-// e4m3: registers of an epilogue thread and of another; 168 of each thread at launch, shared out anew
-constexpr int kGemmEpilogueRegs = 224, kGemmOtherRegs = 56;
-static_assert(256 * kGemmEpilogueRegs + 128 * kGemmOtherRegs <= 168 * kGemmThreads, "register file");
+// e4m3: registers of an epilogue thread and of another; 96 of each thread at launch, shared out anew
+constexpr int kGemmEpilogueRegs = 104, kGemmOtherRegs = 64;
+static_assert(512 * kGemmEpilogueRegs + 128 * kGemmOtherRegs <= 96 * gemm_threads(true), "register file");
 constexpr int kGemmPartFloats = 2 * 128 * kGemmTile;  // a unit's part, both CTAs
 constexpr int kGemmMaxProblems = 3;
 
@@ -73,7 +84,7 @@ enum : int {  // barrier slots (8 bytes each)
   kGBAccFull = 16,   // [2] accumulator complete
   kGBAccEmpty = 18,  // [2] accumulator read in both CTAs (even CTA's)
   kGBDrain = 20,
-  kGBTop = 21,       // [4] both warps of a quadrant have written their rows' largest magnitudes
+  kGBTop = 21,       // [4] the warps of a quadrant have written their rows' largest magnitudes
   kGSlotTmem = 25,   // uint32 tensor-memory base, then the int abort flag
 };
 
@@ -299,12 +310,13 @@ struct Stage {
 }  // namespace gemm
 
 template <int IN, bool AMN, bool BMN, int EPI, int OUT>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams p) {
   using namespace ptx;
   constexpr bool F8 = IN == kGemmE4M3;
   constexpr bool GATE = EPI == kEpiGate || EPI == kEpiGateQuant;
   constexpr int CK = F8 ? 128 : 64;  // K elements of a panel
+  constexpr int kRing = gemm_ring(F8), kWarps = gemm_warps(F8);
   static_assert(!F8 || (!AMN && !BMN && (EPI == kEpiStore || EPI == kEpiGateQuant)), "e4m3 operands are K-major");
   static_assert(F8 || (EPI != kEpiGateQuant && OUT == IN), "16-bit operands and outputs have one type");
 
@@ -328,13 +340,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(bar(kGBFull + lane), 1);
       mbar_init(bar(kGBEmpty + lane), 1);
     } else if (lane < 10) {
-      mbar_init(bar(kGBAccFull + lane - 8), 1);
-      mbar_init(bar(kGBAccEmpty + lane - 8), 16);  // epilogue warps of both CTAs
+      mbar_init(bar(kGBAccFull + lane - 8), F8 ? 3 : 1);  // (e4m3: and the scales, by two warps)
+      mbar_init(bar(kGBAccEmpty + lane - 8), 2 * kWarps);  // epilogue warps of both CTAs
     } else if (lane == 10) {
       mbar_init(bar(kGBDrain), 1);
       *abort_flag = 0;
     } else if (lane < 15) {
-      mbar_init(bar(kGBTop + lane - 11), 2);
+      mbar_init(bar(kGBTop + lane - 11), 4);
     }
     fence_barrier_init();
   } else if (warp == 2) {
@@ -403,17 +415,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
           }
           ++issued;
-          if (++slot == kGemmRing) {
+          if (++slot == kRing) {
             slot = 0;
             phase ^= 1u;
           }
         }
       }
       // Copies in flight land before exit (the even CTA's barriers count both CTAs').
-      const unsigned long long tail = !leader ? 0 : (issued < kGemmRing ? issued : kGemmRing);
+      const unsigned long long tail = !leader ? 0 : (issued < kRing ? issued : kRing);
       for (unsigned long long j = 0; j < tail; ++j) {
         const unsigned long long idx = issued - 1 - j;
-        drain_wait(bar(kGBFull + static_cast<int>(idx % kGemmRing)), static_cast<uint32_t>((idx / kGemmRing) & 1u),
+        drain_wait(bar(kGBFull + static_cast<int>(idx % kRing)), static_cast<uint32_t>((idx / kRing) & 1u),
                    p.budget_ns);
       }
     } else if (warp == 1 && leader) {
@@ -448,7 +460,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 mma_ss<false, 2>(d, a + s * a_step, b + s * b_step, idesc, more);
             }
             tc_commit<2>(bar(kGBEmpty + slot));
-            if (++slot == kGemmRing) {
+            if (++slot == kRing) {
               slot = 0;
               phase ^= 1u;
             }
@@ -462,23 +474,78 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tc_commit<2>(bar(kGBDrain));
         drain_wait(bar(kGBDrain), 0, p.budget_ns);
       }
+    } else if (F8 && warp >= 2) {
+      // ----------------------------------------------------------- scales
+      // Panel n's go into place n % 3 once panel n - 1's product is complete: its
+      // MMAs began when panel n - 3 had been read.
+      float* rows = reinterpret_cast<float*>(gbase + kGemmOffScales);
+      float* cols = rows + 3 * 128;
+      uint32_t place = 0, n = 0;
+      bool ok = true;
+      for (int u = cid; u < p.units && ok; u += ncl) {
+        const GemmUnit c = gemm_unit(p, u);
+        const GemmProblem& q = p.prob[c.prob];
+        const int m0 = c.mt * kGemmTile + rank * 128 + (warp - 2) * 64 + lane;  // and m0 + 32
+        const float* a0 = p.a_scale + (m0 < q.M ? m0 : 0) * p.a_scale_row + c.k0 * p.a_scale_k;
+        const float* a1 = p.a_scale + (m0 + 32 < q.M ? m0 + 32 : 0) * p.a_scale_row + c.k0 * p.a_scale_k;
+        // of the columns: warp 2 of the first 128 (or the gate's), warp 3 of the others
+        const int w = warp - 2, nb = GATE ? c.nt : 2 * c.nt + w;
+        const float* b0 = p.b_scale[GATE ? w : 0] + (nb * 128 < q.N ? nb : 0) * p.b_scale_row[GATE ? w : 0] + c.k0 * p.b_scale_k[GATE ? w : 0];
+        // Asked for four panels ahead: one panel's time is less than a load's.
+        float x0[4], x1[4], y[4];
+        int next = c.k0;
+        auto fetch = [&](int j) {
+          if (next < c.k1) {
+            x0[j] = __ldg(a0);
+            x1[j] = __ldg(a1);
+            y[j] = __ldg(b0);
+          }
+          ++next;
+          a0 += p.a_scale_k;
+          a1 += p.a_scale_k;
+          b0 += p.b_scale_k[GATE ? w : 0];
+        };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fetch(j);
+        for (int k = c.k0; k < c.k1 && ok; k += 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (k + j < c.k1 && ok) {
+              if (n > 0) ok = bw.wait(bar(kGBAccFull + ((n - 1) & 1u)), ((n - 1) >> 1) & 1u);
+              if (ok) {
+                rows[place * 128 + w * 64 + lane] = x0[j];
+                rows[place * 128 + w * 64 + 32 + lane] = x1[j];
+                if (lane == 0) cols[place * 2 + w] = y[j];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kGBAccFull + (n & 1u)));
+                ++n;
+                if (++place == 3) place = 0;
+                fetch(j);
+              }
+            }
+          }
+        }
+      }
     }
   } else {
     // ---------------------------------------------------------- epilogue
     if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGemmEpilogueRegs));
-    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int quad = warp & 3, half = (warp - 4) >> 2;  // (e4m3: of four quarters)
     const int row = quad * 32 + lane;  // of this CTA's 128
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-    const gemm::Stage stage{base + kGemmOffStage + static_cast<uint32_t>(warp - 4) * kGemmStage, lane};
+    const gemm::Stage stage{base + gemm_off_stage(F8) + static_cast<uint32_t>(warp - 4) * kGemmStage, lane};
     const uint32_t empty0 = mapa_shared(bar(kGBAccEmpty), 0);
     auto release = [&](uint32_t acc) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(empty0 + 8u * acc);
     };
-    // first column, in the accumulator, of this warp's 32-column chunk i of four
-    auto column = [&](int i) -> int { return GATE ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * 128 + i * 32; };
-    uint32_t acc = 0, acc_phase = 0, tops = 0;
+    // first column, in the accumulator, of this warp's 32-column chunk i of four (e4m3: of two)
+    auto column = [&](int i) -> int {
+      if constexpr (F8) return GATE ? i * 128 + half * 32 : half * 64 + i * 32;
+      return GATE ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * 128 + i * 32;
+    };
+    uint32_t acc = 0, acc_phase = 0, tops = 0, place = 0;
     bool ok = true;
     for (int u = cid; u < p.units && ok; u += ncl) {
       const GemmUnit c = gemm_unit(p, u);
@@ -489,59 +556,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       float* part = c.part < 0 ? nullptr : p.part + gemm_part_at(c.part, rank * 128 + row, 0);
       const bool mine = m0 + row < q.M;
       if constexpr (F8) {
-        // Scales of this thread's row and of the columns' block(s), four panels ahead of their use.
-        const float* sa = p.a_scale + (mine ? m0 + row : 0) * p.a_scale_row;
-        const int nb = GATE ? c.nt : 2 * c.nt + half;
-        const float* s0 = p.b_scale[0] + (nb * 128 < q.N ? nb : 0) * p.b_scale_row[0];
-        const float* s1 = GATE ? p.b_scale[1] + c.nt * p.b_scale_row[1] : nullptr;
-        uint64_t sum[64];
+        const float* scales = reinterpret_cast<const float*>(gbase + kGemmOffScales);
+        uint64_t sum[32];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) sum[i] = 0;
-        float f0[4], f1[4];
-        auto fetch = [&](int j, int k) {
-          if (k < c.k1) {
-            const float a = __ldg(sa + k * p.a_scale_k);
-            f0[j] = a * __ldg(s0 + k * p.b_scale_k[0]);
-            if constexpr (GATE) f1[j] = a * __ldg(s1 + k * p.b_scale_k[1]);
-          }
-        };
+        for (int i = 0; i < 32; ++i) sum[i] = 0;
+        for (int k = c.k0; k < c.k1; ++k) {
+          ok = bw.wait(bar(kGBAccFull + acc), acc_phase);
+          if (!ok) break;
+          tc_fence_after();
+          if (rows) {
+            const float fr = scales[place * 128 + row];
+            const float2 fc = *reinterpret_cast<const float2*>(scales + 3 * 128 + place * 2);
+            const float f0 = fr * (GATE || !(half & 2) ? fc.x : fc.y), f1 = GATE ? fr * fc.y : f0;
+            const uint64_t g2 = gemm::pack2(f0, f0), u2 = GATE ? gemm::pack2(f1, f1) : g2;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) fetch(j, c.k0 + j);
-        for (int k0 = c.k0; k0 < c.k1 && ok; k0 += 4) {
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[16];
+              tmem_ld16(lanes + acc * 256u + static_cast<uint32_t>(column(i >> 1) + (i & 1) * 16), v);
+              tmem_wait_ld(v);
+              if (i == 3) release(acc);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (k0 + j < c.k1 && ok) {
-              ok = bw.wait(bar(kGBAccFull + acc), acc_phase);
-              if (ok) {
-                tc_fence_after();
-                if (rows) {
-                  const uint64_t g = gemm::pack2(f0[j], f0[j]), h = GATE ? gemm::pack2(f1[j], f1[j]) : g;
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    uint32_t v[32];
-                    tmem_ld32(lanes + acc * 256u + static_cast<uint32_t>(column(i)), v);
-                    tmem_wait_ld();
-                    if (i == 3) release(acc);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                      sum[i * 16 + e] = gemm::fma2(gemm::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
-                                                   i < 2 ? g : h, sum[i * 16 + e]);
-                  }
-                } else {
-                  release(acc);
-                }
-                acc ^= 1u;
-                if (acc == 0) acc_phase ^= 1u;
-                fetch(j, k0 + j + 4);
-              }
+              for (int e = 0; e < 8; ++e)
+                sum[i * 8 + e] = gemm::fma2(gemm::pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), i < 2 ? g2 : u2, sum[i * 8 + e]);
             }
+          } else {
+            release(acc);
           }
+          acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+          if (++place == 3) place = 0;
         }
         if (!ok) break;
         if (part) {
           if (mine) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 float4 v;
@@ -552,49 +601,48 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
         } else if constexpr (EPI == kEpiStore) {
           if (rows) {
+            uint32_t w[32];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              uint32_t w[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float x, y;
-                gemm::unpack2(sum[b * 32 + e], x, y);
-                w[e] = gemm::pack16<OUT>(x, y);
-              }
-              stage.ready();
-              stage.put(w);
-              const int col = c.nt * kGemmTile + half * 128 + b * 64;
-              stage.store(&maps.out[0], col, mw, col < q.N);
+            for (int e = 0; e < 32; ++e) {
+              float x, y;
+              gemm::unpack2(sum[e], x, y);
+              w[e] = gemm::pack16<OUT>(x, y);
             }
+            stage.ready();
+            stage.put(w);
+            const int col = c.nt * kGemmTile + half * 64;
+            stage.store(&maps.out[0], col, mw, col < q.N);
           }
         } else {
-          // h of 64 columns, the row's largest magnitude over both warps' halves, values and scale
-          float h[64];
+          // h of 32 columns, the row's largest magnitude over the four warps' quarters, values and scale
+          float h[32];
           uint32_t top = 0;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 16; ++e) {
             float g0, g1, u0, u1;
             gemm::unpack2(sum[e], g0, g1);
-            gemm::unpack2(sum[32 + e], u0, u1);
+            gemm::unpack2(sum[16 + e], u0, u1);
             h[2 * e] = gemm::activation(p.act, g0) * u0;
             h[2 * e + 1] = gemm::activation(p.act, g1) * u1;
             top = max(top, max(__float_as_uint(h[2 * e]) & 0x7fffffffu, __float_as_uint(h[2 * e + 1]) & 0x7fffffffu));
           }
-          volatile uint32_t* tops_row = reinterpret_cast<volatile uint32_t*>(gbase + kGemmOffTop) + (tops & 1u) * 256u + row;
-          tops_row[half * 128] = top;
+          // (two sets in turn: a warp is at most one tile ahead of the others)
+          volatile uint32_t* all = reinterpret_cast<volatile uint32_t*>(gbase + gemm_off_stage(true)) + (tops & 1u) * 512u + row;
+          all[half * 128] = top;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kGBTop + quad));
           ok = bw.wait(bar(kGBTop + quad), tops & 1u);
           if (!ok) break;
-          top = max(top, tops_row[(half ^ 1) * 128]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = max(top, all[i * 128]);
           ++tops;
           float inv;
           const float scale = gemm::block_scale(top, inv);
           if (mine) {
-            const int col = c.nt * 128 + half * 64;
+            const int col = c.nt * 128 + half * 32;
             uint8_t* dst = p.q + (m0 + row) * p.q_ld + col;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint4 w;
               w.x = gemm::pack_e4m3(h[16 * e] * inv, h[16 * e + 1] * inv, h[16 * e + 2] * inv, h[16 * e + 3] * inv);
               w.y = gemm::pack_e4m3(h[16 * e + 4] * inv, h[16 * e + 5] * inv, h[16 * e + 6] * inv, h[16 * e + 7] * inv);
@@ -617,7 +665,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int i = 0; i < 4; ++i) {
             uint32_t v[32];
             tmem_ld32(src + static_cast<uint32_t>(column(i)), v);
-            tmem_wait_ld();
+            tmem_wait_ld(v);
             if (i == 3) release(acc);
             if (mine) {
 #pragma unroll
@@ -632,7 +680,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             uint32_t v0[32], v1[32];
             tmem_ld32(src + static_cast<uint32_t>(half * 128 + b * 64), v0);
             tmem_ld32(src + static_cast<uint32_t>(half * 128 + b * 64 + 32), v1);
-            tmem_wait_ld();
+            tmem_wait_ld(v0);
+            tmem_wait_ld(v1);
             if (b == 1) release(acc);
             stage.ready();
             store_output_row<OUT == kGemmF16 ? kOutF16 : kOutBF16>(stage.addr, lane, 0, v0);
@@ -645,7 +694,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int i = 0; i < 4; ++i) {
             uint32_t v[32];
             tmem_ld32(src + static_cast<uint32_t>(column(i)), v);
-            tmem_wait_ld();
+            tmem_wait_ld(v);
             if (i == 3) release(acc);
             stage.ready();
             store_output_row<kOutF32>(stage.addr, lane, 0, v);
@@ -661,7 +710,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             uint32_t g[32], v[32];
             tmem_ld32(src + static_cast<uint32_t>(column(i)), g);
             tmem_ld32(src + static_cast<uint32_t>(column(i + 2)), v);
-            tmem_wait_ld();
+            tmem_wait_ld(g);
+            tmem_wait_ld(v);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               w[i * 16 + e] = gemm::pack16<OUT>(
@@ -678,7 +728,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               uint32_t v0[32], v1[32];
               tmem_ld32(src + static_cast<uint32_t>(column(2 * b)), v0);
               tmem_ld32(src + static_cast<uint32_t>(column(2 * b + 1)), v1);
-              tmem_wait_ld();
+              tmem_wait_ld(v0);
+              tmem_wait_ld(v1);
               if (b == 1) release(acc);
               stage.ready();
               store_output_row<OUT == kGemmF16 ? kOutF16 : kOutBF16>(stage.addr, lane, 0, v0);
@@ -706,7 +757,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 g4[e] = in ? __ldg(reinterpret_cast<const uint4*>(gate + at)) : make_uint4(0, 0, 0, 0);
                 u4[e] = in ? __ldg(reinterpret_cast<const uint4*>(up + at)) : make_uint4(0, 0, 0, 0);
               }
-              tmem_wait_ld();
+              tmem_wait_ld(v);
               if (b == 1 && i == 1) release(acc);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {

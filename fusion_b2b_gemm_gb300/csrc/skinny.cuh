@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
           if (c < p.rows) {
             uint32_t v[C];
             skinny::tmem_ld<C>(lanes + static_cast<uint32_t>(c), v);
-            tmem_wait_ld();
+            tmem_wait_ld(v);
 #pragma unroll
             for (int e = 0; e < C; ++e) sum[(c + e) * L::kSumLd + column] = __uint_as_float(v[e]);
           }
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
           for (int c = 0; c < NT; c += C) {
             uint32_t v[C];
             skinny::tmem_ld<C>(lanes + (acc * W + w) * NT + static_cast<uint32_t>(c), v);
-            tmem_wait_ld();
+            tmem_wait_ld(v);
 #pragma unroll
             for (int e = 0; e < C; e += 4) {
               const float4 f = *reinterpret_cast<const float4*>(scales + w * NT + c + e);
