@@ -579,6 +579,8 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
     l.b_rows(0, in[4]);
     l.out(0, dg);
     l.out(1, du);
+    l.map(&l.maps.out[2], type16(p), in[5], 64, 32);
+    l.map(&l.maps.a[2], type16(p), in[6], 64, 32);
     l.p.gate = r->gate.data;
     l.p.gate_ld = r->gate.row_stride;
     l.p.up = r->up.data;

@@ -56,18 +56,19 @@
 
 namespace b2b {
 
-// epilogue warps and threads of a CTA, panels in its ring
+// epilogue warps and threads of a CTA
 __host__ __device__ constexpr int gemm_warps(bool e4m3) { return e4m3 ? 16 : 8; }
 __host__ __device__ constexpr int gemm_threads(bool e4m3) { return 128 + 32 * gemm_warps(e4m3); }
-__host__ __device__ constexpr int gemm_ring(bool e4m3) { return e4m3 ? 5 : 6; }
+// panels in its ring: one less where the epilogue takes twice the room (two boxes for a warp, or twice the warps)
+__host__ __device__ constexpr int gemm_ring(bool wide) { return wide ? 5 : 6; }
 constexpr int kGemmTile = 256;     // rows and columns of a pair's tile
 constexpr int kGemmSlot = 2 * kPanelBytes;  // a panel of A and one of B, 128 rows or columns of 128 bytes each
 constexpr int kGemmStage = 4096;   // output box of a warp: 32 rows of 128 bytes
-__host__ __device__ constexpr int gemm_off_stage(bool e4m3) { return gemm_ring(e4m3) * kGemmSlot; }
+__host__ __device__ constexpr int gemm_off_stage(bool wide) { return gemm_ring(wide) * kGemmSlot; }
 constexpr int kGemmOffScales = 6 * kGemmSlot + 8 * kGemmStage;  // e4m3: [3][128] scales of rows, [3][2] of columns
 static_assert(gemm_off_stage(false) + 8 * kGemmStage == kGemmOffScales && gemm_off_stage(true) + 16 * kGemmStage == kGemmOffScales, "");
 constexpr int kGemmOffBar = kGemmOffScales + 1536 + 32;
-constexpr int kGemmSmem = kGemmOffBar + 224 + 1024;  // (the ring begins on a 1024-byte boundary)
+constexpr int kGemmSmem = kGemmOffBar + 256 + 1024;  // (the ring begins on a 1024-byte boundary)
 static_assert(kGemmSmem <= 232448, "shared memory of a CTA");
 // e4m3: registers of an epilogue thread and of another; 96 of each thread at launch, shared out anew
 constexpr int kGemmEpilogueRegs = 104, kGemmOtherRegs = 64;
@@ -85,7 +86,8 @@ enum : int {  // barrier slots (8 bytes each)
   kGBAccEmpty = 18,  // [2] accumulator read in both CTAs (even CTA's)
   kGBDrain = 20,
   kGBTop = 21,       // [4] the warps of a quadrant have written their rows' largest magnitudes
-  kGSlotTmem = 25,   // uint32 tensor-memory base, then the int abort flag
+  kGBRows = 21,      // [8] (kEpiGateGrad) a warp's boxes of the gate's and the other projection's values landed
+  kGSlotTmem = 29,   // uint32 tensor-memory base, then the int abort flag
 };
 
 // One product of a launch: D [M][N].  Tiles are numbered problem after problem.
@@ -107,7 +109,7 @@ struct GemmParams {
   int group;          // 256-row tiles that share a pass over the columns
   int act;            // activation: 0 silu, 1 gelu
   int keep;           // kEpiGate: store gate and up as well
-  // kEpiGateGrad: rows of the gate's and the other projection's values
+  // kEpiGateGrad: the gate's and the other projection's values, as gemm_combine_kernel reads them
   const void* gate;
   const void* up;
   long long gate_ld, up_ld;
@@ -131,7 +133,7 @@ struct GemmParams {
 };
 
 struct GemmMaps {
-  CUtensorMap a[kGemmMaxProblems], b[kGemmMaxProblems], out[kGemmMaxProblems];
+  CUtensorMap a[kGemmMaxProblems], b[kGemmMaxProblems], out[kGemmMaxProblems];  // (kEpiGateGrad: out[2] and a[2] are of the gate's and the other's values)
 };
 
 struct GemmUnit {
@@ -202,20 +204,40 @@ struct Wait {
   }
 };
 
-__device__ __forceinline__ float sigmoid(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
+__device__ __forceinline__ float sigmoid(float u) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));  // (e infinite: 0)
+  return s;
+}
 constexpr float kGelu = 1.5957691216057308f, kGelu3 = 0.044715f;  // 2 sqrt(2 / pi)
 
-// act(g)
-__device__ __forceinline__ float activation(int act, float g) {
-  const float u = act ? kGelu * (g + kGelu3 * g * g * g) : g;
-  return g * sigmoid(u);
+template <int V>
+struct Constant {
+  static constexpr int value = V;
+};
+
+// ACT 0: silu, 1: gelu
+template <int ACT>
+__device__ __forceinline__ float activation(float g) {
+  return g * sigmoid(ACT ? kGelu * (g + kGelu3 * g * g * g) : g);
 }
+__device__ __forceinline__ float activation(int act, float g) { return act ? activation<1>(g) : activation<0>(g); }
 // act(g) and its slope.  Far out s (1 - s) is 0, times a slope of u that has to stay finite.
-__device__ __forceinline__ void activation_slope(int act, float g, float& a, float& slope) {
-  const float s = sigmoid(act ? kGelu * (g + kGelu3 * g * g * g) : g);
-  const float du = act ? kGelu * (1.0f + 3.0f * kGelu3 * fminf(g * g, 1e30f)) : 1.0f;
+template <int ACT>
+__device__ __forceinline__ void activation_slope(float g, float& a, float& slope) {
+  const float s = sigmoid(ACT ? kGelu * (g + kGelu3 * g * g * g) : g);
   a = g * s;
-  slope = s + a * (1.0f - s) * du;
+  const float t = fmaf(-a, s, a);  // a (1 - s)
+  slope = ACT ? fmaf(t, kGelu * (1.0f + 3.0f * kGelu3 * fminf(g * g, 1e30f)), s) : s + t;
+}
+// f with the activation as a constant: a branch for a whole tile, not for each value.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  if (act)
+    f(Constant<1>{});
+  else
+    f(Constant<0>{});
 }
 
 template <int T>
@@ -316,7 +338,8 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
   constexpr bool F8 = IN == kGemmE4M3;
   constexpr bool GATE = EPI == kEpiGate || EPI == kEpiGateQuant;
   constexpr int CK = F8 ? 128 : 64;  // K elements of a panel
-  constexpr int kRing = gemm_ring(F8), kWarps = gemm_warps(F8);
+  constexpr bool kWide = F8 || EPI == kEpiGateGrad;
+  constexpr int kRing = gemm_ring(kWide), kWarps = gemm_warps(F8);
   static_assert(!F8 || (!AMN && !BMN && (EPI == kEpiStore || EPI == kEpiGateQuant)), "e4m3 operands are K-major");
   static_assert(F8 || (EPI != kEpiGateQuant && OUT == IN), "16-bit operands and outputs have one type");
 
@@ -345,8 +368,8 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
     } else if (lane == 10) {
       mbar_init(bar(kGBDrain), 1);
       *abort_flag = 0;
-    } else if (lane < 15) {
-      mbar_init(bar(kGBTop + lane - 11), 4);
+    } else if (lane < 19) {
+      mbar_init(bar(kGBRows + lane - 11), EPI == kEpiGateQuant ? 4 : 1);  // (the first four are kGBTop)
     }
     fence_barrier_init();
   } else if (warp == 2) {
@@ -533,7 +556,7 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
     const int quad = warp & 3, half = (warp - 4) >> 2;  // (e4m3: of four quarters)
     const int row = quad * 32 + lane;  // of this CTA's 128
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-    const gemm::Stage stage{base + gemm_off_stage(F8) + static_cast<uint32_t>(warp - 4) * kGemmStage, lane};
+    const gemm::Stage stage{base + gemm_off_stage(kWide) + static_cast<uint32_t>(warp - 4) * (EPI == kEpiGateGrad ? 2 * kGemmStage : kGemmStage), lane};
     const uint32_t empty0 = mapa_shared(bar(kGBAccEmpty), 0);
     auto release = [&](uint32_t acc) {
       tc_fence_before();
@@ -544,6 +567,19 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
     auto column = [&](int i) -> int {
       if constexpr (F8) return GATE ? i * 128 + half * 32 : half * 64 + i * 32;
       return GATE ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * 128 + i * 32;
+    };
+    // kEpiGateGrad: bring gate and up of a box, once what left its places has been read
+    uint32_t asked = 0, boxes = 0;
+    auto ask_rows = [&](int at_row, int col, bool inside) {
+      if (inside) ++asked;
+      if (lane == 0 && inside) {
+        bulk_wait_read<0>();
+        const uint32_t full = bar(kGBRows + warp - 4);
+        mbar_arrive_expect_tx(full, 2 * kGemmStage);
+        tma_load_2d(stage.addr, &maps.out[2], full, col, at_row);
+        tma_load_2d(stage.addr + kGemmStage, &maps.a[2], full, col, at_row);
+      }
+      __syncwarp();
     };
     uint32_t acc = 0, acc_phase = 0, tops = 0, place = 0;
     bool ok = true;
@@ -617,13 +653,18 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
           // h of 32 columns, the row's largest magnitude over the four warps' quarters, values and scale
           float h[32];
           uint32_t top = 0;
+          gemm::with_activation(p.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float g0, g1, u0, u1;
+              gemm::unpack2(sum[e], g0, g1);
+              gemm::unpack2(sum[16 + e], u0, u1);
+              h[2 * e] = gemm::activation<act.value>(g0) * u0;
+              h[2 * e + 1] = gemm::activation<act.value>(g1) * u1;
+            }
+          });
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float g0, g1, u0, u1;
-            gemm::unpack2(sum[e], g0, g1);
-            gemm::unpack2(sum[16 + e], u0, u1);
-            h[2 * e] = gemm::activation(p.act, g0) * u0;
-            h[2 * e + 1] = gemm::activation(p.act, g1) * u1;
             top = max(top, max(__float_as_uint(h[2 * e]) & 0x7fffffffu, __float_as_uint(h[2 * e + 1]) & 0x7fffffffu));
           }
           // (two sets in turn: a warp is at most one tile ahead of the others)
@@ -654,6 +695,7 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
           }
         }
       } else {
+        if (EPI == kEpiGateGrad && rows && !part) ask_rows(mw, c.nt * kGemmTile + half * 128, c.nt * kGemmTile + half * 128 < q.N);
         ok = bw.wait(bar(kGBAccFull + acc), acc_phase);
         if (!ok) break;
         tc_fence_after();
@@ -712,11 +754,12 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
             tmem_ld32(src + static_cast<uint32_t>(column(i + 2)), v);
             tmem_wait_ld(g);
             tmem_wait_ld(v);
+            gemm::with_activation(p.act, [&](auto act) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[i * 16 + e] = gemm::pack16<OUT>(
-                  gemm::activation(p.act, __uint_as_float(g[2 * e])) * __uint_as_float(v[2 * e]),
-                  gemm::activation(p.act, __uint_as_float(g[2 * e + 1])) * __uint_as_float(v[2 * e + 1]));
+              for (int e = 0; e < 16; ++e)
+                w[i * 16 + e] = gemm::pack16<OUT>(gemm::activation<act.value>(__uint_as_float(g[2 * e])) * __uint_as_float(v[2 * e]),
+                                                  gemm::activation<act.value>(__uint_as_float(g[2 * e + 1])) * __uint_as_float(v[2 * e + 1]));
+            });
           }
           if (!p.keep) release(acc);
           stage.ready();
@@ -738,52 +781,61 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
             }
           }
         } else {
-          const int row0 = mine ? m0 + row : 0;
-          const uint16_t* gate = static_cast<const uint16_t*>(p.gate) + row0 * p.gate_ld;
-          const uint16_t* up = static_cast<const uint16_t*>(p.up) + row0 * p.up_ld;
+          // Boxes of 64 columns: gate and up were asked for (box 0: before the wait for the
+          // product) into the places that dG and dU then take.
+          const gemm::Stage second{stage.addr + kGemmStage, lane};
+          const uint32_t sw = static_cast<uint32_t>(lane & 7), at = stage.addr + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll 1
           for (int b = 0; b < 2; ++b) {
             const int col = c.nt * kGemmTile + half * 128 + b * 64;
-            uint32_t dg[32], du[32];
+            const bool inside = col < q.N;
+            if (b == 1) ask_rows(mw, col, inside);
+            if (inside) {
+              ok = bw.wait(bar(kGBRows + warp - 4), boxes & 1u);
+              if (!ok) break;
+              ++boxes;
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t v[32];
               tmem_ld32(src + static_cast<uint32_t>(half * 128 + b * 64 + i * 32), v);
-              uint4 g4[4], u4[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int at = col + i * 32 + e * 8;
-                const bool in = mine && at < q.N;
-                g4[e] = in ? __ldg(reinterpret_cast<const uint4*>(gate + at)) : make_uint4(0, 0, 0, 0);
-                u4[e] = in ? __ldg(reinterpret_cast<const uint4*>(up + at)) : make_uint4(0, 0, 0, 0);
-              }
               tmem_wait_ld(v);
               if (b == 1 && i == 1) release(acc);
+              if (!inside) continue;
+              gemm::with_activation(p.act, [&](auto act) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint32_t gw = (&g4[e >> 2].x)[e & 3], uw = (&u4[e >> 2].x)[e & 3];
-                float g0, g1, u0, u1, a0, a1, s0, s1;
-                gemm::unpack16<IN>(gw, g0, g1);
-                gemm::unpack16<IN>(uw, u0, u1);
-                gemm::activation_slope(p.act, g0, a0, s0);
-                gemm::activation_slope(p.act, g1, a1, s1);
-                const float d0 = __uint_as_float(v[2 * e]), d1 = __uint_as_float(v[2 * e + 1]);
-                dg[i * 16 + e] = gemm::pack16<OUT>(d0 * u0 * s0, d1 * u1 * s1);
-                du[i * 16 + e] = gemm::pack16<OUT>(d0 * a0, d1 * a1);
-              }
+                for (uint32_t e = 0; e < 4; ++e) {
+                  const uint32_t unit = at + (((static_cast<uint32_t>(i) * 4u + e) ^ sw) << 4);
+                  uint32_t g4[4], u4[4];
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(g4[0]), "=r"(g4[1]), "=r"(g4[2]), "=r"(g4[3]) : "r"(unit));
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u4[0]), "=r"(u4[1]), "=r"(u4[2]), "=r"(u4[3]) : "r"(unit + kGemmStage));
+#pragma unroll
+                  for (uint32_t w = 0; w < 4; ++w) {
+                    float g0, g1, u0, u1, a0, a1, s0, s1;
+                    gemm::unpack16<IN>(g4[w], g0, g1);
+                    gemm::unpack16<IN>(u4[w], u0, u1);
+                    gemm::activation_slope<act.value>(g0, a0, s0);
+                    gemm::activation_slope<act.value>(g1, a1, s1);
+                    const float d0 = __uint_as_float(v[8 * e + 2 * w]), d1 = __uint_as_float(v[8 * e + 2 * w + 1]);
+                    g4[w] = gemm::pack16<OUT>(d0 * u0 * s0, d1 * u1 * s1);
+                    u4[w] = gemm::pack16<OUT>(d0 * a0, d1 * a1);
+                  }
+                  st_shared_v4(unit, g4[0], g4[1], g4[2], g4[3]);
+                  st_shared_v4(unit + kGemmStage, u4[0], u4[1], u4[2], u4[3]);
+                }
+              });
             }
-            stage.ready();
-            stage.put(dg);
-            stage.store(&maps.out[0], col, mw, col < q.N);
-            stage.ready();
-            stage.put(du);
-            stage.store(&maps.out[1], col, mw, col < q.N);
+            stage.store(&maps.out[0], col, mw, inside);
+            second.store(&maps.out[1], col, mw, inside);
           }
+          if (!ok) break;
         }
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
       }
     }
+    if (EPI == kEpiGateGrad && asked != boxes)  // (after a wait was given up: the boxes land before exit)
+      drain_wait(bar(kGBRows + warp - 4), (asked - 1) & 1u, p.budget_ns);
     if (lane == 0) bulk_wait_all();
   }
 
@@ -868,7 +920,10 @@ __global__ void __launch_bounds__(512) gemm_combine_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float a, s;
-          gemm::activation_slope(p.act, g[k], a, s);
+          if (p.act)
+            gemm::activation_slope<1>(g[k], a, s);
+          else
+            gemm::activation_slope<0>(g[k], a, s);
           dg[2 * e + k] = v[2 * e + k] * w[k] * s;
           du[2 * e + k] = v[2 * e + k] * a;
         }
