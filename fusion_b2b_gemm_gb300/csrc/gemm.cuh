@@ -465,11 +465,10 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
         for (int u = cid; u < p.units && ok; u += ncl) {
           const GemmUnit c = gemm_unit(p, u);
           for (int k = c.k0; k < c.k1; ++k) {
-            if (F8 || k == c.k0) {
-              ok = bw.wait1(bar(kGBAccEmpty + acc), acc_phase ^ 1u);
-              if (!ok) break;
-            }
-            ok = bw.wait1(bar(kGBFull + slot), phase);
+            // (e4m3: the accumulator is what there is to wait for)
+            if (F8) ok = bw.wait1(bar(kGBFull + slot), phase);
+            if (ok && (F8 || k == c.k0)) ok = bw.wait1(bar(kGBAccEmpty + acc), acc_phase ^ 1u);
+            if (!F8 && ok) ok = bw.wait1(bar(kGBFull + slot), phase);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem_base + acc * 256u;
@@ -482,15 +481,15 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
               else
                 mma_ss<false, 2>(d, a + s * a_step, b + s * b_step, idesc, more);
             }
-            tc_commit<2>(bar(kGBEmpty + slot));
-            if (++slot == kRing) {
-              slot = 0;
-              phase ^= 1u;
-            }
             if (F8 || k + 1 == c.k1) {
               tc_commit<2>(bar(kGBAccFull + acc));
               acc ^= 1u;
               if (acc == 0) acc_phase ^= 1u;
+            }
+            tc_commit<2>(bar(kGBEmpty + slot));
+            if (++slot == kRing) {
+              slot = 0;
+              phase ^= 1u;
             }
           }
         }
@@ -601,14 +600,18 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
           if (!ok) break;
           tc_fence_after();
           if (rows) {
-            const float fr = scales[place * 128 + row];
-            const float2 fc = *reinterpret_cast<const float2*>(scales + 3 * 128 + place * 2);
-            const float f0 = fr * (GATE || !(half & 2) ? fc.x : fc.y), f1 = GATE ? fr * fc.y : f0;
-            const uint64_t g2 = gemm::pack2(f0, f0), u2 = GATE ? gemm::pack2(f1, f1) : g2;
+            uint64_t g2, u2;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t v[16];
               tmem_ld16(lanes + acc * 256u + static_cast<uint32_t>(column(i >> 1) + (i & 1) * 16), v);
+              if (i == 0) {
+                const float fr = scales[place * 128 + row];
+                const float2 fc = *reinterpret_cast<const float2*>(scales + 3 * 128 + place * 2);
+                const float f0 = fr * (GATE || !(half & 2) ? fc.x : fc.y), f1 = GATE ? fr * fc.y : f0;
+                g2 = gemm::pack2(f0, f0);
+                u2 = GATE ? gemm::pack2(f1, f1) : g2;
+              }
               tmem_wait_ld(v);
               if (i == 3) release(acc);
 #pragma unroll
