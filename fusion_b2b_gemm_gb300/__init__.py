@@ -34,6 +34,7 @@ __all__ = [
     "b2b_scaled_ffn_plan_create", "b2b_scaled_gemm_plan_create", "b2b_ffn_plan_destroy", "b2b_ffn_plan_device_status",
     "b2b_ffn_plan_set_wait_budget", "b2b_ffn_plan_set_debug", "b2b_ffn_workspace", "b2b_ffn_forward", "b2b_ffn_backward",
     "b2b_scaled_ffn_run", "b2b_scaled_gemm_run", "b2b_quantize_blocks",
+    "b2b_ffn_units",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -106,6 +107,7 @@ def _load() -> ctypes.CDLL:
         "b2b_scaled_ffn_run": [P, P, P],
         "b2b_scaled_gemm_run": [P, P, P],
         "b2b_quantize_blocks": [i32, i64, i64, i32, P, P, P, P],
+        "b2b_ffn_units": [i32, ctypes.POINTER(i64), i32, i64, i32, ctypes.POINTER(i64), i32],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -158,6 +160,7 @@ b2b_ffn_backward = _lib.b2b_ffn_backward
 b2b_scaled_ffn_run = _lib.b2b_scaled_ffn_run
 b2b_scaled_gemm_run = _lib.b2b_scaled_gemm_run
 b2b_quantize_blocks = _lib.b2b_quantize_blocks
+b2b_ffn_units = _lib.b2b_ffn_units
 
 
 def _check(code: int, where: str) -> None:

@@ -30,7 +30,7 @@ struct b2b_ffn_plan_s {
 
 namespace {
 
-constexpr int64_t kMaxExtent = int64_t(1) << 20, kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxExtent = int64_t(1) << 20, kMaxRows = int64_t(1) << 30, kMaxTiles = int64_t(1) << 28;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t rounded(size_t bytes) { return (bytes + 255) & ~size_t(255); }
@@ -143,6 +143,24 @@ Shape cut(int64_t tiles, int64_t kpan, int clusters) {
   return best;
 }
 
+void add_problem(GemmParams& p, int64_t m, int64_t n, bool gate) {
+  GemmProblem& q = p.prob[p.problems++];
+  q.first = p.tiles;
+  q.M = static_cast<int>(m);
+  q.N = static_cast<int>(n);
+  q.m_tiles = static_cast<int>(ceil_div(m, kGemmTile));
+  q.n_tiles = static_cast<int>(ceil_div(n, gate ? 128 : kGemmTile));
+  p.tiles += q.m_tiles * q.n_tiles;
+}
+void set_units(GemmParams& p, int kpan, int clusters) {
+  const Shape s = cut(p.tiles, kpan, clusters);
+  p.kpan = kpan;
+  p.whole = static_cast<int>(s.whole);
+  p.splits = s.splits;
+  p.units = static_cast<int>(s.whole + (s.tiles - s.whole) * s.splits);
+  p.group = 8;
+}
+
 int panels(int64_t k, bool e4m3 = false) { return static_cast<int>(ceil_div(k, e4m3 ? 128 : 64)); }
 int64_t tile_count(int64_t m, int64_t n, bool gate) { return ceil_div(m, kGemmTile) * ceil_div(n, gate ? 128 : kGemmTile); }
 
@@ -168,7 +186,6 @@ struct Launch {
   GemmParams p;
   b2b_status_t st = B2B_OK;
   bool gate, e4m3;
-  int problems = 0;
 
   Launch(const b2b_ffn_plan_s* plan_, bool gate_, bool e4m3_) : plan(plan_), gate(gate_), e4m3(e4m3_) {
     std::memset(&maps, 0, sizeof(maps));
@@ -197,26 +214,12 @@ struct Launch {
     p.out[i] = t.m->data;
     p.out_ld[i] = t.m->row_stride;
   }
-  void problem(int64_t m, int64_t n) {
-    GemmProblem& q = p.prob[problems++];
-    q.first = p.tiles;
-    q.M = static_cast<int>(m);
-    q.N = static_cast<int>(n);
-    q.m_tiles = static_cast<int>(ceil_div(m, kGemmTile));
-    q.n_tiles = static_cast<int>(ceil_div(n, gate ? 128 : kGemmTile));
-    p.tiles += q.m_tiles * q.n_tiles;
-  }
+  void problem(int64_t m, int64_t n) { add_problem(p, m, n, gate); }
   b2b_status_t run(const GemmKernel& kernel, int kpan, void* parts, cudaStream_t stream) {
     if (st != B2B_OK) return st;
     const int clusters = plan->sms / 2;
-    const Shape s = cut(p.tiles, kpan, clusters);
-    p.problems = problems;
-    p.kpan = kpan;
-    p.whole = static_cast<int>(s.whole);
-    p.splits = s.splits;
-    p.units = static_cast<int>(s.whole + (s.tiles - s.whole) * s.splits);
+    set_units(p, kpan, clusters);
     p.part = static_cast<float*>(parts);
-    p.group = 8;
     p.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(plan->budget_ns, 5000ull * kpan), 4000000000ull));
     void* args[] = {&maps, &p};
     cudaError_t e = launch_pdl(kernel.main, dim3(2 * static_cast<unsigned>(std::min(p.units, clusters))), dim3(gemm_threads(e4m3)), args,
@@ -279,7 +282,6 @@ struct FewRows {
 };
 
 size_t part_bytes(const b2b_ffn_plan_s* p, int64_t tiles, int kpan) { return cut(tiles, kpan, p->sms / 2).part_bytes(); }
-constexpr int64_t kMaxTiles = int64_t(1) << 28;
 
 // Workspace of a run, its pieces one after the other.
 struct Pieces {
@@ -603,9 +605,9 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
     Launch l(p, false, false);
     auto add = [&](const Matrix& a, const Matrix& b, const Matrix& c) {
       if (!c.m->data) return;
-      l.a_cols(l.problems, a);
-      l.b_cols(l.problems, b);
-      l.out(l.problems, c);
+      l.a_cols(l.p.problems, a);
+      l.b_cols(l.p.problems, b);
+      l.out(l.p.problems, c);
       l.problem(c.rows, c.cols);
     };
     add(in[1], dg, out[1]);
@@ -729,6 +731,25 @@ b2b_status_t b2b_scaled_gemm_run(b2b_ffn_plan_t p, const b2b_scaled_gemm_t* r, b
   l.p.b_scale_k[0] = r->b_scale.block_stride;
   l.problem(m, n);
   return l.run(p->s.product[p->dtype == B2B_BF16], panels(k, true), r->workspace, reinterpret_cast<cudaStream_t>(stream_));
+}
+
+b2b_status_t b2b_ffn_units(int problems, const int64_t* sizes, int gate, int64_t kpan, int clusters, int64_t* out, int nout) {
+  if (!sizes || !out || problems < 1 || problems > kGemmMaxProblems || kpan < 1 || kpan > kMaxRows || clusters < 1) return B2B_ERR_INVALID_ARG;
+  GemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int i = 0; i < problems; ++i) {
+    const int64_t m = sizes[2 * i], n = sizes[2 * i + 1];
+    if (m < 1 || n < 1 || m > kMaxRows || n > kMaxExtent || tile_count(m, n, gate) > kMaxTiles) return B2B_ERR_INVALID_ARG;
+    add_problem(p, m, n, gate);
+  }
+  set_units(p, static_cast<int>(kpan), clusters);
+  if (nout < 1 + 6 * p.units) return B2B_ERR_INVALID_ARG;
+  *out++ = p.units;
+  for (int u = 0; u < p.units; ++u) {
+    const GemmUnit c = gemm_unit(p, u);
+    for (const int v : {c.prob, c.mt, c.nt, c.k0, c.k1, c.part}) *out++ = v;
+  }
+  return B2B_OK;
 }
 
 b2b_status_t b2b_quantize_blocks(b2b_dtype_t dtype, int64_t rows, int64_t cols, int block_rows, const b2b_matrix_t* x,

@@ -204,6 +204,19 @@ struct Wait {
   }
 };
 
+// Loads of what an earlier kernel may have written while this one had already
+// started: not through the non-coherent path.
+__device__ __forceinline__ float load(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 load(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ float sigmoid(float u) {
   float e, s;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * -1.4426950408889634f));
@@ -518,9 +531,9 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
         int next = c.k0;
         auto fetch = [&](int j) {
           if (next < c.k1) {
-            x0[j] = __ldg(a0);
-            x1[j] = __ldg(a1);
-            y[j] = __ldg(b0);
+            x0[j] = gemm::load(a0);
+            x1[j] = gemm::load(a1);
+            y[j] = gemm::load(b0);
           }
           ++next;
           a0 += p.a_scale_k;
@@ -912,8 +925,8 @@ __global__ void __launch_bounds__(512) gemm_combine_kernel(const __grid_constant
     }
   } else if constexpr (EPI == kEpiGateGrad) {
     if (in) {
-      const uint4 gw = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.gate) + m * p.gate_ld + col));
-      const uint4 uw = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.up) + m * p.up_ld + col));
+      const uint4 gw = gemm::load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.gate) + m * p.gate_ld + col));
+      const uint4 uw = gemm::load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.up) + m * p.up_ld + col));
       float dg[8], du[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

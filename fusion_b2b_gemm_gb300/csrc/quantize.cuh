@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __gr
     const long long col = kb * 128 + lane * 8;
     const bool in = row < p.rows && col < p.cols;
     uint4 w = make_uint4(0, 0, 0, 0);
-    if (in) w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.x_ld + col));
+    if (in) w = gemm::load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.x_ld + col));
     float v[8];
     uint32_t top = 0;
 #pragma unroll
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_tiles_kernel(const __g
       const long long row = row0 + 16 * i;
       w[i] = make_uint4(0, 0, 0, 0);
       if (row < p.rows && col < p.cols)
-        w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.x_ld + col));
+        w[i] = gemm::load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.x_ld + col));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float a, b;

@@ -278,9 +278,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const int r = i * 32 + lane;
-          const float a = r < p.rows ? __ldg(p.a_scale + r * p.a_scale_row + s * p.a_scale_k) : 0.0f;
+          const float a = r < p.rows ? gemm::load(p.a_scale + r * p.a_scale_row + s * p.a_scale_k) : 0.0f;
 #pragma unroll
-          for (int w = 0; w < W; ++w) next[w][i] = a * __ldg(p.b_scale[w] + nb * p.b_scale_row[w] + s * p.b_scale_k[w]);
+          for (int w = 0; w < W; ++w) next[w][i] = a * gemm::load(p.b_scale[w] + nb * p.b_scale_row[w] + s * p.b_scale_k[w]);
         }
       };
       float* scales = reinterpret_cast<float*>(gbase + L::kOffScales) + quad * 2 * NT;
@@ -331,11 +331,13 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (p.splits > 1) cluster_sync();
+  // (before the cluster's CTAs wait for each other: one of them may still wait for
+  // tensor memory that a CTA of another kernel holds, and that for this one's)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, L::kTmemCols);
   }
+  if (p.splits > 1) cluster_sync();
 
   // Rows are shared out over the slice's CTAs, a warp to a row, V columns to a lane.
   if (!*abort_flag) {

@@ -589,6 +589,16 @@ typedef struct {
 b2b_status_t b2b_scaled_gemm_run(b2b_ffn_plan_t plan, const b2b_scaled_gemm_t* run, b2b_stream_t stream);
 
 /*
+ * How the products of one launch are cut into units (test support, host only,
+ * no GPU needed), by the functions the kernels walk: sizes holds (rows, columns)
+ * of each of `problems` (at most 3) results of kpan K panels each; gate is 1 for
+ * the launch of both projections.  out receives the number of units, then for each
+ * (problem, 256-row tile, column tile, first and end K panel, number of its part
+ * or -1).  B2B_ERR_INVALID_ARG for bad arguments or too small an `out`.
+ */
+b2b_status_t b2b_ffn_units(int problems, const int64_t* sizes, int gate, int64_t kpan, int clusters, int64_t* out, int nout);
+
+/*
  * Bring a 16-bit matrix x [rows][cols] (dtype B2B_F16 or B2B_BF16, cols a
  * multiple of 8) to e4m3 with a scale for each block of block_rows (1 or 128) by
  * 128: the smallest power of two that leaves no magnitude above 448 (at least
