@@ -32,7 +32,7 @@ __all__ = [
     "b2b_shared_attention_run",
     "GatedFeedForwardPlan", "ScaledFeedForwardPlan", "ScaledGemmPlan", "quantize_blocks", "b2b_ffn_plan_create",
     "b2b_scaled_ffn_plan_create", "b2b_scaled_gemm_plan_create", "b2b_ffn_plan_destroy", "b2b_ffn_plan_device_status",
-    "b2b_ffn_plan_set_wait_budget", "b2b_ffn_plan_set_debug", "b2b_ffn_workspace", "b2b_ffn_forward", "b2b_ffn_backward",
+    "b2b_ffn_plan_set_wait_budget", "b2b_ffn_plan_set_debug", "b2b_ffn_workspace", "b2b_ffn_kept_bytes", "b2b_ffn_forward", "b2b_ffn_backward",
     "b2b_scaled_ffn_run", "b2b_scaled_gemm_run", "b2b_quantize_blocks",
     "b2b_ffn_units",
 ]
@@ -102,6 +102,7 @@ def _load() -> ctypes.CDLL:
         "b2b_ffn_plan_set_wait_budget": [P, u64],
         "b2b_ffn_plan_set_debug": [P, ctypes.c_uint32],
         "b2b_ffn_workspace": [P, i64, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "b2b_ffn_kept_bytes": [P, i64, ctypes.POINTER(ctypes.c_size_t)],
         "b2b_ffn_forward": [P, P, P],
         "b2b_ffn_backward": [P, P, P],
         "b2b_scaled_ffn_run": [P, P, P],
@@ -155,6 +156,7 @@ b2b_ffn_plan_device_status = _lib.b2b_ffn_plan_device_status
 b2b_ffn_plan_set_wait_budget = _lib.b2b_ffn_plan_set_wait_budget
 b2b_ffn_plan_set_debug = _lib.b2b_ffn_plan_set_debug
 b2b_ffn_workspace = _lib.b2b_ffn_workspace
+b2b_ffn_kept_bytes = _lib.b2b_ffn_kept_bytes
 b2b_ffn_forward = _lib.b2b_ffn_forward
 b2b_ffn_backward = _lib.b2b_ffn_backward
 b2b_scaled_ffn_run = _lib.b2b_scaled_ffn_run

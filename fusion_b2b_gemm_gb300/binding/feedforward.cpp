@@ -22,6 +22,7 @@ namespace {
 // Entries of libb2b.so, which is loaded by path.
 struct {
   decltype(&b2b_ffn_workspace) workspace;
+  decltype(&b2b_ffn_kept_bytes) kept_bytes;
   decltype(&b2b_ffn_forward) forward;
   decltype(&b2b_ffn_backward) backward;
   decltype(&b2b_scaled_ffn_run) scaled_ffn;
@@ -113,16 +114,16 @@ PyObject* forward(Bound& p, PyObject* const* arg) {
     return nullptr;
   a.tokens = x->size(0);
   if (a.tokens == 0) return nullptr;
-  at::Tensor out = fresh(p, *x, a.tokens, p.out_width, a.out), gate, up, hidden, ws;
+  at::Tensor out = fresh(p, *x, a.tokens, p.out_width, a.out), kept, ws;
   if (KEEP) {
-    gate = fresh(p, *x, a.tokens, p.hidden, a.gate);
-    up = fresh(p, *x, a.tokens, p.hidden, a.up);
-    hidden = fresh(p, *x, a.tokens, p.hidden, a.hidden);
+    if (abi.kept_bytes(p.plan, a.tokens, &a.kept_bytes) != B2B_OK) return nullptr;
+    kept = at::empty({static_cast<int64_t>(a.kept_bytes)}, x->options().dtype(c10::kByte));
+    a.kept = kept.data_ptr();
   }
   if (!workspace(p, *x, a.tokens, KEEP ? B2B_FFN_TRAINING : B2B_FFN_INFERENCE, ws, a.workspace, a.workspace_bytes)) return nullptr;
   if (abi.forward(p.plan, &a, stream_of(arg[1])) != B2B_OK) return nullptr;
   if (!KEEP) return THPVariable_Wrap(std::move(out));
-  return tuple(std::move(out), std::move(gate), std::move(up), std::move(hidden));
+  return tuple(std::move(out), std::move(kept));
 }
 
 // Gradients in new tensors.
@@ -133,11 +134,15 @@ PyObject* backward(Bound& p, PyObject* const* arg) {
   const int64_t t = a.tokens = x->size(0);
   if (t == 0 || !matrix(p, arg[2], p.type, t, p.out_width, a.dy) || !matrix(p, arg[4], p.type, p.width, p.hidden, a.w_gate) ||
       !matrix(p, arg[5], p.type, p.width, p.hidden, a.w_up) || !matrix(p, arg[6], p.type, p.hidden, p.out_width, a.w_down) ||
-      !matrix(p, arg[7], p.type, t, p.hidden, a.gate) || !matrix(p, arg[8], p.type, t, p.hidden, a.up) ||
-      !matrix(p, arg[9], p.type, t, p.hidden, a.hidden))
+      !THPVariable_Check(arg[7]))
     return nullptr;
+  const at::Tensor& kept = THPVariable_Unpack(arg[7]);
+  if (kept.scalar_type() != c10::kByte || kept.dim() != 1 || !kept.is_contiguous() || !kept.is_cuda() || kept.get_device() != p.device)
+    return nullptr;
+  a.kept = kept.data_ptr();
+  a.kept_bytes = static_cast<size_t>(kept.numel());
   at::Tensor dx, ws;
-  const int input_grad = PyObject_IsTrue(arg[10]);
+  const int input_grad = PyObject_IsTrue(arg[8]);
   if (input_grad < 0) return nullptr;
   if (input_grad) dx = fresh(p, *x, t, p.width, a.dx);
   at::Tensor dg = fresh(p, *x, p.width, p.hidden, a.dw_gate), du = fresh(p, *x, p.width, p.hidden, a.dw_up),
@@ -191,11 +196,11 @@ PyObject* guarded(PyObject*, PyObject* const* arg, Py_ssize_t n) {
 }
 
 PyObject* connect(PyObject*, PyObject* args) {
-  unsigned long long e[5];
-  if (!PyArg_ParseTuple(args, "KKKKK", &e[0], &e[1], &e[2], &e[3], &e[4])) return nullptr;
-  abi = {reinterpret_cast<decltype(abi.workspace)>(e[0]), reinterpret_cast<decltype(abi.forward)>(e[1]),
-         reinterpret_cast<decltype(abi.backward)>(e[2]), reinterpret_cast<decltype(abi.scaled_ffn)>(e[3]),
-         reinterpret_cast<decltype(abi.scaled_gemm)>(e[4])};
+  unsigned long long e[6];
+  if (!PyArg_ParseTuple(args, "KKKKKK", &e[0], &e[1], &e[2], &e[3], &e[4], &e[5])) return nullptr;
+  abi = {reinterpret_cast<decltype(abi.workspace)>(e[0]),  reinterpret_cast<decltype(abi.kept_bytes)>(e[1]),
+         reinterpret_cast<decltype(abi.forward)>(e[2]),    reinterpret_cast<decltype(abi.backward)>(e[3]),
+         reinterpret_cast<decltype(abi.scaled_ffn)>(e[4]), reinterpret_cast<decltype(abi.scaled_gemm)>(e[5])};
   Py_RETURN_NONE;
 }
 
@@ -218,11 +223,11 @@ PyMethodDef method(const char* name, const char* doc) {
 }
 
 PyMethodDef methods[] = {
-    {"connect", connect, METH_VARARGS, "addresses of the five C functions"},
+    {"connect", connect, METH_VARARGS, "addresses of the six C functions"},
     {"bind", bind, METH_VARARGS, "(plan, bf16, width, hidden, out_width, device) -> what the calls take first"},
     method<forward<false>, 6>("run", "(bound, stream, x, w_gate, w_up, w_down)"),
     method<forward<true>, 6>("forward", "(bound, stream, x, w_gate, w_up, w_down)"),
-    method<backward, 11>("backward", "(bound, stream, dy, x, w_gate, w_up, w_down, gate, up, hidden, input_grad)"),
+    method<backward, 9>("backward", "(bound, stream, dy, x, w_gate, w_up, w_down, kept, input_grad)"),
     method<scaled_ffn, 9>("scaled_ffn", "(bound, stream, x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale)"),
     method<scaled_gemm, 6>("scaled_gemm", "(bound, stream, a, a_scale, b, b_scale)"),
     {nullptr, nullptr, 0, nullptr}};

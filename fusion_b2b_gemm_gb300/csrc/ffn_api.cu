@@ -111,6 +111,7 @@ b2b_status_t check_current_device(const b2b_ffn_plan_s* p) {
   return dev == p->device ? B2B_OK : B2B_ERR_DEVICE;
 }
 
+// Memory of at least `need` bytes: a workspace, or what a forward pass kept.
 b2b_status_t check_workspace(const void* workspace, size_t bytes, size_t need) {
   if (need && (!workspace || bytes < need)) return B2B_ERR_INVALID_ARG;
   return need && !aligned(workspace, 256) ? B2B_ERR_ALIGNMENT : B2B_OK;
@@ -294,6 +295,25 @@ struct Pieces {
 
 // Up to so many rows the products of a plan (but the backward pass's) take the kernel for few rows.
 int few_rows(const b2b_ffn_plan_s* p) { return (p->kind == kFfn ? p->k.gate_few : p->s.gate_few).most_rows(); }
+
+// What a forward pass keeps: G and U, then H.
+struct Kept {
+  int64_t blocks;     // of 32 columns
+  size_t each;        // bytes of G, of U
+  size_t total;
+  Kept(const b2b_ffn_plan_s* p, int64_t tokens) {
+    blocks = ceil_div(p->hidden, 32);
+    each = static_cast<size_t>(ceil_div(tokens, 32)) * static_cast<size_t>(blocks) * 4096;
+    total = 2 * each + rounded(static_cast<size_t>(tokens) * p->hidden * 2);
+  }
+  template <class P>
+  void set(P& p, const void* kept) const {
+    p.kept_gate = static_cast<float*>(const_cast<void*>(kept));
+    p.kept_up = p.kept_gate + each / 4;
+    p.kept_blocks = static_cast<int>(blocks);
+  }
+  void* hidden(const void* kept) const { return static_cast<uint8_t*>(const_cast<void*>(kept)) + 2 * each; }
+};
 
 Pieces pieces(const b2b_ffn_plan_s* p, int64_t rows, int pass) {
   Pieces w;
@@ -485,36 +505,44 @@ b2b_status_t b2b_ffn_workspace(b2b_ffn_plan_t p, int64_t rows, int pass, size_t*
   return B2B_OK;
 }
 
+b2b_status_t b2b_ffn_kept_bytes(b2b_ffn_plan_t p, int64_t tokens, size_t* bytes) {
+  if (!p || !bytes || tokens < 0 || p->kind != kFfn) return B2B_ERR_INVALID_ARG;
+  const b2b_status_t st = check_tiles(p, tokens);
+  if (st != B2B_OK) return st;
+  *bytes = tokens ? Kept(p, tokens).total : 0;
+  return B2B_OK;
+}
+
 b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t p, const b2b_ffn_forward_t* r, b2b_stream_t stream_) {
   if (!p || !r || p->kind != kFfn || r->tokens < 0) return B2B_ERR_INVALID_ARG;
   const int64_t t = r->tokens, d = p->width, f = p->hidden, o = p->out_width;
   b2b_status_t st = check_tiles(p, t);
   if (st != B2B_OK || t == 0) return st;
-  const bool keep = r->gate.data != nullptr;
-  if (keep != (r->up.data != nullptr) || keep != (r->hidden.data != nullptr) || !r->out.data) return B2B_ERR_INVALID_ARG;
+  if (!r->out.data) return B2B_ERR_INVALID_ARG;
+  const bool keep = r->kept != nullptr;
+  const Kept kept(p, t);
+  const int64_t kept_row = keep ? static_cast<int64_t>(kept.total) : 0;
+  const b2b_matrix_t kept_bytes = {r->kept, kept_row};
   const Matrix in[] = {{&r->x, t, d, 2}, {&r->w_gate, d, f, 2}, {&r->w_up, d, f, 2}, {&r->w_down, f, o, 2}};
-  const Matrix out[] = {{&r->out, t, o, 2}, {&r->gate, t, f, 2}, {&r->up, t, f, 2}, {&r->hidden, t, f, 2}};
-  st = check_all(in, out);
+  const Matrix out[] = {{&r->out, t, o, 2}, {&kept_bytes, 1, kept_row, 1}};
+  if (keep) st = check_workspace(r->kept, r->kept_bytes, kept.total);
+  if (st == B2B_OK) st = check_all(in, out);
   const Pieces w = pieces(p, t, keep ? B2B_FFN_TRAINING : B2B_FFN_INFERENCE);
   if (st == B2B_OK) st = check_workspace(r->workspace, r->workspace_bytes, w.total());
   if (st == B2B_OK) st = check_current_device(p);
   if (st != B2B_OK) return st;
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   uint8_t* ws = static_cast<uint8_t*>(r->workspace);
-  const b2b_matrix_t scratch = {ws, f};
+  const b2b_matrix_t h_rows = {keep ? kept.hidden(r->kept) : ws, f};
   void* parts = ws + rounded(w.hidden);
-  const Matrix h = keep ? out[3] : Matrix{&scratch, t, f, 2};
+  const Matrix h = {&h_rows, t, f, 2};
   if (t <= few_rows(p)) {
     FewRows up(p, p->k.gate_few, false, in[0]);
     up.weight(0, in[1]);
     up.weight(1, in[2]);
-    up.p.out = h.m->data;
-    up.p.out_ld = h.m->row_stride;
-    up.p.keep = keep;
-    up.p.gate = r->gate.data;
-    up.p.gate_ld = r->gate.row_stride;
-    up.p.up = r->up.data;
-    up.p.up_ld = r->up.row_stride;
+    up.p.out = h_rows.data;
+    up.p.out_ld = f;
+    if (keep) kept.set(up.p, r->kept);
     st = up.run(stream);
     if (st != B2B_OK) return st;
     FewRows down(p, p->k.down_few, false, h);
@@ -529,11 +557,7 @@ b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t p, const b2b_ffn_forward_t* r, b2b_s
     l.b_cols(0, in[1]);
     l.b_cols(1, in[2]);
     l.out(0, h);
-    if (keep) {
-      l.out(1, out[1]);
-      l.out(2, out[2]);
-    }
-    l.p.keep = keep;
+    if (keep) kept.set(l.p, r->kept);
     l.problem(t, f);
     st = l.run(p->k.gate, panels(d), parts, stream);
   }
@@ -552,10 +576,15 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
   b2b_status_t st = check_tiles(p, t);
   if (st != B2B_OK) return st;
   const int gsz = r->accumulate ? 4 : 2;
-  const Matrix in[] = {{&r->dy, t, o, 2},     {&r->x, t, d, 2},    {&r->w_gate, d, f, 2}, {&r->w_up, d, f, 2},
-                       {&r->w_down, f, o, 2}, {&r->gate, t, f, 2}, {&r->up, t, f, 2},     {&r->hidden, t, f, 2}};
+  const Kept kept(p, t);
+  const int64_t kept_row = t ? static_cast<int64_t>(kept.total) : 0;
+  const b2b_matrix_t kept_bytes = {const_cast<void*>(r->kept), kept_row}, h_rows = {kept.hidden(r->kept), f};
+  const Matrix in[] = {{&r->dy, t, o, 2},   {&r->x, t, d, 2},      {&r->w_gate, d, f, 2},
+                       {&r->w_up, d, f, 2}, {&r->w_down, f, o, 2}, {&kept_bytes, t ? 1 : 0, kept_row, 1}};
+  const Matrix h = {&h_rows, t, f, 2};
   const Matrix out[] = {{&r->dx, t, d, 2}, {&r->dw_gate, d, f, gsz}, {&r->dw_up, d, f, gsz}, {&r->dw_down, f, o, gsz}};
-  st = check_all(in, out);
+  if (t) st = check_workspace(r->kept, r->kept_bytes, kept.total);
+  if (st == B2B_OK) st = check_all(in, out);
   const Pieces w = pieces(p, t, B2B_FFN_BACKWARD);
   if (st == B2B_OK) st = check_workspace(r->workspace, r->workspace_bytes, t ? w.total() : 0);
   if (st == B2B_OK) st = check_current_device(p);
@@ -581,12 +610,7 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
     l.b_rows(0, in[4]);
     l.out(0, dg);
     l.out(1, du);
-    l.map(&l.maps.out[2], type16(p), in[5], 64, 32);
-    l.map(&l.maps.a[2], type16(p), in[6], 64, 32);
-    l.p.gate = r->gate.data;
-    l.p.gate_ld = r->gate.row_stride;
-    l.p.up = r->up.data;
-    l.p.up_ld = r->up.row_stride;
+    kept.set(l.p, r->kept);
     l.problem(t, f);
     st = l.run(p->k.gate_grad, panels(o), parts, stream);
   }
@@ -612,7 +636,7 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
     };
     add(in[1], dg, out[1]);
     add(in[1], du, out[2]);
-    add(in[7], in[0], out[3]);
+    add(h, in[0], out[3]);
     st = l.run(r->accumulate ? p->k.dw_add : p->k.dw, panels(t), parts, stream);
   }
   return st;

@@ -3,13 +3,19 @@
 //
 //   kEpiStore      D = A.B
 //   kEpiAdd        D += A.B                       (fp32 D)
-//   kEpiGate       H = act(A.Bg) * (A.Bu)         (and, kept for the backward pass, A.Bg and A.Bu)
+//   kEpiGate       H = act(A.Bg) * (A.Bu)         (and, kept for the backward pass, G = A.Bg and U = A.Bu)
 //   kEpiGateGrad   dU = (A.B) act(G), dG = (A.B) U act'(G)
 //   kEpiGateQuant  as kEpiGate, brought to e4m3 with a scale for each 128 of a row
 //
 // act(g) = g s(u(g)), s(u) = 1 / (1 + e^-u), u = g (silu) or 2 sqrt(2/pi) (g +
 // 0.044715 g^3) (gelu, tanh form: (1 + tanh z) / 2 = s(2 z)), and act'(g) =
 // s + g s (1 - s) u'(g).
+//
+// G and U are kept in fp32: with both rounded to 16 bits the gradients that come
+// of them were 1.8 times as far off as their own two roundings make them.  They
+// are kept in blocks of 32 rows by 32 columns, four columns of every row together
+// (gemm_kept_at), so that a warp of the epilogue, a row to a lane, writes and
+// reads 512 consecutive bytes.
 //
 // A pair of CTAs computes a tile of 256 rows by 256 columns: each CTA holds 128
 // rows of A and of the accumulator, and half of B's columns.  In kEpiGate the
@@ -86,8 +92,7 @@ enum : int {  // barrier slots (8 bytes each)
   kGBAccEmpty = 18,  // [2] accumulator read in both CTAs (even CTA's)
   kGBDrain = 20,
   kGBTop = 21,       // [4] the warps of a quadrant have written their rows' largest magnitudes
-  kGBRows = 21,      // [8] (kEpiGateGrad) a warp's boxes of the gate's and the other projection's values landed
-  kGSlotTmem = 29,   // uint32 tensor-memory base, then the int abort flag
+  kGSlotTmem = 25,   // uint32 tensor-memory base, then the int abort flag
 };
 
 // One product of a launch: D [M][N].  Tiles are numbered problem after problem.
@@ -108,11 +113,10 @@ struct GemmParams {
   int a_box_rows;     // rows of A's boxes (fewer than 128 for few rows: the others are never looked at)
   int group;          // 256-row tiles that share a pass over the columns
   int act;            // activation: 0 silu, 1 gelu
-  int keep;           // kEpiGate: store gate and up as well
-  // kEpiGateGrad: the gate's and the other projection's values, as gemm_combine_kernel reads them
-  const void* gate;
-  const void* up;
-  long long gate_ld, up_ld;
+  // G and U, of kept_blocks blocks of 32 columns (kEpiGate: null, or written; kEpiGateGrad: read)
+  float* kept_gate;
+  float* kept_up;
+  int kept_blocks;
   // e4m3: scales of A's rows and of B's blocks of 128 columns ([0]; [1]: the other projection's)
   const float* a_scale;
   long long a_scale_row, a_scale_k;
@@ -133,7 +137,7 @@ struct GemmParams {
 };
 
 struct GemmMaps {
-  CUtensorMap a[kGemmMaxProblems], b[kGemmMaxProblems], out[kGemmMaxProblems];  // (kEpiGateGrad: out[2] and a[2] are of the gate's and the other's values)
+  CUtensorMap a[kGemmMaxProblems], b[kGemmMaxProblems], out[kGemmMaxProblems];
 };
 
 struct GemmUnit {
@@ -175,6 +179,11 @@ __host__ __device__ __forceinline__ GemmUnit gemm_unit(const GemmParams& p, int 
 // then rows, so that the 32 rows of a warp are consecutive.
 __host__ __device__ __forceinline__ long long gemm_part_at(int part, int row, int col4) {
   return ((static_cast<long long>(part) * 2 + (row >> 7)) * (kGemmTile / 4) + col4) * 512 + (row & 127) * 4;
+}
+
+// Float of a kept matrix of `blocks` blocks of 32 columns.
+__host__ __device__ __forceinline__ long long gemm_kept_at(int row, int col, int blocks) {
+  return (static_cast<long long>(row >> 5) * blocks + (col >> 5)) * 1024 + ((col & 31) >> 2) * 128 + (row & 31) * 4 + (col & 3);
 }
 
 namespace gemm {
@@ -381,8 +390,8 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
     } else if (lane == 10) {
       mbar_init(bar(kGBDrain), 1);
       *abort_flag = 0;
-    } else if (lane < 19) {
-      mbar_init(bar(kGBRows + lane - 11), EPI == kEpiGateQuant ? 4 : 1);  // (the first four are kGBTop)
+    } else if (lane < 15) {
+      mbar_init(bar(kGBTop + lane - 11), 4);
     }
     fence_barrier_init();
   } else if (warp == 2) {
@@ -580,18 +589,17 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
       if constexpr (F8) return GATE ? i * 128 + half * 32 : half * 64 + i * 32;
       return GATE ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * 128 + i * 32;
     };
-    // kEpiGateGrad: bring gate and up of a box, once what left its places has been read
-    uint32_t asked = 0, boxes = 0;
-    auto ask_rows = [&](int at_row, int col, bool inside) {
-      if (inside) ++asked;
-      if (lane == 0 && inside) {
-        bulk_wait_read<0>();
-        const uint32_t full = bar(kGBRows + warp - 4);
-        mbar_arrive_expect_tx(full, 2 * kGemmStage);
-        tma_load_2d(stage.addr, &maps.out[2], full, col, at_row);
-        tma_load_2d(stage.addr + kGemmStage, &maps.a[2], full, col, at_row);
+    // kEpiGateGrad: G and U of 16 columns of this lane's row
+    uint4 next_gate[4], next_up[4];
+    auto fetch_kept = [&](int at_row, int col, int limit) {
+      if (col < limit) {
+        const long long at = gemm_kept_at(at_row + lane, col, p.kept_blocks);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          next_gate[e] = gemm::load(reinterpret_cast<const uint4*>(p.kept_gate + at + e * 128));
+          next_up[e] = gemm::load(reinterpret_cast<const uint4*>(p.kept_up + at + e * 128));
+        }
       }
-      __syncwarp();
     };
     uint32_t acc = 0, acc_phase = 0, tops = 0, place = 0;
     bool ok = true;
@@ -711,7 +719,7 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
           }
         }
       } else {
-        if (EPI == kEpiGateGrad && rows && !part) ask_rows(mw, c.nt * kGemmTile + half * 128, c.nt * kGemmTile + half * 128 < q.N);
+        if (EPI == kEpiGateGrad && rows && !part) fetch_kept(mw, c.nt * kGemmTile + half * 128, q.N);
         ok = bw.wait(bar(kGBAccFull + acc), acc_phase);
         if (!ok) break;
         tc_fence_after();
@@ -761,7 +769,6 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
           }
         } else if constexpr (EPI == kEpiGate) {
           const int col = c.nt * 128 + half * 64;
-          const bool inside = col < q.N;
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -770,6 +777,15 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
             tmem_ld32(src + static_cast<uint32_t>(column(i + 2)), v);
             tmem_wait_ld(g);
             tmem_wait_ld(v);
+            if (i == 1) release(acc);
+            if (p.kept_gate && col + i * 32 < q.N) {
+              const long long at = gemm_kept_at(mw + lane, col + i * 32, p.kept_blocks);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                *reinterpret_cast<uint4*>(p.kept_gate + at + e * 128) = make_uint4(g[4 * e], g[4 * e + 1], g[4 * e + 2], g[4 * e + 3]);
+                *reinterpret_cast<uint4*>(p.kept_up + at + e * 128) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+              }
+            }
             gemm::with_activation(p.act, [&](auto act) {
 #pragma unroll
               for (int e = 0; e < 16; ++e)
@@ -777,81 +793,59 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
                                                   gemm::activation<act.value>(__uint_as_float(g[2 * e + 1])) * __uint_as_float(v[2 * e + 1]));
             });
           }
-          if (!p.keep) release(acc);
           stage.ready();
           stage.put(w);
-          stage.store(&maps.out[0], col, mw, inside);
-          if (p.keep) {
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-              uint32_t v0[32], v1[32];
-              tmem_ld32(src + static_cast<uint32_t>(column(2 * b)), v0);
-              tmem_ld32(src + static_cast<uint32_t>(column(2 * b + 1)), v1);
-              tmem_wait_ld(v0);
-              tmem_wait_ld(v1);
-              if (b == 1) release(acc);
-              stage.ready();
-              store_output_row<OUT == kGemmF16 ? kOutF16 : kOutBF16>(stage.addr, lane, 0, v0);
-              store_output_row<OUT == kGemmF16 ? kOutF16 : kOutBF16>(stage.addr, lane, 32, v1);
-              stage.store(&maps.out[1 + b], col, mw, inside);
-            }
-          }
+          stage.store(&maps.out[0], col, mw, col < q.N);
         } else {
-          // Boxes of 64 columns: gate and up were asked for (box 0: before the wait for the
-          // product) into the places that dG and dU then take.
+          // 16 columns at a time, G and U of the next ones on their way (of the first ones, since before
+          // the wait); dG and dU to two boxes.
           const gemm::Stage second{stage.addr + kGemmStage, lane};
           const uint32_t sw = static_cast<uint32_t>(lane & 7), at = stage.addr + static_cast<uint32_t>(lane) * 128u;
+          stage.ready();
 #pragma unroll 1
-          for (int b = 0; b < 2; ++b) {
-            const int col = c.nt * kGemmTile + half * 128 + b * 64;
-            const bool inside = col < q.N;
-            if (b == 1) ask_rows(mw, col, inside);
-            if (inside) {
-              ok = bw.wait(bar(kGBRows + warp - 4), boxes & 1u);
-              if (!ok) break;
-              ++boxes;
+          for (int i = 0; i < 8; ++i) {
+            uint32_t v[16];
+            tmem_ld16(src + static_cast<uint32_t>(half * 128 + i * 16), v);
+            uint4 g[4], u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              g[e] = next_gate[e];
+              u[e] = next_up[e];
             }
+            fetch_kept(mw, c.nt * kGemmTile + half * 128 + (i + 1) * 16, i < 7 ? q.N : 0);
+            tmem_wait_ld(v);
+            if (i == 7) release(acc);
+            gemm::with_activation(p.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t v[32];
-              tmem_ld32(src + static_cast<uint32_t>(half * 128 + b * 64 + i * 32), v);
-              tmem_wait_ld(v);
-              if (b == 1 && i == 1) release(acc);
-              if (!inside) continue;
-              gemm::with_activation(p.act, [&](auto act) {
+              for (uint32_t h = 0; h < 2; ++h) {
+                uint32_t dg[4], du[4];
 #pragma unroll
-                for (uint32_t e = 0; e < 4; ++e) {
-                  const uint32_t unit = at + (((static_cast<uint32_t>(i) * 4u + e) ^ sw) << 4);
-                  uint32_t g4[4], u4[4];
-                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(g4[0]), "=r"(g4[1]), "=r"(g4[2]), "=r"(g4[3]) : "r"(unit));
-                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u4[0]), "=r"(u4[1]), "=r"(u4[2]), "=r"(u4[3]) : "r"(unit + kGemmStage));
-#pragma unroll
-                  for (uint32_t w = 0; w < 4; ++w) {
-                    float g0, g1, u0, u1, a0, a1, s0, s1;
-                    gemm::unpack16<IN>(g4[w], g0, g1);
-                    gemm::unpack16<IN>(u4[w], u0, u1);
-                    gemm::activation_slope<act.value>(g0, a0, s0);
-                    gemm::activation_slope<act.value>(g1, a1, s1);
-                    const float d0 = __uint_as_float(v[8 * e + 2 * w]), d1 = __uint_as_float(v[8 * e + 2 * w + 1]);
-                    g4[w] = gemm::pack16<OUT>(d0 * u0 * s0, d1 * u1 * s1);
-                    u4[w] = gemm::pack16<OUT>(d0 * a0, d1 * a1);
-                  }
-                  st_shared_v4(unit, g4[0], g4[1], g4[2], g4[3]);
-                  st_shared_v4(unit + kGemmStage, u4[0], u4[1], u4[2], u4[3]);
+                for (uint32_t w = 0; w < 4; ++w) {
+                  float a0, a1, s0, s1;
+                  const uint4 &gw = g[2 * h + w / 2], &uw = u[2 * h + w / 2];
+                  gemm::activation_slope<act.value>(__uint_as_float(w & 1 ? gw.z : gw.x), a0, s0);
+                  gemm::activation_slope<act.value>(__uint_as_float(w & 1 ? gw.w : gw.y), a1, s1);
+                  const float d0 = __uint_as_float(v[8 * h + 2 * w]), d1 = __uint_as_float(v[8 * h + 2 * w + 1]);
+                  dg[w] = gemm::pack16<OUT>(d0 * __uint_as_float(w & 1 ? uw.z : uw.x) * s0, d1 * __uint_as_float(w & 1 ? uw.w : uw.y) * s1);
+                  du[w] = gemm::pack16<OUT>(d0 * a0, d1 * a1);
                 }
-              });
+                const uint32_t unit = at + (((static_cast<uint32_t>(i & 3) * 2u + h) ^ sw) << 4);
+                st_shared_v4(unit, dg[0], dg[1], dg[2], dg[3]);
+                st_shared_v4(unit + kGemmStage, du[0], du[1], du[2], du[3]);
+              }
+            });
+            if ((i & 3) == 3) {
+              const int col = c.nt * kGemmTile + half * 128 + (i >> 2) * 64;
+              stage.store(&maps.out[0], col, mw, col < q.N);
+              second.store(&maps.out[1], col, mw, col < q.N);
+              if (i == 3) stage.ready();
             }
-            stage.store(&maps.out[0], col, mw, inside);
-            second.store(&maps.out[1], col, mw, inside);
           }
-          if (!ok) break;
         }
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
       }
     }
-    if (EPI == kEpiGateGrad && asked != boxes)  // (after a wait was given up: the boxes land before exit)
-      drain_wait(bar(kGBRows + warp - 4), (asked - 1) & 1u, p.budget_ns);
     if (lane == 0) bulk_wait_all();
   }
 
@@ -925,23 +919,22 @@ __global__ void __launch_bounds__(512) gemm_combine_kernel(const __grid_constant
     }
   } else if constexpr (EPI == kEpiGateGrad) {
     if (in) {
-      const uint4 gw = gemm::load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.gate) + m * p.gate_ld + col));
-      const uint4 uw = gemm::load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.up) + m * p.up_ld + col));
+      const long long at = gemm_kept_at(m, col, p.kept_blocks);
       float dg[8], du[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float g[2], w[2];
-        gemm::unpack16<OUT>((&gw.x)[e], g[0], g[1]);
-        gemm::unpack16<OUT>((&uw.x)[e], w[0], w[1]);
+      for (int h = 0; h < 2; ++h) {
+        const uint4 gw = gemm::load(reinterpret_cast<const uint4*>(p.kept_gate + at + h * 128));
+        const uint4 uw = gemm::load(reinterpret_cast<const uint4*>(p.kept_up + at + h * 128));
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
+          const float g = __uint_as_float((&gw.x)[k]);
           float a, s;
           if (p.act)
-            gemm::activation_slope<1>(g[k], a, s);
+            gemm::activation_slope<1>(g, a, s);
           else
-            gemm::activation_slope<0>(g[k], a, s);
-          dg[2 * e + k] = v[2 * e + k] * w[k] * s;
-          du[2 * e + k] = v[2 * e + k] * a;
+            gemm::activation_slope<0>(g, a, s);
+          dg[4 * h + k] = v[4 * h + k] * __uint_as_float((&uw.x)[k]) * s;
+          du[4 * h + k] = v[4 * h + k] * a;
         }
       }
       store16(0, dg);
@@ -954,9 +947,13 @@ __global__ void __launch_bounds__(512) gemm_combine_kernel(const __grid_constant
     if constexpr (EPI == kEpiGate) {
       if (in) {
         store16(0, h);
-        if (p.keep) {
-          store16(1, v);
-          store16(2, v + 8);
+        if (p.kept_gate) {
+          const long long at = gemm_kept_at(m, col, p.kept_blocks);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            *reinterpret_cast<float4*>(p.kept_gate + at + e * 128) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            *reinterpret_cast<float4*>(p.kept_up + at + e * 128) = make_float4(v[8 + 4 * e], v[9 + 4 * e], v[10 + 4 * e], v[11 + 4 * e]);
+          }
         }
       }
     } else {

@@ -39,12 +39,12 @@ struct SkinnyParams {
   int slots;          // panels of the whole of k
   int splits;         // CTAs of a slice
   int x_box_rows;
-  int act, keep;
+  int act;
   void* out;          // h (or, e4m3 gate, its values), or the product
   long long out_ld;
-  void* gate;         // kept
-  void* up;
-  long long gate_ld, up_ld;
+  float* kept_gate;   // as GemmParams
+  float* kept_up;
+  int kept_blocks;
   const float* a_scale;
   long long a_scale_row, a_scale_k;
   const float* b_scale[2];
@@ -380,9 +380,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
           if (lane == 0) p.q_scale[col0 / 128 * p.q_scale_ld + r] = scale;
         } else if (in) {
           *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) = gemm::pack16<OUT>(h[0], h[1]);
-          if (p.keep) {
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.gate) + r * p.gate_ld + col) = gemm::pack16<OUT>(v[0][0], v[0][1]);
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.up) + r * p.up_ld + col) = gemm::pack16<OUT>(v[1][0], v[1][1]);
+          if (p.kept_gate) {
+            const long long kept = gemm_kept_at(r, col, p.kept_blocks);
+            *reinterpret_cast<float2*>(p.kept_gate + kept) = make_float2(v[0][0], v[0][1]);
+            *reinterpret_cast<float2*>(p.kept_up + kept) = make_float2(v[1][0], v[1][1]);
           }
         }
       }

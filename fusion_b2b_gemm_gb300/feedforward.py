@@ -20,11 +20,10 @@ import importlib.util
 import os
 import struct
 import warnings
-from typing import NamedTuple
 
 from . import DTYPES, _check, _current_device, _lib, _stream_handle, library_path
 
-__all__ = ["GatedFeedForwardPlan", "ScaledFeedForwardPlan", "ScaledGemmPlan", "quantize_blocks", "KeptActivations", "ACTIVATIONS"]
+__all__ = ["GatedFeedForwardPlan", "ScaledFeedForwardPlan", "ScaledGemmPlan", "quantize_blocks", "ACTIVATIONS"]
 
 ACTIVATIONS = {"silu": 0, "gelu": 1}  # b2b_activation_t; gelu in its tanh form
 BLOCK = 128
@@ -36,21 +35,12 @@ torch = _raw_stream = _binding = None
 
 # The argument structures, whose members all take eight bytes (b2b_matrix_t: data, row_stride; b2b_scales_t: data,
 # row_stride, block_stride), as the C functions read them.
-_forward_run = struct.Struct("19q").pack   # tokens; x, w_gate, w_up, w_down, out, gate, up, hidden; workspace, bytes
-_backward_run = struct.Struct("28q").pack  # tokens, accumulate; dy, x, three weights, gate, up, hidden, four gradients; ..
+_forward_run = struct.Struct("15q").pack   # tokens; x, w_gate, w_up, w_down, out; kept, bytes; workspace, bytes
+_backward_run = struct.Struct("24q").pack  # tokens, accumulate; dy, x, three weights; kept, bytes; four gradients; workspace, bytes
 _scaled_run = struct.Struct("22q").pack    # tokens; x, three weights, out; three scales; workspace, bytes
 _product_run = struct.Struct("15q").pack   # rows; a, b, out; two scales; workspace, bytes
 _matrix = struct.Struct("2q").pack
 _scales = struct.Struct("3q").pack
-
-
-class KeptActivations(NamedTuple):
-    """What ``GatedFeedForwardPlan.forward`` keeps for ``backward``, each [tokens, hidden]: the two projections and
-    act(gate) * up."""
-
-    gate: "torch.Tensor"
-    up: "torch.Tensor"
-    hidden: "torch.Tensor"
 
 
 class _NoBinding:
@@ -77,7 +67,8 @@ def _load_binding():
                       "(python fusion_b2b_gemm_gb300/_build.py)", RuntimeWarning, stacklevel=5)
         return _NoBinding
     module.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        _lib.b2b_ffn_workspace, _lib.b2b_ffn_forward, _lib.b2b_ffn_backward, _lib.b2b_scaled_ffn_run, _lib.b2b_scaled_gemm_run)))
+        _lib.b2b_ffn_workspace, _lib.b2b_ffn_kept_bytes, _lib.b2b_ffn_forward, _lib.b2b_ffn_backward, _lib.b2b_scaled_ffn_run,
+        _lib.b2b_scaled_gemm_run)))
     return module
 
 
@@ -259,39 +250,44 @@ class GatedFeedForwardPlan(_Plan):
         self._no_gradient(x, w_gate, w_up, w_down)
         out, oa = self._result(x, tokens, out)
         ws, wsp, need = self._workspace(x, tokens)
-        self._call(_lib.b2b_ffn_forward, _forward_run(tokens, *operands, *oa, 0, 0, 0, 0, 0, 0, wsp, need))
+        self._call(_lib.b2b_ffn_forward, _forward_run(tokens, *operands, *oa, 0, 0, wsp, need))
         return out
 
     def forward(self, x, w_gate, w_up, w_down, out=None, kept=None, stream=None):
-        """As ``run``; returns ``(out, kept)``, what ``backward`` needs (``kept``: tensors for it, as an earlier call
-        returned)."""
+        """As ``run``; returns ``(out, kept)``.  ``kept`` is what ``backward`` needs, a torch.uint8 tensor whose order is the
+        kernels' own (10 bytes a token and hidden column); one that an earlier call on as many tokens returned may be given
+        to be written again."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 done = self.forward(x, w_gate, w_up, w_down, out, kept)
-            _kept(stream, self.device_index, (done[0], *done[1]), (x, w_gate, w_up, w_down, out, *(kept or ())))
+            _kept(stream, self.device_index, done, (x, w_gate, w_up, w_down, out, kept))
             return done
         if out is None and kept is None:
             done = _binding.forward(self._bound, _raw_stream(self.device_index), x, w_gate, w_up, w_down)
             if done is not None:
-                return done[0], KeptActivations(*done[1:])
+                return done
         tokens, operands = self._operands(x, w_gate, w_up, w_down)
         self._no_gradient(x, w_gate, w_up, w_down)
         out, oa = self._result(x, tokens, out)
         if kept is None:
-            kept = (self._new(x, tokens, self.hidden) for _ in range(3))
-        kept = KeptActivations(*kept)
-        ka = self._kept_args(kept, tokens)
+            n = ctypes.c_size_t()
+            _check(_lib.b2b_ffn_kept_bytes(self._h, tokens, ctypes.byref(n)), "b2b_ffn_kept_bytes")
+            kept = torch.empty(n.value, dtype=torch.uint8, device=x.device)
+        ka = self._kept_args(kept)
         if tokens == 0:  # (no address: nothing to keep)
             return out, kept
         ws, wsp, need = self._workspace(x, tokens, _TRAINING)
         self._call(_lib.b2b_ffn_forward, _forward_run(tokens, *operands, *oa, *ka, wsp, need))
         return out, kept
 
-    def _kept_args(self, kept, tokens):
-        args = []
-        for name, t in zip(KeptActivations._fields, kept):
-            args += _rows(name, t, self._torch_dtype, tokens, self.hidden, self.device_index)[1:]
-        return args
+    def _kept_args(self, kept):
+        if not isinstance(kept, torch.Tensor) or kept.dtype is not torch.uint8:
+            raise TypeError(f"kept: {getattr(kept, 'dtype', type(kept).__name__)} given, what forward() returned expected")
+        if kept.dim() != 1 or not kept.is_contiguous():
+            raise ValueError(f"kept: shape {tuple(kept.shape)} given, what forward() returned expected")
+        if kept.get_device() != self.device_index:
+            raise ValueError(f"kept is on {kept.device}, the plan on cuda:{self.device_index}")
+        return kept.data_ptr(), kept.numel()
 
     def backward(self, dy, x, w_gate, w_up, w_down, kept, input_grad: bool = True, weight_grads=True, stream=None):
         """Gradients ``(dx, dw_gate, dw_up, dw_down)`` for ``dy``, the gradient of ``forward``'s output.
@@ -305,17 +301,16 @@ class GatedFeedForwardPlan(_Plan):
         if stream is not None:
             with torch.cuda.stream(stream):
                 done = self.backward(dy, x, w_gate, w_up, w_down, kept, input_grad, weight_grads)
-            _kept(stream, self.device_index, done, (dy, x, w_gate, w_up, w_down, *kept))
+            _kept(stream, self.device_index, done, (dy, x, w_gate, w_up, w_down, kept))
             return done
         if weight_grads is True:
-            done = _binding.backward(self._bound, _raw_stream(self.device_index), dy, x, w_gate, w_up, w_down, *kept, input_grad)
+            done = _binding.backward(self._bound, _raw_stream(self.device_index), dy, x, w_gate, w_up, w_down, kept, input_grad)
             if done is not None:
                 return done
         tokens, (xp, xs, *weights) = self._operands(x, w_gate, w_up, w_down)
         dya = _rows("dy", dy, self._torch_dtype, tokens, self.out_width, self.device_index)[1:]
-        kept = KeptActivations(*kept)
-        ka = self._kept_args(kept, tokens)
-        self._no_gradient(dy, x, w_gate, w_up, w_down, *kept)
+        ka = self._kept_args(kept)
+        self._no_gradient(dy, x, w_gate, w_up, w_down)
         dx = self._new(x, tokens, self.width) if input_grad else None
         shapes = (self.width, self.hidden), (self.width, self.hidden), (self.hidden, self.out_width)
         accumulate = not isinstance(weight_grads, bool)

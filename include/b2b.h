@@ -464,9 +464,8 @@ b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t plan, const b2b_shared_att
  *   b2b_scaled_gemm_plan_create  one product of such operands
  *
  *   - Products are accumulated in fp32; activations and their slopes are fp32
- *     functions of fp32 sums (in the backward pass: of the kept 16-bit values).
- *     Intermediates that a GEMM reads are rounded to its operand type, results
- *     once to theirs.
+ *     functions of fp32 sums, in the backward pass too.  Intermediates that a GEMM
+ *     reads are rounded to its operand type, results once to theirs.
  *   - Where few tiles would leave SMs idle, products are cut along k and the
  *     parts joined in fp32 in a fixed order: equal inputs give equal bits.
  *   - A plan is not modified by a run: runs on several streams may overlap, each
@@ -522,21 +521,25 @@ b2b_status_t b2b_ffn_plan_set_debug(b2b_ffn_plan_t plan, uint32_t flags);
  * run alone until it has finished, 256-byte aligned, of any contents.  pass is
  * one of these (B2B_FFN_INFERENCE for the scaled plans). */
 #define B2B_FFN_INFERENCE 0 /* b2b_ffn_forward that keeps nothing */
-#define B2B_FFN_TRAINING 1  /* b2b_ffn_forward that keeps gate, up and hidden */
+#define B2B_FFN_TRAINING 1  /* b2b_ffn_forward that keeps what the backward pass needs */
 #define B2B_FFN_BACKWARD 2
 b2b_status_t b2b_ffn_workspace(b2b_ffn_plan_t plan, int64_t rows, int pass, size_t* bytes);
 
+/* Bytes of what a forward pass on `tokens` rows keeps for the backward pass: X.Wg
+ * and X.Wu in fp32 and H in the plan's type, in an order of the library's own. */
+b2b_status_t b2b_ffn_kept_bytes(b2b_ffn_plan_t plan, int64_t tokens, size_t* bytes);
+
 /*
  * Y of `tokens` rows of X.
- *   gate, up, hidden   NULL data, or [tokens][hidden] matrices that receive X.Wg,
- *                      X.Wu and H, rounded to the plan's type, for the backward
- *                      pass: all three or none.
- * Outputs must overlap neither inputs nor each other.
+ *   kept        NULL, or device memory of at least b2b_ffn_kept_bytes, 256-byte
+ *               aligned, that receives what the backward pass needs.
+ * The outputs must overlap neither inputs nor each other.
  */
 typedef struct {
   int64_t tokens;
   b2b_matrix_t x, w_gate, w_up, w_down, out;
-  b2b_matrix_t gate, up, hidden;
+  void* kept;
+  size_t kept_bytes;
   void* workspace;
   size_t workspace_bytes;
 } b2b_ffn_forward_t;
@@ -546,7 +549,7 @@ b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t plan, const b2b_ffn_forward_t* run, 
  * Gradients of the block for dy, the gradient of its Y:
  *   dU = dH * act(G), dG = dH * U * act'(G), with dH = dY.Wd^T;
  *   dX = dG.Wg^T + dU.Wu^T; dWg = X^T.dG; dWu = X^T.dU; dWd = H^T.dY.
- *   x, weights, gate, up, hidden   what the forward pass read and kept.
+ *   x, weights, kept   what the forward pass read and kept.
  *   accumulate   0: weight gradients in the plan's type.  Else fp32 matrices to
  *                which they are added.
  * dx, and any of the weight gradients, may have NULL data: not computed.  dG and
@@ -554,7 +557,9 @@ b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t plan, const b2b_ffn_forward_t* run, 
  */
 typedef struct {
   int64_t tokens, accumulate;
-  b2b_matrix_t dy, x, w_gate, w_up, w_down, gate, up, hidden;
+  b2b_matrix_t dy, x, w_gate, w_up, w_down;
+  const void* kept;
+  size_t kept_bytes;
   b2b_matrix_t dx, dw_gate, dw_up, dw_down;
   void* workspace;
   size_t workspace_bytes;

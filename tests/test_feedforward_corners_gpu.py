@@ -61,11 +61,8 @@ def test_column_ranges_of_wider_buffers(t):
     assert plan.run(xs, *ws, out=out) is out
     assert torch.equal(out, y)
     untouched(buf, 24, 72, 5.0)
-    ks = [within(t, 264, torch.bfloat16, 8, 8, 3.0) for _ in range(3)]
-    y2, kept2 = plan.forward(xs, *ws, kept=[k for k, _ in ks])
-    assert torch.equal(y2, y) and all(torch.equal(a, b) for a, b in zip(kept, kept2))
-    for k, b in ks:
-        untouched(b, 8, 264, 3.0)
+    y2, kept2 = plan.forward(xs, *ws, kept=torch.empty_like(kept))
+    assert torch.equal(y2, y)
     dys = within(t, 72, torch.bfloat16, 8, 0, 2.0)[0]
     dys.copy_(dy)
     for a, b in zip(plan.backward(dys, xs, *ws, kept2), grads):
@@ -91,8 +88,8 @@ def test_scaled_operands_in_wider_buffers(rows):
 
 
 # ------------------------------------------------------------------------ training
-def check_grads(plan, dtype, dy, x, w, kept, grads, kind="silu", before=None):
-    wants = want_backward(dy, x, *w, kept, kind, dtype)
+def check_grads(dtype, dy, x, w, grads, kind="silu", before=None):
+    wants = want_backward(dy, x, *w, kind, dtype)
     for i, (v, got) in enumerate(zip(wants, grads)):
         if got is None:
             continue
@@ -115,11 +112,11 @@ def test_weight_gradients_added_to_fp32(t, dtype):
     last = both[:, 784:].clone()
     dx, *got = plan.backward(dy, x, *w, kept, weight_grads=grads)
     assert all(a is b for a, b in zip(got, grads)) and torch.equal(both[:, 784:], last)
-    check_grads(plan, dtype, dy, x, w, kept, (dx, *got), before=before)
+    check_grads(dtype, dy, x, w, (dx, *got), before=before)
     # a second microbatch on top
     middle = [z.clone() for z in grads]
     plan.backward(dy, x, *w, kept, input_grad=False, weight_grads=grads)
-    check_grads(plan, dtype, dy, x, w, kept, (None, *grads), before=middle)
+    check_grads(dtype, dy, x, w, (None, *grads), before=middle)
 
 
 def test_gradients_left_out():
@@ -143,10 +140,7 @@ def test_gradients_left_out():
 def test_gradients_against_differences(kind):
     """Along a random direction of each input: central differences of the formula in 64 bits.
 
-    x and weights are multiples of 1/4 of at most 1 and width is 16, so gate and
-    up, multiples of 1/16 of at most 16, are kept exactly; the gradient's error is
-    then that of want_backward's bounds, and dw_down's also of hidden's rounding.
-    The differences' own error is below 1e-7 of their terms (step 1e-4, third
+    The gradient's error is that of want_backward's bounds.  The differences' own error is below 1e-7 of their terms (step 1e-4, third
     derivatives of order one).
     """
     g = torch.Generator(device="cuda").manual_seed(5)
@@ -158,10 +152,8 @@ def test_gradients_against_differences(kind):
     x, w, dy = quarters(t, d), (quarters(d, f), quarters(d, f), quarters(f, o)), quarters(t, o)
     plan = b2b.GatedFeedForwardPlan("f16", d, f, o, kind)
     y, kept = plan.forward(x, *w)
-    assert torch.equal(kept.gate.double(), x.double() @ w[0].double())
     grads = plan.backward(dy, x, *w, kept)
-    bounds = list(want_backward(dy, x, *w, kept, kind, "f16"))
-    bounds[3] = Val(kept.hidden).rounded("f16").T @ Val(dy)
+    bounds = want_backward(dy, x, *w, kind, "f16")
 
     def loss(i, move):
         z = [m.double() for m in (x, *w)]
@@ -182,7 +174,7 @@ def test_no_tokens():
     none = x[:0]
     assert plan.run(none, *w).shape == (0, 72)
     y, kept = plan.forward(none, *w)
-    assert y.shape == (0, 72) and [k.shape for k in kept] == [(0, 264)] * 3
+    assert y.shape == (0, 72) and kept.shape == (0,)
     dx, *g = plan.backward(dy[:0], none, *w, kept)
     assert dx.shape == (0, 136) and all((z == 0).all() for z in g)
     acc = [torch.ones_like(z, dtype=torch.float32) for z in w]
@@ -218,7 +210,7 @@ def test_far_out_gates(kind, t):
     g, u, h, want = want_forward(x, *w, kind, "bf16")
     want.check(y, "bf16", "y")
     grads = plan.backward(dy, x, *w, kept)
-    for v, got in zip(want_backward(dy, x, *w, kept, kind, "bf16"), grads):
+    for v, got in zip(want_backward(dy, x, *w, kind, "bf16"), grads):
         assert got.isfinite().all()
         v.check(got, "bf16")
 
@@ -251,7 +243,7 @@ def all_calls(t, seed=0):
     kept = plan.forward(x, *w)[1]
     return {
         "run": lambda **k: [plan.run(x, *w, **k)],
-        "forward": lambda **k: (lambda r: [r[0], *r[1]])(plan.forward(x, *w, **k)),
+        "forward": lambda **k: [plan.forward(x, *w, **k)[0]],
         "backward": lambda **k: list(plan.backward(dy, x, *w, kept, **k)),
         "scaled": lambda **k: [plan8.run(x8, *eight[0], *eight[1], *eight[2], **k)],
         "product": lambda **k: [product.run(a, sa, b, sb, **k)],
@@ -340,8 +332,8 @@ def test_the_way_through_python_does_the_same(t):
     run = plan.run(x, *w)
     bound, plan._bound = plan._bound, None
     y2, kept2 = plan.forward(x, *w)
-    assert torch.equal(y, y2) and same(kept, kept2) and torch.equal(run, plan.run(x, *w))
-    assert same(grads, plan.backward(dy, x, *w, kept))
+    assert torch.equal(y, y2) and torch.equal(run, plan.run(x, *w))
+    assert same(grads, plan.backward(dy, x, *w, kept)) and same(grads, plan.backward(dy, x, *w, kept2))
     plan._bound = bound
     (a, sa), (b, sb) = scaled(1, t, 64, 1), scaled(2, 32, 64, 128)
     product = b2b.ScaledGemmPlan("bf16", 64, 32)
@@ -359,12 +351,9 @@ def test_offsets_past_32_bits():
     dx = plan.backward(dy, x, *w, kept, weight_grads=False)[0]
     assert plan.status() == 0
     rows = torch.cat([torch.arange(0, t, 9973, device="cuda"), torch.arange(t - 40, t, device="cuda")])
-    part = b2b.feedforward.KeptActivations(*(k[rows] for k in kept))
     del kept
-    g, u, h, want = want_forward(x[rows], *w, "silu", "bf16")
-    want.check(y[rows], "bf16", "y")
-    h.check(part.hidden, "bf16", "hidden")
-    want_backward(dy[rows], x[rows], *w, part, "silu", "bf16")[0].check(dx[rows], "bf16", "dx")
+    want_forward(x[rows], *w, "silu", "bf16")[3].check(y[rows], "bf16", "y")
+    want_backward(dy[rows], x[rows], *w, "silu", "bf16")[0].check(dx[rows], "bf16", "dx")
 
 
 # ------------------------------------------------------------- waits that run out
@@ -417,8 +406,13 @@ def test_refusals_by_type_shape_and_place():
     refused(ValueError, "out: shape", lambda: plan.run(x, *w, out=y[:3]))
     refused(TypeError, "out: torch.float32", lambda: plan.run(x, *w, out=y.float()))
     refused(ValueError, "dy: shape", lambda: plan.backward(dy[:3], x, *w, kept))
-    refused(ValueError, "gate: shape", lambda: plan.backward(dy, x, *w, (kept.gate[:2], kept.up, kept.hidden)))
-    refused(TypeError, "", lambda: plan.backward(dy, x, *w, kept[:2]))
+    refused(ValueError, "kept: shape", lambda: plan.backward(dy, x, *w, kept[::2]))
+    refused(TypeError, "kept: torch.float32", lambda: plan.backward(dy, x, *w, kept.view(torch.float32)))
+    refused(TypeError, "kept: tuple", lambda: plan.backward(dy, x, *w, (kept,)))
+    refused(ValueError, "kept is on cpu", lambda: plan.backward(dy, x, *w, kept.cpu()))
+    refused(b2b.B2BError, "INVALID_ARG", lambda: plan.backward(dy, x, *w, kept[:-256]))
+    refused(b2b.B2BError, "INVALID_ARG", lambda: plan.forward(x, *w, kept=kept[:-256]))
+    refused(b2b.B2BError, "ALIGNMENT", lambda: plan.forward(x, *w, kept=torch.cat([kept, kept])[16:]))
     refused(ValueError, "three expected", lambda: plan.backward(dy, x, *w, kept, weight_grads=(None,)))
     refused(TypeError, "gradient of w_up", lambda: plan.backward(dy, x, *w, kept, weight_grads=(None, wu.clone(), None)))
     (a, sa), (b, sb) = scaled(1, 6, 64, 1), scaled(2, 32, 64, 128)
@@ -462,7 +456,8 @@ def test_refusals_by_alignment_and_overlap():
     code(ALIAS, lambda: square.run(buf[:, :72], *ws, out=buf[:, 64:136]))
     buf[:, :72] = xs
     assert torch.equal(square.run(buf[:, :72], *ws, out=buf[:, 72:]), square.run(xs, *ws))  # side by side
-    code(ALIAS, lambda: plan.forward(x, *w, kept=(kept.gate, kept.gate, kept.hidden)))
+    whole = torch.zeros(kept.numel() + 2 * 6 * 72, dtype=torch.uint8, device="cuda")
+    code(ALIAS, lambda: plan.forward(x, *w, kept=whole, out=whole[-2 * 6 * 72 - 512:-512].view(torch.bfloat16).view(6, 72)))
     g = torch.zeros(136, 264, device="cuda")
     code(ALIAS, lambda: plan.backward(dy, x, *w, kept, weight_grads=(g, g, None)))
     (a, sa), (b, sb) = scaled(1, 6, 64, 1), scaled(2, 32, 64, 128)
@@ -482,20 +477,22 @@ def test_refusals_at_the_c_entries():
     out = torch.zeros(600, 72, dtype=torch.bfloat16, device="cuda")
     ws = torch.zeros(n.value + 256, dtype=torch.uint8, device="cuda")
 
-    def forward(tokens=600, gate=0, wsp=ws.data_ptr(), size=n.value, outp=out.data_ptr()):
-        args = struct.pack("19q", tokens, x.data_ptr(), 136, w[0].data_ptr(), 264, w[1].data_ptr(), 264, w[2].data_ptr(), 72, outp, 72,
-                           gate, 264, 0, 0, 0, 0, wsp, size)
+    def forward(tokens=600, kept=0, kept_bytes=0, wsp=ws.data_ptr(), size=n.value, outp=out.data_ptr()):
+        args = struct.pack("15q", tokens, x.data_ptr(), 136, w[0].data_ptr(), 264, w[1].data_ptr(), 264, w[2].data_ptr(), 72, outp, 72,
+                           kept, kept_bytes, wsp, size)
         return lib.b2b_ffn_forward(plan._h, args, None)
 
     torch.cuda.synchronize()
     assert forward() == 0
     assert forward(tokens=-1) == INVALID and forward(wsp=0) == INVALID and forward(size=n.value - 1) == INVALID
     assert forward(wsp=ws.data_ptr() + 16) == ALIGNMENT and forward(outp=0) == INVALID
-    assert forward(gate=ws.data_ptr()) == INVALID  # one of three kept
+    assert forward(kept=ws.data_ptr(), kept_bytes=256) == INVALID  # too little
+    assert lib.b2b_ffn_kept_bytes(plan._h, -1, ctypes.byref(n)) == INVALID
+    assert lib.b2b_ffn_kept_bytes(plan._h, 1, None) == INVALID
     assert lib.b2b_ffn_backward(plan._h, None, None) == INVALID
     product = b2b.ScaledGemmPlan("bf16", 64, 32)
     assert lib.b2b_ffn_workspace(product._h, 5, 1, ctypes.byref(n)) == INVALID  # (training: not of this kind)
-    assert lib.b2b_ffn_forward(product._h, b"\0" * 152, None) == INVALID  # another kind of plan
+    assert lib.b2b_ffn_forward(product._h, b"\0" * 120, None) == INVALID  # another kind of plan
     assert lib.b2b_scaled_gemm_run(plan._h, b"\0" * 120, None) == INVALID
     torch.cuda.synchronize()
     assert torch.equal(out, plan.run(x, *w))
@@ -515,7 +512,7 @@ def test_trained_then_served_in_8_bits():
     for part, want in zip(x.chunk(3), target.chunk(3)):
         y, kept = plan.forward(part, *weights_)
         dy = ((y.float() - want.float()) * (2 * 100 / target.numel())).bfloat16()
-        b = want_backward(dy, part, *weights_, kept, "silu", "bf16")[1:]
+        b = want_backward(dy, part, *weights_, "silu", "bf16")[1:]
         total = b if total is None else [p + q for p, q in zip(total, b)]
     for g, v in zip(got, total):
         Val(v.x / 100, v.w / 100 + 2.0 ** -22 * v.x.abs() / 100, v.v / 1e4).check(g)

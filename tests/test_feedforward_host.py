@@ -74,6 +74,7 @@ def test_calls_refuse_null_plans():
     assert b2b.b2b_ffn_plan_set_wait_budget(None, 0) == INVALID
     assert b2b.b2b_ffn_plan_set_debug(None, 0) == INVALID
     assert b2b.b2b_ffn_workspace(None, 1, 0, ctypes.byref(n)) == INVALID
+    assert b2b.b2b_ffn_kept_bytes(None, 1, ctypes.byref(n)) == INVALID
     for run in (b2b.b2b_ffn_forward, b2b.b2b_ffn_backward, b2b.b2b_scaled_ffn_run, b2b.b2b_scaled_gemm_run):
         assert run(None, None, None) == INVALID
 
