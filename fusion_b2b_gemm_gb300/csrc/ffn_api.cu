@@ -373,20 +373,34 @@ b2b_status_t create(b2b_ffn_plan_t* out, FfnKind kind, b2b_dtype_t dtype, int64_
   p->k = dtype == B2B_F16 ? ffn_kernels_f16() : ffn_kernels_bf16();
   p->s = scaled_kernels();
   p->budget_ns = kDefaultBudgetNs;
-  const GemmKernel all[] = {p->k.gate, p->k.down, p->k.gate_grad, p->k.dx, p->k.dw, p->k.dw_add,
-                            p->s.gate, p->s.product[0], p->s.product[1]};
+  // Shared memory of the kernels that this kind of plan launches.
   bool ok = true;
-  for (const SkinnyKernels& k : {p->k.gate_few, p->k.down_few, p->s.gate_few, p->s.product_few[0], p->s.product_few[1]})
+  auto use = [&](const GemmKernel& k) {
+    ok = ok && cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem) == cudaSuccess;
+  };
+  auto use_few = [&](const SkinnyKernels& k) {
     for (int i = 0; i < k.sizes; ++i)
       ok = ok && cudaFuncSetAttribute(k.main[i], cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem[i]) == cudaSuccess;
-  for (const GemmKernel& k : all)
-    ok = ok && cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem) == cudaSuccess;
+  };
   // The registers of the e4m3 kernels' roles (setmaxnreg) are drawn from what
   // the kernel is launched with: compiled to fewer, it would wait for them.
-  for (const GemmKernel& k : {p->s.gate, p->s.product[0], p->s.product[1]}) {
+  auto use_e4m3 = [&](const GemmKernel& k) {
+    use(k);
     cudaFuncAttributes fa;
     ok = ok && cudaFuncGetAttributes(&fa, k.main) == cudaSuccess &&
          fa.numRegs * gemm_threads(true) >= 512 * kGemmEpilogueRegs + 128 * kGemmOtherRegs;
+  };
+  if (kind == kFfn) {
+    for (const GemmKernel& k : {p->k.gate, p->k.down, p->k.gate_grad, p->k.dx, p->k.dw, p->k.dw_add}) use(k);
+    use_few(p->k.gate_few);
+    use_few(p->k.down_few);
+  } else {
+    use_e4m3(p->s.product[dtype == B2B_BF16]);
+    use_few(p->s.product_few[dtype == B2B_BF16]);
+    if (kind == kScaledFfn) {
+      use_e4m3(p->s.gate);
+      use_few(p->s.gate_few);
+    }
   }
   ok = ok && cudaMalloc(&p->d_status, sizeof(int)) == cudaSuccess;
   if (ok && cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) {
@@ -432,7 +446,8 @@ b2b_status_t quantize(const FfnKernels& k, int64_t rows, int64_t cols, int block
   p.scale_k = scale.block_stride;
   void* args[] = {&p};
   const int64_t per = block_rows == 1 ? kQuantThreads / 16 : 128;
-  const dim3 grid(static_cast<unsigned>(ceil_div(rows, per)), static_cast<unsigned>(std::min<int64_t>(ceil_div(cols, 128), 65535)));
+  const dim3 grid(static_cast<unsigned>(ceil_div(rows, per)),
+                  static_cast<unsigned>(std::min<int64_t>(ceil_div(cols, block_rows == 1 ? 128 * kQuantBlocks : 128), 65535)));
   if (launch_pdl(block_rows == 1 ? k.quantize_rows : k.quantize_tiles, grid, dim3(kQuantThreads), args, 0, stream) != cudaSuccess) {
     cudaGetLastError();
     return B2B_ERR_CUDA;

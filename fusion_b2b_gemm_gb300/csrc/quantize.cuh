@@ -20,34 +20,44 @@ struct QuantParams {
 };
 
 // Blocks of 128 of a row: 16 lanes take a block, 8 values each, so a warp takes
-// two rows; a thread block 16 rows of one column block.
+// two rows; a thread block 16 rows of kQuantBlocks column blocks, whose loads
+// overlap (one at a time: 2048 x 4096 in 8.2 us, four 7.4 us).
+constexpr int kQuantBlocks = 4;
 template <int T>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __grid_constant__ QuantParams p) {
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
   const int lane = threadIdx.x & 15;
   const long long row = static_cast<long long>(blockIdx.x) * (kQuantThreads / 16) + (threadIdx.x >> 4);
-  for (long long kb = blockIdx.y; kb * 128 < p.cols; kb += gridDim.y) {
-    const long long col = kb * 128 + lane * 8;
-    const bool in = row < p.rows && col < p.cols;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (in) w = gemm::load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.x_ld + col));
-    float v[8];
-    uint32_t top = 0;
+  for (long long kb0 = static_cast<long long>(blockIdx.y) * kQuantBlocks; kb0 * 128 < p.cols; kb0 += static_cast<long long>(gridDim.y) * kQuantBlocks) {
+    uint4 w[kQuantBlocks];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      gemm::unpack16<T>((&w.x)[e], v[2 * e], v[2 * e + 1]);
-      top = max(top, max(__float_as_uint(v[2 * e]) & 0x7fffffffu, __float_as_uint(v[2 * e + 1]) & 0x7fffffffu));
+    for (int i = 0; i < kQuantBlocks; ++i) {
+      const long long col = (kb0 + i) * 128 + lane * 8;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (row < p.rows && col < p.cols)
+        w[i] = gemm::load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.x_ld + col));
     }
 #pragma unroll
-    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float inv;
-    const float scale = gemm::block_scale(top, inv);
-    if (in)
-      *reinterpret_cast<uint2*>(p.q + row * p.q_ld + col) =
-          make_uint2(gemm::pack_e4m3(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                     gemm::pack_e4m3(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-    if (lane == 0 && row < p.rows) p.scale[row * p.scale_row + kb * p.scale_k] = scale;
+    for (int i = 0; i < kQuantBlocks; ++i) {
+      const long long kb = kb0 + i, col = kb * 128 + lane * 8;
+      float v[8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        gemm::unpack16<T>((&w[i].x)[e], v[2 * e], v[2 * e + 1]);
+        top = max(top, max(__float_as_uint(v[2 * e]) & 0x7fffffffu, __float_as_uint(v[2 * e + 1]) & 0x7fffffffu));
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float inv;
+      const float scale = gemm::block_scale(top, inv);
+      if (row < p.rows && col < p.cols)
+        *reinterpret_cast<uint2*>(p.q + row * p.q_ld + col) =
+            make_uint2(gemm::pack_e4m3(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                       gemm::pack_e4m3(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+      if (lane == 0 && row < p.rows && kb * 128 < p.cols) p.scale[row * p.scale_row + kb * p.scale_k] = scale;
+    }
   }
 }
 
