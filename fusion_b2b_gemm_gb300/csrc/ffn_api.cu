@@ -249,19 +249,28 @@ struct FewRows {
   FewRows(const b2b_ffn_plan_s* plan_, const SkinnyKernels& k_, bool e4m3_, const Matrix& x) : plan(plan_), k(k_), e4m3(e4m3_) {
     std::memset(&p, 0, sizeof(p));
     p.rows = static_cast<int>(x.rows);
-    p.slots = static_cast<int>(ceil_div(x.cols, k.depth));
     p.x_box_rows = static_cast<int>((x.rows + 7) & ~int64_t(7));
+    p.segment = 1 << 30;
     p.act = plan->act;
     p.debug = plan->debug;
     p.status = plan->d_status;
-    st = encode(&maps.x, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(plan), x, e4m3 ? 128 : 64, static_cast<uint32_t>(p.x_box_rows));
+    rows(0, x);
+    maps.x[1] = maps.x[0];
   }
-  // 16 bits [k][columns], e4m3 [columns][k]
+  void rows(int i, const Matrix& x) {
+    p.slots += static_cast<int>(ceil_div(x.cols, k.depth));
+    if (st == B2B_OK)
+      st = encode(&maps.x[i], e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(plan), x, e4m3 ? 128 : 64, static_cast<uint32_t>(p.x_box_rows));
+  }
+  // A product to add: rows and, set by weight(1, ..), their weight.
+  void more(const Matrix& x) {
+    p.segment = p.slots;
+    rows(1, x);
+  }
   void weight(int i, const Matrix& w) {
     if (st != B2B_OK) return;
-    p.N = static_cast<int>(e4m3 ? w.rows : w.cols);
-    st = e4m3 ? encode(&maps.w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w, 128, 128)
-              : encode(&maps.w[i], type16(plan), w, 64, 64);
+    p.N = static_cast<int>(k.k_major ? w.rows : w.cols);
+    st = encode(&maps.w[i], e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16(plan), w, e4m3 ? 128 : 64, k.k_major ? 128 : 64);
   }
   b2b_status_t run(cudaStream_t stream) {
     if (st != B2B_OK) return st;
@@ -293,7 +302,7 @@ struct Pieces {
   size_t total() const { return rounded(hidden) + rounded(second) + rounded(x_scale) + rounded(h_scale) + parts; }
 };
 
-// Up to so many rows the products of a plan (but the backward pass's) take the kernel for few rows.
+// Up to so many rows a plan's products take the kernel for few rows (not the weights' gradients, whose sums are over rows).
 int few_rows(const b2b_ffn_plan_s* p) { return (p->kind == kFfn ? p->k.gate_few : p->s.gate_few).most_rows(); }
 
 // What a forward pass keeps: G and U, then H.
@@ -334,8 +343,10 @@ Pieces pieces(const b2b_ffn_plan_s* p, int64_t rows, int pass) {
     part(tile_count(rows, o, false), panels(f, true));
   } else if (pass == B2B_FFN_BACKWARD) {
     w.hidden = w.second = 2 * t * f;
-    part(tile_count(rows, f, false), panels(o));
-    part(tile_count(rows, d, false), 2 * panels(f));
+    if (rows > few_rows(p)) {
+      part(tile_count(rows, f, false), panels(o));
+      part(tile_count(rows, d, false), 2 * panels(f));
+    }
     // (any of the weights' gradients may be left out)
     for (int g = 0; g <= 2; ++g)
       for (int e = 0; e <= 1; ++e)
@@ -394,6 +405,8 @@ b2b_status_t create(b2b_ffn_plan_t* out, FfnKind kind, b2b_dtype_t dtype, int64_
     for (const GemmKernel& k : {p->k.gate, p->k.down, p->k.gate_grad, p->k.dx, p->k.dw, p->k.dw_add}) use(k);
     use_few(p->k.gate_few);
     use_few(p->k.down_few);
+    use_few(p->k.gate_grad_few);
+    use_few(p->k.dx_few);
   } else {
     use_e4m3(p->s.product[dtype == B2B_BF16]);
     use_few(p->s.product_few[dtype == B2B_BF16]);
@@ -619,7 +632,26 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
   const b2b_matrix_t dg_rows = {ws, f}, du_rows = {ws + rounded(w.hidden), f};
   void* parts = ws + rounded(w.hidden) + rounded(w.second);
   const Matrix dg = {&dg_rows, t, f, 2}, du = {&du_rows, t, f, 2};
-  if (r->dx.data || r->dw_gate.data || r->dw_up.data) {
+  const bool few = t <= few_rows(p);
+  if (few && (r->dx.data || r->dw_gate.data || r->dw_up.data)) {
+    FewRows l(p, p->k.gate_grad_few, false, in[0]);
+    l.weight(0, in[4]);
+    l.p.out = dg_rows.data;
+    l.p.out2 = du_rows.data;
+    l.p.out_ld = f;
+    kept.set(l.p, r->kept);
+    st = l.run(stream);
+    if (st == B2B_OK && r->dx.data) {
+      FewRows x(p, p->k.dx_few, false, dg);
+      x.weight(0, in[2]);
+      x.more(du);
+      x.weight(1, in[3]);
+      x.p.out = r->dx.data;
+      x.p.out_ld = r->dx.row_stride;
+      st = x.run(stream);
+    }
+  }
+  if (!few && (r->dx.data || r->dw_gate.data || r->dw_up.data)) {
     Launch l(p, false, false);
     l.a_rows(0, in[0]);
     l.b_rows(0, in[4]);
@@ -629,7 +661,7 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
     l.problem(t, f);
     st = l.run(p->k.gate_grad, panels(o), parts, stream);
   }
-  if (st == B2B_OK && r->dx.data) {
+  if (!few && st == B2B_OK && r->dx.data) {
     Launch l(p, false, false);
     l.a_rows(0, dg);
     l.a_rows(1, du);

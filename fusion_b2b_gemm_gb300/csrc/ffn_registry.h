@@ -23,19 +23,21 @@ GemmKernel gemm_kernel_pair() {
 struct SkinnyKernels {
   const void* main[4];
   int smem[4], sizes, columns, depth;
+  bool k_major;  // order of the weights
   int most_rows() const { return 8 << sizes; }
 };
-template <int IN, int OUT, bool GATE>
+template <int IN, int OUT, int EPI, bool KM>
 SkinnyKernels skinny_kernels() {
-  constexpr bool F8 = IN == kGemmE4M3;
-  SkinnyKernels k = {{reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, GATE, 16>), reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, GATE, 32>),
-                      reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, GATE, 64>), nullptr},
+  constexpr bool F8 = IN == kGemmE4M3, GATE = EPI == kEpiGate || EPI == kEpiGateQuant;
+  SkinnyKernels k = {{reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 16>), reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 32>),
+                      reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 64>), nullptr},
                      {SkinnyShape<F8, GATE, 16>::kBytes, SkinnyShape<F8, GATE, 32>::kBytes, SkinnyShape<F8, GATE, 64>::kBytes, 0},
                      3,
                      SkinnyShape<F8, GATE, 16>::kColumns,
-                     SkinnyShape<F8, GATE, 16>::kDepth};
+                     SkinnyShape<F8, GATE, 16>::kDepth,
+                     KM};
   if constexpr (!F8) {
-    k.main[3] = reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, GATE, 128>);
+    k.main[3] = reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 128>);
     k.smem[3] = SkinnyShape<F8, GATE, 128>::kBytes;
     k.sizes = 4;
   }
@@ -50,7 +52,7 @@ struct FfnKernels {
   GemmKernel dx;         // dG.Wg^T + dU.Wu^T
   GemmKernel dw;         // X^T.dG, X^T.dU, H^T.dY
   GemmKernel dw_add;     // the same, added to fp32
-  SkinnyKernels gate_few, down_few;
+  SkinnyKernels gate_few, down_few, gate_grad_few, dx_few;
   const void* quantize_rows;
   const void* quantize_tiles;
 };
@@ -63,8 +65,10 @@ FfnKernels ffn_kernels() {
           gemm_kernel_pair<T, false, false, kEpiStore, T>(),
           gemm_kernel_pair<T, true, true, kEpiStore, T>(),
           gemm_kernel_pair<T, true, true, kEpiAdd, T>(),
-          skinny_kernels<T, T, true>(),
-          skinny_kernels<T, T, false>(),
+          skinny_kernels<T, T, kEpiGate, false>(),
+          skinny_kernels<T, T, kEpiStore, false>(),
+          skinny_kernels<T, T, kEpiGateGrad, true>(),
+          skinny_kernels<T, T, kEpiStore, true>(),
           reinterpret_cast<const void*>(&quantize_rows_kernel<T>),
           reinterpret_cast<const void*>(&quantize_tiles_kernel<T>)};
 }

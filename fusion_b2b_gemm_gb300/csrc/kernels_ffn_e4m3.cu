@@ -6,7 +6,7 @@ ScaledKernels scaled_kernels() {
   return {gemm_kernel_pair<kGemmE4M3, false, false, kEpiGateQuant, kGemmF16>(),
           {gemm_kernel_pair<kGemmE4M3, false, false, kEpiStore, kGemmF16>(),
            gemm_kernel_pair<kGemmE4M3, false, false, kEpiStore, kGemmBF16>()},
-          skinny_kernels<kGemmE4M3, kGemmF16, true>(),
-          {skinny_kernels<kGemmE4M3, kGemmF16, false>(), skinny_kernels<kGemmE4M3, kGemmBF16, false>()}};
+          skinny_kernels<kGemmE4M3, kGemmF16, kEpiGateQuant, true>(),
+          {skinny_kernels<kGemmE4M3, kGemmF16, kEpiStore, true>(), skinny_kernels<kGemmE4M3, kGemmBF16, kEpiStore, true>()}};
 }
 }  // namespace b2b

@@ -16,9 +16,10 @@
 // no second launch and no workspace.  TMA brings panels of the weight(s) and of
 // the rows into a ring; two CTAs share an SM, some 160 KB in flight.
 //
-//   16 bits: weights as stored, [k][column], an MN-major A of 128 columns by 64 k
-//            a slot; the gate takes 64 columns of either weight as the two halves
-//            of one A.  The sums stay in tensor memory to the end.
+//   16 bits: weights as stored, [k][column] (an MN-major A) or, in the backward
+//            pass, [column][k] (K-major), 128 columns by 64 k a slot; the gate takes
+//            64 columns of either weight as the two halves of one A.  The sums stay in
+//            tensor memory to the end.
 //   e4m3:    weights [column][k], 128 columns (whole blocks of scales) by 128 k, of
 //            both weights for the gate.  Each slot's product is an accumulator of
 //            its own, multiplied by its scales and added up in registers.
@@ -37,11 +38,13 @@ constexpr int kSkinnyMaxSplits = 8;  // CTAs of a cluster
 struct SkinnyParams {
   int rows, N;
   int slots;          // panels of the whole of k
+  int segment;        // panels of the first product (then x and the weight go on in the second maps)
   int splits;         // CTAs of a slice
   int x_box_rows;
   int act;
   void* out;          // h (or, e4m3 gate, its values), or the product
   long long out_ld;
+  void* out2;         // kEpiGateGrad: dU (out: dG)
   float* kept_gate;   // as GemmParams
   float* kept_up;
   int kept_blocks;
@@ -57,7 +60,7 @@ struct SkinnyParams {
 };
 
 struct SkinnyMaps {
-  CUtensorMap x, w[2];
+  CUtensorMap x[2], w[2];
 };
 
 enum : int {  // barrier slots (8 bytes each)
@@ -116,12 +119,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[C]) {
 
 }  // namespace skinny
 
-// IN: operands; OUT: 16-bit type of the result (not of the e4m3 gate, which is quantised).  NT: 16, 32, 64 or 128 tokens.
-template <int IN, int OUT, bool GATE, int NT>
+// IN: operands; OUT: 16-bit type of the result (not of kEpiGateQuant's); EPI: of gemm.cuh's, what follows the product;
+// KM: K-major weights; NT: 16, 32, 64 or 128 tokens.
+template <int IN, int OUT, int EPI, bool KM, int NT>
 __global__ void __launch_bounds__(kSkinnyThreads, 2)
     skinny_kernel(const __grid_constant__ SkinnyMaps maps, const __grid_constant__ SkinnyParams p) {
   using namespace ptx;
-  constexpr bool F8 = IN == kGemmE4M3;
+  constexpr bool F8 = IN == kGemmE4M3, GATE = EPI == kEpiGate || EPI == kEpiGateQuant;
+  static_assert(F8 ? KM && (EPI == kEpiStore || EPI == kEpiGateQuant) : !(KM && GATE), "weights' order");
   using L = SkinnyShape<F8, GATE, NT>;
   constexpr int W = F8 && GATE ? 2 : 1;      // accumulators of a slot
   constexpr int C = NT < 32 ? NT : 32;       // columns read at a time
@@ -137,11 +142,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   const int part = static_cast<int>(blockIdx.x) % p.splits, col0 = static_cast<int>(blockIdx.x) / p.splits * L::kColumns;
   const int s0 = static_cast<int>(static_cast<long long>(p.slots) * part / p.splits);
   const int s1 = static_cast<int>(static_cast<long long>(p.slots) * (part + 1) / p.splits);
-  // 16 bits: columns of a row are consecutive, two blocks of 64 a slot; e4m3: k
+  // MN-major: two blocks of 64 columns a slot; K-major: 128 bytes of k of 128 columns
   auto weights = [&](int s, auto&& each) {
-    if constexpr (F8) {
+    if constexpr (F8 && GATE) {
       each(0, &maps.w[0], s * 128, col0);
-      if constexpr (GATE) each(16384, &maps.w[1], s * 128, col0);
+      each(16384, &maps.w[1], s * 128, col0);
+    } else if constexpr (KM) {
+      const int seg = s >= p.segment ? 1 : 0;
+      each(0, &maps.w[seg], (s - (seg ? p.segment : 0)) * L::kDepth, col0);
     } else {
       each(0, &maps.w[0], col0, s * 64);
       each(8192, &maps.w[GATE ? 1 : 0], GATE ? col0 : col0 + 64, s * 64);
@@ -192,7 +200,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         mbar_arrive_expect_tx(full, bytes);
         if (!((p.debug & 1u) && issued == 0)) {  // (test support: the first slot is armed but never filled)
           weights(s, [&](int off, const CUtensorMap* m, int x, int y) { tma_load_2d(dst + off, m, full, x, y); });
-          tma_load_2d(dst + L::kWeight, &maps.x, full, s * L::kDepth, 0);
+          const int seg = s >= p.segment ? 1 : 0;
+          tma_load_2d(dst + L::kWeight, &maps.x[seg], full, (s - (seg ? p.segment : 0)) * L::kDepth, 0);
         }
         ++issued;
         if (++slot == L::kRing) {
@@ -209,8 +218,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   } else if (warp == 1) {
     if (elect_one()) {
       constexpr uint32_t kFmt = IN == kGemmBF16 ? 1u : 0u;
-      constexpr uint32_t idesc = make_idesc(kFmt, NT, 128, false) | (F8 ? 0u : 1u << 15);
-      constexpr uint32_t a_step = F8 ? 2 : 128;
+      constexpr uint32_t idesc = make_idesc(kFmt, NT, 128, false) | (KM ? 0u : 1u << 15);
+      constexpr uint32_t a_step = KM ? 2 : 128;
       uint32_t slot = 0, phase = 0, acc = 0, acc_phase = 0;
       for (int s = s0; s < s1; ++s) {
         if (F8 && !bw.wait1(bar(kSBAccEmpty + acc), acc_phase ^ 1u)) break;
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         const uint64_t b = desc_sw128(src + L::kWeight, 16u, 1024u);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const uint64_t a = desc_sw128(src + w * 16384u, F8 ? 16u : 8192u, 1024u);
+          const uint64_t a = desc_sw128(src + w * 16384u, KM ? 16u : 8192u, 1024u);
           const uint32_t d = tmem_base + (F8 ? (acc * W + w) * NT : 0u);
 #pragma unroll
           for (uint32_t i = 0; i < 4; ++i) {
@@ -357,7 +366,28 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         if constexpr (GATE) skinny::add_remote<V>(v[GATE ? 1 : 0], from + L::kColumns * 4u);
       }
       const bool in = col < p.N;  // (N is a multiple of V)
-      if constexpr (!GATE) {
+      if constexpr (EPI == kEpiGateGrad) {
+        if (in) {
+          const long long kept = gemm_kept_at(r, col, p.kept_blocks);
+          const uint4 gw = gemm::load(reinterpret_cast<const uint4*>(p.kept_gate + kept)), uw = gemm::load(reinterpret_cast<const uint4*>(p.kept_up + kept));
+          float dg[V], du[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float g = __uint_as_float((&gw.x)[e]);
+            float a, s;
+            if (p.act)
+              gemm::activation_slope<1>(g, a, s);
+            else
+              gemm::activation_slope<0>(g, a, s);
+            dg[e] = v[0][e] * __uint_as_float((&uw.x)[e]) * s;
+            du[e] = v[0][e] * a;
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) =
+              make_uint2(gemm::pack16<OUT>(dg[0], dg[1]), gemm::pack16<OUT>(dg[2], dg[3]));
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out2) + r * p.out_ld + col) =
+              make_uint2(gemm::pack16<OUT>(du[0], du[1]), gemm::pack16<OUT>(du[2], du[3]));
+        }
+      } else if constexpr (!GATE) {
         uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col);
         if (in) {
 #pragma unroll
