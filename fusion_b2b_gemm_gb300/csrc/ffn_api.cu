@@ -278,8 +278,8 @@ struct FewRows {
     while (p.rows > 16 << size) ++size;
     const int slices = static_cast<int>(ceil_div(p.N, k.columns)), room = 2 * plan->sms;
     // As many CTAs as are resident at once, two slots each at least.
-    p.splits = 1;
-    while (p.splits < kSkinnyMaxSplits && 2 * p.splits * slices <= room && p.slots >= 4 * p.splits) p.splits *= 2;
+    while ((1 << p.split_bits) < kSkinnyMaxSplits && (2 << p.split_bits) * slices <= room && p.slots >= (4 << p.split_bits)) ++p.split_bits;
+    p.splits = 1 << p.split_bits;
     p.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(plan->budget_ns, 5000ull * p.slots), 4000000000ull));
     void* args[] = {&maps, &p};
     if (launch_pdl(k.main[size], dim3(static_cast<unsigned>(slices * p.splits)), dim3(kSkinnyThreads), args, k.smem[size], stream, p.splits) !=

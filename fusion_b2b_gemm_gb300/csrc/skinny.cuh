@@ -11,10 +11,16 @@
 // whose tile of 256 rows is mostly empty, takes 72 us for one token, this one 54.)
 //
 // A CTA takes a slice of the columns and, where slices alone are too few to keep
-// the memory busy, a range of k; the CTAs of a slice are a cluster and add
-// their sums up through each other's shared memory in a fixed order, so there is
-// no second launch and no workspace.  TMA brings panels of the weight(s) and of
-// the rows into a ring; two CTAs share an SM, some 160 KB in flight.
+// the memory busy, a range of k; the CTAs of a slice are a cluster and add their
+// sums up through each other's shared memory in a fixed order, so there is no
+// second launch and no workspace.  Up to 32 tokens each CTA writes its sums into
+// the CTA that adds them up, as soon as it has them; for more, that would cost a slot
+// of the ring, and the sums lie in the ring's place and are read from there (a block of
+// 1024/2816/1024 for one token: 7.9 us written, 8.8 read; of 2048/5632/2048 for 33: 20.3
+// read, 20.8 written into the ring's place, 21.5 written beside a shorter ring).
+//
+// TMA brings panels of the weight(s) and of the rows into a ring; two CTAs share an
+// SM, some 160 KB in flight.
 //
 //   16 bits: weights as stored, [k][column] (an MN-major A) or, in the backward
 //            pass, [column][k] (K-major), 128 columns by 64 k a slot; the gate takes
@@ -39,7 +45,7 @@ struct SkinnyParams {
   int rows, N;
   int slots;          // panels of the whole of k
   int segment;        // panels of the first product (then x and the weight go on in the second maps)
-  int splits;         // CTAs of a slice
+  int splits, split_bits;  // CTAs of a slice, a power of two
   int x_box_rows;
   int act;
   void* out;          // h (or, e4m3 gate, its values), or the product
@@ -78,14 +84,19 @@ struct SkinnyShape {
   static constexpr int kDepth = F8 ? 128 : 64;             // k of a slot
   static constexpr int kWeight = F8 && GATE ? 32768 : 16384;
   static constexpr int kSlot = kWeight + NT * 128;
-  static constexpr int kRing = 104 * 1024 / kSlot;
   static constexpr int kSumLd = GATE ? 2 * kColumns : kColumns;
-  static constexpr int kOffScales = kRing * kSlot;          // e4m3: [4 warps][2 weights][NT]
+  // Sums of the CTAs of a slice: apart from the ring, written there by the CTA that has
+  // them while another may still multiply, or in the ring's place, its CTA's own.
+  static constexpr bool kApart = NT <= 32 && !(F8 && GATE);  // (one accumulator's)
+  static constexpr int kSumBytes = NT * kSumLd * 4;
+  static constexpr int kRing = (105 * 1024 - (kApart ? kSumBytes : 0)) / kSlot;
+  static constexpr int kOffSums = kApart ? kRing * kSlot : 0;
+  static constexpr int kOffScales = kRing * kSlot + (kApart ? kSumBytes : 0);  // e4m3: [4 warps][2 weights][NT]
   static constexpr int kOffBar = kOffScales + (F8 ? 4 * 2 * NT * 4 : 0);
   static constexpr int kBytes = kOffBar + 256 + 1024;
   // columns of tensor memory: an accumulator, or two (of both weights)
   static constexpr int kTmemCols = F8 ? 2 * NT * (GATE ? 2 : 1) : (NT < 32 ? 32 : NT);
-  static_assert(kRing <= 8 && kRing >= 2 && NT * kSumLd * 4 <= kRing * kSlot, "the sums take the ring's place");
+  static_assert(kRing <= 8 && kRing >= 2 && kSumBytes <= kRing * kSlot, "the sums take the ring's place");
   static_assert(2 * (kBytes + 1024) <= 233472 && 2 * kTmemCols <= 512, "two CTAs on an SM");
 };
 
@@ -107,6 +118,9 @@ __device__ __forceinline__ void add_remote(float (&sum)[V], uint32_t addr) {
     sum[2] += z;
     sum[3] += w;
   }
+}
+__device__ __forceinline__ void store_remote(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 // C columns of this warp's lanes, C = 16 or 32
 template <int C>
@@ -155,6 +169,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       each(8192, &maps.w[GATE ? 1 : 0], GATE ? col0 : col0 + 64, s * 64);
     }
   };
+  // (before anything is waited for: the others may then write to this CTA's sums)
+  if (L::kApart && p.splits > 1) cluster_arrive();
   if (warp == 0) {
     if (elect_one()) {
       // The first slots into L2, before anything is waited for (a prefetch reads no value).
@@ -187,7 +203,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   grid_launch_dependents();
   grid_dependency_wait();
   const gemm::Wait bw{abort_flag, p.budget_ns};
-  float* sum = reinterpret_cast<float*>(gbase);  // [token][column], in the ring's place
+  float acc_sum[W][NT];  // of an epilogue thread: its column's sums
+  float* sum = reinterpret_cast<float*>(gbase + L::kOffSums);
 
   if (warp == 0) {
     if (elect_one()) {
@@ -269,12 +286,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
             skinny::tmem_ld<C>(lanes + static_cast<uint32_t>(c), v);
             tmem_wait_ld(v);
 #pragma unroll
-            for (int e = 0; e < C; ++e) sum[(c + e) * L::kSumLd + column] = __uint_as_float(v[e]);
+            for (int e = 0; e < C; ++e) {
+              acc_sum[0][c + e] = __uint_as_float(v[e]);
+              if (!L::kApart) sum[(c + e) * L::kSumLd + column] = acc_sum[0][c + e];
+            }
           }
         }
       }
     } else {
-      float acc_sum[W][NT];
 #pragma unroll
       for (auto& a : acc_sum)
 #pragma unroll
@@ -330,7 +349,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         if (acc == 0) acc_phase ^= 1u;
       }
       // every copy into the ring has been waited for by the MMAs that these sums came from
-      if (ok) {
+      if (ok && !L::kApart) {
 #pragma unroll
         for (int w = 0; w < W; ++w)
 #pragma unroll
@@ -346,24 +365,45 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     tc_fence_after();
     tmem_dealloc(tmem_base, L::kTmemCols);
   }
-  if (p.splits > 1) cluster_sync();
+  // Sums of token r are added up by CTA r % splits.  Apart: there, [CTA they come
+  // from][r / splits][column], once the others have begun; else, already, here, [r][column].
+  const int share = (p.rows + p.splits - 1) >> p.split_bits;
+  if constexpr (L::kApart) {
+    if (p.splits > 1) cluster_wait();
+    if (warp >= 2) {
+      const uint32_t mine = base + L::kOffSums + static_cast<uint32_t>(part * share * L::kSumLd + (warp & 3) * 32 + lane) * 4u;
+#pragma unroll
+      for (int e = 0; e < NT; ++e) {
+        if (e < p.rows)
+          skinny::store_remote(mapa_shared(mine + static_cast<uint32_t>((e >> p.split_bits) * L::kSumLd) * 4u,
+                                           static_cast<uint32_t>(e & (p.splits - 1))),
+                               acc_sum[0][e]);
+      }
+    }
+  }
+  if (p.splits > 1)
+    cluster_sync();
+  else if (L::kApart)
+    __syncthreads();
 
-  // Rows are shared out over the slice's CTAs, a warp to a row, V columns to a lane.
+  // A warp to a row, V columns to a lane.
   if (!*abort_flag) {
     constexpr int V = L::kColumns / 32;
     const int col = col0 + lane * V;
-    for (int r = part + warp * p.splits; r < p.rows; r += kSkinnyThreads / 32 * p.splits) {
+    const uint32_t sums = base + L::kOffSums + static_cast<uint32_t>(lane * V) * 4u;
+    for (int r = part + (warp << p.split_bits); r < p.rows; r += (kSkinnyThreads / 32) << p.split_bits) {
       float v[GATE ? 2 : 1][V];
 #pragma unroll
       for (auto& a : v)
 #pragma unroll
         for (float& b : a) b = 0.0f;
-      const uint32_t at = base + static_cast<uint32_t>(r * L::kSumLd + lane * V) * 4u;
+      uint32_t from = sums + static_cast<uint32_t>((L::kApart ? r >> p.split_bits : r) * L::kSumLd) * 4u;
 #pragma unroll 4
       for (int c = 0; c < p.splits; ++c) {
-        const uint32_t from = mapa_shared(at, static_cast<uint32_t>(c));
-        skinny::add_remote<V>(v[0], from);
-        if constexpr (GATE) skinny::add_remote<V>(v[GATE ? 1 : 0], from + L::kColumns * 4u);
+        const uint32_t at = L::kApart ? from : mapa_shared(from, static_cast<uint32_t>(c));
+        skinny::add_remote<V>(v[0], at);
+        if constexpr (GATE) skinny::add_remote<V>(v[GATE ? 1 : 0], at + L::kColumns * 4u);
+        if (L::kApart) from += static_cast<uint32_t>(share * L::kSumLd) * 4u;
       }
       const bool in = col < p.N;  // (N is a multiple of V)
       if constexpr (EPI == kEpiGateGrad) {
@@ -420,7 +460,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     }
   }
   if (threadIdx.x == 0 && *abort_flag && p.status) atomicCAS(p.status, 0, kTimeoutCode);
-  if (p.splits > 1) cluster_sync();  // (the sums have been read)
+  if (!L::kApart && p.splits > 1) cluster_sync();  // (the sums have been read)
 }
 
 }  // namespace b2b
