@@ -102,22 +102,14 @@ struct SkinnyShape {
 
 namespace skinny {
 
-// V consecutive floats of a CTA of the cluster
-template <int V>
-__device__ __forceinline__ void add_remote(float (&sum)[V], uint32_t addr) {
-  if constexpr (V == 2) {
-    float x, y;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(addr));
-    sum[0] += x;
-    sum[1] += y;
-  } else {
-    float x, y, z, w;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x), "=f"(y), "=f"(z), "=f"(w) : "r"(addr));
-    sum[0] += x;
-    sum[1] += y;
-    sum[2] += z;
-    sum[3] += w;
-  }
+// four consecutive floats of a CTA of the cluster
+__device__ __forceinline__ void add_remote(float (&sum)[4], uint32_t addr) {
+  float x, y, z, w;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x), "=f"(y), "=f"(z), "=f"(w) : "r"(addr));
+  sum[0] += x;
+  sum[1] += y;
+  sum[2] += z;
+  sum[3] += w;
 }
 __device__ __forceinline__ void store_remote(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -386,12 +378,12 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   else if (L::kApart)
     __syncthreads();
 
-  // A warp to a row, V columns to a lane.
+  // A warp to a row (the 16-bit gate's 64 columns: to two), four columns to a lane.
   if (!*abort_flag) {
-    constexpr int V = L::kColumns / 32;
-    const int col = col0 + lane * V;
-    const uint32_t sums = base + L::kOffSums + static_cast<uint32_t>(lane * V) * 4u;
-    for (int r = part + (warp << p.split_bits); r < p.rows; r += (kSkinnyThreads / 32) << p.split_bits) {
+    constexpr int V = 4, kLanes = L::kColumns / V, kRows = 32 / kLanes;
+    const int at_col = lane % kLanes * V, col = col0 + at_col;
+    const uint32_t sums = base + L::kOffSums + static_cast<uint32_t>(at_col) * 4u;
+    for (int r = part + ((warp * kRows + lane / kLanes) << p.split_bits); r < p.rows; r += (kSkinnyThreads / 32 * kRows) << p.split_bits) {
       float v[GATE ? 2 : 1][V];
 #pragma unroll
       for (auto& a : v)
@@ -401,8 +393,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll 4
       for (int c = 0; c < p.splits; ++c) {
         const uint32_t at = L::kApart ? from : mapa_shared(from, static_cast<uint32_t>(c));
-        skinny::add_remote<V>(v[0], at);
-        if constexpr (GATE) skinny::add_remote<V>(v[GATE ? 1 : 0], at + L::kColumns * 4u);
+        skinny::add_remote(v[0], at);
+        if constexpr (GATE) skinny::add_remote(v[GATE ? 1 : 0], at + L::kColumns * 4u);
         if (L::kApart) from += static_cast<uint32_t>(share * L::kSumLd) * 4u;
       }
       const bool in = col < p.N;  // (N is a multiple of V)
@@ -428,11 +420,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
               make_uint2(gemm::pack16<OUT>(du[0], du[1]), gemm::pack16<OUT>(du[2], du[3]));
         }
       } else if constexpr (!GATE) {
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col);
-        if (in) {
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) dst[e] = gemm::pack16<OUT>(v[0][2 * e], v[0][2 * e + 1]);
-        }
+        if (in)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) =
+              make_uint2(gemm::pack16<OUT>(v[0][0], v[0][1]), gemm::pack16<OUT>(v[0][2], v[0][3]));
       } else {
         float h[V];
 #pragma unroll
@@ -449,11 +439,12 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
                 gemm::pack_e4m3(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
           if (lane == 0) p.q_scale[col0 / 128 * p.q_scale_ld + r] = scale;
         } else if (in) {
-          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) = gemm::pack16<OUT>(h[0], h[1]);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) =
+              make_uint2(gemm::pack16<OUT>(h[0], h[1]), gemm::pack16<OUT>(h[2], h[3]));
           if (p.kept_gate) {
             const long long kept = gemm_kept_at(r, col, p.kept_blocks);
-            *reinterpret_cast<float2*>(p.kept_gate + kept) = make_float2(v[0][0], v[0][1]);
-            *reinterpret_cast<float2*>(p.kept_up + kept) = make_float2(v[1][0], v[1][1]);
+            *reinterpret_cast<float4*>(p.kept_gate + kept) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+            *reinterpret_cast<float4*>(p.kept_up + kept) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
           }
         }
       }
