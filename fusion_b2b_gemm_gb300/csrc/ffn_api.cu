@@ -121,6 +121,7 @@ b2b_status_t check_workspace(const void* workspace, size_t bytes, size_t need) {
 struct Shape {
   int64_t tiles, whole;
   int splits;
+  double time;  // in K panels of a unit
   size_t part_bytes() const { return static_cast<size_t>(tiles - whole) * splits * kGemmPartFloats * sizeof(float) * (splits > 1); }
 };
 
@@ -129,17 +130,13 @@ struct Shape {
 // the weights' bytes alike): 8 for a unit's beginning and end, 9 more for the
 // second launch, and the parts' traffic at some 4 TB/s.
 Shape cut(int64_t tiles, int64_t kpan, int clusters) {
-  Shape best = {tiles, tiles, 1};
   const int64_t rounds = tiles / clusters, rest = tiles - rounds * clusters;
+  Shape best = {tiles, tiles, 1, static_cast<double>((rounds + (rest > 0)) * kpan)};
   if (rest == 0) return best;
-  double best_t = static_cast<double>((rounds + 1) * kpan);
   for (int s = 2; s <= 32 && kpan >= 4 * s; ++s) {
     const double t = static_cast<double>(rounds * kpan + ceil_div(rest * s, clusters) * ceil_div(kpan, s)) + 9.0 +
                      static_cast<double>(rest * s) * kGemmPartFloats * 8.0 / 1.4e6;
-    if (t < best_t) {
-      best_t = t;
-      best = {tiles, rounds * clusters, s};
-    }
+    if (t < best.time) best = {tiles, rounds * clusters, s, t};
   }
   return best;
 }
@@ -237,19 +234,52 @@ struct Launch {
   }
 };
 
+// How the kernel for few rows takes a product: tiles of 16 << size rows, a slice's
+// k cut in 1 << split_bits; size -1: the pair kernel is quicker.
+struct FewShape {
+  int size, row_tiles, split_bits;
+};
+FewShape few_shape(const b2b_ffn_plan_s* p, const SkinnyKernels& k, int64_t rows, int64_t n, int kpan) {
+  const int64_t room = 2 * p->sms;  // CTAs resident at once
+  double best = k.cost.pair + k.cost.pair_panel * cut(tile_count(rows, n, k.gate), kpan, p->sms / 2).time;
+  FewShape shape = {-1, 0, 0};
+  if (p->debug & B2B_DEBUG_PAIR_KERNEL) return shape;
+  for (int size = 0; size < k.sizes; ++size) {
+    const int64_t row_tiles = ceil_div(rows, 16 << size), tiles = row_tiles * ceil_div(n, k.columns);
+    // As many CTAs as are resident at once, two slots each at least.
+    int bits = 0;
+    while ((1 << bits) < kSkinnyMaxSplits && (tiles << (bits + 1)) <= room && kpan >= (4 << bits)) ++bits;
+    const double second = (tiles << bits) > p->sms ? 1.0 + k.cost.second : 1.0;
+    const double t = static_cast<double>(ceil_div(tiles << bits, room)) * second *
+                         (1.5 + static_cast<double>(ceil_div(kpan, 1 << bits)) * (k.cost.slot + k.cost.slot_row * (16 << size))) +
+                     0.14 * (1 << bits);
+    if (t < best) {
+      best = t;
+      shape = {size, static_cast<int>(row_tiles), bits};
+    }
+    if (row_tiles == 1) break;  // (a larger tile would be emptier)
+  }
+  return shape;
+}
+
 // A product for few rows in the making.
 struct FewRows {
   const b2b_ffn_plan_s* plan;
   const SkinnyKernels& k;
+  FewShape shape;
   bool e4m3;
   SkinnyMaps maps;
   SkinnyParams p;
   b2b_status_t st = B2B_OK;
 
-  FewRows(const b2b_ffn_plan_s* plan_, const SkinnyKernels& k_, bool e4m3_, const Matrix& x) : plan(plan_), k(k_), e4m3(e4m3_) {
+  FewRows(const b2b_ffn_plan_s* plan_, const SkinnyKernels& k_, const FewShape& shape_, bool e4m3_, const Matrix& x)
+      : plan(plan_), k(k_), shape(shape_), e4m3(e4m3_) {
     std::memset(&p, 0, sizeof(p));
     p.rows = static_cast<int>(x.rows);
-    p.x_box_rows = static_cast<int>((x.rows + 7) & ~int64_t(7));
+    p.row_tiles = shape.row_tiles;
+    p.split_bits = shape.split_bits;
+    p.splits = 1 << p.split_bits;
+    p.x_box_rows = static_cast<int>(std::min<int64_t>(16 << shape.size, (x.rows + 7) & ~int64_t(7)));
     p.segment = 1 << 30;
     p.act = plan->act;
     p.debug = plan->debug;
@@ -274,15 +304,10 @@ struct FewRows {
   }
   b2b_status_t run(cudaStream_t stream) {
     if (st != B2B_OK) return st;
-    int size = 0;
-    while (p.rows > 16 << size) ++size;
-    const int slices = static_cast<int>(ceil_div(p.N, k.columns)), room = 2 * plan->sms;
-    // As many CTAs as are resident at once, two slots each at least.
-    while ((1 << p.split_bits) < kSkinnyMaxSplits && (2 << p.split_bits) * slices <= room && p.slots >= (4 << p.split_bits)) ++p.split_bits;
-    p.splits = 1 << p.split_bits;
+    const int64_t ctas = ceil_div(p.N, k.columns) * p.row_tiles * p.splits;
     p.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(plan->budget_ns, 5000ull * p.slots), 4000000000ull));
     void* args[] = {&maps, &p};
-    if (launch_pdl(k.main[size], dim3(static_cast<unsigned>(slices * p.splits)), dim3(kSkinnyThreads), args, k.smem[size], stream, p.splits) !=
+    if (launch_pdl(k.main[shape.size], dim3(static_cast<unsigned>(ctas)), dim3(kSkinnyThreads), args, k.smem[shape.size], stream, p.splits) !=
         cudaSuccess) {
       cudaGetLastError();
       return B2B_ERR_CUDA;
@@ -301,9 +326,6 @@ struct Pieces {
   size_t parts = 0;
   size_t total() const { return rounded(hidden) + rounded(second) + rounded(x_scale) + rounded(h_scale) + parts; }
 };
-
-// Up to so many rows a plan's products take the kernel for few rows (not the weights' gradients, whose sums are over rows).
-int few_rows(const b2b_ffn_plan_s* p) { return (p->kind == kFfn ? p->k.gate_few : p->s.gate_few).most_rows(); }
 
 // What a forward pass keeps: G and U, then H.
 struct Kept {
@@ -324,37 +346,37 @@ struct Kept {
   void* hidden(const void* kept) const { return static_cast<uint8_t*>(const_cast<void*>(kept)) + 2 * each; }
 };
 
+const SkinnyKernels& product_few(const b2b_ffn_plan_s* p) { return p->s.product_few[p->dtype == B2B_BF16]; }
+
 Pieces pieces(const b2b_ffn_plan_s* p, int64_t rows, int pass) {
   Pieces w;
   const int64_t d = p->width, f = p->hidden, o = p->out_width;
   const size_t t = static_cast<size_t>(rows);
-  const bool few = rows <= few_rows(p) && pass != B2B_FFN_BACKWARD;
-  auto part = [&](int64_t tiles, int kpan) {
-    if (!few) w.parts = std::max(w.parts, part_bytes(p, tiles, kpan));
+  auto part = [&](int64_t tiles, int kpan) { w.parts = std::max(w.parts, part_bytes(p, tiles, kpan)); };
+  auto product = [&](const SkinnyKernels& k, int64_t n, int kpan) {
+    if (few_shape(p, k, rows, n, kpan).size < 0) part(tile_count(rows, n, k.gate), kpan);
   };
   if (p->kind == kScaledGemm) {
-    part(tile_count(rows, o, false), panels(d, true));
+    product(product_few(p), o, panels(d, true));
   } else if (p->kind == kScaledFfn) {
     w.hidden = t * f;
     w.second = t * d;
     w.x_scale = 4 * t * ceil_div(d, 128);
     w.h_scale = 4 * t * ceil_div(f, 128);
-    part(tile_count(rows, f, true), panels(d, true));
-    part(tile_count(rows, o, false), panels(f, true));
+    product(p->s.gate_few, f, panels(d, true));
+    product(product_few(p), o, panels(f, true));
   } else if (pass == B2B_FFN_BACKWARD) {
     w.hidden = w.second = 2 * t * f;
-    if (rows > few_rows(p)) {
-      part(tile_count(rows, f, false), panels(o));
-      part(tile_count(rows, d, false), 2 * panels(f));
-    }
+    product(p->k.gate_grad_few, f, panels(o));
+    product(p->k.dx_few, d, 2 * panels(f));
     // (any of the weights' gradients may be left out)
     for (int g = 0; g <= 2; ++g)
       for (int e = 0; e <= 1; ++e)
         if (g + e) part(g * tile_count(d, f, false) + e * tile_count(f, o, false), panels(rows));
   } else {
     w.hidden = pass == B2B_FFN_TRAINING ? 0 : 2 * t * f;
-    part(tile_count(rows, f, true), panels(d));
-    part(tile_count(rows, o, false), panels(f));
+    product(p->k.gate_few, f, panels(d));
+    product(p->k.down_few, o, panels(f));
   }
   return w;
 }
@@ -409,7 +431,7 @@ b2b_status_t create(b2b_ffn_plan_t* out, FfnKind kind, b2b_dtype_t dtype, int64_
     use_few(p->k.dx_few);
   } else {
     use_e4m3(p->s.product[dtype == B2B_BF16]);
-    use_few(p->s.product_few[dtype == B2B_BF16]);
+    use_few(product_few(p));
     if (kind == kScaledFfn) {
       use_e4m3(p->s.gate);
       use_few(p->s.gate_few);
@@ -429,9 +451,9 @@ b2b_status_t create(b2b_ffn_plan_t* out, FfnKind kind, b2b_dtype_t dtype, int64_
   return B2B_OK;
 }
 
-b2b_status_t scaled_few(const b2b_ffn_plan_s* p, const Matrix& a, const b2b_scales_t& a_scale, const Matrix& b, const b2b_scales_t& b_scale,
-                        const Matrix& out, cudaStream_t stream) {
-  FewRows l(p, p->s.product_few[p->dtype == B2B_BF16], true, a);
+b2b_status_t scaled_few(const b2b_ffn_plan_s* p, const FewShape& shape, const Matrix& a, const b2b_scales_t& a_scale, const Matrix& b,
+                        const b2b_scales_t& b_scale, const Matrix& out, cudaStream_t stream) {
+  FewRows l(p, product_few(p), shape, true, a);
   l.weight(0, b);
   l.p.out = out.m->data;
   l.p.out_ld = out.m->row_stride;
@@ -519,7 +541,7 @@ b2b_status_t b2b_ffn_plan_set_wait_budget(b2b_ffn_plan_t p, uint64_t budget_ns) 
 
 b2b_status_t b2b_ffn_plan_set_debug(b2b_ffn_plan_t p, uint32_t flags) {
   if (!p) return B2B_ERR_INVALID_ARG;
-  if (flags & ~B2B_DEBUG_DROP_FIRST_LOAD) return B2B_ERR_INVALID_ARG;
+  if (flags & ~(B2B_DEBUG_DROP_FIRST_LOAD | B2B_DEBUG_PAIR_KERNEL)) return B2B_ERR_INVALID_ARG;
   p->debug = flags;
   return B2B_OK;
 }
@@ -564,22 +586,16 @@ b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t p, const b2b_ffn_forward_t* r, b2b_s
   const b2b_matrix_t h_rows = {keep ? kept.hidden(r->kept) : ws, f};
   void* parts = ws + rounded(w.hidden);
   const Matrix h = {&h_rows, t, f, 2};
-  if (t <= few_rows(p)) {
-    FewRows up(p, p->k.gate_few, false, in[0]);
-    up.weight(0, in[1]);
-    up.weight(1, in[2]);
-    up.p.out = h_rows.data;
-    up.p.out_ld = f;
-    if (keep) kept.set(up.p, r->kept);
-    st = up.run(stream);
-    if (st != B2B_OK) return st;
-    FewRows down(p, p->k.down_few, false, h);
-    down.weight(0, in[3]);
-    down.p.out = r->out.data;
-    down.p.out_ld = r->out.row_stride;
-    return down.run(stream);
-  }
-  {
+  const FewShape up_few = few_shape(p, p->k.gate_few, t, f, panels(d)), down_few = few_shape(p, p->k.down_few, t, o, panels(f));
+  if (up_few.size >= 0) {
+    FewRows l(p, p->k.gate_few, up_few, false, in[0]);
+    l.weight(0, in[1]);
+    l.weight(1, in[2]);
+    l.p.out = h_rows.data;
+    l.p.out_ld = f;
+    if (keep) kept.set(l.p, r->kept);
+    st = l.run(stream);
+  } else {
     Launch l(p, true, false);
     l.a_rows(0, in[0]);
     l.b_cols(0, in[1]);
@@ -590,6 +606,13 @@ b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t p, const b2b_ffn_forward_t* r, b2b_s
     st = l.run(p->k.gate, panels(d), parts, stream);
   }
   if (st != B2B_OK) return st;
+  if (down_few.size >= 0) {
+    FewRows l(p, p->k.down_few, down_few, false, h);
+    l.weight(0, in[3]);
+    l.p.out = r->out.data;
+    l.p.out_ld = r->out.row_stride;
+    return l.run(stream);
+  }
   Launch l(p, false, false);
   l.a_rows(0, h);
   l.b_cols(0, in[3]);
@@ -632,45 +655,47 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
   const b2b_matrix_t dg_rows = {ws, f}, du_rows = {ws + rounded(w.hidden), f};
   void* parts = ws + rounded(w.hidden) + rounded(w.second);
   const Matrix dg = {&dg_rows, t, f, 2}, du = {&du_rows, t, f, 2};
-  const bool few = t <= few_rows(p);
-  if (few && (r->dx.data || r->dw_gate.data || r->dw_up.data)) {
-    FewRows l(p, p->k.gate_grad_few, false, in[0]);
-    l.weight(0, in[4]);
-    l.p.out = dg_rows.data;
-    l.p.out2 = du_rows.data;
-    l.p.out_ld = f;
-    kept.set(l.p, r->kept);
-    st = l.run(stream);
-    if (st == B2B_OK && r->dx.data) {
-      FewRows x(p, p->k.dx_few, false, dg);
-      x.weight(0, in[2]);
-      x.more(du);
-      x.weight(1, in[3]);
-      x.p.out = r->dx.data;
-      x.p.out_ld = r->dx.row_stride;
-      st = x.run(stream);
+  const FewShape grad_few = few_shape(p, p->k.gate_grad_few, t, f, panels(o)), dx_few = few_shape(p, p->k.dx_few, t, d, 2 * panels(f));
+  if (r->dx.data || r->dw_gate.data || r->dw_up.data) {
+    if (grad_few.size >= 0) {
+      FewRows l(p, p->k.gate_grad_few, grad_few, false, in[0]);
+      l.weight(0, in[4]);
+      l.p.out = dg_rows.data;
+      l.p.out2 = du_rows.data;
+      l.p.out_ld = f;
+      kept.set(l.p, r->kept);
+      st = l.run(stream);
+    } else {
+      Launch l(p, false, false);
+      l.a_rows(0, in[0]);
+      l.b_rows(0, in[4]);
+      l.out(0, dg);
+      l.out(1, du);
+      kept.set(l.p, r->kept);
+      l.problem(t, f);
+      st = l.run(p->k.gate_grad, panels(o), parts, stream);
     }
   }
-  if (!few && (r->dx.data || r->dw_gate.data || r->dw_up.data)) {
-    Launch l(p, false, false);
-    l.a_rows(0, in[0]);
-    l.b_rows(0, in[4]);
-    l.out(0, dg);
-    l.out(1, du);
-    kept.set(l.p, r->kept);
-    l.problem(t, f);
-    st = l.run(p->k.gate_grad, panels(o), parts, stream);
-  }
-  if (!few && st == B2B_OK && r->dx.data) {
-    Launch l(p, false, false);
-    l.a_rows(0, dg);
-    l.a_rows(1, du);
-    l.b_rows(0, in[2]);
-    l.b_rows(1, in[3]);
-    l.out(0, out[0]);
-    l.p.kseg = panels(f);
-    l.problem(t, d);
-    st = l.run(p->k.dx, 2 * panels(f), parts, stream);
+  if (st == B2B_OK && r->dx.data) {
+    if (dx_few.size >= 0) {
+      FewRows l(p, p->k.dx_few, dx_few, false, dg);
+      l.weight(0, in[2]);
+      l.more(du);
+      l.weight(1, in[3]);
+      l.p.out = r->dx.data;
+      l.p.out_ld = r->dx.row_stride;
+      st = l.run(stream);
+    } else {
+      Launch l(p, false, false);
+      l.a_rows(0, dg);
+      l.a_rows(1, du);
+      l.b_rows(0, in[2]);
+      l.b_rows(1, in[3]);
+      l.out(0, out[0]);
+      l.p.kseg = panels(f);
+      l.problem(t, d);
+      st = l.run(p->k.dx, 2 * panels(f), parts, stream);
+    }
   }
   if (st == B2B_OK && (r->dw_gate.data || r->dw_up.data || r->dw_down.data)) {
     Launch l(p, false, false);
@@ -718,26 +743,25 @@ b2b_status_t b2b_scaled_ffn_run(b2b_ffn_plan_t p, const b2b_scaled_ffn_t* r, b2b
   void* parts = hs + rounded(w.h_scale) / 4;
   st = quantize(p->k, t, d, 1, r->x, xq, {xs, 1, t}, stream);
   if (st != B2B_OK) return st;
-  if (t <= few_rows(p)) {
-    FewRows up(p, p->s.gate_few, true, {&xq, t, d, 1});
-    up.weight(0, in[1]);
-    up.weight(1, in[2]);
-    up.p.out = ws;
-    up.p.out_ld = f;
-    up.p.a_scale = xs;
-    up.p.a_scale_row = 1;
-    up.p.a_scale_k = t;
+  const FewShape up_few = few_shape(p, p->s.gate_few, t, f, panels(d, true)), down_few = few_shape(p, product_few(p), t, o, panels(f, true));
+  if (up_few.size >= 0) {
+    FewRows l(p, p->s.gate_few, up_few, true, {&xq, t, d, 1});
+    l.weight(0, in[1]);
+    l.weight(1, in[2]);
+    l.p.out = ws;
+    l.p.out_ld = f;
+    l.p.a_scale = xs;
+    l.p.a_scale_row = 1;
+    l.p.a_scale_k = t;
     for (int i = 0; i < 2; ++i) {
-      up.p.b_scale[i] = scales[i]->data;
-      up.p.b_scale_row[i] = scales[i]->row_stride;
-      up.p.b_scale_k[i] = scales[i]->block_stride;
+      l.p.b_scale[i] = scales[i]->data;
+      l.p.b_scale_row[i] = scales[i]->row_stride;
+      l.p.b_scale_k[i] = scales[i]->block_stride;
     }
-    up.p.q_scale = hs;
-    up.p.q_scale_ld = t;
-    st = up.run(stream);
-    return st == B2B_OK ? scaled_few(p, {&hq, t, f, 1}, {hs, 1, t}, in[3], r->down_scale, out[0], stream) : st;
-  }
-  {
+    l.p.q_scale = hs;
+    l.p.q_scale_ld = t;
+    st = l.run(stream);
+  } else {
     Launch l(p, true, true);
     l.a_rows(0, {&xq, t, d, 1});
     l.b_rows(0, in[1]);
@@ -758,6 +782,7 @@ b2b_status_t b2b_scaled_ffn_run(b2b_ffn_plan_t p, const b2b_scaled_ffn_t* r, b2b
     st = l.run(p->s.gate, panels(d, true), parts, stream);
   }
   if (st != B2B_OK) return st;
+  if (down_few.size >= 0) return scaled_few(p, down_few, {&hq, t, f, 1}, {hs, 1, t}, in[3], r->down_scale, out[0], stream);
   Launch l(p, false, true);
   l.a_rows(0, {&hq, t, f, 1});
   l.b_rows(0, in[3]);
@@ -789,7 +814,9 @@ b2b_status_t b2b_scaled_gemm_run(b2b_ffn_plan_t p, const b2b_scaled_gemm_t* r, b
   if (st == B2B_OK) st = check_workspace(r->workspace, r->workspace_bytes, w.total());
   if (st == B2B_OK) st = check_current_device(p);
   if (st != B2B_OK) return st;
-  if (m <= few_rows(p)) return scaled_few(p, in[0], r->a_scale, in[1], r->b_scale, out[0], reinterpret_cast<cudaStream_t>(stream_));
+  const FewShape few = few_shape(p, product_few(p), m, n, panels(k, true));
+  if (few.size >= 0)
+    return scaled_few(p, few, in[0], r->a_scale, in[1], r->b_scale, out[0], reinterpret_cast<cudaStream_t>(stream_));
   Launch l(p, false, true);
   l.a_rows(0, in[0]);
   l.b_rows(0, in[1]);

@@ -19,12 +19,13 @@ GemmKernel gemm_kernel_pair() {
           reinterpret_cast<const void*>(&gemm_combine_kernel<EPI, OUT>)};
 }
 
-// The kernels for at most 16, 32, 64 and (16-bit operands) 128 rows.
+// The kernels for tiles of 16, 32, 64 and (16-bit operands) 128 rows.
 struct SkinnyKernels {
   const void* main[4];
   int smem[4], sizes, columns, depth;
   bool k_major;  // order of the weights
-  int most_rows() const { return 8 << sizes; }
+  bool gate;
+  SkinnyCost cost;
 };
 template <int IN, int OUT, int EPI, bool KM>
 SkinnyKernels skinny_kernels() {
@@ -35,7 +36,9 @@ SkinnyKernels skinny_kernels() {
                      3,
                      SkinnyShape<F8, GATE, 16>::kColumns,
                      SkinnyShape<F8, GATE, 16>::kDepth,
-                     KM};
+                     KM,
+                     GATE,
+                     SkinnyShape<F8, GATE, 16>::kCost};
   if constexpr (!F8) {
     k.main[3] = reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 128>);
     k.smem[3] = SkinnyShape<F8, GATE, 128>::kBytes;

@@ -1,6 +1,6 @@
-// The feed-forward operators' products for few rows (16-bit operands: at most
-// 128, e4m3: 64): the weights' bytes are what they cost, so every weight is read
-// once, by many CTAs at a time, and nothing is written but the result.
+// The feed-forward operators' products for few rows: the weights' bytes are what
+// they cost, so every weight is read by many CTAs at a time, and nothing is
+// written but the result.
 //
 // The product is taken transposed: the weights' columns are the 128 rows of
 // tcgen05.mma's A, the tokens the N columns of its B, so that a token more costs
@@ -9,6 +9,15 @@
 // this GPU bounds it from there on: a block of 4096/14336/4096, bf16, 59, 77 and
 // 111 us for 16, 32 and 64 tokens, against 56, 58 and 61 us; the pair kernel,
 // whose tile of 256 rows is mostly empty, takes 72 us for one token, this one 54.)
+//
+// More rows make several tiles of 16, 32, 64 or (16 bits) 128, side by side on one
+// slice of the columns, so that its weights come from memory once.  That is quicker
+// than the pair kernel as long as its tiles of 256 x 256 leave most SMs idle: an
+// e4m3 product of 128 rows by 2000 k by 1368 columns takes 6.3 us, 12.5 there, of
+// 128 rows by 14336 by 4096 23 and 25 us; a training step of 192 tokens on
+// 1024/2816/1024 41 and 55 us.  It reads an operand's panel for 1/4 to 1/16 of the
+// work, and loses where many tiles run one after the other: 500 tokens on
+// 4096/14336/4096 160 us, 110 there.  few_shape() weighs them.
 //
 // A CTA takes a slice of the columns and, where slices alone are too few to keep
 // the memory busy, a range of k; the CTAs of a slice are a cluster and add their
@@ -46,6 +55,7 @@ struct SkinnyParams {
   int slots;          // panels of the whole of k
   int segment;        // panels of the first product (then x and the weight go on in the second maps)
   int splits, split_bits;  // CTAs of a slice, a power of two
+  int row_tiles;           // of NT rows
   int x_box_rows;
   int act;
   void* out;          // h (or, e4m3 gate, its values), or the product
@@ -78,8 +88,18 @@ enum : int {  // barrier slots (8 bytes each)
   kSSlotTmem = 21,   // uint32 tensor-memory base, then the int abort flag
 };
 
+// Times in us, for the choice between this kernel and the pair kernel (fitted to
+// 16..1024 rows by 1024..14336 columns by 1024..14336 k, to 9-14 %): a slot of this
+// one, the same for each of its rows, what a second CTA on the SM adds, relatively,
+// and the pair kernel's start beyond this one's and its K panel.
+struct SkinnyCost {
+  float slot, slot_row, second, pair, pair_panel;
+};
+
 template <bool F8, bool GATE, int NT>
 struct SkinnyShape {
+  static constexpr SkinnyCost kCost = !F8 ? SkinnyCost{0.17f, 0.0024f, 0.14f, 2.0f, 0.31f}
+                                      : GATE ? SkinnyCost{0.10f, 0.0102f, 0.72f, 6.5f, 0.53f} : SkinnyCost{0.11f, 0.0047f, 0.53f, 4.2f, 0.35f};
   static constexpr int kColumns = F8 || !GATE ? 128 : 64;  // of a slice
   static constexpr int kDepth = F8 ? 128 : 64;             // k of a slot
   static constexpr int kWeight = F8 && GATE ? 32768 : 16384;
@@ -126,7 +146,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[C]) {
 }  // namespace skinny
 
 // IN: operands; OUT: 16-bit type of the result (not of kEpiGateQuant's); EPI: of gemm.cuh's, what follows the product;
-// KM: K-major weights; NT: 16, 32, 64 or 128 tokens.
+// KM: K-major weights; NT: rows of a tile, 16, 32, 64 or 128.
 template <int IN, int OUT, int EPI, bool KM, int NT>
 __global__ void __launch_bounds__(kSkinnyThreads, 2)
     skinny_kernel(const __grid_constant__ SkinnyMaps maps, const __grid_constant__ SkinnyParams p) {
@@ -145,7 +165,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kOffBar + 8 * kSSlotTmem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = static_cast<int>(blockIdx.x) % p.splits, col0 = static_cast<int>(blockIdx.x) / p.splits * L::kColumns;
+  const int part = static_cast<int>(blockIdx.x) & (p.splits - 1), tile = static_cast<int>(blockIdx.x) >> p.split_bits;
+  const int col0 = tile / p.row_tiles * L::kColumns, row0 = tile % p.row_tiles * NT;
+  const int rows = min(NT, p.rows - row0);
   const int s0 = static_cast<int>(static_cast<long long>(p.slots) * part / p.splits);
   const int s1 = static_cast<int>(static_cast<long long>(p.slots) * (part + 1) / p.splits);
   // MN-major: two blocks of 64 columns a slot; K-major: 128 bytes of k of 128 columns
@@ -210,7 +232,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         if (!((p.debug & 1u) && issued == 0)) {  // (test support: the first slot is armed but never filled)
           weights(s, [&](int off, const CUtensorMap* m, int x, int y) { tma_load_2d(dst + off, m, full, x, y); });
           const int seg = s >= p.segment ? 1 : 0;
-          tma_load_2d(dst + L::kWeight, &maps.x[seg], full, (s - (seg ? p.segment : 0)) * L::kDepth, 0);
+          tma_load_2d(dst + L::kWeight, &maps.x[seg], full, (s - (seg ? p.segment : 0)) * L::kDepth, row0);
         }
         ++issued;
         if (++slot == L::kRing) {
@@ -273,7 +295,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       if (ok) {
 #pragma unroll
         for (int c = 0; c < NT; c += C) {
-          if (c < p.rows) {
+          if (c < rows) {
             uint32_t v[C];
             skinny::tmem_ld<C>(lanes + static_cast<uint32_t>(c), v);
             tmem_wait_ld(v);
@@ -298,7 +320,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const int r = i * 32 + lane;
-          const float a = r < p.rows ? gemm::load(p.a_scale + r * p.a_scale_row + s * p.a_scale_k) : 0.0f;
+          const float a = r < rows ? gemm::load(p.a_scale + (row0 + r) * p.a_scale_row + s * p.a_scale_k) : 0.0f;
 #pragma unroll
           for (int w = 0; w < W; ++w) next[w][i] = a * gemm::load(p.b_scale[w] + nb * p.b_scale_row[w] + s * p.b_scale_k[w]);
         }
@@ -359,14 +381,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   }
   // Sums of token r are added up by CTA r % splits.  Apart: there, [CTA they come
   // from][r / splits][column], once the others have begun; else, already, here, [r][column].
-  const int share = (p.rows + p.splits - 1) >> p.split_bits;
+  const int share = (rows + p.splits - 1) >> p.split_bits;
   if constexpr (L::kApart) {
     if (p.splits > 1) cluster_wait();
     if (warp >= 2) {
       const uint32_t mine = base + L::kOffSums + static_cast<uint32_t>(part * share * L::kSumLd + (warp & 3) * 32 + lane) * 4u;
 #pragma unroll
       for (int e = 0; e < NT; ++e) {
-        if (e < p.rows)
+        if (e < rows)
           skinny::store_remote(mapa_shared(mine + static_cast<uint32_t>((e >> p.split_bits) * L::kSumLd) * 4u,
                                            static_cast<uint32_t>(e & (p.splits - 1))),
                                acc_sum[0][e]);
@@ -383,7 +405,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     constexpr int V = 4, kLanes = L::kColumns / V, kRows = 32 / kLanes;
     const int at_col = lane % kLanes * V, col = col0 + at_col;
     const uint32_t sums = base + L::kOffSums + static_cast<uint32_t>(at_col) * 4u;
-    for (int r = part + ((warp * kRows + lane / kLanes) << p.split_bits); r < p.rows; r += (kSkinnyThreads / 32 * kRows) << p.split_bits) {
+    for (int r = part + ((warp * kRows + lane / kLanes) << p.split_bits); r < rows; r += (kSkinnyThreads / 32 * kRows) << p.split_bits) {
       float v[GATE ? 2 : 1][V];
 #pragma unroll
       for (auto& a : v)
@@ -400,7 +422,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       const bool in = col < p.N;  // (N is a multiple of V)
       if constexpr (EPI == kEpiGateGrad) {
         if (in) {
-          const long long kept = gemm_kept_at(r, col, p.kept_blocks);
+          const long long kept = gemm_kept_at(row0 + r, col, p.kept_blocks);
           const uint4 gw = gemm::load(reinterpret_cast<const uint4*>(p.kept_gate + kept)), uw = gemm::load(reinterpret_cast<const uint4*>(p.kept_up + kept));
           float dg[V], du[V];
 #pragma unroll
@@ -414,14 +436,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
             dg[e] = v[0][e] * __uint_as_float((&uw.x)[e]) * s;
             du[e] = v[0][e] * a;
           }
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) =
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (row0 + r) * p.out_ld + col) =
               make_uint2(gemm::pack16<OUT>(dg[0], dg[1]), gemm::pack16<OUT>(dg[2], dg[3]));
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out2) + r * p.out_ld + col) =
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out2) + (row0 + r) * p.out_ld + col) =
               make_uint2(gemm::pack16<OUT>(du[0], du[1]), gemm::pack16<OUT>(du[2], du[3]));
         }
       } else if constexpr (!GATE) {
         if (in)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) =
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (row0 + r) * p.out_ld + col) =
               make_uint2(gemm::pack16<OUT>(v[0][0], v[0][1]), gemm::pack16<OUT>(v[0][2], v[0][3]));
       } else {
         float h[V];
@@ -435,14 +457,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
           float inv;
           const float scale = gemm::block_scale(top, inv);
           if (in)
-            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + r * p.out_ld + col) =
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (row0 + r) * p.out_ld + col) =
                 gemm::pack_e4m3(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
-          if (lane == 0) p.q_scale[col0 / 128 * p.q_scale_ld + r] = scale;
+          if (lane == 0) p.q_scale[col0 / 128 * p.q_scale_ld + row0 + r] = scale;
         } else if (in) {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.out_ld + col) =
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (row0 + r) * p.out_ld + col) =
               make_uint2(gemm::pack16<OUT>(h[0], h[1]), gemm::pack16<OUT>(h[2], h[3]));
           if (p.kept_gate) {
-            const long long kept = gemm_kept_at(r, col, p.kept_blocks);
+            const long long kept = gemm_kept_at(row0 + r, col, p.kept_blocks);
             *reinterpret_cast<float4*>(p.kept_gate + kept) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
             *reinterpret_cast<float4*>(p.kept_up + kept) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
           }

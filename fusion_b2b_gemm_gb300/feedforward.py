@@ -187,7 +187,7 @@ class _Plan:
         _check(_lib.b2b_ffn_plan_set_wait_budget(self._h, int(ns)), "b2b_ffn_plan_set_wait_budget")
 
     def set_debug(self, flags: int) -> None:
-        """Test support (see b2b_plan_set_debug in include/b2b.h)."""
+        """Test support (see b2b_plan_set_debug and B2B_DEBUG_PAIR_KERNEL in include/b2b.h)."""
         _check(_lib.b2b_ffn_plan_set_debug(self._h, int(flags)), "b2b_ffn_plan_set_debug")
 
     def close(self) -> None:

@@ -18,7 +18,7 @@ b2b = pytest.importorskip("fusion_b2b_gemm_gb300")
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 sys.path.insert(0, os.path.join(ROOT, "tests"))
 from test_feedforward_gpu import (  # noqa: E402
-    E4M3, TINY, TYPES, U, Val, act, normal, scaled, want_backward, want_forward, want_product, weights)
+    E4M3, TINY, TYPES, U, Val, act, kernels, normal, scaled, want_backward, want_forward, want_product, weights)
 
 INVALID, UNSUPPORTED, ALIGNMENT, ALIAS, TIMEOUT = 1, 2, 3, 4, 7
 
@@ -473,7 +473,7 @@ def test_refusals_at_the_c_entries():
     assert lib.b2b_ffn_workspace(plan._h, 1, 3, ctypes.byref(n)) == INVALID
     assert lib.b2b_ffn_workspace(plan._h, 1 << 31, 0, ctypes.byref(n)) == UNSUPPORTED
     assert lib.b2b_ffn_workspace(plan._h, 600, 0, ctypes.byref(n)) == 0 and n.value > 0
-    assert lib.b2b_ffn_plan_set_debug(plan._h, 2) == INVALID
+    assert lib.b2b_ffn_plan_set_debug(plan._h, 4) == INVALID
     out = torch.zeros(600, 72, dtype=torch.bfloat16, device="cuda")
     ws = torch.zeros(n.value + 256, dtype=torch.uint8, device="cuda")
 

@@ -36,6 +36,23 @@ def _cuda():
     torch.cuda.set_device(0)
 
 
+@pytest.fixture(params=[0, 2], ids=["chosen", "pair"], autouse=True)
+def kernels(request, monkeypatch):
+    """Every test twice: with the kernels that the sizes lead to, and with the one for large products everywhere."""
+    if not request.param:
+        return
+    for cls in (b2b.GatedFeedForwardPlan, b2b.ScaledFeedForwardPlan, b2b.ScaledGemmPlan):
+        def init(self, *args, _init=cls.__init__, **kwargs):
+            _init(self, *args, **kwargs)
+            self.set_debug(0)
+
+        def set_debug(self, flags, _set=cls.set_debug):
+            _set(self, flags | request.param)
+
+        monkeypatch.setattr(cls, "__init__", init)
+        monkeypatch.setattr(cls, "set_debug", set_debug)
+
+
 def normal(seed, *shape, dtype="bf16", scale=1.0):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return (scale * torch.randn(shape, generator=g, device="cuda")).to(TYPES[dtype])
@@ -146,6 +163,13 @@ def test_token_counts(tokens):
                                    (2048, 136, 264, 520)], ids=str)
 def test_long_products_are_cut_along_k(sizes):
     case("f16", *sizes)
+
+
+@pytest.mark.parametrize("tokens", [15, 17, 33, 48, 65, 97, 130, 200, 320, 450])
+def test_tiles_of_few_rows(tokens):
+    """Several tiles of 16 to 128 rows, the last of them cut short, of slices whose k is cut or not."""
+    case("f16", tokens, 1032, 1416, 520, seed=tokens)
+    case("bf16", tokens, 96, 3080, 1608, "gelu", seed=tokens)
 
 
 # ------------------------------------------------------------------------- 8 bits
@@ -262,3 +286,13 @@ def ffn8_case(dtype, t, d, f, o, kind="silu", seed=0):
                                    (700, 512, 1024, 512)], ids=str)
 def test_block_in_8_bits(dtype, kind, sizes):
     ffn8_case(dtype, *sizes, kind)
+
+
+@pytest.mark.parametrize("rows", [15, 17, 33, 48, 65, 97, 130, 200, 320, 1000])
+def test_tiles_of_few_rows_in_8_bits(rows):
+    (a, sa), (b, sb) = scaled(1, rows, 2000, 1), scaled(2, 1368, 2000, 128)
+    plan = b2b.ScaledGemmPlan("f16", 2000, 1368)
+    out = plan.run(a, sa, b, sb)
+    assert plan.status() == 0
+    want_product(a, sa, b, sb).check(out, "f16")
+    ffn8_case("bf16", rows, 528, 1424, 272, seed=rows)
