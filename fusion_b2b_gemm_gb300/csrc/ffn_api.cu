@@ -307,7 +307,7 @@ struct FewRows {
     const int64_t ctas = ceil_div(p.N, k.columns) * p.row_tiles * p.splits;
     p.budget_ns = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(plan->budget_ns, 5000ull * p.slots), 4000000000ull));
     void* args[] = {&maps, &p};
-    if (launch_pdl(k.main[shape.size], dim3(static_cast<unsigned>(ctas)), dim3(kSkinnyThreads), args, k.smem[shape.size], stream, p.splits) !=
+    if (launch_pdl(k.main[shape.size], dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(k.threads[shape.size])), args, k.smem[shape.size], stream, p.splits) !=
         cudaSuccess) {
       cudaGetLastError();
       return B2B_ERR_CUDA;

@@ -22,7 +22,7 @@ GemmKernel gemm_kernel_pair() {
 // The kernels for tiles of 16, 32, 64 and (16-bit operands) 128 rows.
 struct SkinnyKernels {
   const void* main[4];
-  int smem[4], sizes, columns, depth;
+  int smem[4], threads[4], sizes, columns, depth;
   bool k_major;  // order of the weights
   bool gate;
   SkinnyCost cost;
@@ -33,6 +33,7 @@ SkinnyKernels skinny_kernels() {
   SkinnyKernels k = {{reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 16>), reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 32>),
                       reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 64>), nullptr},
                      {SkinnyShape<F8, GATE, 16>::kBytes, SkinnyShape<F8, GATE, 32>::kBytes, SkinnyShape<F8, GATE, 64>::kBytes, 0},
+                     {SkinnyShape<F8, GATE, 16>::kThreads, SkinnyShape<F8, GATE, 32>::kThreads, SkinnyShape<F8, GATE, 64>::kThreads, 0},
                      3,
                      SkinnyShape<F8, GATE, 16>::kColumns,
                      SkinnyShape<F8, GATE, 16>::kDepth,
@@ -42,6 +43,7 @@ SkinnyKernels skinny_kernels() {
   if constexpr (!F8) {
     k.main[3] = reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 128>);
     k.smem[3] = SkinnyShape<F8, GATE, 128>::kBytes;
+    k.threads[3] = SkinnyShape<F8, GATE, 128>::kThreads;
     k.sizes = 4;
   }
   return k;

@@ -39,15 +39,14 @@
 //            both weights for the gate.  Each slot's product is an accumulator of
 //            its own, multiplied by its scales and added up in registers.
 //
-// Warp 0 loads, warp 1 multiplies (one elected thread), warps 2-5 read tensor
-// memory.  Every wait is bounded.
+// Warp 0 loads, warp 1 multiplies (one elected thread), warps 2-5 (or 2-9) read
+// tensor memory.  Every wait is bounded.
 #pragma once
 
 #include "gemm.cuh"
 
 namespace b2b {
 
-constexpr int kSkinnyThreads = 192;
 constexpr int kSkinnyMaxSplits = 8;  // CTAs of a cluster
 
 struct SkinnyParams {
@@ -99,19 +98,28 @@ struct SkinnyCost {
 template <bool F8, bool GATE, int NT>
 struct SkinnyShape {
   static constexpr SkinnyCost kCost = !F8 ? SkinnyCost{0.17f, 0.0024f, 0.14f, 2.0f, 0.31f}
-                                      : GATE ? SkinnyCost{0.10f, 0.0102f, 0.72f, 6.5f, 0.53f} : SkinnyCost{0.11f, 0.0047f, 0.53f, 4.2f, 0.35f};
+                                      : GATE ? SkinnyCost{0.08f, 0.008f, 0.4f, 1.0f, 0.5f} : SkinnyCost{0.11f, 0.0047f, 0.53f, 4.2f, 0.35f};
   static constexpr int kColumns = F8 || !GATE ? 128 : 64;  // of a slice
   static constexpr int kDepth = F8 ? 128 : 64;             // k of a slot
   static constexpr int kWeight = F8 && GATE ? 32768 : 16384;
   static constexpr int kSlot = kWeight + NT * 128;
   static constexpr int kSumLd = GATE ? 2 * kColumns : kColumns;
+  // Warps that read tensor memory, and what a thread adds up of a column: both weights'
+  // rows, or half of them, or (kByWeight) one weight's.  Eight where four have too much to
+  // hold or to add (64 rows on 4096/14336/4096 46.5 -> 43.8 us, where the gate spilled
+  // registers; the product of 64 x 4096 x 14336 18.0 -> 17.1); four for the product of
+  // 32 rows (64 x 14336 x 4096 17.2 us, with eight 17.5).
+  static constexpr int kWarps = F8 && NT >= (GATE ? 32 : 64) ? 8 : 4;
+  static constexpr bool kByWeight = GATE && kWarps == 8 && NT == 64;
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kTake = kByWeight ? NT : NT / (kWarps / 4);
   // Sums of the CTAs of a slice: apart from the ring, written there by the CTA that has
   // them while another may still multiply, or in the ring's place, its CTA's own.
   static constexpr bool kApart = NT <= 32 && !(F8 && GATE);  // (one accumulator's)
   static constexpr int kSumBytes = NT * kSumLd * 4;
   static constexpr int kRing = (105 * 1024 - (kApart ? kSumBytes : 0)) / kSlot;
   static constexpr int kOffSums = kApart ? kRing * kSlot : 0;
-  static constexpr int kOffScales = kRing * kSlot + (kApart ? kSumBytes : 0);  // e4m3: [4 warps][2 weights][NT]
+  static constexpr int kOffScales = kRing * kSlot + (kApart ? kSumBytes : 0);  // e4m3: [warp][weights][kTake]
   static constexpr int kOffBar = kOffScales + (F8 ? 4 * 2 * NT * 4 : 0);
   static constexpr int kBytes = kOffBar + 256 + 1024;
   // columns of tensor memory: an accumulator, or two (of both weights)
@@ -148,14 +156,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[C]) {
 // IN: operands; OUT: 16-bit type of the result (not of kEpiGateQuant's); EPI: of gemm.cuh's, what follows the product;
 // KM: K-major weights; NT: rows of a tile, 16, 32, 64 or 128.
 template <int IN, int OUT, int EPI, bool KM, int NT>
-__global__ void __launch_bounds__(kSkinnyThreads, 2)
+__global__ void __launch_bounds__(SkinnyShape<IN == kGemmE4M3, EPI == kEpiGate || EPI == kEpiGateQuant, NT>::kThreads, 2)
     skinny_kernel(const __grid_constant__ SkinnyMaps maps, const __grid_constant__ SkinnyParams p) {
   using namespace ptx;
   constexpr bool F8 = IN == kGemmE4M3, GATE = EPI == kEpiGate || EPI == kEpiGateQuant;
   static_assert(F8 ? KM && (EPI == kEpiStore || EPI == kEpiGateQuant) : !(KM && GATE), "weights' order");
   using L = SkinnyShape<F8, GATE, NT>;
   constexpr int W = F8 && GATE ? 2 : 1;      // accumulators of a slot
-  constexpr int C = NT < 32 ? NT : 32;       // columns read at a time
+  constexpr int WT = L::kByWeight ? 1 : W;   // of them a thread takes
+  constexpr int T = L::kTake, C = T < 32 || L::kWarps == 8 ? 16 : 32;  // columns read at a time
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       mbar_init(bar(kSBEmpty + lane), 1);
     } else if (lane < 10 && lane >= 8) {
       mbar_init(bar(kSBAccFull + lane - 8), 1);
-      mbar_init(bar(kSBAccEmpty + lane - 8), 4);
+      mbar_init(bar(kSBAccEmpty + lane - 8), L::kWarps);
     } else if (lane == 10) {
       mbar_init(bar(kSBDrain), 1);
       *abort_flag = 0;
@@ -217,7 +226,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   grid_launch_dependents();
   grid_dependency_wait();
   const gemm::Wait bw{abort_flag, p.budget_ns};
-  float acc_sum[W][NT];  // of an epilogue thread: its column's sums
+  float acc_sum[WT][T];  // of an epilogue thread: its column's sums, of rows [first, first + T)
+  const int half = L::kWarps > 4 ? (warp - 2) / 4 : 0, first = L::kByWeight ? 0 : half * T, w0 = L::kByWeight ? half : 0;
   float* sum = reinterpret_cast<float*>(gbase + L::kOffSums);
 
   if (warp == 0) {
@@ -294,7 +304,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       tc_fence_after();
       if (ok) {
 #pragma unroll
-        for (int c = 0; c < NT; c += C) {
+        for (int c = 0; c < T; c += C) {
           if (c < rows) {
             uint32_t v[C];
             skinny::tmem_ld<C>(lanes + static_cast<uint32_t>(c), v);
@@ -313,43 +323,43 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll
         for (float& x : a) x = 0.0f;
       // Scales of the tokens times that of the weights' block, a slot ahead of their use.
-      constexpr int R = NT < 32 ? 1 : NT / 32;
-      float next[W][R];
+      constexpr int R = T < 32 ? 1 : T / 32;
+      float next[WT][R];
       const int nb = col0 / 128;
       auto fetch = [&](int s) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          const int r = i * 32 + lane;
+          const int r = first + i * 32 + lane;
           const float a = r < rows ? gemm::load(p.a_scale + (row0 + r) * p.a_scale_row + s * p.a_scale_k) : 0.0f;
 #pragma unroll
-          for (int w = 0; w < W; ++w) next[w][i] = a * gemm::load(p.b_scale[w] + nb * p.b_scale_row[w] + s * p.b_scale_k[w]);
+          for (int w = 0; w < WT; ++w) next[w][i] = a * gemm::load(p.b_scale[w0 + w] + nb * p.b_scale_row[w0 + w] + s * p.b_scale_k[w0 + w]);
         }
       };
-      float* scales = reinterpret_cast<float*>(gbase + L::kOffScales) + quad * 2 * NT;
+      float* scales = reinterpret_cast<float*>(gbase + L::kOffScales) + (warp - 2) * WT * T;
       if (s0 < s1) fetch(s0);
       uint32_t acc = 0, acc_phase = 0;
       for (int s = s0; s < s1; ++s) {
         __syncwarp();
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+        for (int w = 0; w < WT; ++w)
 #pragma unroll
           for (int i = 0; i < R; ++i)
-            if (i * 32 + lane < NT) scales[w * NT + i * 32 + lane] = next[w][i];
+            if (i * 32 + lane < T) scales[w * T + i * 32 + lane] = next[w][i];
         __syncwarp();
         if (s + 1 < s1) fetch(s + 1);
         ok = bw.wait(bar(kSBAccFull + acc), acc_phase);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+        for (int w = 0; w < WT; ++w)
 #pragma unroll
-          for (int c = 0; c < NT; c += C) {
+          for (int c = 0; c < T; c += C) {
             uint32_t v[C];
-            skinny::tmem_ld<C>(lanes + (acc * W + w) * NT + static_cast<uint32_t>(c), v);
+            skinny::tmem_ld<C>(lanes + (acc * W + static_cast<uint32_t>(w0 + w)) * NT + static_cast<uint32_t>(first + c), v);
             tmem_wait_ld(v);
 #pragma unroll
             for (int e = 0; e < C; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(scales + w * NT + c + e);
+              const float4 f = *reinterpret_cast<const float4*>(scales + w * T + c + e);
               acc_sum[w][c + e] += __uint_as_float(v[e]) * f.x;
               acc_sum[w][c + e + 1] += __uint_as_float(v[e + 1]) * f.y;
               acc_sum[w][c + e + 2] += __uint_as_float(v[e + 2]) * f.z;
@@ -365,9 +375,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       // every copy into the ring has been waited for by the MMAs that these sums came from
       if (ok && !L::kApart) {
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+        for (int w = 0; w < WT; ++w)
 #pragma unroll
-          for (int e = 0; e < NT; ++e) sum[e * L::kSumLd + w * 128 + column] = acc_sum[w][e];
+          for (int e = 0; e < T; ++e) sum[(first + e) * L::kSumLd + (w0 + w) * 128 + column] = acc_sum[w][e];
       }
     }
   }
@@ -387,10 +397,11 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     if (warp >= 2) {
       const uint32_t mine = base + L::kOffSums + static_cast<uint32_t>(part * share * L::kSumLd + (warp & 3) * 32 + lane) * 4u;
 #pragma unroll
-      for (int e = 0; e < NT; ++e) {
-        if (e < rows)
-          skinny::store_remote(mapa_shared(mine + static_cast<uint32_t>((e >> p.split_bits) * L::kSumLd) * 4u,
-                                           static_cast<uint32_t>(e & (p.splits - 1))),
+      for (int e = 0; e < T; ++e) {
+        const int r = first + e;
+        if (r < rows)
+          skinny::store_remote(mapa_shared(mine + static_cast<uint32_t>((r >> p.split_bits) * L::kSumLd) * 4u,
+                                           static_cast<uint32_t>(r & (p.splits - 1))),
                                acc_sum[0][e]);
       }
     }
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     constexpr int V = 4, kLanes = L::kColumns / V, kRows = 32 / kLanes;
     const int at_col = lane % kLanes * V, col = col0 + at_col;
     const uint32_t sums = base + L::kOffSums + static_cast<uint32_t>(at_col) * 4u;
-    for (int r = part + ((warp * kRows + lane / kLanes) << p.split_bits); r < rows; r += (kSkinnyThreads / 32 * kRows) << p.split_bits) {
+    for (int r = part + ((warp * kRows + lane / kLanes) << p.split_bits); r < rows; r += (L::kThreads / 32 * kRows) << p.split_bits) {
       float v[GATE ? 2 : 1][V];
 #pragma unroll
       for (auto& a : v)
