@@ -861,8 +861,12 @@ b2b_status_t b2b_quantize_blocks(b2b_dtype_t dtype, int64_t rows, int64_t cols, 
   if (st == B2B_OK) st = check(qm, 8);
   const int64_t scale_rows = ceil_div(rows, block_rows), blocks = ceil_div(cols, 128);
   if (st == B2B_OK) st = check(*scale, scale_rows);
-  // (scales are written: blocks may not share one)
-  if (st == B2B_OK && ((scale_rows > 1 && scale->row_stride == 0) || (blocks > 1 && scale->block_stride == 0))) st = B2B_ERR_INVALID_ARG;
+  // (scales are written: one direction's stride steps over the other's whole extent, so that blocks share none)
+  const double by_row = static_cast<double>(scale->row_stride), by_block = static_cast<double>(scale->block_stride);
+  const bool apart = scale_rows == 1 ? blocks == 1 || by_block > 0
+                                     : by_row > 0 && (blocks == 1 || (by_block > 0 && (by_row > static_cast<double>(blocks - 1) * by_block ||
+                                                                                       by_block > static_cast<double>(scale_rows - 1) * by_row)));
+  if (st == B2B_OK && !apart) st = B2B_ERR_INVALID_ARG;
   if (st == B2B_OK && (share(xm, qm) || overlaps_scales(xm, *scale, scale_rows, blocks) || overlaps_scales(qm, *scale, scale_rows, blocks)))
     st = B2B_ERR_ALIAS;
   if (st == B2B_OK) st = check_device(nullptr, nullptr);

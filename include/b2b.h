@@ -612,7 +612,8 @@ b2b_status_t b2b_ffn_units(int problems, const int64_t* sizes, int gate, int64_t
  * 128: the smallest power of two that leaves no magnitude above 448 (at least
  * 2^-126), so that scaling itself rounds nothing; values are rounded to nearest
  * even.  A block that holds an infinity or a NaN gets NaN as its scale and in
- * each value.  q's rows lie on 8-byte boundaries.  Works on the current device;
+ * each value.  q's rows lie on 8-byte boundaries; one of the scales' strides steps
+ * over all of the other's, so that no two share a place.  Works on the current device;
  * asynchronous on `stream`, without waits.
  */
 b2b_status_t b2b_quantize_blocks(b2b_dtype_t dtype, int64_t rows, int64_t cols, int block_rows, const b2b_matrix_t* x,

@@ -100,6 +100,10 @@ def test_quantize_refusals():
     assert quantize(x=(0x10000, 248)) == INVALID and quantize(q=(0x20000, 0)) == INVALID  # rows that overlap
     assert quantize(scale=(0x30000, 0, 10)) == INVALID and quantize(scale=(0x30000, 1, 0)) == INVALID
     assert quantize(scale=(0x30000, -1, 10)) == INVALID
+    # scales of two blocks in one place: rows 0, 1 and blocks 1, 0; every stride that keeps them apart will do
+    assert quantize(scale=(0x30000, 1, 1)) == INVALID and quantize(scale=(0x30000, 1, 9)) == INVALID
+    assert quantize(scale=(0x30000, 2, 1)) in NO_DEVICE and quantize(scale=(0x30000, 7, 5)) in NO_DEVICE
+    assert quantize(rows=1, scale=(0x30000, 0, 1)) in NO_DEVICE and quantize(cols=128, scale=(0x30000, 1, 0)) in NO_DEVICE
     assert quantize(q=(0x10100, 512)) == ALIAS and quantize(scale=(0x10000, 1, 10)) == ALIAS
     # rows of q between those of x, in one buffer
     assert quantize(x=(0x10000, 512), q=(0x10000 + 512, 1024)) in NO_DEVICE

@@ -275,6 +275,8 @@ def few_rows_kernel(seed, slots_of_k, ring, e4m3, warps=4, plant=None):
 def test_few_rows_kernel(e4m3, n):
     for seed in range(40):
         few_rows_kernel(seed, n, 3 if e4m3 else 5, e4m3)
+        if e4m3:
+            few_rows_kernel(seed, n, 4, True, warps=8)
 
 
 def test_few_rows_kernel_planted_error():
