@@ -301,7 +301,8 @@ class GatedFeedForwardPlan(_Plan):
         if stream is not None:
             with torch.cuda.stream(stream):
                 done = self.backward(dy, x, w_gate, w_up, w_down, kept, input_grad, weight_grads)
-            _kept(stream, self.device_index, done, (dy, x, w_gate, w_up, w_down, kept))
+            _kept(stream, self.device_index, done,
+                  (dy, x, w_gate, w_up, w_down, kept, *(() if isinstance(weight_grads, bool) else done[1:])))
             return done
         if weight_grads is True:
             done = _binding.backward(self._bound, _raw_stream(self.device_index), dy, x, w_gate, w_up, w_down, kept, input_grad)

@@ -291,6 +291,23 @@ def test_memory_of_a_run_on_another_stream_is_kept():
         del junk
 
 
+def test_memory_of_gradients_added_on_another_stream_is_kept():
+    plan, x, w, dy = setup(t=600, d=1024, f=2048, o=512)
+    kept = plan.forward(x, *w)[1]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(10):
+        grads = [torch.zeros_like(z, dtype=torch.float32) for z in w]
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(2_000_000)
+        plan.backward(dy, x, *w, kept, weight_grads=grads, stream=s)
+        del grads
+        others = [torch.full_like(z, 9.0, dtype=torch.float32) for z in w]
+        torch.cuda.synchronize()
+        assert all((z == 9).all() for z in others)
+
+
 @pytest.mark.parametrize("t", [4, 200])
 def test_captured_calls_follow_their_inputs(t):
     calls, inputs = all_calls(t)
