@@ -235,11 +235,17 @@ struct Launch {
 };
 
 // How the kernel for few rows takes a product: tiles of 16 << size rows, a slice's
-// k cut in 1 << split_bits; size -1: the pair kernel is quicker.
+// k cut in 1 << split_bits; size -1: the pair kernel is quicker.  Of `products`
+// over k each.  Rows of 16-bit operands that do not lie on 128 bytes cost a box two
+// lines for each of its rows (309 tokens on 1408/5376/2304 28 us, on 1400/5416/2280
+// 44 us here, 36 and 41 us by the pair kernel).
 struct FewShape {
   int size, row_tiles, split_bits;
 };
-FewShape few_shape(const b2b_ffn_plan_s* p, const SkinnyKernels& k, int64_t rows, int64_t n, int kpan) {
+FewShape few_shape(const b2b_ffn_plan_s* p, const SkinnyKernels& k, int64_t rows, int64_t n, int64_t depth, int products = 1) {
+  const bool e4m3 = k.depth == 128;
+  const int kpan = products * panels(depth, e4m3);
+  const double lines = e4m3 ? 1.0 : 1.0 + 0.25 * (depth % 64 != 0) + 0.25 * ((k.k_major ? depth : n) % 64 != 0);
   const int64_t room = 2 * p->sms;  // CTAs resident at once
   double best = k.cost.pair + k.cost.pair_panel * cut(tile_count(rows, n, k.gate), kpan, p->sms / 2).time;
   FewShape shape = {-1, 0, 0};
@@ -251,7 +257,7 @@ FewShape few_shape(const b2b_ffn_plan_s* p, const SkinnyKernels& k, int64_t rows
     while ((1 << bits) < kSkinnyMaxSplits && (tiles << (bits + 1)) <= room && kpan >= (4 << bits)) ++bits;
     const double second = (tiles << bits) > p->sms ? 1.0 + k.cost.second : 1.0;
     const double t = static_cast<double>(ceil_div(tiles << bits, room)) * second *
-                         (1.5 + static_cast<double>(ceil_div(kpan, 1 << bits)) * (k.cost.slot + k.cost.slot_row * (16 << size))) +
+                         (1.5 + static_cast<double>(ceil_div(kpan, 1 << bits)) * lines * (k.cost.slot + k.cost.slot_row * (16 << size))) +
                      0.14 * (1 << bits);
     if (t < best) {
       best = t;
@@ -353,30 +359,30 @@ Pieces pieces(const b2b_ffn_plan_s* p, int64_t rows, int pass) {
   const int64_t d = p->width, f = p->hidden, o = p->out_width;
   const size_t t = static_cast<size_t>(rows);
   auto part = [&](int64_t tiles, int kpan) { w.parts = std::max(w.parts, part_bytes(p, tiles, kpan)); };
-  auto product = [&](const SkinnyKernels& k, int64_t n, int kpan) {
-    if (few_shape(p, k, rows, n, kpan).size < 0) part(tile_count(rows, n, k.gate), kpan);
+  auto product = [&](const SkinnyKernels& k, int64_t n, int64_t depth, int products = 1) {
+    if (few_shape(p, k, rows, n, depth, products).size < 0) part(tile_count(rows, n, k.gate), products * panels(depth, k.depth == 128));
   };
   if (p->kind == kScaledGemm) {
-    product(product_few(p), o, panels(d, true));
+    product(product_few(p), o, d);
   } else if (p->kind == kScaledFfn) {
     w.hidden = t * f;
     w.second = t * d;
     w.x_scale = 4 * t * ceil_div(d, 128);
     w.h_scale = 4 * t * ceil_div(f, 128);
-    product(p->s.gate_few, f, panels(d, true));
-    product(product_few(p), o, panels(f, true));
+    product(p->s.gate_few, f, d);
+    product(product_few(p), o, f);
   } else if (pass == B2B_FFN_BACKWARD) {
     w.hidden = w.second = 2 * t * f;
-    product(p->k.gate_grad_few, f, panels(o));
-    product(p->k.dx_few, d, 2 * panels(f));
+    product(p->k.gate_grad_few, f, o);
+    product(p->k.dx_few, d, f, 2);
     // (any of the weights' gradients may be left out)
     for (int g = 0; g <= 2; ++g)
       for (int e = 0; e <= 1; ++e)
         if (g + e) part(g * tile_count(d, f, false) + e * tile_count(f, o, false), panels(rows));
   } else {
     w.hidden = pass == B2B_FFN_TRAINING ? 0 : 2 * t * f;
-    product(p->k.gate_few, f, panels(d));
-    product(p->k.down_few, o, panels(f));
+    product(p->k.gate_few, f, d);
+    product(p->k.down_few, o, f);
   }
   return w;
 }
@@ -586,7 +592,7 @@ b2b_status_t b2b_ffn_forward(b2b_ffn_plan_t p, const b2b_ffn_forward_t* r, b2b_s
   const b2b_matrix_t h_rows = {keep ? kept.hidden(r->kept) : ws, f};
   void* parts = ws + rounded(w.hidden);
   const Matrix h = {&h_rows, t, f, 2};
-  const FewShape up_few = few_shape(p, p->k.gate_few, t, f, panels(d)), down_few = few_shape(p, p->k.down_few, t, o, panels(f));
+  const FewShape up_few = few_shape(p, p->k.gate_few, t, f, d), down_few = few_shape(p, p->k.down_few, t, o, f);
   if (up_few.size >= 0) {
     FewRows l(p, p->k.gate_few, up_few, false, in[0]);
     l.weight(0, in[1]);
@@ -655,7 +661,7 @@ b2b_status_t b2b_ffn_backward(b2b_ffn_plan_t p, const b2b_ffn_backward_t* r, b2b
   const b2b_matrix_t dg_rows = {ws, f}, du_rows = {ws + rounded(w.hidden), f};
   void* parts = ws + rounded(w.hidden) + rounded(w.second);
   const Matrix dg = {&dg_rows, t, f, 2}, du = {&du_rows, t, f, 2};
-  const FewShape grad_few = few_shape(p, p->k.gate_grad_few, t, f, panels(o)), dx_few = few_shape(p, p->k.dx_few, t, d, 2 * panels(f));
+  const FewShape grad_few = few_shape(p, p->k.gate_grad_few, t, f, o), dx_few = few_shape(p, p->k.dx_few, t, d, f, 2);
   if (r->dx.data || r->dw_gate.data || r->dw_up.data) {
     if (grad_few.size >= 0) {
       FewRows l(p, p->k.gate_grad_few, grad_few, false, in[0]);
@@ -743,7 +749,7 @@ b2b_status_t b2b_scaled_ffn_run(b2b_ffn_plan_t p, const b2b_scaled_ffn_t* r, b2b
   void* parts = hs + rounded(w.h_scale) / 4;
   st = quantize(p->k, t, d, 1, r->x, xq, {xs, 1, t}, stream);
   if (st != B2B_OK) return st;
-  const FewShape up_few = few_shape(p, p->s.gate_few, t, f, panels(d, true)), down_few = few_shape(p, product_few(p), t, o, panels(f, true));
+  const FewShape up_few = few_shape(p, p->s.gate_few, t, f, d), down_few = few_shape(p, product_few(p), t, o, f);
   if (up_few.size >= 0) {
     FewRows l(p, p->s.gate_few, up_few, true, {&xq, t, d, 1});
     l.weight(0, in[1]);
@@ -814,7 +820,7 @@ b2b_status_t b2b_scaled_gemm_run(b2b_ffn_plan_t p, const b2b_scaled_gemm_t* r, b
   if (st == B2B_OK) st = check_workspace(r->workspace, r->workspace_bytes, w.total());
   if (st == B2B_OK) st = check_current_device(p);
   if (st != B2B_OK) return st;
-  const FewShape few = few_shape(p, product_few(p), m, n, panels(k, true));
+  const FewShape few = few_shape(p, product_few(p), m, n, k);
   if (few.size >= 0)
     return scaled_few(p, few, in[0], r->a_scale, in[1], r->b_scale, out[0], reinterpret_cast<cudaStream_t>(stream_));
   Launch l(p, false, true);

@@ -39,7 +39,7 @@ SkinnyKernels skinny_kernels() {
                      SkinnyShape<F8, GATE, 16>::kDepth,
                      KM,
                      GATE,
-                     SkinnyShape<F8, GATE, 16>::kCost};
+                     SkinnyShape<F8, GATE, 16>::cost(KM)};
   if constexpr (!F8) {
     k.main[3] = reinterpret_cast<const void*>(&skinny_kernel<IN, OUT, EPI, KM, 128>);
     k.smem[3] = SkinnyShape<F8, GATE, 128>::kBytes;

@@ -87,18 +87,21 @@ enum : int {  // barrier slots (8 bytes each)
   kSSlotTmem = 21,   // uint32 tensor-memory base, then the int abort flag
 };
 
-// Times in us, for the choice between this kernel and the pair kernel (fitted to
-// 16..1024 rows by 1024..14336 columns by 1024..14336 k, to 9-14 %): a slot of this
-// one, the same for each of its rows, what a second CTA on the SM adds, relatively,
-// and the pair kernel's start beyond this one's and its K panel.
+// Times in us, for the choice between this kernel and the pair kernel, and of its tile
+// (fitted to 1..1024 rows on widths of 512 to 14336, aligned and not: what they choose
+// is on average 2-4 % slower than the quickest choice): a slot of this one, the same
+// for each of its rows, what a second CTA on the SM adds, relatively, and the pair
+// kernel's start beyond this one's and its K panel.
 struct SkinnyCost {
   float slot, slot_row, second, pair, pair_panel;
 };
 
 template <bool F8, bool GATE, int NT>
 struct SkinnyShape {
-  static constexpr SkinnyCost kCost = !F8 ? SkinnyCost{0.17f, 0.0024f, 0.14f, 2.0f, 0.31f}
-                                      : GATE ? SkinnyCost{0.08f, 0.008f, 0.4f, 1.0f, 0.5f} : SkinnyCost{0.11f, 0.0047f, 0.53f, 4.2f, 0.35f};
+  static constexpr SkinnyCost cost(bool km) {
+    return !F8 ? km ? SkinnyCost{0.17f, 0.0024f, 0.14f, 2.0f, 0.31f} : SkinnyCost{0.12f, 0.003f, 0.15f, 2.0f, 0.31f}
+           : GATE ? SkinnyCost{0.08f, 0.008f, 0.4f, 1.0f, 0.5f} : SkinnyCost{0.11f, 0.0047f, 0.53f, 4.2f, 0.35f};
+  }
   static constexpr int kColumns = F8 || !GATE ? 128 : 64;  // of a slice
   static constexpr int kDepth = F8 ? 128 : 64;             // k of a slot
   static constexpr int kWeight = F8 && GATE ? 32768 : 16384;
