@@ -252,16 +252,21 @@ FewShape few_shape(const b2b_ffn_plan_s* p, const SkinnyKernels& k, int64_t rows
   if (p->debug & B2B_DEBUG_PAIR_KERNEL) return shape;
   for (int size = 0; size < k.sizes; ++size) {
     const int64_t row_tiles = ceil_div(rows, 16 << size), tiles = row_tiles * ceil_div(n, k.columns);
-    // As many CTAs as are resident at once, two slots each at least.
-    int bits = 0;
-    while ((1 << bits) < kSkinnyMaxSplits && (tiles << (bits + 1)) <= room && kpan >= (4 << bits)) ++bits;
-    const double second = (tiles << bits) > p->sms ? 1.0 + k.cost.second : 1.0;
-    const double t = static_cast<double>(ceil_div(tiles << bits, room)) * second *
-                         (1.5 + static_cast<double>(ceil_div(kpan, 1 << bits)) * lines * (k.cost.slot + k.cost.slot_row * (16 << size))) +
-                     0.14 * (1 << bits);
-    if (t < best) {
-      best = t;
-      shape = {size, static_cast<int>(row_tiles), bits};
+    // k cut while all CTAs are resident at once, with two slots each at least: 16 bits as
+    // often as that goes (fewer cuts where this model prefers them were no quicker on
+    // average), e4m3, whose slots' sums take more of an SM, where the model says so (33 x
+    // 2048 x 1368 5.7 -> 4.9 us, the block of 33 tokens on 4096/2816/4096 20.4 -> 18.0).
+    int most = 0;
+    while ((2 << most) <= kSkinnyMaxSplits && (tiles << (most + 1)) <= room && kpan >= (4 << most)) ++most;
+    for (int bits = e4m3 ? 0 : most; bits <= most; ++bits) {
+      const double second = (tiles << bits) > p->sms ? 1.0 + k.cost.second : 1.0;
+      const double t = static_cast<double>(ceil_div(tiles << bits, room)) * second *
+                           (1.2 + static_cast<double>(ceil_div(kpan, 1 << bits)) * lines * (k.cost.slot + k.cost.slot_row * (16 << size))) +
+                       0.14 * ((1 << bits) - 1);
+      if (t < best) {
+        best = t;
+        shape = {size, static_cast<int>(row_tiles), bits};
+      }
     }
     if (row_tiles == 1) break;  // (a larger tile would be emptier)
   }

@@ -98,9 +98,10 @@ struct SkinnyCost {
 
 template <bool F8, bool GATE, int NT>
 struct SkinnyShape {
+  // km: K-major weights
   static constexpr SkinnyCost cost(bool km) {
-    return !F8 ? km ? SkinnyCost{0.17f, 0.0024f, 0.14f, 2.0f, 0.31f} : SkinnyCost{0.12f, 0.003f, 0.15f, 2.0f, 0.31f}
-           : GATE ? SkinnyCost{0.08f, 0.008f, 0.4f, 1.0f, 0.5f} : SkinnyCost{0.11f, 0.0047f, 0.53f, 4.2f, 0.35f};
+    return F8 ? GATE ? SkinnyCost{0.04f, 0.016f, 0.16f, 0.9f, 0.64f} : SkinnyCost{0.25f, 0.0044f, 0.6f, 10.0f, 0.29f}
+              : km ? SkinnyCost{0.17f, 0.0024f, 0.14f, 1.6f, 0.31f} : SkinnyCost{0.12f, 0.003f, 0.15f, 1.6f, 0.31f};
   }
   static constexpr int kColumns = F8 || !GATE ? 128 : 64;  // of a slice
   static constexpr int kDepth = F8 ? 128 : 64;             // k of a slot
