@@ -1,7 +1,7 @@
 // The common calls of the feed-forward plans, from torch's tensors to the C ABI
 // (include/b2b.h): checks, outputs and workspace, launch.  In Python these take
 // longer than the kernels of a small call (one token on 1024/2816/1024: 20 us a
-// call in Python, 10 here; the kernels take 8.4).  Whatever is not as the call
+// call in Python, 9 here; the kernels take 8).  Whatever is not as the call
 // wants it makes a function here return None, and feedforward.py, which does the
 // same in Python, finds out what and says it.
 #include <Python.h>
