@@ -88,8 +88,8 @@ enum : int {  // barrier slots (8 bytes each)
 };
 
 // Times in us, for the choice between this kernel and the pair kernel, and of its tile
-// (fitted to 1..1024 rows on widths of 512 to 14336, aligned and not: what they choose
-// is on average 2-4 % slower than the quickest choice): a slot of this one, the same
+// (fitted to 1..1024 rows on widths of 512 to 65536, aligned and not: what they choose
+// is on average 1-2 % slower than the quickest choice): a slot of this one, the same
 // for each of its rows, what a second CTA on the SM adds, relatively, and the pair
 // kernel's start beyond this one's and its K panel.
 struct SkinnyCost {
@@ -100,8 +100,9 @@ template <bool F8, bool GATE, int NT>
 struct SkinnyShape {
   // km: K-major weights
   static constexpr SkinnyCost cost(bool km) {
-    return F8 ? GATE ? SkinnyCost{0.04f, 0.016f, 0.16f, 0.9f, 0.64f} : SkinnyCost{0.25f, 0.0044f, 0.6f, 10.0f, 0.29f}
-              : km ? SkinnyCost{0.17f, 0.0024f, 0.14f, 1.6f, 0.31f} : SkinnyCost{0.12f, 0.003f, 0.15f, 1.6f, 0.31f};
+    return F8   ? GATE ? SkinnyCost{0.055f, 0.009f, 0.065f, 1.6f, 0.28f} : SkinnyCost{0.23f, 0.0033f, 0.55f, 5.7f, 0.37f}
+           : km ? SkinnyCost{0.17f, 0.0024f, 0.14f, 1.6f, 0.31f}
+                : SkinnyCost{0.12f, 0.003f, 0.15f, 1.6f, 0.31f};
   }
   static constexpr int kColumns = F8 || !GATE ? 128 : 64;  // of a slice
   static constexpr int kDepth = F8 ? 128 : 64;             // k of a slot
