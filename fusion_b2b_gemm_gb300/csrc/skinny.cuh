@@ -17,7 +17,7 @@
 // 128 rows by 14336 by 4096 23 and 25 us; a training step of 192 tokens on
 // 1024/2816/1024 41 and 55 us.  It reads an operand's panel for 1/4 to 1/16 of the
 // work, and loses where many tiles run one after the other: 500 tokens on
-// 4096/14336/4096 160 us, 110 there.  few_shape() weighs them.
+// 4096/14336/4096 149 us, 110 there.  few_shape() weighs them.
 //
 // A CTA takes a slice of the columns and, where slices alone are too few to keep
 // the memory busy, a range of k; the CTAs of a slice are a cluster and add their
