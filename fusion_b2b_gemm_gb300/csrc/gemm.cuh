@@ -466,6 +466,15 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
           }
         }
       }
+      // The releases of the last round's slots arrive in both CTAs, and before exit.  (A
+      // slot that was never filled passes at once.)
+      for (int j = 0; j < kRing && ok; ++j) {
+        ok = bw.wait1(bar(kGBEmpty + slot), phase ^ 1u);
+        if (++slot == kRing) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
       // Copies in flight land before exit (the even CTA's barriers count both CTAs').
       const unsigned long long tail = !leader ? 0 : (issued < kRing ? issued : kRing);
       for (unsigned long long j = 0; j < tail; ++j) {
@@ -847,11 +856,14 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
       }
     }
     if (lane == 0) bulk_wait_all();
+    // The even CTA's MMA thread commits to the odd CTA's barriers too, this one last.
+    if (!leader && warp == 4 && lane == 0) drain_wait(bar(kGBDrain), 0, p.budget_ns);
   }
 
   __syncthreads();
   // Neither CTA leaves, or frees tensor memory, while the other may still
-  // arrive on its barriers or the even CTA's MMAs may still write it.
+  // arrive on its barriers or the even CTA's MMAs may still write it: what the
+  // MMAs' commits have to deliver has arrived in either, by the waits above.
   cluster_sync();
   if (warp == 2) {
     tc_fence_after();

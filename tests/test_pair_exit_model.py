@@ -1,0 +1,118 @@
+"""How the kernels on CTA pairs end, replayed on the CPU in random interleavings (no GPU needed).
+
+gemm_kernel (gemm.cuh) and chainn_kernel (chainn.cuh) commit their MMAs to
+barriers of both CTAs: each commit of the even CTA's MMA thread becomes an
+arrival in either CTA, delivered some time after the MMAs are done, and not in
+step with the other CTA's.  Shared memory that an arrival is still on its way to
+must not be given up: an arrival at a CTA that has left is an error here.  What
+each CTA waits for before the closing cluster barrier has to rule it out: its
+loader for the release of the last ring round's slots, its epilogue for the last
+accumulator, and one thread (the even CTA's MMA thread, the odd CTA's epilogue)
+for the last commit of all.  The waits that the kernels had before, and each of
+these left out, are caught.
+"""
+import pytest
+
+from test_feedforward_protocol_model import Barrier, Broken, World
+
+
+class Inbox(Barrier):
+    """A barrier of a CTA that may have left."""
+
+    def __init__(self, count, cta):
+        super().__init__(count)
+        self.cta = cta
+
+    def arrive(self):
+        if self.cta["left"]:
+            raise Broken("an arrival at a CTA that has left")
+        super().arrive()
+
+
+def pair_exit(seed, units, ring, missing=()):
+    """units: slots of each unit in turn.  An accumulator a unit, two in turn."""
+    w = World(seed)
+    ctas = [{"left": False}, {"left": False}]
+    full = [Inbox(2, ctas[0]) for _ in range(ring)]
+    empty = [[Inbox(1, c) for _ in range(ring)] for c in ctas]
+    acc_full = [[Inbox(1, c) for _ in range(2)] for c in ctas]
+    acc_empty = [Inbox(2, ctas[0]) for _ in range(2)]
+    drain = [Inbox(1, c) for c in ctas]
+    copies, tensor = [w.engine(), w.engine()], w.engine()
+    panels = [(u, k) for u, n in enumerate(units) for k in range(n)]
+    running = [0]
+
+    def commit(*bars):
+        """An arrival at each barrier once the MMAs issued so far are done: on its own from then on."""
+        def done():
+            for b in bars:
+                w.engine().append(b.arrive)
+        tensor.append(done)
+
+    def loader(cta):
+        slot = phase = uses = 0
+        for _ in panels:
+            yield (empty[cta][slot], phase ^ 1, uses - 1)
+            copies[cta].append(full[slot].arrive)
+            slot += 1
+            if slot == ring:
+                slot, phase, uses = 0, phase ^ 1, uses + 1
+        if "releases" not in missing:
+            for _ in range(ring):  # (a slot without a use passes at once)
+                yield (empty[cta][slot], phase ^ 1, uses - 1)
+                slot += 1
+                if slot == ring:
+                    slot, phase, uses = 0, phase ^ 1, uses + 1
+
+    def mma():
+        for i, (u, k) in enumerate(panels):
+            a, slot = u & 1, i % ring
+            if k == 0:
+                yield (acc_empty[a], (u >> 1 & 1) ^ 1, (u >> 1) - 1)
+            yield (full[slot], i // ring & 1, i // ring)
+            commit(*(empty[c][slot] for c in range(2)))
+            if k + 1 == units[u]:
+                commit(*(acc_full[c][a] for c in range(2)))
+        commit(*drain)
+        yield (drain[0], 0, 0)
+
+    def epilogue(cta):
+        for u in range(len(units)):
+            yield (acc_full[cta][u & 1], u >> 1 & 1, u >> 1)
+            yield True  # (the loads)
+            acc_empty[u & 1].arrive()
+        if cta == 1 and "last commit" not in missing:
+            yield (drain[1], 0, 0)
+
+    def role(r):
+        running[0] += 1
+        yield from r
+        running[0] -= 1
+        if not running[0]:  # (the cluster barrier: both CTAs leave)
+            for c in ctas:
+                c["left"] = True
+
+    w.run([role(r) for r in (loader(0), loader(1), mma(), epilogue(0), epilogue(1))])
+    assert all(c["left"] for c in ctas)
+
+
+UNITS = [[1], [1, 1, 1, 1], [7, 2, 5], [16], [3, 1, 1, 9, 4, 4]]
+
+
+@pytest.mark.parametrize("units", UNITS, ids=str)
+@pytest.mark.parametrize("ring", [2, 5, 6])
+def test_no_arrival_finds_its_cta_gone(units, ring):
+    for seed in range(60):
+        pair_exit(seed, units, ring)
+
+
+@pytest.mark.parametrize("missing", [("releases", "last commit"), ("releases",), ("last commit",)], ids="-".join)
+def test_waits_left_out_are_caught(missing):
+    caught = 0
+    for seed in range(200):
+        try:
+            pair_exit(seed, [3, 1, 1, 9], 5, missing)
+        except Broken as e:
+            assert "left" in str(e)
+            caught += 1
+    assert caught
