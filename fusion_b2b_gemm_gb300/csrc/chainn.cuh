@@ -421,6 +421,15 @@ __global__ void __launch_bounds__(kChainNThreads, 1)
           for (int kb = 0; kb < kpan_last && ok; kb += kps_last)
             ok = load(S - 1, c.b, m0, kb, j * NF, NF, kps_last);
       }
+      // the releases of the last round's slots arrive in both CTAs, and
+      // before exit (a slot that was never filled passes at once)
+      for (int j = 0; j < p.nslot && ok; ++j) {
+        ok = bw.wait(bar(knEmpty + slot), phase ^ 1u);
+        if (++slot == static_cast<uint32_t>(p.nslot)) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
       // copies in flight land before exit (the even CTA's barriers count both
       // CTAs' copies; the odd CTA waits at the cluster barrier before exit)
       const uint64_t n = static_cast<uint64_t>(p.nslot);
@@ -811,11 +820,15 @@ __global__ void __launch_bounds__(kChainNThreads, 1)
       }
     }
     if (epi && lane == 0) bulk_wait_all();
+    // the even CTA's MMA thread commits to the odd CTA's barriers too, this
+    // one last
+    if (!leader && elected) drain_wait(bar(knDrain), 0, p.budget_ns);
   }
 
   __syncthreads();
   // neither CTA leaves (or frees tensor memory) while the other may still
-  // arrive on its barriers or the even CTA's MMAs may still write it
+  // arrive on its barriers or the even CTA's MMAs may still write it: what the
+  // MMAs' commits have to deliver has arrived in either, by the waits above
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
