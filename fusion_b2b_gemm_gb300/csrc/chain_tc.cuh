@@ -286,6 +286,15 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
   }
 }
 
+// The odd CTA of a pair after a wait that ran out: its last copies are counted
+// by the even CTA, which may have given up without arming its barrier for them.
+// They get 0.1 ms to land, some hundred times what a copy takes.
+__device__ __forceinline__ void settle() {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (ptx::globaltimer_ns() - t0 < 100000) {
+  }
+}
+
 // Tiles of one CTA, walked without divisions: batch b and 128-row tile mt.
 // A scheduled CTA walks a list of contiguous segments instead (`segs`: tile
 // count of the current one in `left`, then (first, count) pairs).

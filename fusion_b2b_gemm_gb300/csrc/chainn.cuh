@@ -430,6 +430,7 @@ __global__ void __launch_bounds__(kChainNThreads, 1)
           phase ^= 1u;
         }
       }
+      if (!leader && !ok) settle();
       // copies in flight land before exit (the even CTA's barriers count both
       // CTAs' copies; the odd CTA waits at the cluster barrier before exit)
       const uint64_t n = static_cast<uint64_t>(p.nslot);

@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
           phase ^= 1u;
         }
       }
+      if (!leader && !ok) settle();
       // Copies in flight land before exit (the even CTA's barriers count both CTAs').
       const unsigned long long tail = !leader ? 0 : (issued < kRing ? issued : kRing);
       for (unsigned long long j = 0; j < tail; ++j) {

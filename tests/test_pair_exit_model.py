@@ -116,3 +116,53 @@ def test_waits_left_out_are_caught(missing):
             assert "left" in str(e)
             caught += 1
     assert caught
+
+
+def gives_up(seed, ring, settle):
+    """A wait runs out: the even CTA's loader stops before the odd one's, whose last copies it has not armed its barrier for
+    and does not wait for."""
+    w = World(seed)
+    ctas = [{"left": False}, {"left": False}]
+    full = [Inbox(2, ctas[0]) for _ in range(ring)]
+    copies = [w.engine(), w.engine()]
+    even = w.rng.randint(0, ring - 1)
+    running = [0]
+
+    class Landed:
+        """The time that settle() waits is more than a copy takes."""
+
+        def ready(self, *_):
+            return not copies[1]
+
+    def loader(cta, n):
+        yield True
+        for i in range(n):
+            copies[cta].append(full[i].arrive)
+            yield True
+        if cta == 0:
+            for i in range(n):
+                yield (full[i], 0, 0)
+        elif settle:
+            yield (Landed(), 0, 0)
+
+    def role(r):
+        running[0] += 1
+        yield from r
+        running[0] -= 1
+        if not running[0]:
+            for c in ctas:
+                c["left"] = True
+
+    w.run([role(loader(0, even)), role(loader(1, w.rng.randint(even, ring)))])
+
+
+def test_copies_of_a_run_that_gave_up_land_before_exit():
+    for seed in range(300):
+        gives_up(seed, 6, True)
+    caught = 0
+    for seed in range(300):
+        try:
+            gives_up(seed, 6, False)
+        except Broken:
+            caught += 1
+    assert caught
