@@ -147,12 +147,17 @@ class _Plan:
         self._h = h
         self._torch_dtype = getattr(torch, _TYPES[dtype])
         self.device_index = _current_device()
+        self._bind_args = h.value, dtype == "bf16", *(n or 0 for n in sizes), self.device_index
+        self._bind()
+
+    def _bind(self):
+        """Without the sizes of workspaces that are known so far, which depend on the plan's flags."""
         self._workspace_sizes = {}
         # What the binding's calls need to know of the plan.  They take the
         # common call, with no tensors for the results and no stream, and return
         # None where anything is not as they want it: the same in Python below
         # finds out what.
-        self._bound = _binding.bind(h.value, dtype == "bf16", *(n or 0 for n in sizes), self.device_index)
+        self._bound = _binding.bind(*self._bind_args)
 
     def _no_gradient(self, *inputs):
         if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
@@ -189,6 +194,7 @@ class _Plan:
     def set_debug(self, flags: int) -> None:
         """Test support (see b2b_plan_set_debug and B2B_DEBUG_PAIR_KERNEL in include/b2b.h)."""
         _check(_lib.b2b_ffn_plan_set_debug(self._h, int(flags)), "b2b_ffn_plan_set_debug")
+        self._bind()
 
     def close(self) -> None:
         self._bound = None

@@ -512,9 +512,9 @@ b2b_status_t b2b_scaled_gemm_plan_create(b2b_ffn_plan_t* out, b2b_dtype_t dtype,
 b2b_status_t b2b_ffn_plan_destroy(b2b_ffn_plan_t plan);
 /* As b2b_plan_device_status, b2b_plan_set_wait_budget (budgets above 4 s count
  * as 4 s, and one shorter than 5 us for each 64 of a product's k (128 for
- * e4m3) as that), b2b_plan_set_debug.  Feed-forward plans know another flag,
- * to be set before a plan's first run: B2B_DEBUG_PAIR_KERNEL keeps to the
- * kernel for large products where another would be quicker. */
+ * e4m3) as that), b2b_plan_set_debug.  Feed-forward plans know another flag:
+ * B2B_DEBUG_PAIR_KERNEL keeps to the kernel for large products where another would
+ * be quicker.  It changes what b2b_ffn_workspace answers. */
 #define B2B_DEBUG_PAIR_KERNEL 2u
 b2b_status_t b2b_ffn_plan_device_status(b2b_ffn_plan_t plan, b2b_stream_t stream);
 b2b_status_t b2b_ffn_plan_set_wait_budget(b2b_ffn_plan_t plan, uint64_t budget_ns);
