@@ -47,7 +47,7 @@ const at::Tensor* tensor(const Bound& p, PyObject* o, c10::ScalarType type) {
   if (!THPVariable_Check(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
   return t.layout() == c10::kStrided && t.scalar_type() == type && t.is_cuda() && t.get_device() == p.device && t.dim() == 2 &&
-                 !(t.requires_grad() && at::GradMode::is_enabled())
+                 !(t.requires_grad() && at::GradMode::is_enabled()) && !t._fw_grad(0).defined()  // (no gradient is recorded)
              ? &t
              : nullptr;
 }

@@ -10,7 +10,8 @@ plan holds the widths; a run takes any number of rows.  Matrices have
 consecutive elements in a row (last stride 1), rows on 16-byte boundaries and any
 row stride that keeps them there, so a column range of a wider buffer will do.
 Gradients are computed by ``backward`` alone: inputs that require a gradient are
-refused where gradients are recorded.  There is no CPU path.
+refused where gradients are recorded, and so are inputs with a forward-mode
+tangent.  There is no CPU path.
 """
 from __future__ import annotations
 
@@ -130,6 +131,17 @@ def _kept(stream, device, done, given):
                 t.record_stream(current)
 
 
+_WITHOUT = "(run it under torch.no_grad(), on the primals of dual tensors)"
+
+
+def _differentiated(*inputs):
+    """Whether autograd would record a gradient for what is computed of these, or carry a tangent on (which no_grad does
+    not keep it from)."""
+    forward_ad = torch.autograd.forward_ad
+    return (torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
+            or not torch.is_inference_mode_enabled() and any(forward_ad.unpack_dual(t).tangent is not None for t in inputs))
+
+
 def _blocks(n):
     return -(-n // BLOCK)
 
@@ -160,8 +172,8 @@ class _Plan:
         self._bound = _binding.bind(*self._bind_args)
 
     def _no_gradient(self, *inputs):
-        if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
-            raise RuntimeError(f"{type(self).__name__} records no gradient for its outputs (run it under torch.no_grad())")
+        if _differentiated(*inputs):
+            raise RuntimeError(f"{type(self).__name__} records no gradient for its outputs {_WITHOUT}")
 
     def _workspace(self, like, rows, which=_INFERENCE):
         """Workspace of one run, from the pool of the current stream, with its address and size."""
@@ -446,8 +458,8 @@ def quantize_blocks(x, block_rows: int = 1, stream=None):
         raise TypeError(f"x: {x.dtype} given, torch.float16 or torch.bfloat16 expected")
     if block_rows not in (1, BLOCK):
         raise ValueError(f"block_rows {block_rows!r}: 1 or {BLOCK} expected")
-    if torch.is_grad_enabled() and x.requires_grad:
-        raise RuntimeError("quantize_blocks records no gradient for its outputs (run it under torch.no_grad())")
+    if _differentiated(x):
+        raise RuntimeError(f"quantize_blocks records no gradient for its outputs {_WITHOUT}")
     rows, cols = x.shape
     device = x.get_device()
     if device < 0:
