@@ -228,6 +228,15 @@ def _current_device() -> int:
     return torch.cuda.current_device()
 
 
+def _differentiated(*inputs) -> bool:
+    """Whether autograd would record a gradient for what is computed of these tensors, or carry a tangent on (which no_grad
+    does not keep it from)."""
+    import torch
+    forward_ad = torch.autograd.forward_ad
+    return (torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
+            or not torch.is_inference_mode_enabled() and any(forward_ad.unpack_dual(t).tangent is not None for t in inputs))
+
+
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None

@@ -7,8 +7,8 @@ new tokens of a batch of requests that share one long prefix.  A plan holds
 the head layout; a run takes tensors of any length on 16-byte boundaries, with
 any positive strides that are multiples of 8 elements, the last one 1 (a stride
 of 0, as of keys expanded over heads, is refused).  Inference only: inputs that
-require a gradient are refused where gradients are recorded.  There is no CPU
-path.
+require a gradient are refused where gradients are recorded, and so are inputs
+with a forward-mode tangent.  There is no CPU path.
 """
 from __future__ import annotations
 
@@ -20,7 +20,7 @@ import os
 import struct
 import warnings
 
-from . import DTYPES, _check, _current_device, _lib, _stream_handle, library_path
+from . import DTYPES, _check, _current_device, _differentiated, _lib, _stream_handle, library_path
 
 __all__ = ["PromptAttentionPlan", "SharedPrefixAttentionPlan"]
 
@@ -137,9 +137,9 @@ class _AttentionPlan:
         return shape[0], shape[1], t.data_ptr(), stride[1], stride[2], stride[0]
 
     def _no_gradient(self, *inputs):
-        if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+        if _differentiated(*inputs):
             raise RuntimeError(f"{type(self).__name__} is inference-only: its output has no gradient "
-                               "(run it under torch.no_grad())")
+                               "(run it under torch.no_grad(), on the primals of dual tensors)")
 
     def _placed(self, name, t):
         if t.get_device() != self.device_index:  # (-1 for a CPU tensor)

@@ -45,8 +45,8 @@ const at::Tensor* tensor(const Bound& p, PyObject* o, c10::ScalarType type, int6
              : nullptr;
 }
 
-// Whether a gradient would have to be recorded, which no run does.
-bool recorded(const at::Tensor& t) { return t.requires_grad() && at::GradMode::is_enabled(); }
+// Whether a gradient would have to be recorded, or a tangent carried on, which no run does.
+bool recorded(const at::Tensor& t) { return (t.requires_grad() && at::GradMode::is_enabled()) || t._fw_grad(0).defined(); }
 
 // [rows][heads][dim], or [blocks][rows][heads][dim]
 const at::Tensor* rows(const Bound& p, PyObject* o, int64_t dims, int64_t heads, b2b_attn_rows_t& r) {

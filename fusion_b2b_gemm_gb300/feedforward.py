@@ -22,7 +22,7 @@ import os
 import struct
 import warnings
 
-from . import DTYPES, _check, _current_device, _lib, _stream_handle, library_path
+from . import DTYPES, _check, _current_device, _differentiated, _lib, _stream_handle, library_path
 
 __all__ = ["GatedFeedForwardPlan", "ScaledFeedForwardPlan", "ScaledGemmPlan", "quantize_blocks", "ACTIVATIONS"]
 
@@ -132,14 +132,6 @@ def _kept(stream, device, done, given):
 
 
 _WITHOUT = "(run it under torch.no_grad(), on the primals of dual tensors)"
-
-
-def _differentiated(*inputs):
-    """Whether autograd would record a gradient for what is computed of these, or carry a tangent on (which no_grad does
-    not keep it from)."""
-    forward_ad = torch.autograd.forward_ad
-    return (torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
-            or not torch.is_inference_mode_enabled() and any(forward_ad.unpack_dual(t).tangent is not None for t in inputs))
 
 
 def _blocks(n):
