@@ -9,9 +9,9 @@ such operands; :func:`quantize_blocks` brings 16-bit matrices to that form.  A
 plan holds the widths; a run takes any number of rows.  Matrices have
 consecutive elements in a row (last stride 1), rows on 16-byte boundaries and any
 row stride that keeps them there, so a column range of a wider buffer will do.
-Gradients are computed by ``backward`` alone: inputs that require a gradient are
-refused where gradients are recorded, and so are inputs with a forward-mode
-tangent.  There is no CPU path.
+Gradients are computed by ``backward`` alone: inputs that require a gradient, and
+tensors to write into that do, are refused where gradients are recorded, and so
+are those with a forward-mode tangent.  There is no CPU path.
 """
 from __future__ import annotations
 
@@ -131,6 +131,13 @@ def _kept(stream, device, done, given):
                 t.record_stream(current)
 
 
+def _written(*given):
+    """Tells autograd that a call has changed tensors it was given, so that none of them passes for what was saved of it."""
+    for t in given:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 _WITHOUT = "(run it under torch.no_grad(), on the primals of dual tensors)"
 
 
@@ -163,8 +170,9 @@ class _Plan:
         # finds out what.
         self._bound = _binding.bind(*self._bind_args)
 
-    def _no_gradient(self, *inputs):
-        if _differentiated(*inputs):
+    def _no_gradient(self, *inputs, into=()):
+        """Of inputs, and of tensors (or None) that results are written into."""
+        if _differentiated(*inputs, *(t for t in into if isinstance(t, torch.Tensor))):
             raise RuntimeError(f"{type(self).__name__} records no gradient for its outputs {_WITHOUT}")
 
     def _workspace(self, like, rows, which=_INFERENCE):
@@ -257,10 +265,12 @@ class GatedFeedForwardPlan(_Plan):
             if done is not None:
                 return done
         tokens, operands = self._operands(x, w_gate, w_up, w_down)
-        self._no_gradient(x, w_gate, w_up, w_down)
+        self._no_gradient(x, w_gate, w_up, w_down, into=(out,))
+        given = out
         out, oa = self._result(x, tokens, out)
         ws, wsp, need = self._workspace(x, tokens)
         self._call(_lib.b2b_ffn_forward, _forward_run(tokens, *operands, *oa, 0, 0, wsp, need))
+        _written(given)
         return out
 
     def forward(self, x, w_gate, w_up, w_down, out=None, kept=None, stream=None):
@@ -277,7 +287,8 @@ class GatedFeedForwardPlan(_Plan):
             if done is not None:
                 return done
         tokens, operands = self._operands(x, w_gate, w_up, w_down)
-        self._no_gradient(x, w_gate, w_up, w_down)
+        self._no_gradient(x, w_gate, w_up, w_down, into=(out,))
+        given = out, kept
         out, oa = self._result(x, tokens, out)
         if kept is None:
             n = ctypes.c_size_t()
@@ -288,6 +299,7 @@ class GatedFeedForwardPlan(_Plan):
             return out, kept
         ws, wsp, need = self._workspace(x, tokens, _TRAINING)
         self._call(_lib.b2b_ffn_forward, _forward_run(tokens, *operands, *oa, *ka, wsp, need))
+        _written(*given)
         return out, kept
 
     def _kept_args(self, kept):
@@ -321,12 +333,12 @@ class GatedFeedForwardPlan(_Plan):
         tokens, (xp, xs, *weights) = self._operands(x, w_gate, w_up, w_down)
         dya = _rows("dy", dy, self._torch_dtype, tokens, self.out_width, self.device_index)[1:]
         ka = self._kept_args(kept)
-        self._no_gradient(dy, x, w_gate, w_up, w_down)
+        accumulate = not isinstance(weight_grads, bool)
+        grads = tuple(weight_grads) if accumulate else ()
+        self._no_gradient(dy, x, w_gate, w_up, w_down, into=grads)
         dx = self._new(x, tokens, self.width) if input_grad else None
         shapes = (self.width, self.hidden), (self.width, self.hidden), (self.hidden, self.out_width)
-        accumulate = not isinstance(weight_grads, bool)
         if accumulate:
-            grads = tuple(weight_grads)
             if len(grads) != 3:
                 raise ValueError(f"weight_grads: {len(grads)} tensors given, three expected")
         elif weight_grads:
@@ -340,6 +352,8 @@ class GatedFeedForwardPlan(_Plan):
                                                  *shape, self.device_index)[1:]
         ws, wsp, need = self._workspace(x, tokens, _BACKWARD)
         self._call(_lib.b2b_ffn_backward, _backward_run(tokens, accumulate, *dya, xp, xs, *weights, *ka, *ga, wsp, need))
+        if accumulate:
+            _written(*grads)
         return (dx, *grads)
 
 
@@ -383,12 +397,14 @@ class ScaledFeedForwardPlan(_Plan):
         scales = (*_scale("gate_scale", gate_scale, _blocks(f), _blocks(d), dev),
                   *_scale("up_scale", up_scale, _blocks(f), _blocks(d), dev),
                   *_scale("down_scale", down_scale, _blocks(o), _blocks(f), dev))
-        self._no_gradient(x, w_gate, w_up, w_down, gate_scale, up_scale, down_scale)
+        self._no_gradient(x, w_gate, w_up, w_down, gate_scale, up_scale, down_scale, into=(out,))
+        given = out
         if out is None:
             out = self._new(x, tokens, o)
         oa = _rows("out", out, self._torch_dtype, tokens, o, dev)[1:]
         ws, wsp, need = self._workspace(x, tokens)
         self._call(_lib.b2b_scaled_ffn_run, _scaled_run(tokens, *xa, *weights, *oa, *scales, wsp, need))
+        _written(given)
         return out
 
 
@@ -418,12 +434,14 @@ class ScaledGemmPlan(_Plan):
         ba = _rows("b", b, f8, self.n, self.k, dev)[1:]
         scales = (*_scale("a_scale", a_scale, rows, _blocks(self.k), dev),
                   *_scale("b_scale", b_scale, _blocks(self.n), _blocks(self.k), dev))
-        self._no_gradient(a, b, a_scale, b_scale)
+        self._no_gradient(a, b, a_scale, b_scale, into=(out,))
+        given = out
         if out is None:
             out = self._new(a, rows, self.n)
         oa = _rows("out", out, self._torch_dtype, rows, self.n, dev)[1:]
         ws, wsp, need = self._workspace(a, rows)
         self._call(_lib.b2b_scaled_gemm_run, _product_run(rows, *aa, *ba, *oa, *scales, wsp, need))
+        _written(given)
         return out
 
 

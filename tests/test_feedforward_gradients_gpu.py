@@ -56,3 +56,56 @@ def test_tangents_are_refused(no_grad):
                     call(*moved)
                 moved[i] = forward_ad.unpack_dual(moved[i]).primal
                 assert all(torch.equal(a.float(), b.float()) for a, b in zip(flat(call(*moved)), want)), name
+
+
+def into(t=6, d=144, f=272, o=80):
+    """Each call that writes into tensors it is given, with these: (call, tensors)."""
+    (block, (x, *w)), (eight, served), (product, operands) = (calls(t, d, f, o)[k] for k in ("run", "scaled", "product"))
+    plan, dy = block.__self__, normal(2, t, o)
+    y, kept = plan.forward(x, *w)
+    grads = [torch.zeros_like(z, dtype=torch.float32) for z in w]
+
+    def new():
+        return torch.zeros(t, o, dtype=torch.bfloat16, device="cuda")
+
+    return {
+        "run": (lambda z: block(x, *w, out=z), [new()]),
+        "forward": (lambda z: plan.forward(x, *w, out=z), [new()]),
+        "kept": (lambda z: plan.forward(x, *w, kept=z), [kept]),
+        "backward": (lambda *z: plan.backward(dy, x, *w, kept, weight_grads=z), grads),
+        "some": (lambda z: plan.backward(dy, x, *w, kept, weight_grads=(None, z, None)), grads[1:2]),
+        "scaled": (lambda z: eight(*served, out=z), [new()]),
+        "product": (lambda z: product(*operands, out=z), [new()]),
+    }
+
+
+def test_tensors_to_write_into_that_require_a_gradient_are_refused():
+    for name, (call, given) in into().items():
+        for i, z in enumerate(given):
+            if not z.is_floating_point():
+                continue
+            leaf = z.clone().requires_grad_()
+            some = given[:i] + [leaf] + given[i + 1:]
+            with pytest.raises(RuntimeError, match="no_grad"):
+                call(*some)
+            assert torch.equal(leaf, z), name
+            with torch.no_grad():
+                call(*some)
+            assert not torch.equal(leaf, z), name
+
+
+def test_tensors_written_into_have_a_new_version():
+    """What autograd saved of a tensor before a call wrote into it is not taken for its contents afterwards."""
+    for name, (call, given) in into().items():
+        before = [z._version for z in given]
+        call(*given)
+        assert all(z._version > v for z, v in zip(given, before)), name
+        if given[0].is_floating_point():
+            p = torch.ones_like(given[0], requires_grad=True)
+            product = (given[0] * p).sum()
+            call(*given)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                product.backward()
+    with torch.inference_mode():
+        for call, given in into().values():
+            call(*given)
