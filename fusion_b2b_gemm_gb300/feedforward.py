@@ -133,9 +133,7 @@ def _kept(stream, device, done, given):
 
 def _written(*given):
     """Tells autograd that a call has changed tensors it was given, so that none of them passes for what was saved of it."""
-    for t in given:
-        if t is not None and not t.is_inference():
-            torch.autograd.graph.increment_version(t)
+    torch.autograd.graph.increment_version([t for t in given if t is not None and not t.is_inference()])
 
 
 _WITHOUT = "(run it under torch.no_grad(), on the primals of dual tensors)"
