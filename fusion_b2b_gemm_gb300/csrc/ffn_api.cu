@@ -127,8 +127,10 @@ struct Shape {
 
 // How many units the tiles that do not fill the SMs a whole number of times are
 // cut into.  Times in K panels of a unit (about 0.35 us, bound by the MMAs or by
-// the weights' bytes alike): 8 for a unit's beginning and end, 9 more for the
-// second launch, and the parts' traffic at some 4 TB/s.
+// the weights' bytes alike): those of the SMs with most of them, where tiles are cut
+// 9 more for the second launch, and the parts' traffic at some 4 TB/s.  A unit's own
+// beginning and end count nothing; the constants that few_shape() sets this time
+// against (SkinnyCost) were fitted to it as it is.
 Shape cut(int64_t tiles, int64_t kpan, int clusters) {
   const int64_t rounds = tiles / clusters, rest = tiles - rounds * clusters;
   Shape best = {tiles, tiles, 1, static_cast<double>((rounds + (rest > 0)) * kpan)};
@@ -236,7 +238,9 @@ struct Launch {
 
 // How the kernel for few rows takes a product: tiles of 16 << size rows, a slice's
 // k cut in 1 << split_bits; size -1: the pair kernel is quicker.  Of `products`
-// over k each.  Rows of 16-bit operands that do not lie on 128 bytes cost a box two
+// over k each.  What it compares are not times where the weights' bytes bound a
+// launch, as they have no term here: the e4m3 gate of 16 tokens on 8192/28672 counts
+// as 15 us, and reading its weights takes 69.  Rows of 16-bit operands that do not lie on 128 bytes cost a box two
 // lines for each of its rows (309 tokens on 1408/5376/2304 28 us, on 1400/5416/2280
 // 44 us here, 36 and 41 us by the pair kernel).
 struct FewShape {

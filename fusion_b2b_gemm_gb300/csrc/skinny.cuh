@@ -87,11 +87,12 @@ enum : int {  // barrier slots (8 bytes each)
   kSSlotTmem = 21,   // uint32 tensor-memory base, then the int abort flag
 };
 
-// Times in us, for the choice between this kernel and the pair kernel, and of its tile
+// Weights, in us, for the choice between this kernel and the pair kernel, and of its tile
 // (fitted to 1..1024 rows on widths of 512 to 65536, aligned and not: what they choose
 // is on average 1-2 % slower than the quickest choice): a slot of this one, the same
 // for each of its rows, what a second CTA on the SM adds, relatively, and the pair
-// kernel's start beyond this one's and its K panel.
+// kernel's start beyond this one's and its K panel.  They put the choices in order; the
+// sums are a launch's time only where its weights lie in L2 or its MMAs bound it.
 struct SkinnyCost {
   float slot, slot_row, second, pair, pair_panel;
 };

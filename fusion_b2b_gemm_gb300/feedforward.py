@@ -231,7 +231,9 @@ class GatedFeedForwardPlan(_Plan):
 
     ``dtype`` is "f16" or "bf16"; weights are ``w_gate``, ``w_up`` [width,
     hidden] and ``w_down`` [hidden, out_width] (default: width), all multiples
-    of 8; ``activation`` "silu" or "gelu" (tanh form).
+    of 8; ``activation`` "silu" or "gelu" (tanh form).  Hidden activations, and
+    gradients of the projections, are rounded to the plan's type: in "f16" a
+    magnitude of 65520 or more becomes an infinity.
     """
 
     def __init__(self, dtype: str, width: int, hidden: int, out_width: int | None = None, activation: str = "silu"):
@@ -417,7 +419,8 @@ class ScaledGemmPlan(_Plan):
     def run(self, a, a_scale, b, b_scale, out=None, stream=None):
         """The product [rows, n], on ``stream`` (default: torch's current one).  ``a_scale`` is fp32 [rows, k / 128],
         ``b_scale`` [n / 128, k / 128], rounded up, with any strides; a column of ``a_scale`` is best consecutive, as
-        :func:`quantize_blocks` lays it out."""
+        :func:`quantize_blocks` lays it out.  The two scales of a block are multiplied with each other, in fp32, before
+        they are applied."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 done = self.run(a, a_scale, b, b_scale, out)

@@ -465,7 +465,8 @@ b2b_status_t b2b_shared_attention_run(b2b_attn_plan_t plan, const b2b_shared_att
  *
  *   - Products are accumulated in fp32; activations and their slopes are fp32
  *     functions of fp32 sums, in the backward pass too.  Intermediates that a GEMM
- *     reads are rounded to its operand type, results once to theirs.
+ *     reads (H, dG, dU) are rounded to its operand type, results once to theirs: in
+ *     fp16 a magnitude of 65520 or more becomes an infinity, in H too.
  *   - Where few tiles would leave SMs idle, products are cut along k and the
  *     parts joined in fp32 in a fixed order: equal inputs give equal bits.
  *   - A plan is not modified by a run: runs on several streams may overlap, each
@@ -584,8 +585,10 @@ b2b_status_t b2b_scaled_ffn_run(b2b_ffn_plan_t plan, const b2b_scaled_ffn_t* run
 
 /*
  * D[r][c] = sum over blocks b of 128 of k:  a_scale(r, b) b_scale(c / 128, b) sum_j a[r][j] b[c][j],
- * the inner sums and the outer one in fp32.  A NaN among a block's values or in
- * its scale makes the results that it takes part in NaN.
+ * the inner sums and the outer one in fp32.  The two scales are multiplied with each
+ * other first, in fp32: where their product overflows, a result is an infinity or, of
+ * an inner sum of zero, NaN; below 2^-126 the product loses bits.  A NaN among a
+ * block's values or in its scale makes the results that it takes part in NaN.
  */
 typedef struct {
   int64_t rows;
