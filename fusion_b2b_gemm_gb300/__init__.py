@@ -232,12 +232,15 @@ def _differentiated(*inputs) -> bool:
     """Whether autograd would record a gradient for what is computed of these tensors, or carry a tangent on (which no_grad
     does not keep it from)."""
     import torch
-    if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
-        return True
+    if torch.is_grad_enabled():
+        for t in inputs:
+            if t.requires_grad:
+                return True
     forward_ad = torch.autograd.forward_ad
     # (outside every dual_level no tensor has a tangent; asking each takes half a microsecond)
-    return (getattr(forward_ad, "_current_level", 0) >= 0 and not torch.is_inference_mode_enabled()
-            and any(forward_ad.unpack_dual(t).tangent is not None for t in inputs))
+    if getattr(forward_ad, "_current_level", 0) < 0 or torch.is_inference_mode_enabled():
+        return False
+    return any(forward_ad.unpack_dual(t).tangent is not None for t in inputs)
 
 
 def _ptr(t) -> Optional[int]:

@@ -32,7 +32,7 @@ _TYPES = {"f16": "float16", "bf16": "bfloat16"}
 _INFERENCE, _TRAINING, _BACKWARD = 0, 1, 2  # B2B_FFN_*
 
 # Set when the first plan is made (_load): the package's other parts need neither torch nor the compiled module.
-torch = _raw_stream = _binding = None
+torch = _raw_stream = _increment_version = _binding = None
 
 # The argument structures, whose members all take eight bytes (b2b_matrix_t: data, row_stride; b2b_scales_t: data,
 # row_stride, block_stride), as the C functions read them.
@@ -74,11 +74,12 @@ def _load_binding():
 
 
 def _load():
-    global torch, _raw_stream, _binding
+    global torch, _raw_stream, _increment_version, _binding
     if _binding is None:
         import torch
         # (the public torch.cuda.current_stream() builds an object each time, 3 us)
         _raw_stream = torch._C._cuda_getCurrentRawStream
+        _increment_version = torch.autograd.graph.increment_version
         _binding = _load_binding()
 
 
@@ -133,7 +134,9 @@ def _kept(stream, device, done, given):
 
 def _written(*given):
     """Tells autograd that a call has changed tensors it was given, so that none of them passes for what was saved of it."""
-    torch.autograd.graph.increment_version([t for t in given if t is not None and not t.is_inference()])
+    changed = [t for t in given if t is not None and not t.is_inference()]
+    if changed:
+        _increment_version(changed)
 
 
 _WITHOUT = "(run it under torch.no_grad(), on the primals of dual tensors)"
@@ -168,9 +171,9 @@ class _Plan:
         # finds out what.
         self._bound = _binding.bind(*self._bind_args)
 
-    def _no_gradient(self, *inputs, into=()):
-        """Of inputs, and of tensors (or None) that results are written into."""
-        if _differentiated(*inputs, *(t for t in into if isinstance(t, torch.Tensor))):
+    def _no_gradient(self, *tensors):
+        """Of inputs, and of tensors that results are written into."""
+        if _differentiated(*tensors):
             raise RuntimeError(f"{type(self).__name__} records no gradient for its outputs {_WITHOUT}")
 
     def _workspace(self, like, rows, which=_INFERENCE):
@@ -265,9 +268,9 @@ class GatedFeedForwardPlan(_Plan):
             if done is not None:
                 return done
         tokens, operands = self._operands(x, w_gate, w_up, w_down)
-        self._no_gradient(x, w_gate, w_up, w_down, into=(out,))
         given = out
         out, oa = self._result(x, tokens, out)
+        self._no_gradient(x, w_gate, w_up, w_down, out)
         ws, wsp, need = self._workspace(x, tokens)
         self._call(_lib.b2b_ffn_forward, _forward_run(tokens, *operands, *oa, 0, 0, wsp, need))
         _written(given)
@@ -287,9 +290,9 @@ class GatedFeedForwardPlan(_Plan):
             if done is not None:
                 return done
         tokens, operands = self._operands(x, w_gate, w_up, w_down)
-        self._no_gradient(x, w_gate, w_up, w_down, into=(out,))
         given = out, kept
         out, oa = self._result(x, tokens, out)
+        self._no_gradient(x, w_gate, w_up, w_down, out)
         if kept is None:
             n = ctypes.c_size_t()
             _check(_lib.b2b_ffn_kept_bytes(self._h, tokens, ctypes.byref(n)), "b2b_ffn_kept_bytes")
@@ -335,7 +338,7 @@ class GatedFeedForwardPlan(_Plan):
         ka = self._kept_args(kept)
         accumulate = not isinstance(weight_grads, bool)
         grads = tuple(weight_grads) if accumulate else ()
-        self._no_gradient(dy, x, w_gate, w_up, w_down, into=grads)
+        self._no_gradient(dy, x, w_gate, w_up, w_down, *[g for g in grads if isinstance(g, torch.Tensor)])
         dx = self._new(x, tokens, self.width) if input_grad else None
         shapes = (self.width, self.hidden), (self.width, self.hidden), (self.hidden, self.out_width)
         if accumulate:
@@ -397,11 +400,11 @@ class ScaledFeedForwardPlan(_Plan):
         scales = (*_scale("gate_scale", gate_scale, _blocks(f), _blocks(d), dev),
                   *_scale("up_scale", up_scale, _blocks(f), _blocks(d), dev),
                   *_scale("down_scale", down_scale, _blocks(o), _blocks(f), dev))
-        self._no_gradient(x, w_gate, w_up, w_down, gate_scale, up_scale, down_scale, into=(out,))
         given = out
         if out is None:
             out = self._new(x, tokens, o)
         oa = _rows("out", out, self._torch_dtype, tokens, o, dev)[1:]
+        self._no_gradient(x, w_gate, w_up, w_down, gate_scale, up_scale, down_scale, out)
         ws, wsp, need = self._workspace(x, tokens)
         self._call(_lib.b2b_scaled_ffn_run, _scaled_run(tokens, *xa, *weights, *oa, *scales, wsp, need))
         _written(given)
@@ -435,11 +438,11 @@ class ScaledGemmPlan(_Plan):
         ba = _rows("b", b, f8, self.n, self.k, dev)[1:]
         scales = (*_scale("a_scale", a_scale, rows, _blocks(self.k), dev),
                   *_scale("b_scale", b_scale, _blocks(self.n), _blocks(self.k), dev))
-        self._no_gradient(a, b, a_scale, b_scale, into=(out,))
         given = out
         if out is None:
             out = self._new(a, rows, self.n)
         oa = _rows("out", out, self._torch_dtype, rows, self.n, dev)[1:]
+        self._no_gradient(a, b, a_scale, b_scale, out)
         ws, wsp, need = self._workspace(a, rows)
         self._call(_lib.b2b_scaled_gemm_run, _product_run(rows, *aa, *ba, *oa, *scales, wsp, need))
         _written(given)
