@@ -286,13 +286,30 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
   }
 }
 
-// The odd CTA of a pair after a wait that ran out: its last copies are counted
-// by the even CTA, which may have given up without arming its barrier for them.
-// They get 0.1 ms to land, some hundred times what a copy takes.
-__device__ __forceinline__ void settle() {
-  const uint64_t t0 = ptx::globaltimer_ns();
-  while (ptx::globaltimer_ns() - t0 < 100000) {
+// The end of a kernel on CTA pairs, by warp 0 once this CTA's roles have ended.
+// The even CTA's MMA thread commits to barriers of both CTAs, and what those
+// commits have still to deliver may find neither gone: the releases of the last
+// round's ring slots, and in the odd CTA the closing commit.  `words`: address of
+// the tensor-memory base, the abort flag, a word that is not read, and where the
+// loader stopped, its next slot and its parity << 8 (a slot that was never filled
+// passes at once).  After a wait that ran out not every slot is released, and
+// the odd CTA's last copies are counted by the even one, which may not have armed
+// its barrier for them: both get 0.1 ms, some hundred times what a copy takes.
+// (With these waits at the ends of the roles, the cascades of 16-bit operands spilled
+// 12 to 20 bytes more: four_stage_bf16 32.7 -> 34.1 us.)
+__device__ __forceinline__ void pair_exit(uint32_t empty0, int ring, uint32_t drain, uint32_t words, uint64_t budget_ns) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t gave_up, ring_end;
+  asm volatile("ld.shared.u32 %0, [%2 + 4];\n\tld.shared.u32 %1, [%2 + 12];" : "=&r"(gave_up), "=&r"(ring_end) : "r"(words) : "memory");
+  if (gave_up) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - t0 < 100000) {
+    }
+  } else if (lane < static_cast<uint32_t>(ring)) {
+    drain_wait(empty0 + 8u * lane, (ring_end >> 8) ^ (lane < (ring_end & 255u) ? 0u : 1u), budget_ns);
   }
+  if (lane == 31 && ptx::cluster_ctarank()) drain_wait(drain, 0, budget_ns);
+  __syncwarp();
 }
 
 // Tiles of one CTA, walked without divisions: batch b and 128-row tile mt.

@@ -72,7 +72,8 @@ enum : int {
                      //     epilogue (even CTA's)
   knDrain = 45,      // every MMA complete (exit)
   knSlotTmem = 46,   // uint32 TMEM base, then the int abort flag
-  knSlotReady = 47,  // uint32: ring slots whose copies have landed (even CTA)
+  knSlotReady = 47,  // uint32: ring slots whose copies have landed (even CTA), then the
+                     // uint32 where the ring's loader stopped
   knCFull0 = 48,     // [4] pass j of the first GEMM complete: converters
 };
 
@@ -421,16 +422,7 @@ __global__ void __launch_bounds__(kChainNThreads, 1)
           for (int kb = 0; kb < kpan_last && ok; kb += kps_last)
             ok = load(S - 1, c.b, m0, kb, j * NF, NF, kps_last);
       }
-      // the releases of the last round's slots arrive in both CTAs, and
-      // before exit (a slot that was never filled passes at once)
-      for (int j = 0; j < p.nslot && ok; ++j) {
-        ok = bw.wait(bar(knEmpty + slot), phase ^ 1u);
-        if (++slot == static_cast<uint32_t>(p.nslot)) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!leader && !ok) settle();
+      tmem_slot[3] = slot | phase << 8;
       // copies in flight land before exit (the even CTA's barriers count both
       // CTAs' copies; the odd CTA waits at the cluster barrier before exit)
       const uint64_t n = static_cast<uint64_t>(p.nslot);
@@ -821,15 +813,13 @@ __global__ void __launch_bounds__(kChainNThreads, 1)
       }
     }
     if (epi && lane == 0) bulk_wait_all();
-    // the even CTA's MMA thread commits to the odd CTA's barriers too, this
-    // one last
-    if (!leader && elected) drain_wait(bar(knDrain), 0, p.budget_ns);
   }
 
   __syncthreads();
   // neither CTA leaves (or frees tensor memory) while the other may still
   // arrive on its barriers or the even CTA's MMAs may still write it: what the
-  // MMAs' commits have to deliver has arrived in either, by the waits above
+  // MMAs' commits have to deliver has arrived in either
+  if (threadIdx.x < 32) pair_exit(bar(knEmpty), p.nslot, bar(knDrain), bar(knSlotTmem), p.budget_ns);
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();

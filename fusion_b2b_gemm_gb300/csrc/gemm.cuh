@@ -93,6 +93,7 @@ enum : int {  // barrier slots (8 bytes each)
   kGBDrain = 20,
   kGBTop = 21,       // [4] the warps of a quadrant have written their rows' largest magnitudes
   kGSlotTmem = 25,   // uint32 tensor-memory base, then the int abort flag
+  kGSlotEnd = 26,    // nothing, then the uint32 where the ring's loader stopped
 };
 
 // One product of a launch: D [M][N].  Tiles are numbered problem after problem.
@@ -466,16 +467,7 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
           }
         }
       }
-      // The releases of the last round's slots arrive in both CTAs, and before exit.  (A
-      // slot that was never filled passes at once.)
-      for (int j = 0; j < kRing && ok; ++j) {
-        ok = bw.wait1(bar(kGBEmpty + slot), phase ^ 1u);
-        if (++slot == kRing) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!leader && !ok) settle();
+      tmem_slot[3] = slot | phase << 8;
       // Copies in flight land before exit (the even CTA's barriers count both CTAs').
       const unsigned long long tail = !leader ? 0 : (issued < kRing ? issued : kRing);
       for (unsigned long long j = 0; j < tail; ++j) {
@@ -857,14 +849,13 @@ __global__ void __launch_bounds__(gemm_threads(IN == kGemmE4M3), 1)
       }
     }
     if (lane == 0) bulk_wait_all();
-    // The even CTA's MMA thread commits to the odd CTA's barriers too, this one last.
-    if (!leader && warp == 4 && lane == 0) drain_wait(bar(kGBDrain), 0, p.budget_ns);
   }
 
   __syncthreads();
   // Neither CTA leaves, or frees tensor memory, while the other may still
   // arrive on its barriers or the even CTA's MMAs may still write it: what the
-  // MMAs' commits have to deliver has arrived in either, by the waits above.
+  // MMAs' commits have to deliver has arrived in either.
+  if (warp == 0) pair_exit(bar(kGBEmpty), kRing, bar(kGBDrain), bar(kGSlotTmem), p.budget_ns);
   cluster_sync();
   if (warp == 2) {
     tc_fence_after();

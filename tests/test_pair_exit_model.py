@@ -6,9 +6,9 @@ arrival in either CTA, delivered some time after the MMAs are done, and not in
 step with the other CTA's.  Shared memory that an arrival is still on its way to
 must not be given up: an arrival at a CTA that has left is an error here.  What
 each CTA waits for before the closing cluster barrier has to rule it out: its
-loader for the release of the last ring round's slots, its epilogue for the last
-accumulator, and one thread (the even CTA's MMA thread, the odd CTA's epilogue)
-for the last commit of all.  The waits that the kernels had before, and each of
+epilogue for the last accumulator, and pair_exit (chain_tc.cuh), once the CTA's roles
+have ended, for the release of the last ring round's slots and, in the odd CTA, for
+the last commit of all (in the even one its MMA thread does).  The waits that the kernels had before, and each of
 these left out, are caught.
 """
 import pytest
@@ -40,7 +40,7 @@ def pair_exit(seed, units, ring, missing=()):
     drain = [Inbox(1, c) for c in ctas]
     copies, tensor = [w.engine(), w.engine()], w.engine()
     panels = [(u, k) for u, n in enumerate(units) for k in range(n)]
-    running = [0]
+    running, ends, at_barrier = [0, 0], [None, None], set()
 
     def commit(*bars):
         """An arrival at each barrier once the MMAs issued so far are done: on its own from then on."""
@@ -57,12 +57,7 @@ def pair_exit(seed, units, ring, missing=()):
             slot += 1
             if slot == ring:
                 slot, phase, uses = 0, phase ^ 1, uses + 1
-        if "releases" not in missing:
-            for _ in range(ring):  # (a slot without a use passes at once)
-                yield (empty[cta][slot], phase ^ 1, uses - 1)
-                slot += 1
-                if slot == ring:
-                    slot, phase, uses = 0, phase ^ 1, uses + 1
+        ends[cta] = slot, phase, uses
 
     def mma():
         for i, (u, k) in enumerate(panels):
@@ -81,18 +76,29 @@ def pair_exit(seed, units, ring, missing=()):
             yield (acc_full[cta][u & 1], u >> 1 & 1, u >> 1)
             yield True  # (the loads)
             acc_empty[u & 1].arrive()
+
+    def leave(cta):
+        """pair_exit: the slots before the loader's next one in this round, the others in the last (without a use: at once)."""
+        slot, phase, uses = ends[cta]
+        if "releases" not in missing:
+            for i in range(ring):
+                yield (empty[cta][i], phase, uses) if i < slot else (empty[cta][i], phase ^ 1, uses - 1)
         if cta == 1 and "last commit" not in missing:
             yield (drain[1], 0, 0)
 
-    def role(r):
-        running[0] += 1
+    def role(cta, r):
+        running[cta] += 1
         yield from r
-        running[0] -= 1
-        if not running[0]:  # (the cluster barrier: both CTAs leave)
+        running[cta] -= 1
+        if running[cta]:
+            return
+        yield from leave(cta)  # (this CTA's roles have ended)
+        at_barrier.add(cta)
+        if len(at_barrier) == 2:  # (the cluster barrier: both CTAs leave)
             for c in ctas:
                 c["left"] = True
 
-    w.run([role(r) for r in (loader(0), loader(1), mma(), epilogue(0), epilogue(1))])
+    w.run([role(*r) for r in ((0, loader(0)), (1, loader(1)), (0, mma()), (0, epilogue(0)), (1, epilogue(1)))])
     assert all(c["left"] for c in ctas)
 
 
@@ -109,9 +115,9 @@ def test_no_arrival_finds_its_cta_gone(units, ring):
 @pytest.mark.parametrize("missing", [("releases", "last commit"), ("releases",), ("last commit",)], ids="-".join)
 def test_waits_left_out_are_caught(missing):
     caught = 0
-    for seed in range(200):
+    for seed in range(400):
         try:
-            pair_exit(seed, [3, 1, 1, 9], 5, missing)
+            pair_exit(seed, [3, 1, 1, 9], 2, missing)
         except Broken as e:
             assert "left" in str(e)
             caught += 1
@@ -129,7 +135,7 @@ def gives_up(seed, ring, settle):
     running = [0]
 
     class Landed:
-        """The time that settle() waits is more than a copy takes."""
+        """The time that pair_exit then waits is more than a copy takes."""
 
         def ready(self, *_):
             return not copies[1]
